@@ -30,7 +30,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm_epi
 
 EXPORTED = ["gemm_epi_plan", "gemm_epi_execute", "drelu_bgrad_execute", "gemm_epi_free", "gemm_epi_last_error",
             "gemm_epi_query", "gemm_epi_status", "gemm_epi_unfused_execute", "drelu_bgrad_unfused_execute",
-            "drelu_bgrad_execute_noalloc", "gemm_epi_wgrad_execute", "gemm_epi_set_bias_f32", "gemm_epi_plan_ex"]
+            "drelu_bgrad_execute_noalloc", "gemm_epi_wgrad_execute", "gemm_epi_set_bias_f32", "gemm_epi_plan_ex",
+            "gemm_epi_grouped_plan", "gemm_epi_grouped_execute", "gemm_epi_grouped_drelu_bgrad_execute",
+            "gemm_epi_grouped_wgrad_execute"]
 FLAG_W_NK = 1  # GEMM_EPI_FLAG_W_NK
 FLAG_OUT_F32 = 2  # GEMM_EPI_FLAG_OUT_F32
 
@@ -91,6 +93,14 @@ def lib() -> ctypes.CDLL:
         L.gemm_epi_set_bias_f32.argtypes = [vp, ci]
         L.gemm_epi_wgrad_execute.restype = ci
         L.gemm_epi_wgrad_execute.argtypes = [vp] * 6
+        L.gemm_epi_grouped_plan.restype = vp
+        L.gemm_epi_grouped_plan.argtypes = [i64, i64, i64, i64, ci, ci, ctypes.c_uint32]
+        L.gemm_epi_grouped_execute.restype = ci
+        L.gemm_epi_grouped_execute.argtypes = [vp] * 8
+        L.gemm_epi_grouped_drelu_bgrad_execute.restype = ci
+        L.gemm_epi_grouped_drelu_bgrad_execute.argtypes = [vp] * 8
+        L.gemm_epi_grouped_wgrad_execute.restype = ci
+        L.gemm_epi_grouped_wgrad_execute.argtypes = [vp] * 7
         _lib = L
     return _lib
 
@@ -316,4 +326,86 @@ class Plan:
         dW = torch.empty((self.K, self.N), dtype=self.out_dtype, device=X.device)
         dbias = torch.empty((self.K,), dtype=torch.float32, device=X.device) if with_dbias else None
         self.gemm_epi_wgrad_execute(X, dZ, dW, dbias, stream)
+        return (dW, dbias) if with_dbias else dW
+
+
+class GroupedPlan(Plan):
+    """A plan for E products over rows sorted by expert: expert e owns rows
+    ``offsets[e] .. offsets[e+1] - 1`` of X (T rows in all), where ``offsets``
+    is an int32 CUDA tensor of E + 1 entries that only the kernel reads.
+
+    W is E x K x N (``w_nk``: E x N x K), bias E x N, dW E x K x N, dbias E x N
+    (DRELU_BGRAD) or E x K (WGRAD). Rows outside every expert are left as they
+    were in Y, dZ and aux; an expert without rows gets zeros in dW and dbias.
+    Tensors must be on the device that was current when the plan was made; the
+    default stream is that device's current one."""
+
+    def __init__(self, E: int, T: int, N: int, K: int, dtype: torch.dtype, epilog: str | int, w_nk: bool = False,
+                 out_f32: bool = False):
+        self.E, self.T, self.N, self.K = E, T, N, K
+        self.out_dtype = torch.float32 if out_f32 else dtype
+        self.w_shape = (E, N, K) if w_nk else (E, K, N)
+        self.dtype = self.bias_dtype = dtype
+        self.epilog = EPILOGS[epilog] if isinstance(epilog, str) else epilog
+        self.aux_words = (N + 31) // 32
+        self.handle = None
+        self.handle = lib().gemm_epi_grouped_plan(E, T, N, K, DTYPES[dtype], self.epilog,
+                                                  (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0))
+        if not self.handle:
+            raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _p(self, t, shape, dtype, name):
+        ptr = _ptr(t, shape, dtype, name)
+        if t is not None and t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
+        return ptr
+
+    def _s(self, stream) -> int:
+        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _aux(self, aux):
+        spec = self.aux_spec() or ((self.T, self.aux_words), torch.int32)
+        return self._p(aux, spec[0], spec[1], "aux")
+
+    def gemm_epi_grouped_execute(self, X, W, bias, offsets, Y, aux=None, stream=None):
+        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        _check(lib().gemm_epi_grouped_execute(
+            self.handle, self._p(X, (T, K), dt, "X"), self._p(W, self.w_shape, dt, "W"),
+            self._p(bias, (E, N), self.bias_dtype, "bias"), self._p(offsets, (E + 1,), torch.int32, "offsets"),
+            self._p(Y, (T, N), self.out_dtype, "Y"), self._aux(aux), self._s(stream)))
+
+    def gemm_epi_grouped_drelu_bgrad_execute(self, dY2, W2, aux, offsets, dZ, dbias, stream=None):
+        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        _check(lib().gemm_epi_grouped_drelu_bgrad_execute(
+            self.handle, self._p(dY2, (T, K), dt, "dY2"), self._p(W2, self.w_shape, dt, "W2"),
+            self._p(aux, (T, self.aux_words), torch.int32, "aux"),
+            self._p(offsets, (E + 1,), torch.int32, "offsets"), self._p(dZ, (T, N), self.out_dtype, "dZ"),
+            self._p(dbias, (E, N), torch.float32, "dbias"), self._s(stream)))
+
+    def gemm_epi_grouped_wgrad_execute(self, X, dZ, offsets, dW, dbias=None, stream=None):
+        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        _check(lib().gemm_epi_grouped_wgrad_execute(
+            self.handle, self._p(X, (T, K), dt, "X"), self._p(dZ, (T, N), dt, "dZ"),
+            self._p(offsets, (E + 1,), torch.int32, "offsets"), self._p(dW, (E, K, N), self.out_dtype, "dW"),
+            self._p(dbias, (E, K), torch.float32, "dbias"), self._s(stream)))
+
+    # conveniences that allocate their outputs (rows outside every expert: zeros)
+    def forward(self, X, W, bias, offsets, stream=None):
+        Y = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=X.device)
+        spec = self.aux_spec()
+        aux = torch.zeros(spec[0], dtype=spec[1], device=X.device) if spec else None
+        self.gemm_epi_grouped_execute(X, W, bias, offsets, Y, aux, stream)
+        return Y, aux
+
+    def backward(self, dY2, W2, aux, offsets, stream=None):
+        dZ = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=dY2.device)
+        dbias = torch.empty((self.E, self.N), dtype=torch.float32, device=dY2.device)
+        self.gemm_epi_grouped_drelu_bgrad_execute(dY2, W2, aux, offsets, dZ, dbias, stream)
+        return dZ, dbias
+
+    def wgrad(self, X, dZ, offsets, with_dbias=False, stream=None):
+        dW = torch.empty((self.E, self.K, self.N), dtype=self.out_dtype, device=X.device)
+        dbias = torch.empty((self.E, self.K), dtype=torch.float32, device=X.device) if with_dbias else None
+        self.gemm_epi_grouped_wgrad_execute(X, dZ, offsets, dW, dbias, stream)
         return (dW, dbias) if with_dbias else dW

@@ -1,102 +1,15 @@
 // gemm_epi.cu -- C ABI of the fused linear-layer GEMM + epilogue library
 // (declared in include/gemm_epi.h): plan validation and kernel choice,
 // TMA descriptor encoding, launches, the watchdog status word and errors.
-#include <cuda.h>
-#include <cuda_runtime.h>
-
-#include <cstdarg>
-#include <cstdio>
-#include <cstdlib>
-#include <cstring>
-#include <mutex>
-#include <string>
-#include <unordered_set>
-
-#include "../../include/gemm_epi.h"
 #include "aux_kernels.cuh"
-#include "kernel_table.h"
+#include "host_common.h"
 #include "skinny_kernel.cuh"
 #include "tile2_kernel.cuh"
 #include "tile_kernel.cuh"
 
+using namespace ge_host;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(GEMM_EPI_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-// ---------------------------------------------------------------- registry
-std::mutex g_mu;
-std::unordered_set<gemm_epi_plan_s*>& live_plans() {
-  static std::unordered_set<gemm_epi_plan_s*> s;
-  return s;
-}
-
-// ----------------------------------------------------- driver entry points
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Fault-injection hooks for the tests take effect only while
-// GEMM_EPI_TEST_HOOKS=1 is set as well, so that one stray variable inherited
-// by a production process cannot make its plans stall or fail.
-bool test_hooks_on() {
-  const char* f = getenv("GEMM_EPI_TEST_HOOKS");
-  return f && atoi(f) == 1;
-}
-bool test_hook(const char* name) {
-  const char* f = test_hooks_on() ? getenv(name) : nullptr;
-  return f && atoi(f) != 0;
-}
-
-// GEMM_EPI_INJECT_ENCODE_FAILURE makes every tensor-map encode fail, so an
-// execute call must return GEMM_EPI_ERR_CUDA before it launches anything.
-bool inject_encode_failure() { return test_hook("GEMM_EPI_INJECT_ENCODE_FAILURE"); }
-
-// The watchdog settings a launch carries: the limit of each bounded wait
-// (2 s; GEMM_EPI_WAIT_TIMEOUT_MS overrides) and, for the watchdog tests,
-// GEMM_EPI_INJECT_STALL -- the MMA issuer withholds its first tile's
-// completion signal, so the epilogue's wait runs out and the kernel reports
-// ERR_TIMEOUT. Read when a plan is created and on every call of the
-// allocation-free entry point.
-struct WatchdogEnv {
-  uint64_t timeout_ns = 2000000000ull;
-  int inject_stall = 0;
-};
-WatchdogEnv watchdog_env() {
-  WatchdogEnv w;
-  if (const char* t = getenv("GEMM_EPI_WAIT_TIMEOUT_MS")) {
-    const long long ms = atoll(t);
-    if (ms > 0) w.timeout_ns = (uint64_t)ms * 1000000ull;
-  }
-  w.inject_stall = test_hook("GEMM_EPI_INJECT_STALL") ? 1 : 0;
-  return w;
-}
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 // 2-D row-major tensor of 16-bit elements: `inner` contiguous columns,
 // `outer` rows; box of box_inner x box_outer with 128-byte swizzle (operand
@@ -177,14 +90,6 @@ static_assert(static_cast<int>(GEMM_EPI_BIAS) == ge::EPI_BIAS && static_cast<int
                   static_cast<int>(GEMM_EPI_GELU_AUX_BIAS) == ge::EPI_GELU_AUX_BIAS,
               "the public epilog values are the kernels' epilog kinds");
 
-struct TileCfg {
-  int BN = 256, stages = 4;
-  TileKernelFn fn = nullptr;
-  uint32_t smem = 0;
-  bool pair = false;  // CTA-pair kernel, launched in clusters of 2
-  int threads = ge::kThreads;
-};
-
 // bk: the weight is given N x K (GEMM_EPI_FLAG_W_NK); never with WGRAD
 TileCfg pair_cfg(int epi, bool bf16, bool bk, bool split = false) {
   TileCfg c;
@@ -251,16 +156,6 @@ TileCfg tile_cfg(int BN, int epi, bool bf16, bool bk) {
             : (bf16 ? ge_inst::tile_bf16_mn(c.BN, epi) : ge_inst::tile_f16_mn(c.BN, epi));
   return c;
 }
-
-int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
-
-struct SkinnyCfg {
-  int TP = 16;
-  int KPS = 1;  // 64-deep k-blocks per pipeline stage
-  SkinnyKernelFn fn = nullptr;
-  uint32_t smem = 0;
-  int stages = 0;
-};
 
 template <int TP, int KPS>
 SkinnyCfg skinny_cfg_kps(int epi, bool bf16) {
@@ -387,76 +282,7 @@ bool use_skinny(int64_t T) {
 
 }  // namespace
 
-struct gemm_epi_plan_s {
-  int64_t T, N, K;   // the kernels' rows, columns and contraction length
-  int64_t uT, uK;    // the caller's T and K (WGRAD: rows = uK, contraction = uT)
-  int dtype, epilog;
-  int device, num_sms;
-  int m_tiles, n_tiles, k_blocks, num_tiles, aux_words, grid, group_m;
-  int raster_n = 0;  // tile order by column groups (see choose_raster)
-  int pair_split = 0;        // CTA pairs in stream-K mode
-  int pair_sk_first = 1;     // stream-K tiles before the whole tiles
-  int pair_max_segs = 1;
-  float* pair_slots = nullptr;  // stream-K fp32 partials
-  int* pair_flags = nullptr;    // stream-K segment counters, zero between launches
-  int n_pair_flags = 0;
-  size_t pair_bytes = 0;
-  TileCfg cfg;       // fused kernel
-  TileCfg cfg_store; // unfused GEMM (plain store)
-  float* partials = nullptr;  // DRELU_BGRAD: m_tiles x N
-  size_t partial_bytes = 0;
-  int* col_tickets = nullptr;  // DRELU_BGRAD on the tile kernels: n_tickets counters
-  int n_tickets = 0;
-  int* status_host = nullptr;
-  int* status_dev = nullptr;
-  uint64_t timeout_ns = 0;
-  int inject_stall = 0;  // GEMM_EPI_INJECT_STALL at plan time (watchdog tests)
-  int tail_split = 1;    // GEMM_EPI_TAIL_SPLIT=0 keeps whole tiles in the pair kernel's last round
-  int bias_f32 = 0;      // gemm_epi_set_bias_f32: the forward bias is fp32
-  int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
-  int out_f32 = 0;       // GEMM_EPI_FLAG_OUT_F32: Y / dZ / dW written as fp32
-  int cache_hints = 0;   // few-row kernel: L2 eviction policies on the operand loads (GEMM_EPI_CACHE_HINTS)
-  // tensor-map cache
-  const void* a_ptr = nullptr;
-  const void* b_ptr = nullptr;
-  const void* y_ptr = nullptr;
-  const void* aux_ptr = nullptr;
-  CUtensorMap tmA, tmB, tmY, tmAux;
-  // few-row kernel (kernel == 1)
-  int kernel = 0;
-  SkinnyCfg sk;
-  int sk_grid = 0, sk_kbt = 0, sk_total = 0, sk_max_segs = 1, sk_prefetch = 0;
-  float* sk_partials = nullptr;
-  int* sk_tickets = nullptr;
-  size_t sk_bytes = 0;
-  const void* xs_ptr = nullptr;
-  CUtensorMap tmXs;  // the row operand with a TP-row box
-  const void* ws_ptr = nullptr;
-  CUtensorMap tmWs;  // the weight operand with a 64·KPS-row box
-};
-
 namespace {
-
-gemm_epi_plan_s* lookup(gemm_epi_plan_t p) {
-  std::lock_guard<std::mutex> g(g_mu);
-  return live_plans().count(p) ? p : nullptr;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int take_status(gemm_epi_plan_s* p) {
-  volatile int* s = p->status_host;
-  const int v = *s;
-  if (v != 0) {
-    *s = 0;
-    // an interrupted launch may have left split-tile tickets counted
-    if (p->sk_tickets) cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)ceil_div(p->N, 128));
-    if (p->col_tickets) cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
-    if (p->pair_flags) cudaMemset(p->pair_flags, 0, sizeof(int) * (size_t)p->n_pair_flags);
-    return fail(GEMM_EPI_ERR_TIMEOUT, "a kernel of this plan gave up waiting (watchdog code 0x%x)", v);
-  }
-  return GEMM_EPI_OK;
-}
 
 int prepare_maps(gemm_epi_plan_s* p, const void* A, const void* B) {
   if (A != p->a_ptr && p->epilog == GEMM_EPI_WGRAD) {
@@ -924,7 +750,16 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
   info->epilog = p->epilog;
   info->kernel = p->kernel;
   info->num_sms = p->num_sms;
-  if (p->kernel == 1) {
+  if (p->kind != 0) {
+    info->tile_m = p->gr.pair ? 256 : 128;  // features per tile (the MMA's M)
+    info->tile_n = p->gr.TR;                // rows per tile at most (the MMA's N)
+    info->tile_k = p->gr.BK;
+    info->stages = p->gr.stages;
+    info->split_k = 1;
+    info->grid = p->grid;
+    info->launches = p->gr.launches;
+    info->workspace_bytes = p->partial_bytes + sizeof(int) * (size_t)p->n_tickets;
+  } else if (p->kernel == 1) {
     info->tile_m = 128;  // features per tile (the MMA's M)
     info->tile_n = p->sk.TP;  // padded rows (the MMA's N)
     info->tile_k = ge::kBK * p->sk.KPS;  // k per pipeline stage
@@ -957,8 +792,9 @@ int gemm_epi_status(gemm_epi_plan_t plan) {
 
 int gemm_epi_execute(gemm_epi_plan_t plan, const void* X, const void* W, const void* bias, void* Y, uint32_t* aux,
                      cudaStream_t stream) {
-  gemm_epi_plan_s* p = lookup(plan);
-  if (!p) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_execute: unknown plan");
+  int code = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 0, "gemm_epi_execute", &code);
+  if (!p) return code;
   if (p->epilog == GEMM_EPI_DRELU_BGRAD || p->epilog == GEMM_EPI_WGRAD)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_execute called on a %s plan",
                 p->epilog == GEMM_EPI_WGRAD ? "WGRAD" : "DRELU_BGRAD");
@@ -993,8 +829,9 @@ int gemm_epi_execute(gemm_epi_plan_t plan, const void* X, const void* W, const v
 
 int drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2, const uint32_t* aux, void* dZ,
                         float* dbias, cudaStream_t stream) {
-  gemm_epi_plan_s* p = lookup(plan);
-  if (!p) return fail(GEMM_EPI_ERR_INVALID_ARG, "drelu_bgrad_execute: unknown plan");
+  int code = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 0, "drelu_bgrad_execute", &code);
+  if (!p) return code;
   if (p->epilog != GEMM_EPI_DRELU_BGRAD)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "drelu_bgrad_execute called on a forward plan");
   if (!dY2 || !W2 || !aux || !dZ || !dbias)
@@ -1026,8 +863,9 @@ int drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2, c
 
 int gemm_epi_unfused_execute(gemm_epi_plan_t plan, const void* X, const void* W, const void* bias, void* T1, void* T2,
                              void* Y, uint32_t* aux, cudaStream_t stream) {
-  gemm_epi_plan_s* p = lookup(plan);
-  if (!p) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_unfused_execute: unknown plan");
+  int code = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 0, "gemm_epi_unfused_execute", &code);
+  if (!p) return code;
   if (p->epilog == GEMM_EPI_DRELU_BGRAD || p->epilog == GEMM_EPI_WGRAD || p->epilog == GEMM_EPI_NONE)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_unfused_execute: the plan's epilog has nothing to unfuse");
   if (p->out_f32)
@@ -1094,8 +932,9 @@ int gemm_epi_set_bias_f32(gemm_epi_plan_t plan, int bias_f32) {
 
 int gemm_epi_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ, void* dW, float* dbias,
                            cudaStream_t stream) {
-  gemm_epi_plan_s* p = lookup(plan);
-  if (!p) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_wgrad_execute: unknown plan");
+  int code = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 0, "gemm_epi_wgrad_execute", &code);
+  if (!p) return code;
   if (p->epilog != GEMM_EPI_WGRAD)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_wgrad_execute called on a plan whose epilog is not WGRAD");
   if (!X || !dZ || !dW) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_wgrad_execute: NULL X, dZ or dW");
@@ -1124,8 +963,9 @@ int gemm_epi_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ, 
 
 int drelu_bgrad_unfused_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2, const uint32_t* aux, void* G,
                                 void* dZ, float* dbias, cudaStream_t stream) {
-  gemm_epi_plan_s* p = lookup(plan);
-  if (!p) return fail(GEMM_EPI_ERR_INVALID_ARG, "drelu_bgrad_unfused_execute: unknown plan");
+  int code = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 0, "drelu_bgrad_unfused_execute", &code);
+  if (!p) return code;
   if (p->epilog != GEMM_EPI_DRELU_BGRAD)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "drelu_bgrad_unfused_execute called on a forward plan");
   if (p->out_f32)

@@ -1,0 +1,359 @@
+// grouped.cu -- C ABI of the products grouped by expert: plan validation and
+// kernel choice, TMA descriptors, launches.
+#include "grouped_kernel.cuh"
+#include "host_common.h"
+
+using namespace ge_host;
+
+namespace {
+
+// Rows per tile, from the mean number of rows per expert (the plan knows no
+// offsets; any division of the rows is computed right by each).
+int choose_tr(int64_t E, int64_t T, int epilog) {
+  if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
+    const int v = atoi(f);
+    if (v == 128 || v == 256 || (v == 32 && epilog != GEMM_EPI_WGRAD)) return v;
+  }
+  const int64_t mean = (T + E - 1) / E;
+  if (epilog == GEMM_EPI_WGRAD) return 256;
+  return mean <= 32 ? 32 : mean <= 128 ? 128 : 256;
+}
+
+void release(gemm_epi_plan_s* p) {
+  if (p->partials) cudaFree(p->partials);
+  if (p->col_tickets) cudaFree(p->col_tickets);
+  if (p->status_host) cudaFreeHost(p->status_host);
+  delete p;
+}
+
+int max_pairs(const GroupedCfg& g, int sms) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
+  lc.blockDim = dim3((unsigned)g.threads, 1, 1);
+  lc.dynamicSmemBytes = g.smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, (const void*)g.fn, &lc) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return sms / 2;
+  }
+  return n < sms / 2 ? n : sms / 2;
+}
+
+ge::GroupedParams params(const gemm_epi_plan_s* p, const int32_t* offsets) {
+  ge::GroupedParams k{};
+  k.T = (int32_t)p->uT;
+  k.N = (int32_t)p->N;
+  k.K = (int32_t)p->uK;
+  k.E = p->gr.E;
+  k.n_ft = p->gr.n_ft;
+  k.n_kt = p->gr.n_kt;
+  k.k_blocks = p->k_blocks;
+  k.group = p->gr.group;
+  k.aux_words = p->aux_words;
+  k.nfb = ceil_div(p->N, 128);
+  k.offsets = offsets;
+  k.status = p->status_dev;
+  k.timeout_ns = p->timeout_ns;
+  k.bias_f32 = p->bias_f32;
+  k.out_f32 = p->out_f32;
+  k.inject_stall = p->inject_stall;
+  return k;
+}
+
+int launch(const gemm_epi_plan_s* p, const CUtensorMap& a, const CUtensorMap& b, const ge::GroupedParams& k,
+           cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p->grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)p->gr.threads, 1, 1);
+  cfg.dynamicSmemBytes = p->gr.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p->gr.pair ? 2 : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, p->gr.fn, a, b, k);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped kernel launch");
+  return GEMM_EPI_OK;
+}
+
+// the operands of a forward or DRELU_BGRAD call
+int forward_maps(const gemm_epi_plan_s* p, const void* X, const void* W, CUtensorMap* a, CUtensorMap* b) {
+  const auto u16 = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  const uint64_t N = (uint64_t)p->N, K = (uint64_t)p->uK, E = (uint64_t)p->gr.E;
+  int rc = p->w_nk ? encode_3d(a, u16, W, K, N, E, ge::kBK, 128, "the weights")
+                   : encode_3d(a, u16, W, N, K, E, 64, (uint32_t)p->gr.BK, "the weights");
+  if (rc) return rc;
+  const int trc = p->gr.pair ? p->gr.TR / 2 : p->gr.TR;
+  return encode_3d(b, u16, X, K, (uint64_t)p->uT, 1, ge::kBK, trc < 64 ? (uint32_t)trc : 64u, "the row operand");
+}
+
+gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype, gemm_epi_epilog epilog,
+                          uint32_t flags) {
+  if ((flags & ~(uint32_t)(GEMM_EPI_FLAG_W_NK | GEMM_EPI_FLAG_OUT_F32)) != 0) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags);
+    return nullptr;
+  }
+  const bool w_nk = (flags & GEMM_EPI_FLAG_W_NK) != 0;
+  if (w_nk && epilog == GEMM_EPI_WGRAD) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "GEMM_EPI_FLAG_W_NK applies to the weight of forward and DRELU_BGRAD plans");
+    return nullptr;
+  }
+  if (E < 1 || E > ge::kMaxExperts) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "bad number of experts %lld (need 1 to %d)", (long long)E, ge::kMaxExperts);
+    return nullptr;
+  }
+  if (T < 1 || N < 8 || K < 8 || (N % 8) != 0 || (K % 8) != 0) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "bad shape T=%lld N=%lld K=%lld (need T>=1, N,K>=8 and multiples of 8)",
+         (long long)T, (long long)N, (long long)K);
+    return nullptr;
+  }
+  if (T > (int64_t)1 << 30 || N > (int64_t)1 << 24 || K > (int64_t)1 << 24 || T * N > ((int64_t)1 << 40) ||
+      K * N > ((int64_t)1 << 37)) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
+    return nullptr;
+  }
+  if (dtype != GEMM_EPI_F16 && dtype != GEMM_EPI_BF16) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    return nullptr;
+  }
+  if (epilog < GEMM_EPI_BIAS || epilog > GEMM_EPI_GELU_AUX_BIAS) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown epilog %d", (int)epilog);
+    return nullptr;
+  }
+  const bool wgrad = epilog == GEMM_EPI_WGRAD;
+  const int tr = choose_tr(E, T, (int)epilog);
+  const int64_t n_ft = (N + (tr == 256 ? 255 : 127)) / (tr == 256 ? 256 : 128);
+  const int64_t row_tiles = T / tr + (E < T ? E : T);  // at most: every expert may end in a part of a tile
+  const int64_t tiles = wgrad ? E * n_ft * ((K + tr - 1) / tr) : row_tiles * n_ft;
+  if (tiles >= ((int64_t)1 << 31) - 65536) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
+    return nullptr;
+  }
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "cudaGetDevice");
+    return nullptr;
+  }
+  int major = 0, minor = 0, sms = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (major != 10 || minor != 0) {
+    fail(GEMM_EPI_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.0 (sm_100a)", dev,
+         major, minor);
+    return nullptr;
+  }
+  auto* p = new gemm_epi_plan_s();
+  p->kind = 1;
+  p->uT = p->T = T;
+  p->uK = p->K = K;
+  p->N = N;
+  p->dtype = dtype;
+  p->epilog = epilog;
+  p->device = dev;
+  p->num_sms = sms;
+  p->w_nk = w_nk ? 1 : 0;
+  p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
+  p->aux_words = ceil_div(N, 32);
+  const bool bf16 = dtype == GEMM_EPI_BF16;
+  const ge_inst::GroupedInstance inst =
+      bf16 ? (w_nk ? ge_inst::grouped_bf16_nk(tr, (int)epilog) : ge_inst::grouped_bf16_mn(tr, (int)epilog))
+           : (w_nk ? ge_inst::grouped_f16_nk(tr, (int)epilog) : ge_inst::grouped_f16_mn(tr, (int)epilog));
+  GroupedCfg& g = p->gr;
+  g.fn = inst.fn;
+  g.smem = inst.smem;
+  g.threads = inst.threads;
+  g.stages = inst.stages;
+  g.BK = inst.bk;
+  g.TR = tr;
+  g.pair = tr == 256;
+  g.E = (int)E;
+  g.n_ft = (int)n_ft;
+  g.n_kt = ceil_div(K, tr);
+  p->kernel = tr == 32 ? 3 : tr == 128 ? 4 : 5;
+  p->k_blocks = ceil_div(K, g.BK);
+  // row tiles whose X (about 48 MB, under half of the L2) stays in L2 while
+  // the group sweeps the expert's features, each block of the weight being
+  // read once per group; WGRAD holds a group of k tiles of X the same way
+  const int64_t rows = wgrad ? (T + E - 1) / E : K;
+  int64_t group = (int64_t)(48 << 20) / (2 * (int64_t)tr * rows);
+  g.group = (int)(group < 1 ? 1 : group > 65536 ? 65536 : group);
+  if (wgrad && g.group > g.n_kt) g.group = g.n_kt;
+  const WatchdogEnv wd = watchdog_env();
+  p->timeout_ns = wd.timeout_ns;
+  p->inject_stall = wd.inject_stall;
+  if (!g.fn) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "no kernel instance for this epilog and layout");
+    release(p);
+    return nullptr;
+  }
+  e = cudaFuncSetAttribute(g.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+    release(p);
+    return nullptr;
+  }
+  if (g.pair) {
+    const int pairs = max_pairs(g, sms);
+    p->grid = 2 * (int)(tiles < pairs ? tiles : pairs);
+  } else {
+    p->grid = (int)(tiles < sms ? tiles : sms);
+  }
+  e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "cudaHostAlloc(status word)");
+    release(p);
+    return nullptr;
+  }
+  *p->status_host = 0;
+  e = cudaHostGetDevicePointer((void**)&p->status_dev, p->status_host, 0);
+  if (e == cudaSuccess && epilog == GEMM_EPI_DRELU_BGRAD) {
+    if (test_hook("GEMM_EPI_INJECT_PLAN_ALLOC_FAILURE")) {
+      fail(GEMM_EPI_ERR_CUDA, "injected workspace allocation failure");
+      release(p);
+      return nullptr;
+    }
+    // one row of column sums per row tile, and per expert and 128 features a
+    // count of the row tiles that are in
+    p->partial_bytes = (size_t)row_tiles * (size_t)N * sizeof(float);
+    p->n_tickets = (int)(E * ceil_div(N, 128));
+    e = cudaMalloc((void**)&p->partials, p->partial_bytes);
+    if (e == cudaSuccess) e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
+    if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+  }
+  if (e != cudaSuccess) {
+    cuda_fail(e, "grouped plan workspace");
+    release(p);
+    return nullptr;
+  }
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    live_plans().insert(p);
+  }
+  g_last_error.clear();
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_epi_plan_t gemm_epi_grouped_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
+                                      gemm_epi_epilog epilog, uint32_t flags) {
+  try {
+    return make_plan(E, T, N, K, dtype, epilog, flags);
+  } catch (...) {  // host memory ran out
+    return nullptr;
+  }
+}
+
+int gemm_epi_grouped_execute(gemm_epi_plan_t plan, const void* X, const void* W, const void* bias,
+                             const int32_t* offsets, void* Y, uint32_t* aux, cudaStream_t stream) {
+  int rc = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 1, "gemm_epi_grouped_execute", &rc);
+  if (!p) return rc;
+  if (p->epilog == GEMM_EPI_DRELU_BGRAD || p->epilog == GEMM_EPI_WGRAD)
+    return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_grouped_execute called on a %s plan",
+                p->epilog == GEMM_EPI_WGRAD ? "WGRAD" : "DRELU_BGRAD");
+  if (!X || !W || !Y || !offsets || (!bias && p->epilog != GEMM_EPI_NONE))
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_grouped_execute: NULL X, W, bias, offsets or Y");
+  const bool gelu_aux = p->epilog == GEMM_EPI_GELU_AUX_BIAS;
+  if ((p->epilog == GEMM_EPI_RELU_AUX_BIAS || gelu_aux) && !aux)
+    return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "%s needs an aux buffer", gelu_aux ? "GELU_AUX_BIAS" : "RELU_AUX_BIAS");
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(offsets, 4) ||
+      !aligned(bias, p->bias_f32 ? 4 : 2) || (p->epilog == GEMM_EPI_RELU_AUX_BIAS && !aligned(aux, 4)) ||
+      (gelu_aux && !aligned(aux, 16)))
+    return fail(GEMM_EPI_ERR_MISALIGNED,
+                "gemm_epi_grouped_execute: X, W, Y need 16-byte, offsets and aux 4-byte (GELU_AUX_BIAS: 16-byte), bias "
+                "2-byte (fp32: 4-byte) alignment");
+  DeviceScope scope(p->device);
+  rc = take_status(p);
+  if (rc) return rc;
+  CUtensorMap a, b;
+  rc = forward_maps(p, X, W, &a, &b);
+  if (rc) return rc;
+  ge::GroupedParams k = params(p, offsets);
+  k.bias = bias;
+  k.out = Y;
+  k.aux_out = aux;
+  return launch(p, a, b, k, stream);
+}
+
+int gemm_epi_grouped_drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2, const uint32_t* aux,
+                                         const int32_t* offsets, void* dZ, float* dbias, cudaStream_t stream) {
+  int rc = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 1, "gemm_epi_grouped_drelu_bgrad_execute", &rc);
+  if (!p) return rc;
+  if (p->epilog != GEMM_EPI_DRELU_BGRAD)
+    return fail(GEMM_EPI_ERR_EPILOG_MISMATCH,
+                "gemm_epi_grouped_drelu_bgrad_execute called on a plan whose epilog is not DRELU_BGRAD");
+  if (!dY2 || !W2 || !aux || !offsets || !dZ || !dbias)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_grouped_drelu_bgrad_execute: NULL dY2, W2, aux, offsets, dZ or dbias");
+  if (!aligned(dY2, 16) || !aligned(W2, 16) || !aligned(dZ, 16) || !aligned(aux, 4) || !aligned(offsets, 4) ||
+      !aligned(dbias, 4))
+    return fail(GEMM_EPI_ERR_MISALIGNED,
+                "gemm_epi_grouped_drelu_bgrad_execute: dY2, W2, dZ need 16-byte, aux, offsets, dbias 4-byte alignment");
+  DeviceScope scope(p->device);
+  rc = take_status(p);
+  if (rc) return rc;
+  CUtensorMap a, b;
+  rc = forward_maps(p, dY2, W2, &a, &b);
+  if (rc) return rc;
+  ge::GroupedParams k = params(p, offsets);
+  k.out = dZ;
+  k.aux_in = aux;
+  k.dbias = dbias;
+  k.partials = p->partials;
+  k.tickets = p->col_tickets;
+  return launch(p, a, b, k, stream);
+}
+
+int gemm_epi_grouped_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ, const int32_t* offsets, void* dW,
+                                   float* dbias, cudaStream_t stream) {
+  int rc = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 1, "gemm_epi_grouped_wgrad_execute", &rc);
+  if (!p) return rc;
+  if (p->epilog != GEMM_EPI_WGRAD)
+    return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_grouped_wgrad_execute called on a plan whose epilog is not WGRAD");
+  if (!X || !dZ || !offsets || !dW)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_grouped_wgrad_execute: NULL X, dZ, offsets or dW");
+  if (!aligned(X, 16) || !aligned(dZ, 16) || !aligned(dW, 16) || !aligned(offsets, 4) || (dbias && !aligned(dbias, 4)))
+    return fail(GEMM_EPI_ERR_MISALIGNED,
+                "gemm_epi_grouped_wgrad_execute: X, dZ, dW need 16-byte, offsets and dbias 4-byte alignment");
+  DeviceScope scope(p->device);
+  rc = take_status(p);
+  if (rc) return rc;
+  const auto u16 = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  CUtensorMap a, b;
+  rc = encode_3d(&a, u16, dZ, (uint64_t)p->N, (uint64_t)p->uT, 1, 64, ge::kBK, "dZ");
+  if (rc) return rc;
+  rc = encode_3d(&b, u16, X, (uint64_t)p->uK, (uint64_t)p->uT, 1, 64, ge::kBK, "X");
+  if (rc) return rc;
+  ge::GroupedParams k = params(p, offsets);
+  k.out = dW;
+  rc = launch(p, a, b, k, stream);
+  if (rc || !dbias) return rc;
+  const dim3 grid((unsigned)ceil_div(p->uK, 64), (unsigned)p->gr.E);
+  if (p->dtype == GEMM_EPI_BF16)
+    ge::grouped_colsum_kernel<true><<<grid, 256, 0, stream>>>((const uint16_t*)X, offsets, (int)p->uT, p->gr.E,
+                                                              (int)p->uK, dbias);
+  else
+    ge::grouped_colsum_kernel<false><<<grid, 256, 0, stream>>>((const uint16_t*)X, offsets, (int)p->uT, p->gr.E,
+                                                               (int)p->uK, dbias);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "grouped bias-gradient launch");
+  return GEMM_EPI_OK;
+}
+
+}  // extern "C"

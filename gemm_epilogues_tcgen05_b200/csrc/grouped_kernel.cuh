@@ -1,0 +1,708 @@
+// grouped_kernel.cuh -- the linear-layer products grouped by expert: the rows
+// of X are sorted by expert, expert e owns rows offsets[e] .. offsets[e+1]
+// (any number of them, known only on the device) and its own weight.
+//
+//   forward / DRELU_BGRAD   Y[t][n] = epilog(sum_k X[t][k] W_e[k][n])
+//   WGRAD                   dW_e[k][n] = sum over e's rows t of X[t][k] dZ[t][n]
+//
+// Swap-AB for every size: the features n are the MMA's M slot (128 per CTA,
+// 256 per CTA pair) and the ragged dimension sits in the N slot, whose width
+// is a field of the instruction descriptor -- a tile of 40 rows costs 64
+// columns of MMA work, not 128 or 256, and no row of another expert is ever
+// stored, because each accumulator column is one row and is stored or not on
+// its own (a TMA store box cannot be clipped at an expert's last row). An
+// expert's rows are cut into equal tiles of at most TR. WGRAD contracts over
+// the ragged dimension instead; its N slot holds the k of dW.
+//
+// The tile list is made in the kernel: one warp of every CTA reads the
+// offsets, and a prefix sum of each expert's tile count maps a tile index to
+// its expert (binary search), so nothing is copied to the host, there is one
+// launch, and a captured graph follows new offsets. Offsets are read as their
+// running maximum cut to [0, T], so no value of them reaches outside X or Y.
+//
+// WGRAD's last k-block of an expert also loads rows of the next expert (or
+// past the last one, where any bit pattern may stand). The MMA steps past the
+// expert's rows are not issued, and within the last step of 16 the foreign
+// rows are overwritten with zeros in both operands before it is issued: a
+// zero in one operand alone would still let a NaN of the other through.
+#pragma once
+
+#include "skinny_kernel.cuh"
+#include "tile2_kernel.cuh"
+
+namespace ge {
+
+constexpr int kMaxExperts = 1024;
+
+struct GroupedParams {
+  int32_t T, N, K, E;
+  int32_t n_ft;             // feature tiles (of 128, CTA pairs 256)
+  int32_t n_kt;             // WGRAD: k tiles of TR
+  int32_t k_blocks;         // forward: stages of 64·KPS k
+  int32_t group;            // row tiles per raster group
+  int32_t aux_words;
+  int32_t nfb;              // 128-feature blocks (DRELU_BGRAD tickets)
+  const int32_t* offsets;   // E + 1
+  const void* bias;         // E x N
+  void* out;                // Y, dZ (T x N) or dW (E x K x N)
+  uint32_t* aux_out;        // RELU_AUX_BIAS words; GELU_AUX_BIAS: T x N 16-bit Z
+  const uint32_t* aux_in;
+  float* dbias;             // DRELU_BGRAD: E x N
+  float* partials;          // DRELU_BGRAD: [row tile][N]
+  int* tickets;             // DRELU_BGRAD: [E][nfb], zero between launches
+  int* status;
+  uint64_t timeout_ns;
+  int32_t bias_f32, out_f32;
+  int32_t inject_stall;
+};
+
+// Shared memory: a ring of stages (W: 128 features x 64·KPS k; X: this CTA's
+// share of the row tile x 64·KPS k), the barriers and the tile table.
+template <bool PAIR, int TR, int KPS>
+struct GroupedSmem {
+  static constexpr int BK = kBK * KPS;
+  static constexpr int TRC = PAIR ? TR / 2 : TR;       // rows of the N slot held by this CTA
+  static constexpr uint32_t A_CHUNK = 64 * BK * 2;     // MN-major: 64 features x BK
+  static constexpr uint32_t A_SUB_MN = 64 * kBK * 2;   // MN-major: 64 k-rows of one chunk
+  static constexpr uint32_t A_SUB_K = 128 * kBK * 2;   // K-major: 128 features x 64 k
+  static constexpr uint32_t A_BYTES = 2 * A_CHUNK;
+  static constexpr uint32_t B_SUB = TRC * kBK * 2;     // TRC rows x 64 k
+  static constexpr uint32_t B_BYTES = KPS * B_SUB;
+  static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+  static constexpr uint32_t TABLE = 2 * (kMaxExperts + 1) * 4;
+  static constexpr uint32_t FIXED = TABLE + 32 * 8 + 128 * 4 + 64 + 1024;
+  static constexpr int STAGES = (232448 - FIXED) / STAGE > 10 ? 10 : (232448 - FIXED) / STAGE;
+  static constexpr uint32_t OFF_A = 0;
+  static constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_B + STAGES * B_BYTES;
+  static constexpr uint32_t N_BARS = 2 * STAGES + 5;   // full, empty, tfull[2], tempty[2], drain
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 32 * 8;
+  static constexpr uint32_t OFF_SUM = OFF_MISC + 64;   // column sums of the second half of the epilogue warps
+  static constexpr uint32_t OFF_TABLE = OFF_SUM + 128 * 4;
+  static constexpr uint32_t BYTES = OFF_TABLE + TABLE + 1024;
+  static_assert(N_BARS <= 32, "barrier space");
+  static_assert(STAGES >= 3 && BYTES <= 232448, "grouped shared memory above the per-CTA limit");
+};
+
+// Epilogue warps: two per TMEM lane quarter (each every other chunk of 32
+// rows) from 128-row tiles up, else one.
+template <int TR>
+struct GroupedEpiWarps {
+  static constexpr int value = TR >= 128 ? 8 : 4;
+};
+
+// The expert table in shared memory, made by one warp: offs[0..E] (sanitised)
+// and start[0..E], the first tile of each expert. Each lane takes a
+// contiguous run of entries, so two warp scans do.
+template <int TR>
+__device__ __forceinline__ void grouped_table(const GroupedParams& p, int* offs, int* start, int tiles_per_mt) {
+  const int lane = static_cast<int>(lane_id());
+  const int per = (p.E + 1 + 31) / 32;
+  const int a = min(lane * per, p.E + 1), b = min(a + per, p.E + 1);
+  int mx = 0;
+  for (int i = a; i < b; ++i) {
+    mx = max(mx, min(p.offsets[i], p.T));
+    offs[i] = mx;  // running maximum within the lane's run
+  }
+  int incl = mx;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl = max(incl, o);
+  }
+  int before = __shfl_up_sync(0xffffffffu, incl, 1);
+  if (lane == 0) before = 0;
+  for (int i = a; i < b; ++i) offs[i] = max(offs[i], before);
+  __syncwarp();
+  int sum = 0;
+  for (int i = a; i < b; ++i)
+    if (i < p.E) sum += (offs[i + 1] - offs[i] + TR - 1) / TR;
+  int s = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += o;
+  }
+  s -= sum;  // row tiles of the experts before this lane's
+  for (int i = a; i < b; ++i) {
+    start[i] = s * tiles_per_mt;
+    if (i < p.E) s += (offs[i + 1] - offs[i] + TR - 1) / TR;
+  }
+}
+
+// One output tile: features f0.., and `n` columns of the MMA's N slot of
+// which the first `cols` are stored.
+struct GroupedTile {
+  int e;         // expert
+  int f0;        // first feature of the (pair's) tile
+  int c0;        // forward: first row of X; WGRAD: first k of dW
+  int cols, n;   // stored columns; columns computed (a multiple of 32)
+  int row0, rows;  // WGRAD: the expert's rows, the contraction
+  int mt, mb;    // forward: the expert's row tiles and this tile's among them
+};
+
+template <int EPI, int TR, int FM>
+__device__ __forceinline__ bool grouped_tile(const GroupedParams& p, const int* offs, const int* start, int tile,
+                                             GroupedTile& w) {
+  int mb, fb;
+  if constexpr (EPI == EPI_WGRAD) {
+    const int per = p.n_ft * p.n_kt;
+    w.e = tile / per;
+    if (w.e >= p.E) return false;
+    tile_coords(tile - w.e * per, p.n_kt, p.n_ft, p.group, 0, mb, fb);
+    w.c0 = mb * TR;
+    w.cols = min(TR, p.K - w.c0);
+    w.row0 = offs[w.e];
+    w.rows = offs[w.e + 1] - w.row0;
+    w.mt = 1;
+    w.mb = mb;
+  } else {
+    if (tile >= start[p.E]) return false;
+    int lo = 0, hi = p.E;  // start[lo] <= tile < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    w.e = lo;
+    w.row0 = offs[lo];
+    w.rows = offs[lo + 1] - w.row0;
+    w.mt = (w.rows + TR - 1) / TR;
+    tile_coords(tile - start[lo], w.mt, p.n_ft, min(p.group, w.mt), 0, mb, fb);
+    // equal tiles: since rows > (mt - 1) TR and a tile is at most TR, none is empty
+    const int per = ((w.rows + w.mt - 1) / w.mt + 31) & ~31;
+    w.c0 = w.row0 + mb * per;
+    w.cols = min(per, w.rows - mb * per);
+    w.mb = mb;
+  }
+  w.f0 = fb * FM;
+  w.n = (w.cols + 31) & ~31;
+  return true;
+}
+
+// Rows r .. r+3 of this lane's feature (a[0..3]) -> four features of one row:
+// lane l ends with row r + (l & 3), features (l & ~3) .. + 3 of the warp's 32.
+// Two exchanges (lanes l ^ 1, then l ^ 2). A warp then stores four rows with
+// one instruction, 64 contiguous bytes (16-bit) or 128 (fp32) of each, instead
+// of one row per instruction.
+__device__ __forceinline__ void exchange4(float (&a)[4]) {
+  const uint32_t lane = lane_id();
+  const bool odd = (lane & 1u) != 0, hi = (lane & 2u) != 0;
+  const float r0 = __shfl_xor_sync(0xffffffffu, odd ? a[0] : a[1], 1);
+  const float r1 = __shfl_xor_sync(0xffffffffu, odd ? a[2] : a[3], 1);
+  // even: rows 0 and 2, features l, l+1; odd: rows 1 and 3, features l-1, l
+  const float p0 = odd ? r0 : a[0], p1 = odd ? a[1] : r0;
+  const float q0 = odd ? r1 : a[2], q1 = odd ? a[3] : r1;
+  const float s0 = __shfl_xor_sync(0xffffffffu, hi ? p0 : q0, 2);
+  const float s1 = __shfl_xor_sync(0xffffffffu, hi ? p1 : q1, 2);
+  a[0] = hi ? s0 : p0;
+  a[1] = hi ? s1 : p1;
+  a[2] = hi ? q0 : s0;
+  a[3] = hi ? q1 : s1;
+}
+
+// the same for 16-bit results, packed in pairs before the second exchange
+template <bool BF16>
+__device__ __forceinline__ uint2 exchange4_16(const float* a) {
+  const uint32_t lane = lane_id();
+  const bool odd = (lane & 1u) != 0, hi = (lane & 2u) != 0;
+  const float r0 = __shfl_xor_sync(0xffffffffu, odd ? a[0] : a[1], 1);
+  const float r1 = __shfl_xor_sync(0xffffffffu, odd ? a[2] : a[3], 1);
+  const uint32_t p = pack2<BF16>(odd ? r0 : a[0], odd ? a[1] : r0);
+  const uint32_t q = pack2<BF16>(odd ? r1 : a[2], odd ? a[3] : r1);
+  const uint32_t s = __shfl_xor_sync(0xffffffffu, hi ? p : q, 2);
+  return hi ? make_uint2(s, q) : make_uint2(p, s);
+}
+
+// Store 32 columns of the accumulator (this lane's feature, v[j] = row j of
+// the chunk) into a row-major matrix of row length N: `base` is the address of
+// (first row, the warp's first feature), `rows` the rows to store, `nvalid`
+// the features of the warp below N (a multiple of 8, as N is).
+template <bool BF16>
+__device__ __forceinline__ void store_cols16(const float (&v)[32], void* base, int64_t N, int rows, int nvalid) {
+  const int lane = static_cast<int>(lane_id());
+  const int r = lane & 3, f = lane & ~3;
+  uint16_t* dst = reinterpret_cast<uint16_t*>(base) + r * N + f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint2 w = exchange4_16<BF16>(v + 4 * q);
+    if (4 * q + r < rows && f < nvalid) *reinterpret_cast<uint2*>(dst) = w;
+    dst += 4 * N;
+  }
+}
+
+__device__ __forceinline__ void store_cols32(const float (&v)[32], void* base, int64_t N, int rows, int nvalid) {
+  const int lane = static_cast<int>(lane_id());
+  const int r = lane & 3, f = lane & ~3;
+  float* dst = reinterpret_cast<float*>(base) + r * N + f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float a[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    exchange4(a);
+    if (4 * q + r < rows && f < nvalid) *reinterpret_cast<float4*>(dst) = make_float4(a[0], a[1], a[2], a[3]);
+    dst += 4 * N;
+  }
+}
+
+// zero rows [r0, r1) of a stage's MN-major operand chunks (128-byte rows; the
+// swizzle moves 16-byte units only within a row), by one warp, at a
+// shared::cluster address
+__device__ __forceinline__ void zero_rows_cluster(uint32_t addr, uint32_t chunk, int chunks, int r0, int r1) {
+  const int units = (r1 - r0) * 8;  // 16-byte units per chunk
+  for (int u = static_cast<int>(lane_id()); u < units * chunks; u += 32) {
+    const int c = u / units, x = u - c * units;
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr + c * chunk + r0 * 128 + x * 16),
+                 "r"(0u)
+                 : "memory");
+  }
+}
+
+template <bool PAIR, int TR, int KPS, int EPI, bool BF16, bool WK>
+__global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const GroupedParams p) {
+  using L = GroupedSmem<PAIR, TR, KPS>;
+  constexpr bool WG = EPI == EPI_WGRAD;
+  static_assert(!WG || (KPS == 1 && !WK && TR >= 128), "WGRAD stages one k-block of 64 rows");
+  constexpr int STAGES = L::STAGES;
+  constexpr int EW = GroupedEpiWarps<TR>::value;
+  constexpr int ET = 32 * EW;
+  constexpr int FM = PAIR ? 256 : 128;
+  constexpr int BXR = L::TRC < 64 ? L::TRC : 64;  // rows per X box
+  constexpr uint32_t TMEM_COLS = 2 * TR < 32 ? 32 : 2 * TR;
+  constexpr uint32_t IDESC0 = idesc_f16(BF16, /*A MN-major*/ !WK, /*B MN-major*/ WG, FM, 0);
+  constexpr uint16_t BOTH = 0x3;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem + L::OFF_A;
+  uint8_t* sB = smem + L::OFF_B;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
+  float* half_sum = reinterpret_cast<float*>(smem + L::OFF_SUM);
+  int* offs = reinterpret_cast<int*>(smem + L::OFF_TABLE);
+  int* start = offs + kMaxExperts + 1;
+
+  const uint32_t warp = threadIdx.x >> 5;
+  const uint32_t lane = lane_id();
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int unit = static_cast<int>(PAIR ? blockIdx.x >> 1 : blockIdx.x);
+  const int units = static_cast<int>(PAIR ? gridDim.x >> 1 : gridDim.x);
+
+  TileParams wp{};  // what the bounded wait reads
+  wp.status = p.status;
+  wp.timeout_ns = p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], PAIR ? 2 * EW : EW);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *last_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  if (warp == 2) grouped_table<TR>(p, offs, start, p.n_ft);
+  tc_fence_before();
+  if constexpr (PAIR)
+    cluster_sync();  // both CTAs' barriers exist before either side signals the other
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
+      GroupedTile w;
+      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+        const int f0 = w.f0 + static_cast<int>(rank) * 128;
+        const int nloc = PAIR ? w.n / 2 : w.n;
+        const int c0 = w.c0 + static_cast<int>(rank) * nloc;
+        const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
+        const int boxes = (nloc + (WG ? 64 : BXR) - 1) / (WG ? 64 : BXR);
+        const uint32_t tx = (PAIR ? 2u : 1u) *
+                            (L::A_BYTES + static_cast<uint32_t>(boxes) * (WG ? 64 * kBK * 2 : KPS * BXR * kBK * 2));
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const uint32_t s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1u;
+          if (!wait_bounded(&empty[s], ph ^ 1u, wp, abort_flag, 1)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+          const uint32_t bar = full0 + s * 8;
+          uint8_t* a = sA + s * L::A_BYTES;
+          uint8_t* b = sB + s * L::B_BYTES;
+          if constexpr (WG) {
+            const int t = w.row0 + kb * kBK;
+            tma_load_3d<PAIR>(a, &tmA, bar, f0, t, 0);
+            tma_load_3d<PAIR>(a + L::A_CHUNK, &tmA, bar, f0 + 64, t, 0);
+            for (int i = 0; i < boxes; ++i) tma_load_3d<PAIR>(b + i * (64 * kBK * 2), &tmB, bar, c0 + i * 64, t, 0);
+          } else {
+            const int k = kb * L::BK;
+            if constexpr (WK) {
+#pragma unroll
+              for (int j = 0; j < KPS; ++j) tma_load_3d<PAIR>(a + j * L::A_SUB_K, &tmA, bar, k + j * kBK, f0, w.e);
+            } else {
+              tma_load_3d<PAIR>(a, &tmA, bar, f0, k, w.e);
+              tma_load_3d<PAIR>(a + L::A_CHUNK, &tmA, bar, f0 + 64, k, w.e);
+            }
+#pragma unroll
+            for (int j = 0; j < KPS; ++j)
+              for (int i = 0; i < boxes; ++i)
+                tma_load_3d<PAIR>(b + j * L::B_SUB + i * (BXR * kBK * 2), &tmB, bar, k + j * kBK, c0 + i * BXR, 0);
+          }
+        }
+      }
+      // every issued copy has landed before the CTA can exit (in a pair the
+      // leader's barriers count them: there the release by the MMA shows it)
+      const uint32_t inflight = it < STAGES ? it : STAGES;
+      for (uint32_t i = it - inflight; i < it; ++i)
+        wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
+                     /*honour_abort=*/false);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    uint32_t it = 0, tcount = 0;
+    bool ok = true;
+    const uint32_t peerA = PAIR ? mapa_shared(smem_u32(sA), 1) : 0u;
+    const uint32_t peerB = PAIR ? mapa_shared(smem_u32(sB), 1) : 0u;
+    if (rank == 0) {
+      GroupedTile w;
+      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+        const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
+        if (WG && kbs == 0) continue;  // an expert without rows: the epilogue stores zeros
+        const uint32_t buf = tcount & 1u;
+        const uint32_t tph = (tcount >> 1) & 1u;
+        const int tail = WG ? w.rows - (kbs - 1) * kBK : 0;  // rows in the last k-block
+        const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
+        const uint32_t d_tmem = tmem_base + buf * TR;
+        if (lane == 0) {
+          ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
+          tc_fence_after();
+        }
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const uint32_t s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1u;
+          const bool last = WG && kb == kbs - 1;
+          if (lane == 0 && ok) {
+            ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
+            tc_fence_after();
+          }
+          if (WG && last && (tail & 15)) {
+            // zero the foreign rows of the last step in both operands
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (ok) {
+              const int r1 = (tail + 15) & ~15;
+              const int bch = ((PAIR ? w.n / 2 : w.n) + 63) / 64;
+              zero_rows_cluster(smem_u32(sA) + s * L::A_BYTES, L::A_CHUNK, 2, tail, r1);
+              zero_rows_cluster(smem_u32(sB) + s * L::B_BYTES, 64 * kBK * 2, bch, tail, r1);
+              if constexpr (PAIR) {
+                zero_rows_cluster(peerA + s * L::A_BYTES, L::A_CHUNK, 2, tail, r1);
+                zero_rows_cluster(peerB + s * L::B_BYTES, 64 * kBK * 2, bch, tail, r1);
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+              }
+              asm volatile("fence.proxy.async;" ::: "memory");
+            }
+            __syncwarp();
+          }
+          if (lane == 0 && ok) {
+            const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
+            const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
+            const int steps = last ? (tail + 15) / 16 : 4;
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) {
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                if (WG && kk >= steps) break;
+                // A MN-major: chunks A_CHUNK apart, 8 k-rows 1 KB apart, a step is 16 rows; K-major: 32 bytes a step
+                const uint64_t ad = WK ? smem_desc_sw128(a0 + j * L::A_SUB_K + kk * 32, 16, 1024)
+                                       : smem_desc_sw128(a0 + j * L::A_SUB_MN + kk * 2048, L::A_CHUNK, 1024);
+                const uint64_t bd = WG ? smem_desc_sw128(b0 + kk * 2048, 64 * kBK * 2, 1024)
+                                       : smem_desc_sw128(b0 + j * L::B_SUB + kk * 32, 16, 1024);
+                const uint32_t acc = (kb > 0 || j > 0 || kk > 0) ? 1u : 0u;
+                if constexpr (PAIR)
+                  umma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                else
+                  umma_f16(d_tmem, ad, bd, idesc, acc);
+              }
+            }
+            if constexpr (PAIR)
+              umma_commit_pair(&empty[s], BOTH);
+            else
+              umma_commit(&empty[s]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        // (fault injection: the epilogue then waits on a barrier nothing arrives on)
+        if (lane == 0 && ok && !(p.inject_stall && tcount == 0)) {
+          if constexpr (PAIR)
+            umma_commit_pair(&tfull[buf], BOTH);
+          else
+            umma_commit(&tfull[buf]);
+        }
+        ++tcount;
+      }
+      if (lane == 0) {
+        if constexpr (PAIR)
+          umma_commit_pair(drain, BOTH);
+        else
+          umma_commit(drain);
+      }
+    }
+    // every MMA that writes this CTA's tensor memory is done before it is freed
+    if (lane == 0) wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const uint32_t ew = warp & 3u;         // TMEM lane quarter
+    const uint32_t eh = (warp - 2u) >> 2;  // which of the quarter's warps
+    const uint32_t et = threadIdx.x - 64;
+    uint32_t tcount = 0;
+    bool ok = true;
+    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : smem_u32(&tempty[0]);
+    if constexpr (EPI == EPI_DRELU_BGRAD) {
+      // experts without rows: no tile of theirs exists, and their bias gradient is zero
+      for (int e = static_cast<int>(blockIdx.x); e < p.E; e += static_cast<int>(gridDim.x))
+        if (offs[e] == offs[e + 1])
+          for (int n = static_cast<int>(et); n < p.N; n += ET) p.dbias[static_cast<int64_t>(e) * p.N + n] = 0.f;
+    }
+    GroupedTile w;
+    for (int tile = unit; grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+      const int fw = w.f0 + static_cast<int>(rank * 128u + ew * 32u);  // the warp's first feature
+      const int n = fw + static_cast<int>(lane);
+      const bool n_ok = n < p.N;
+      const int nvalid = max(0, min(32, p.N - fw));
+      const int word = fw >> 5;
+      const bool empty_tile = WG && w.rows == 0;
+      const uint32_t buf = tcount & 1u;
+      const uint32_t tph = (tcount >> 1) & 1u;
+      float bias_n = 0.f;
+      if constexpr (AddsBias<EPI>::value)
+        if (n_ok) bias_n = load_bias<BF16>(p.bias, p.bias_f32, static_cast<int64_t>(w.e) * p.N + n);
+      float dsum = 0.f;
+      // DRELU_BGRAD: the first chunk's mask words, loaded before the accumulator wait
+      uint32_t mnext = 0u;
+      const auto mask_word = [&](int c) -> uint32_t {
+        const int r = c * 32 + static_cast<int>(lane);
+        return (r < w.cols && word < p.aux_words)
+                   ? __ldg(p.aux_in + static_cast<int64_t>(w.c0 + r) * p.aux_words + word)
+                   : 0u;
+      };
+      if constexpr (EPI == EPI_DRELU_BGRAD) mnext = mask_word(static_cast<int>(eh));
+      if (!empty_tile) {
+        if (ok) ok = wait_bounded(&tfull[buf], tph, wp, abort_flag, 6);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      if (ok) {
+        const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TR;
+        const int64_t orow = WG ? static_cast<int64_t>(w.e) * p.K + w.c0 : static_cast<int64_t>(w.c0);
+#pragma unroll 1
+        for (int c = static_cast<int>(eh); c * 32 < w.n; c += EW / 4) {
+          float v[32];
+          if (empty_tile) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          } else {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tbase + c * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          }
+          const int rows = w.cols - c * 32;
+          const int64_t at = (orow + c * 32) * p.N + fw;
+          if constexpr (EPI == EPI_DRELU_BGRAD) {
+            const uint32_t mine = mnext;
+            if ((c + EW / 4) * 32 < w.n) mnext = mask_word(c + EW / 4);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t m = __shfl_sync(0xffffffffu, mine, j);
+              v[j] = ((m >> lane) & 1u) ? v[j] : 0.f;
+              dsum += v[j];  // rows past the tile have no mask bit set
+            }
+          } else if constexpr (!PlainStore<EPI>::value) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += bias_n;
+            if constexpr (EPI == EPI_GELU_AUX_BIAS)
+              store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.aux_out) + at, p.N, rows, nvalid);
+            if constexpr (AppliesGelu<EPI>::value) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = gelu_erf(v[j]);
+            }
+            if constexpr (EPI == EPI_RELU_BIAS || EPI == EPI_RELU_AUX_BIAS) {
+              uint32_t myword = 0u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const bool pos = v[j] > 0.f;
+                if constexpr (EPI == EPI_RELU_AUX_BIAS) {
+                  const uint32_t b = __ballot_sync(0xffffffffu, pos && n_ok);
+                  if (lane == static_cast<uint32_t>(j)) myword = b;
+                }
+                v[j] = pos ? v[j] : 0.f;
+              }
+              if constexpr (EPI == EPI_RELU_AUX_BIAS)
+                if (static_cast<int>(lane) < rows && word < p.aux_words)
+                  p.aux_out[(orow + c * 32 + static_cast<int>(lane)) * p.aux_words + word] = myword;
+            }
+          }
+          if (p.out_f32)
+            store_cols32(v, reinterpret_cast<float*>(p.out) + at, p.N, rows, nvalid);
+          else
+            store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.out) + at, p.N, rows, nvalid);
+        }
+        if (!empty_tile) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              mbar_arrive_cluster(tempty0 + buf * 8);
+            else
+              mbar_arrive(&tempty[buf]);
+          }
+        }
+      }
+      if (!empty_tile) ++tcount;
+      if constexpr (EPI == EPI_DRELU_BGRAD) {
+        // column sums: the quarter's two warps in order, then (more than one
+        // row tile) one partial row per tile, summed in tile order by the
+        // block of features' last tile, so the result does not depend on timing
+        const int fl = static_cast<int>(ew * 32u + lane);
+        if constexpr (EW == 8) {
+          if (eh == 1) half_sum[fl] = dsum;
+          named_bar_sync(1, ET);
+          if (eh == 0) dsum += half_sum[fl];
+        }
+        if (w.mt == 1) {
+          if (eh == 0 && n_ok && ok) p.dbias[static_cast<int64_t>(w.e) * p.N + n] = dsum;
+          if constexpr (EW == 8) named_bar_sync(1, ET);  // half_sum is reused by the next tile
+        } else {
+          const int64_t mrow = start[w.e] / p.n_ft;
+          if (eh == 0 && n_ok && ok) p.partials[(mrow + w.mb) * p.N + n] = dsum;
+          __threadfence();
+          named_bar_sync(1, ET);
+          if (et == 0) {
+            int last = 0;
+            const int fb = (w.f0 >> 7) + static_cast<int>(rank);
+            if (ok && fb < p.nfb) {
+              int* t = p.tickets + static_cast<int64_t>(w.e) * p.nfb + fb;
+              last = atomicAdd(t, 1) == w.mt - 1;
+              if (last) *t = 0;  // ready for the next launch
+            }
+            *last_flag = last;
+          }
+          named_bar_sync(1, ET);
+          if (*last_flag && eh == 0 && n_ok) {
+            __threadfence();
+            const float* src = p.partials + mrow * p.N + n;
+            float s = 0.f;
+            for (int m = 0; m < w.mt; ++m) s += __ldcg(src + static_cast<int64_t>(m) * p.N);
+            p.dbias[static_cast<int64_t>(w.e) * p.N + n] = s;
+          }
+          named_bar_sync(1, ET);  // last_flag and half_sum are reused by the next tile
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  if constexpr (PAIR)
+    cluster_sync();  // neither CTA leaves while the other may still signal it
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// Column sums of X per expert (WGRAD's optional bias gradient): a block takes
+// one expert and 64 columns; 8 row lanes stride over the expert's rows and are
+// added in lane order. Bound by one read of X.
+template <bool BF16>
+__global__ void __launch_bounds__(256) grouped_colsum_kernel(const uint16_t* __restrict__ X, const int32_t* offsets, int T,
+                                                             int E, int K, float* __restrict__ dbias) {
+  __shared__ float2 part[8][32];
+  __shared__ int span[2];
+  const int e = blockIdx.y;
+  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  if (threadIdx.x < 32) {  // offsets as the products read them: the running maximum cut to [0, T]
+    int m = 0, at_e = 0;
+    for (int i = static_cast<int>(threadIdx.x); i <= e + 1; i += 32) {
+      m = max(m, min(offsets[i], T));
+      if (i <= e) at_e = m;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      at_e = max(at_e, __shfl_xor_sync(0xffffffffu, at_e, d));
+    }
+    if (threadIdx.x == 0) {
+      span[0] = at_e;
+      span[1] = m;
+    }
+  }
+  __syncthreads();
+  const int k = blockIdx.x * 64 + c * 2;
+  float2 s = make_float2(0.f, 0.f);
+  if (k < K)
+    for (int t = span[0] + r; t < span[1]; t += 8) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(X + static_cast<int64_t>(t) * K + k);
+      if constexpr (BF16) {
+        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&u);
+        s.x += __low2float(h);
+        s.y += __high2float(h);
+      } else {
+        const __half2 h = *reinterpret_cast<const __half2*>(&u);
+        s.x += __low2float(h);
+        s.y += __high2float(h);
+      }
+    }
+  part[r][c] = s;
+  __syncthreads();
+  if (r == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      s.x += part[i][c].x;
+      s.y += part[i][c].y;
+    }
+    float* d = dbias + static_cast<int64_t>(e) * K + k;
+    d[0] = s.x;
+    d[1] = s.y;
+  }
+}
+
+}  // namespace ge

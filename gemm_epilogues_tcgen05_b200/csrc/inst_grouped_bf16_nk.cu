@@ -1,0 +1,6 @@
+// inst_grouped_bf16_nk.cu -- expert-grouped kernels, bf16 operands, weights N x K.
+#include "inst_grouped.cuh"
+
+namespace ge_inst {
+GroupedInstance grouped_bf16_nk(int tr, int epi) { return grouped_any<true, true>(tr, epi); }
+}  // namespace ge_inst

@@ -11,11 +11,13 @@
 namespace ge {
 struct TileParams;
 struct SkinnyParams;
+struct GroupedParams;
 }  // namespace ge
 
 namespace ge_inst {
 
 using TileKernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ge::TileParams);
+using GroupedKernelFn = void (*)(CUtensorMap, CUtensorMap, ge::GroupedParams);
 using SkinnyKernelFn = void (*)(CUtensorMap, CUtensorMap, ge::SkinnyParams);
 
 // One CTA per tile, BN = 64, 128, 192 or 256 columns (8, 6, 4 or 4 stages); `epi` is
@@ -38,5 +40,18 @@ SkinnyKernelFn skinny_f16_kps1(int tp, int epi);
 SkinnyKernelFn skinny_f16_kps2(int tp, int epi);
 SkinnyKernelFn skinny_bf16_kps1(int tp, int epi);
 SkinnyKernelFn skinny_bf16_kps2(int tp, int epi);
+
+// Products grouped by expert: tiles of at most tr = 32 or 128 rows (one CTA,
+// 128 features) or 256 (CTA pair, 256 features); wk: the weights are N x K.
+// WGRAD has no tr = 32 and no wk instance (nullptr).
+struct GroupedInstance {
+  GroupedKernelFn fn;
+  uint32_t smem;
+  int threads, stages, bk;
+};
+GroupedInstance grouped_f16_mn(int tr, int epi);
+GroupedInstance grouped_f16_nk(int tr, int epi);
+GroupedInstance grouped_bf16_mn(int tr, int epi);
+GroupedInstance grouped_bf16_nk(int tr, int epi);
 
 }  // namespace ge_inst

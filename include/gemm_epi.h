@@ -45,6 +45,7 @@
  *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny, GEMM_EPI_FORCE_BN=64|128|192|256,
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
  *   GEMM_EPI_SKINNY_PREFETCH, GEMM_EPI_TAIL_SPLIT=0|1, GEMM_EPI_CACHE_HINTS=0|1,
+ *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped plans),
  *   GEMM_EPI_PAIR_SPLIT=0|1 (stream-K CTA pairs; off by default),
  *   GEMM_EPI_PAIR_SK_FIRST=0|1 (with stream-K: its tiles before the whole tiles, the
  *   default, or after them)
@@ -318,6 +319,52 @@ GEMM_EPI_API int drelu_bgrad_unfused_execute(gemm_epi_plan_t plan, const void* d
 GEMM_EPI_API int drelu_bgrad_execute_noalloc(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
                                              const void* dY2, const void* W2, const uint32_t* aux, void* dZ,
                                              float* dbias, cudaStream_t stream);
+
+/*
+ * Products grouped by expert (a mixture-of-experts layer): the T rows are
+ * sorted by expert, expert e owning rows offsets[e] .. offsets[e+1] - 1, and
+ * each expert has a weight and a bias of its own. The group sizes are known
+ * only on the device: offsets is a device array of E + 1 int32 (any sizes, 0
+ * and 1 among them), read by the kernel itself, so a call needs no host copy
+ * and a captured graph follows new offsets.
+ *   X     T x K        rows sorted by expert
+ *   W     E x K x N    (GEMM_EPI_FLAG_W_NK: E x N x K)
+ *   bias  E x N
+ *   Y, dZ T x N;  aux as for one product, one row per row of Y
+ *   dW    E x K x N;  dbias E x N (DRELU_BGRAD) or E x K (WGRAD)
+ * Rows before offsets[0] and from offsets[E] on belong to no expert: they are
+ * not computed, and Y, dZ and aux are left as they were there (X and aux may
+ * hold anything). An expert without rows gets zeros in dW and dbias. Offsets
+ * are used as their running maximum, cut to [0, T]: decreasing or larger
+ * values cannot reach outside the tensors, and name the rows that this gives.
+ * Results, rounding, the 16-bit types, epilogs, flags, error codes, watchdog,
+ * streams and ownership are those of one product; sums are in a fixed order,
+ * so equal calls give equal bits. A call runs on the plan's device whichever
+ * is current. gemm_epi_free, _query, _status, _last_error and _set_bias_f32
+ * take these plans too; the other calls return GEMM_EPI_ERR_EPILOG_MISMATCH.
+ */
+
+/*
+ * gemm_epi_grouped_plan: E experts (1 to 1024), T rows in all (the capacity
+ * of X and Y), N, K, dtype, epilog and flags as for gemm_epi_plan_ex, K x N
+ * at most 2^37. The kernel's tile is chosen by the mean rows per expert, T / E.
+ */
+GEMM_EPI_API gemm_epi_plan_t gemm_epi_grouped_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
+                                                   gemm_epi_epilog epilog, uint32_t flags);
+
+/* Forward epilogs and NONE; arguments as gemm_epi_execute, offsets 4-byte aligned. */
+GEMM_EPI_API int gemm_epi_grouped_execute(gemm_epi_plan_t plan, const void* X, const void* W, const void* bias,
+                                          const int32_t* offsets, void* Y, uint32_t* aux, cudaStream_t stream);
+
+/* DRELU_BGRAD, as drelu_bgrad_execute: dbias[e][n] is the sum over expert e's rows. */
+GEMM_EPI_API int gemm_epi_grouped_drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2,
+                                                      const uint32_t* aux, const int32_t* offsets, void* dZ,
+                                                      float* dbias, cudaStream_t stream);
+
+/* WGRAD, as gemm_epi_wgrad_execute: dW[e] = sum over expert e's rows of X[t]^T dZ[t];
+ * dbias NULL, or E x K floats receiving the sums of X's rows (a second launch). */
+GEMM_EPI_API int gemm_epi_grouped_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ,
+                                                const int32_t* offsets, void* dW, float* dbias, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
