@@ -32,7 +32,9 @@ EXPORTED = ["gemm_epi_plan", "gemm_epi_execute", "drelu_bgrad_execute", "gemm_ep
             "gemm_epi_query", "gemm_epi_status", "gemm_epi_unfused_execute", "drelu_bgrad_unfused_execute",
             "drelu_bgrad_execute_noalloc", "gemm_epi_wgrad_execute", "gemm_epi_set_bias_f32", "gemm_epi_plan_ex",
             "gemm_epi_grouped_plan", "gemm_epi_grouped_execute", "gemm_epi_grouped_drelu_bgrad_execute",
-            "gemm_epi_grouped_wgrad_execute"]
+            "gemm_epi_grouped_wgrad_execute", "gemm_epi_mx_scales_bytes", "gemm_epi_mx_quantize",
+            "gemm_epi_mx_dequantize", "gemm_epi_mx_plan", "gemm_epi_mx_execute"]
+MX_TRANSPOSED = 1  # GEMM_EPI_MX_TRANSPOSED
 FLAG_W_NK = 1  # GEMM_EPI_FLAG_W_NK
 FLAG_OUT_F32 = 2  # GEMM_EPI_FLAG_OUT_F32
 
@@ -101,6 +103,16 @@ def lib() -> ctypes.CDLL:
         L.gemm_epi_grouped_drelu_bgrad_execute.argtypes = [vp] * 8
         L.gemm_epi_grouped_wgrad_execute.restype = ci
         L.gemm_epi_grouped_wgrad_execute.argtypes = [vp] * 7
+        L.gemm_epi_mx_scales_bytes.restype = i64
+        L.gemm_epi_mx_scales_bytes.argtypes = [i64] * 4
+        L.gemm_epi_mx_quantize.restype = ci
+        L.gemm_epi_mx_quantize.argtypes = [i64, i64, i64, ci, ctypes.c_uint32, vp, vp, i64, vp, vp, vp]
+        L.gemm_epi_mx_dequantize.restype = ci
+        L.gemm_epi_mx_dequantize.argtypes = [i64, i64, i64, ci, ctypes.c_uint32, vp, vp, vp, i64, vp, vp]
+        L.gemm_epi_mx_plan.restype = vp
+        L.gemm_epi_mx_plan.argtypes = [i64, i64, i64, i64, ci, ci, ctypes.c_uint32]
+        L.gemm_epi_mx_execute.restype = ci
+        L.gemm_epi_mx_execute.argtypes = [vp] * 9
         _lib = L
     return _lib
 
@@ -329,7 +341,27 @@ class Plan:
         return (dW, dbias) if with_dbias else dW
 
 
-class GroupedPlan(Plan):
+class _DevicePlan(Plan):
+    """What plans bound to one device share: tensors are checked to be on it,
+    and the default stream is its current one."""
+
+    def _own(self, handle):
+        self.handle = handle
+        if not handle:
+            raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _p(self, t, shape, dtype, name):
+        ptr = _ptr(t, shape, dtype, name)
+        if t is not None and t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
+        return ptr
+
+    def _s(self, stream) -> int:
+        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+
+class GroupedPlan(_DevicePlan):
     """A plan for E products over rows sorted by expert: expert e owns rows
     ``offsets[e] .. offsets[e+1] - 1`` of X (T rows in all), where ``offsets``
     is an int32 CUDA tensor of E + 1 entries that only the kernel reads.
@@ -348,21 +380,8 @@ class GroupedPlan(Plan):
         self.dtype = self.bias_dtype = dtype
         self.epilog = EPILOGS[epilog] if isinstance(epilog, str) else epilog
         self.aux_words = (N + 31) // 32
-        self.handle = None
-        self.handle = lib().gemm_epi_grouped_plan(E, T, N, K, DTYPES[dtype], self.epilog,
-                                                  (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0))
-        if not self.handle:
-            raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
-        self.device = torch.device("cuda", torch.cuda.current_device())
-
-    def _p(self, t, shape, dtype, name):
-        ptr = _ptr(t, shape, dtype, name)
-        if t is not None and t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
-        return ptr
-
-    def _s(self, stream) -> int:
-        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+        self._own(lib().gemm_epi_grouped_plan(E, T, N, K, DTYPES[dtype], self.epilog,
+                                              (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0)))
 
     def _aux(self, aux):
         spec = self.aux_spec() or ((self.T, self.aux_words), torch.int32)
@@ -409,3 +428,97 @@ class GroupedPlan(Plan):
         dbias = torch.empty((self.E, self.K), dtype=torch.float32, device=X.device) if with_dbias else None
         self.gemm_epi_grouped_wgrad_execute(X, dZ, offsets, dW, dbias, stream)
         return (dW, dbias) if with_dbias else dW
+
+
+def mx_scales_bytes(rows: int, cols: int, batch: int = 1, groups: int | None = None) -> int:
+    """Bytes of the scales of ``batch`` microscaled matrices (or of rows in ``groups`` groups)."""
+    n = lib().gemm_epi_mx_scales_bytes(batch, rows, cols, groups or 0)
+    if n < 0:
+        raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
+    return n
+
+
+def _mx_args(values, q, scales, offsets, transposed, names):
+    """Checked shapes of one quantisation call: (batch, rows, cols, pointers...)."""
+    if values.dim() not in (2, 3):
+        raise ValueError(f"{names[0]} must have 2 or 3 dimensions")
+    batch = values.shape[0] if values.dim() == 3 else 1
+    rows, cols = values.shape[-2:]
+    if transposed:
+        rows, cols = cols, rows
+    groups = 0 if offsets is None else offsets.numel() - 1
+    dev = values.device
+    for t, name in ((q, "q"), (scales, "scales"), (offsets, "offsets")):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {names[0]} on {dev}")
+    shape = (batch, rows, cols // 2) if values.dim() == 3 else (rows, cols // 2)
+    return batch, rows, cols, (
+        _ptr(values, tuple(values.shape), values.dtype, names[0]), _ptr(q, shape, torch.uint8, "q"),
+        _ptr(scales, (mx_scales_bytes(rows, cols, batch, groups),), torch.uint8, "scales"),
+        _ptr(offsets, (groups + 1,), torch.int32, "offsets"), groups)
+
+
+def gemm_epi_mx_quantize(src, q, scales, offsets=None, transposed=False, stream=None):
+    """Quantise src (rows x cols, or batch x rows x cols; 16-bit) to microscaled
+    4 bits: q (... x cols / 2, uint8) and scales (uint8, ``mx_scales_bytes``).
+    transposed: src is (batch x) cols x rows. offsets: int32, rows in groups."""
+    if src.dtype not in DTYPES:
+        raise ValueError(f"src has dtype {src.dtype}, expected float16 or bfloat16")
+    batch, rows, cols, (ps, pq, pc, po, groups) = _mx_args(src, q, scales, offsets, transposed, ("src",))
+    with torch.cuda.device(src.device):
+        _check(lib().gemm_epi_mx_quantize(batch, rows, cols, DTYPES[src.dtype], MX_TRANSPOSED if transposed else 0, ps,
+                                          po, groups, pq, pc, _stream_ptr(stream)))
+
+
+def gemm_epi_mx_dequantize(q, scales, out, offsets=None, stream=None):
+    """The values that q and scales stand for, into out (float16, bfloat16 or float32)."""
+    f32 = out.dtype == torch.float32
+    if not f32 and out.dtype not in DTYPES:
+        raise ValueError(f"out has dtype {out.dtype}, expected float16, bfloat16 or float32")
+    batch, rows, cols, (ps, pq, pc, po, groups) = _mx_args(out, q, scales, offsets, False, ("out",))
+    with torch.cuda.device(out.device):
+        _check(lib().gemm_epi_mx_dequantize(batch, rows, cols, BF16 if f32 else DTYPES[out.dtype],
+                                            FLAG_OUT_F32 if f32 else 0, pq, pc, po, groups, ps, _stream_ptr(stream)))
+
+
+def mx_quantize(src, offsets=None, transposed=False, stream=None):
+    """gemm_epi_mx_quantize with allocated outputs: (q, scales)."""
+    rows, cols = (src.shape[-1], src.shape[-2]) if transposed else src.shape[-2:]
+    q = torch.zeros((*src.shape[:-2], rows, cols // 2), dtype=torch.uint8, device=src.device)
+    n = mx_scales_bytes(rows, cols, src.shape[0] if src.dim() == 3 else 1, None if offsets is None else offsets.numel() - 1)
+    scales = torch.zeros(n, dtype=torch.uint8, device=src.device)
+    gemm_epi_mx_quantize(src, q, scales, offsets, transposed, stream)
+    return q, scales
+
+
+class MxPlan(_DevicePlan):
+    """A plan for Y = epilog(X . W^T) of microscaled 4-bit operands: X T x K, W
+    N x K (E given: E weights, rows grouped by expert as in GroupedPlan);
+    epilog BIAS, RELU_BIAS, GELU_BIAS or NONE; Y and bias of ``dtype``."""
+
+    def __init__(self, T: int, N: int, K: int, dtype: torch.dtype, epilog: str | int, E: int | None = None,
+                 out_f32: bool = False):
+        self.E, self.T, self.N, self.K = E, T, N, K
+        self.out_dtype = torch.float32 if out_f32 else dtype
+        self.dtype = self.bias_dtype = dtype
+        self.epilog = EPILOGS[epilog] if isinstance(epilog, str) else epilog
+        self._own(lib().gemm_epi_mx_plan(E or 0, T, N, K, DTYPES[dtype], self.epilog, FLAG_OUT_F32 if out_f32 else 0))
+        self.x_scales = mx_scales_bytes(T, K, groups=E)
+        self.w_scales = mx_scales_bytes(N, K, batch=E or 1)
+
+    def gemm_epi_mx_execute(self, Xq, Xs, Wq, Ws, bias, Y, offsets=None, stream=None):
+        """Operands as ``mx_quantize`` makes them; bias N (or E x N) values, or None for NONE."""
+        E, T, N, K, u8 = self.E, self.T, self.N, self.K, torch.uint8
+        w_shape = (N, K // 2) if Wq.dim() == 2 and E in (None, 1) else (E or 1, N, K // 2)
+        b_shape = (N,) if bias is not None and bias.dim() == 1 and E in (None, 1) else (E or 1, N)
+        _check(lib().gemm_epi_mx_execute(
+            self.handle, self._p(Xq, (T, K // 2), u8, "Xq"), self._p(Xs, (self.x_scales,), u8, "Xs"),
+            self._p(Wq, w_shape, u8, "Wq"), self._p(Ws, (self.w_scales,), u8, "Ws"),
+            self._p(bias, b_shape, self.bias_dtype, "bias"),
+            None if offsets is None else self._p(offsets, ((E or 0) + 1,), torch.int32, "offsets"),
+            self._p(Y, (T, N), self.out_dtype, "Y"), self._s(stream)))
+
+    def forward(self, Xq, Xs, Wq, Ws, bias, offsets=None, stream=None):
+        Y = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=Xq.device)
+        self.gemm_epi_mx_execute(Xq, Xs, Wq, Ws, bias, Y, offsets, stream)
+        return Y

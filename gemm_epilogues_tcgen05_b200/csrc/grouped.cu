@@ -26,26 +26,6 @@ void release(gemm_epi_plan_s* p) {
   delete p;
 }
 
-int max_pairs(const GroupedCfg& g, int sms) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
-  lc.blockDim = dim3((unsigned)g.threads, 1, 1);
-  lc.dynamicSmemBytes = g.smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, (const void*)g.fn, &lc) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return sms / 2;
-  }
-  return n < sms / 2 ? n : sms / 2;
-}
-
 ge::GroupedParams params(const gemm_epi_plan_s* p, const int32_t* offsets) {
   ge::GroupedParams k{};
   k.T = (int32_t)p->uT;
@@ -69,19 +49,8 @@ ge::GroupedParams params(const gemm_epi_plan_s* p, const int32_t* offsets) {
 
 int launch(const gemm_epi_plan_s* p, const CUtensorMap& a, const CUtensorMap& b, const ge::GroupedParams& k,
            cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p->grid, 1, 1);
-  cfg.blockDim = dim3((unsigned)p->gr.threads, 1, 1);
-  cfg.dynamicSmemBytes = p->gr.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p->gr.pair ? 2 : 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, p->gr.fn, a, b, k);
+  Launch l(p->grid, p->gr.threads, p->gr.smem, p->gr.pair, s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, p->gr.fn, a, b, k);
   if (e != cudaSuccess) return cuda_fail(e, "grouped kernel launch");
   return GEMM_EPI_OK;
 }
@@ -139,21 +108,8 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
     return nullptr;
   }
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) {
-    cuda_fail(e, "cudaGetDevice");
-    return nullptr;
-  }
-  int major = 0, minor = 0, sms = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (major != 10 || minor != 0) {
-    fail(GEMM_EPI_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.0 (sm_100a)", dev,
-         major, minor);
-    return nullptr;
-  }
+  int dev = 0, sms = 0;
+  if (require_b200(&dev, &sms)) return nullptr;
   auto* p = new gemm_epi_plan_s();
   p->kind = 1;
   p->uT = p->T = T;
@@ -198,14 +154,14 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     release(p);
     return nullptr;
   }
-  e = cudaFuncSetAttribute(g.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
+  cudaError_t e = cudaFuncSetAttribute(g.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
   if (e != cudaSuccess) {
     cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
     release(p);
     return nullptr;
   }
   if (g.pair) {
-    const int pairs = max_pairs(g, sms);
+    const int pairs = resident_pairs((const void*)g.fn, g.threads, g.smem, sms);
     p->grid = 2 * (int)(tiles < pairs ? tiles : pairs);
   } else {
     p->grid = (int)(tiles < sms ? tiles : sms);

@@ -91,6 +91,27 @@ struct GroupedEpiWarps {
   static constexpr int value = TR >= 128 ? 8 : 4;
 };
 
+// start[i] for i in this lane's run [a, b): tiles of TR rows (times `mult`) of
+// the experts before i.
+template <int TR>
+__device__ __forceinline__ void grouped_prefix(const GroupedParams& p, const int* offs, int* start, int mult, int a, int b) {
+  const int lane = static_cast<int>(lane_id());
+  int sum = 0;
+  for (int i = a; i < b; ++i)
+    if (i < p.E) sum += (offs[i + 1] - offs[i] + TR - 1) / TR;
+  int s = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += o;
+  }
+  s -= sum;  // tiles of the experts before this lane's
+  for (int i = a; i < b; ++i) {
+    start[i] = s * mult;
+    if (i < p.E) s += (offs[i + 1] - offs[i] + TR - 1) / TR;
+  }
+}
+
 // The expert table in shared memory, made by one warp: offs[0..E] (sanitised)
 // and start[0..E], the first tile of each expert. Each lane takes a
 // contiguous run of entries, so two warp scans do.
@@ -101,7 +122,7 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* offs,
   const int a = min(lane * per, p.E + 1), b = min(a + per, p.E + 1);
   int mx = 0;
   for (int i = a; i < b; ++i) {
-    mx = max(mx, min(p.offsets[i], p.T));
+    mx = p.offsets ? max(mx, min(p.offsets[i], p.T)) : i * p.T;  // no offsets: one group of T rows
     offs[i] = mx;  // running maximum within the lane's run
   }
   int incl = mx;
@@ -114,20 +135,7 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* offs,
   if (lane == 0) before = 0;
   for (int i = a; i < b; ++i) offs[i] = max(offs[i], before);
   __syncwarp();
-  int sum = 0;
-  for (int i = a; i < b; ++i)
-    if (i < p.E) sum += (offs[i + 1] - offs[i] + TR - 1) / TR;
-  int s = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += o;
-  }
-  s -= sum;  // row tiles of the experts before this lane's
-  for (int i = a; i < b; ++i) {
-    start[i] = s * tiles_per_mt;
-    if (i < p.E) s += (offs[i + 1] - offs[i] + TR - 1) / TR;
-  }
+  grouped_prefix<TR>(p, offs, start, tiles_per_mt, a, b);
 }
 
 // One output tile: features f0.., and `n` columns of the MMA's N slot of

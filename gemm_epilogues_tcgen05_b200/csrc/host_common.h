@@ -108,33 +108,79 @@ struct SkinnyCfg {
   int stages = 0;
 };
 
-// A plan of products grouped by expert.
+// A plan of products grouped by expert, or of a microscaled product.
 struct GroupedCfg {
   ge_inst::GroupedKernelFn fn = nullptr;
+  ge_inst::MxKernelFn mx_fn = nullptr;  // kind == 2
   uint32_t smem = 0;
   int threads = 0, stages = 0;
   int TR = 0, BK = 64;  // rows of a tile; k per stage
   bool pair = false;
   int launches = 1;
-  int E = 0, n_ft = 0, n_kt = 0, group = 1;
+  int E = 0 /* 0: no groups (kind 2) */, n_ft = 0, n_kt = 0, group = 1;
 };
 
-// Row-major matrices of 16-bit elements or of bytes: `d2` of them, `d1` rows of
-// `d0` contiguous elements each; boxes of b0 x b1, 128-byte swizzle.
+// Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`
+// rows of `d0` contiguous elements each; boxes of b0 x b1.
 inline int encode_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                     uint32_t b0, uint32_t b1, const char* name) {
+                     uint32_t b0, uint32_t b1, const char* name,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(GEMM_EPI_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   if (inject_encode_failure()) return fail(GEMM_EPI_ERR_CUDA, "injected tensor map encode failure");
-  const uint64_t row = d0 * (type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2);
+  const uint64_t size = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : type == CU_TENSOR_MAP_DATA_TYPE_UINT16 ? 2 : 4;
   const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {row, row * d1};
+  const cuuint64_t strides[2] = {d0 * size, d0 * size * d1};
   const cuuint32_t box[3] = {b0, b1, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(GEMM_EPI_ERR_CUDA, "tensor map encode for %s failed (CUresult %d)", name, (int)r);
   return GEMM_EPI_OK;
+}
+
+// The current device's number and SM count; an error unless it is a B200.
+inline int require_b200(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
+  cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  if (major != 10 || minor != 0)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.0 (sm_100a)", *dev,
+                major, minor);
+  return GEMM_EPI_OK;
+}
+
+// A launch configuration with clusters of two for CTA pairs.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  Launch(int grid, int threads, uint32_t smem, bool pair, cudaStream_t s) {
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pair ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+// CTA pairs of this kernel that the device holds at once; one per two SMs if
+// the query fails.
+inline int resident_pairs(const void* fn, int threads, uint32_t smem, int sms) {
+  Launch l(sms / 2 * 2, threads, smem, true, nullptr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return sms / 2;
+  }
+  return n < sms / 2 ? n : sms / 2;
 }
 
 // Makes `device` current for the calls of one entry point and puts the
@@ -205,7 +251,7 @@ struct gemm_epi_plan_s {
   CUtensorMap tmXs;  // the row operand with a TP-row box
   const void* ws_ptr = nullptr;
   CUtensorMap tmWs;  // the weight operand with a 64·KPS-row box
-  ge_host::GroupedCfg gr;  // kind == 1
+  ge_host::GroupedCfg gr;  // kind 1 and 2
 };
 
 namespace ge_host {

@@ -12,6 +12,7 @@ namespace ge {
 struct TileParams;
 struct SkinnyParams;
 struct GroupedParams;
+struct MxParams;
 }  // namespace ge
 
 namespace ge_inst {
@@ -53,5 +54,15 @@ GroupedInstance grouped_f16_mn(int tr, int epi);
 GroupedInstance grouped_f16_nk(int tr, int epi);
 GroupedInstance grouped_bf16_mn(int tr, int epi);
 GroupedInstance grouped_bf16_nk(int tr, int epi);
+
+// Microscaled product: tiles of 128 rows (one CTA) or 256 (CTA pair); BIAS,
+// RELU_BIAS, GELU_BIAS and STORE.
+using MxKernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ge::MxParams);
+struct MxInstance {
+  MxKernelFn fn;
+  uint32_t smem;
+  int threads, stages, bk;
+};
+MxInstance mx_any(int tr, int epi, bool bf16);
 
 }  // namespace ge_inst

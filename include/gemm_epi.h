@@ -45,7 +45,7 @@
  *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny, GEMM_EPI_FORCE_BN=64|128|192|256,
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
  *   GEMM_EPI_SKINNY_PREFETCH, GEMM_EPI_TAIL_SPLIT=0|1, GEMM_EPI_CACHE_HINTS=0|1,
- *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped plans),
+ *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped and microscaled plans),
  *   GEMM_EPI_PAIR_SPLIT=0|1 (stream-K CTA pairs; off by default),
  *   GEMM_EPI_PAIR_SK_FIRST=0|1 (with stream-K: its tiles before the whole tiles, the
  *   default, or after them)
@@ -365,6 +365,75 @@ GEMM_EPI_API int gemm_epi_grouped_drelu_bgrad_execute(gemm_epi_plan_t plan, cons
  * dbias NULL, or E x K floats receiving the sums of X's rows (a second launch). */
 GEMM_EPI_API int gemm_epi_grouped_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ,
                                                 const int32_t* offsets, void* dW, float* dbias, cudaStream_t stream);
+
+/*
+ * Microscaled 4-bit operands (for serving: a weight takes 17/32 of a byte an
+ * element, and the tensor cores multiply such operands at four times the
+ * 16-bit rate).
+ *
+ * Values: blocks of 32 consecutive elements of a row share a power-of-two
+ * scale s = 2^(floor(log2 max|x|) - 2), at least 2^-127; each x / s is rounded
+ * to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 with its sign (e2m1; ties to the
+ * even code, larger magnitudes to 6). A block of zeros has s = 2^-127; a block
+ * with an infinity or NaN has scale byte 255 and stands for NaN throughout.
+ * Storage: q holds cols / 2 bytes a row, the lower column in the low 4 bits.
+ * Scales are biased exponents (one byte; 127 is 1) in tiles of 128 rows x 4
+ * blocks, 512 bytes each: tile (i, j) of ceil(cols / 128) = kt tiles a row of
+ * tiles starts at byte 512 (i kt + j), and row r, block b of it is byte
+ * 16 (r % 32) + 4 (r / 32) + b. Matrices of a batch follow one another in whole
+ * tiles. Rows of several groups (offsets as for grouped products) start a new
+ * row of tiles each. Bytes of rows past the last are not written; blocks past
+ * the last column are written as 0.
+ */
+
+/* Flag of gemm_epi_mx_quantize: src is cols x rows (rows contiguous), as a K x N
+ * weight, whose blocks run along K. */
+enum { GEMM_EPI_MX_TRANSPOSED = 1u };
+
+/* Bytes of the scales of `batch` matrices of rows x cols; groups > 0 (with batch
+ * 1): of rows in that many groups. -1 with the error set for a bad shape. */
+GEMM_EPI_API int64_t gemm_epi_mx_scales_bytes(int64_t batch, int64_t rows, int64_t cols, int64_t groups);
+
+/*
+ * gemm_epi_mx_quantize: `batch` matrices of rows x cols (dtype; row-major, or
+ * cols x rows with GEMM_EPI_MX_TRANSPOSED, which needs rows a multiple of 8 and
+ * no groups) to q (batch x rows x cols / 2 bytes) and scales. cols is a
+ * multiple of 32. With groups > 0 (1 to 1024, batch 1) offsets are groups + 1
+ * int32 on the device, and rows of no group are not read or written. src, q,
+ * scales 16-byte, offsets 4-byte aligned. Asynchronous on `stream`, one launch
+ * on the current device, no workspace.
+ */
+GEMM_EPI_API int gemm_epi_mx_quantize(int64_t batch, int64_t rows, int64_t cols, gemm_epi_dtype dtype, uint32_t flags,
+                                      const void* src, const int32_t* offsets, int64_t groups, uint8_t* q,
+                                      uint8_t* scales, cudaStream_t stream);
+
+/* gemm_epi_mx_dequantize: the values that q and scales stand for, rounded to dtype
+ * (exact in bf16 unless below its range), or as fp32 with GEMM_EPI_FLAG_OUT_F32 (exact). */
+GEMM_EPI_API int gemm_epi_mx_dequantize(int64_t batch, int64_t rows, int64_t cols, gemm_epi_dtype dtype, uint32_t flags,
+                                        const uint8_t* q, const uint8_t* scales, const int32_t* offsets,
+                                        int64_t groups, void* out, cudaStream_t stream);
+
+/*
+ * gemm_epi_mx_plan: Y = epilog(X . W^T) of microscaled operands, X T x K and W
+ * N x K, accumulated in fp32. E = 0: one weight; E = 1 to 1024: grouped by
+ * expert, as gemm_epi_grouped_plan. K a multiple of 32, N of 8; epilog BIAS,
+ * RELU_BIAS, GELU_BIAS or NONE; dtype is Y's and the bias's; flags
+ * GEMM_EPI_FLAG_OUT_F32 or 0. gemm_epi_free, _query, _status and _set_bias_f32
+ * take the plan too.
+ */
+GEMM_EPI_API gemm_epi_plan_t gemm_epi_mx_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
+                                              gemm_epi_epilog epilog, uint32_t flags);
+
+/*
+ * gemm_epi_mx_execute: Xq, Xs as gemm_epi_mx_quantize makes them of T rows (with
+ * the same offsets and groups = E for a grouped plan), Wq, Ws of a batch of
+ * max(E, 1) weights of N rows x K. offsets: NULL exactly when E = 0. Values,
+ * scales and Y 16-byte, offsets 4-byte aligned; bias as gemm_epi_execute
+ * (max(E, 1) x N). Returns as gemm_epi_grouped_execute.
+ */
+GEMM_EPI_API int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                                     const uint8_t* Ws, const void* bias, const int32_t* offsets, void* Y,
+                                     cudaStream_t stream);
 
 #ifdef __cplusplus
 }
