@@ -70,17 +70,17 @@ struct GroupedSmem {
   static constexpr uint32_t B_BYTES = KPS * B_SUB;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
   static constexpr uint32_t TABLE = 2 * (kMaxExperts + 1) * 4;
-  static constexpr uint32_t FIXED = TABLE + 32 * 8 + 128 * 4 + 64 + 1024;
+  static constexpr uint32_t FIXED = TABLE + 40 * 8 + 128 * 4 + 64 + 1024;
   static constexpr int STAGES = (232448 - FIXED) / STAGE > 10 ? 10 : (232448 - FIXED) / STAGE;
   static constexpr uint32_t OFF_A = 0;
   static constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_B + STAGES * B_BYTES;
-  static constexpr uint32_t N_BARS = 2 * STAGES + 5;   // full, empty, tfull[2], tempty[2], drain
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 32 * 8;
+  static constexpr uint32_t N_BARS = 3 * STAGES + 5;   // full, empty, tail, tfull[2], tempty[2], drain
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 40 * 8;
   static constexpr uint32_t OFF_SUM = OFF_MISC + 64;   // column sums of the second half of the epilogue warps
   static constexpr uint32_t OFF_TABLE = OFF_SUM + 128 * 4;
   static constexpr uint32_t BYTES = OFF_TABLE + TABLE + 1024;
-  static_assert(N_BARS <= 32, "barrier space");
+  static_assert(N_BARS <= 40, "barrier space");
   static_assert(STAGES >= 3 && BYTES <= 232448, "grouped shared memory above the per-CTA limit");
 };
 
@@ -254,21 +254,23 @@ __device__ __forceinline__ void store_cols32(const float (&v)[32], void* base, i
   }
 }
 
-// zero rows [r0, r1) of a stage's MN-major operand chunks (128-byte rows; the
-// swizzle moves 16-byte units only within a row), by one warp, at a
-// shared::cluster address
-__device__ __forceinline__ void zero_rows_cluster(uint32_t addr, uint32_t chunk, int chunks, int r0, int r1) {
-  const int units = (r1 - r0) * 8;  // 16-byte units per chunk
-  for (int u = static_cast<int>(lane_id()); u < units * chunks; u += 32) {
-    const int c = u / units, x = u - c * units;
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr + c * chunk + r0 * 128 + x * 16),
-                 "r"(0u)
-                 : "memory");
-  }
+// Zero rows [r0, r1) of `chunks` MN-major operand chunks of 64 x 64 (128-byte
+// rows; the swizzle moves 16-byte units only within a row), by one warp.
+__device__ __forceinline__ void zero_rows(uint32_t addr, int chunks, int r0, int r1) {
+  for (int c = 0; c < chunks; ++c)
+    for (int x = r0 * 128 + static_cast<int>(lane_id()) * 16; x < r1 * 128; x += 512)
+      st_shared_v4(addr + c * (64 * kBK * 2) + x, make_uint4(0u, 0u, 0u, 0u));
 }
 
+// Threads: producer and MMA warps, the epilogue's, and for WGRAD the warp that
+// zeroes foreign rows.
+template <int EPI, int TR>
+struct GroupedThreads {
+  static constexpr int value = 64 + 32 * GroupedEpiWarps<TR>::value + (EPI == EPI_WGRAD ? 32 : 0);
+};
+
 template <bool PAIR, int TR, int KPS, int EPI, bool BF16, bool WK>
-__global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
+__global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const GroupedParams p) {
   using L = GroupedSmem<PAIR, TR, KPS>;
@@ -289,7 +291,8 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
   uint8_t* sB = smem + L::OFF_B;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  uint64_t* tailbar = empty + STAGES;
+  uint64_t* tfull = tailbar + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -311,8 +314,9 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], WG && PAIR ? 2 : 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&tailbar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -345,36 +349,49 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
-      GroupedTile w;
-      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
-        const int f0 = w.f0 + static_cast<int>(rank) * 128;
-        const int nloc = PAIR ? w.n / 2 : w.n;
-        const int c0 = w.c0 + static_cast<int>(rank) * nloc;
-        const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
-        const int boxes = (nloc + (WG ? 64 : BXR) - 1) / (WG ? 64 : BXR);
-        const uint32_t tx = (PAIR ? 2u : 1u) *
-                            (L::A_BYTES + static_cast<uint32_t>(boxes) * (WG ? 64 * kBK * 2 : KPS * BXR * kBK * 2));
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-          const uint32_t s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!wait_bounded(&empty[s], ph ^ 1u, wp, abort_flag, 1)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-          const uint32_t bar = full0 + s * 8;
-          uint8_t* a = sA + s * L::A_BYTES;
-          uint8_t* b = sB + s * L::B_BYTES;
+    // (the whole warp walks the tiles, one elected lane issues: elect_one)
+    const bool issuer = elect_one();
+    uint32_t it = 0, s = 0, ph = 1;
+    bool ok = true;
+    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
+    GroupedTile w;
+    for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+      const int f0 = w.f0 + static_cast<int>(rank) * 128;
+      const int nloc = PAIR ? w.n / 2 : w.n;
+      const int c0 = w.c0 + static_cast<int>(rank) * nloc;
+      const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
+      const bool cut = WG && (w.rows & 15) != 0;  // the last k-block holds foreign rows within a step of 16
+      const int boxes = (nloc + (WG ? 64 : BXR) - 1) / (WG ? 64 : BXR);
+      const uint32_t tx = L::A_BYTES + static_cast<uint32_t>(boxes) * (WG ? 64 * kBK * 2 : KPS * BXR * kBK * 2);
+      for (int kb = 0; kb < kbs; ++kb, ++it) {
+        ok = wait_bounded(&empty[s], ph, wp, abort_flag, 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* a = sA + s * L::A_BYTES;
+        uint8_t* b = sB + s * L::B_BYTES;
+        if (issuer) {
           if constexpr (WG) {
             const int t = w.row0 + kb * kBK;
-            tma_load_3d<PAIR>(a, &tmA, bar, f0, t, 0);
-            tma_load_3d<PAIR>(a + L::A_CHUNK, &tmA, bar, f0 + 64, t, 0);
-            for (int i = 0; i < boxes; ++i) tma_load_3d<PAIR>(b + i * (64 * kBK * 2), &tmB, bar, c0 + i * 64, t, 0);
+            if (cut && kb == kbs - 1) {
+              // signalled to this CTA's zeroing warp, which passes it on to the MMA
+              mbar_arrive_expect_tx(&tailbar[s], tx);
+              const uint32_t bar = smem_u32(&tailbar[s]);
+              tma_load_3d<false>(a, &tmA, bar, f0, t, 0);
+              tma_load_3d<false>(a + L::A_CHUNK, &tmA, bar, f0 + 64, t, 0);
+              for (int i = 0; i < boxes; ++i) tma_load_3d<false>(b + i * (64 * kBK * 2), &tmB, bar, c0 + i * 64, t, 0);
+            } else {
+              if (rank == 0)
+                mbar_arrive_expect_tx(&full[s], PAIR ? 2 * tx : tx);
+              else
+                mbar_arrive_peer(full0 + s * 8);
+              const uint32_t bar = full0 + s * 8;
+              tma_load_3d<PAIR>(a, &tmA, bar, f0, t, 0);
+              tma_load_3d<PAIR>(a + L::A_CHUNK, &tmA, bar, f0 + 64, t, 0);
+              for (int i = 0; i < boxes; ++i) tma_load_3d<PAIR>(b + i * (64 * kBK * 2), &tmB, bar, c0 + i * 64, t, 0);
+            }
           } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], PAIR ? 2 * tx : tx);
+            const uint32_t bar = full0 + s * 8;
             const int k = kb * L::BK;
             if constexpr (WK) {
 #pragma unroll
@@ -389,79 +406,65 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
                 tma_load_3d<PAIR>(b + j * L::B_SUB + i * (BXR * kBK * 2), &tmB, bar, k + j * kBK, c0 + i * BXR, 0);
           }
         }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      // every issued copy has landed before the CTA can exit (in a pair the
-      // leader's barriers count them: there the release by the MMA shows it)
-      const uint32_t inflight = it < STAGES ? it : STAGES;
-      for (uint32_t i = it - inflight; i < it; ++i)
-        wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
-                     /*honour_abort=*/false);
     }
+    // every issued copy has landed before the CTA can exit (in a pair the
+    // leader's barriers count them: there the release by the MMA shows it)
+    const uint32_t inflight = it < STAGES ? it : STAGES;
+    for (uint32_t i = it - inflight; i < it; ++i)
+      wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
+                   /*honour_abort=*/false);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    uint32_t it = 0, tcount = 0;
-    bool ok = true;
-    const uint32_t peerA = PAIR ? mapa_shared(smem_u32(sA), 1) : 0u;
-    const uint32_t peerB = PAIR ? mapa_shared(smem_u32(sB), 1) : 0u;
+    const bool issuer = elect_one();
     if (rank == 0) {
+      uint32_t tcount = 0, s = 0, ph = 0;
+      bool ok = true;
       GroupedTile w;
       for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
         const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
         if (WG && kbs == 0) continue;  // an expert without rows: the epilogue stores zeros
         const uint32_t buf = tcount & 1u;
         const uint32_t tph = (tcount >> 1) & 1u;
+        ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
         const int tail = WG ? w.rows - (kbs - 1) * kBK : 0;  // rows in the last k-block
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
         const uint32_t d_tmem = tmem_base + buf * TR;
-        if (lane == 0) {
-          ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
+        for (int kb = 0; kb < kbs; ++kb) {
+          ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-        }
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-          const uint32_t s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
           const bool last = WG && kb == kbs - 1;
-          if (lane == 0 && ok) {
-            ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
-            tc_fence_after();
-          }
-          if (WG && last && (tail & 15)) {
-            // zero the foreign rows of the last step in both operands
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (ok) {
-              const int r1 = (tail + 15) & ~15;
-              const int bch = ((PAIR ? w.n / 2 : w.n) + 63) / 64;
-              zero_rows_cluster(smem_u32(sA) + s * L::A_BYTES, L::A_CHUNK, 2, tail, r1);
-              zero_rows_cluster(smem_u32(sB) + s * L::B_BYTES, 64 * kBK * 2, bch, tail, r1);
-              if constexpr (PAIR) {
-                zero_rows_cluster(peerA + s * L::A_BYTES, L::A_CHUNK, 2, tail, r1);
-                zero_rows_cluster(peerB + s * L::B_BYTES, 64 * kBK * 2, bch, tail, r1);
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-              }
-              asm volatile("fence.proxy.async;" ::: "memory");
-            }
-            __syncwarp();
-          }
-          if (lane == 0 && ok) {
-            const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
-            const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
-            const int steps = last ? (tail + 15) / 16 : 4;
+          if (PAIR && last) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the peer's zeroed rows
+          const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
+          const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
+          const int steps = last ? (tail + 15) / 16 : 4;
+          if (issuer) {
 #pragma unroll
             for (int j = 0; j < KPS; ++j) {
 #pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk) {
-                if (WG && kk >= steps) break;
                 // A MN-major: chunks A_CHUNK apart, 8 k-rows 1 KB apart, a step is 16 rows; K-major: 32 bytes a step
                 const uint64_t ad = WK ? smem_desc_sw128(a0 + j * L::A_SUB_K + kk * 32, 16, 1024)
                                        : smem_desc_sw128(a0 + j * L::A_SUB_MN + kk * 2048, L::A_CHUNK, 1024);
                 const uint64_t bd = WG ? smem_desc_sw128(b0 + kk * 2048, 64 * kBK * 2, 1024)
                                        : smem_desc_sw128(b0 + j * L::B_SUB + kk * 32, 16, 1024);
                 const uint32_t acc = (kb > 0 || j > 0 || kk > 0) ? 1u : 0u;
-                if constexpr (PAIR)
-                  umma_f16_pair(d_tmem, ad, bd, idesc, acc);
-                else
-                  umma_f16(d_tmem, ad, bd, idesc, acc);
+                if (!WG || kk < steps) {
+                  if constexpr (PAIR)
+                    umma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                  else
+                    umma_f16(d_tmem, ad, bd, idesc, acc);
+                }
               }
             }
             if constexpr (PAIR)
@@ -469,10 +472,14 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
             else
               umma_commit(&empty[s]);
           }
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
         // (fault injection: the epilogue then waits on a barrier nothing arrives on)
-        if (lane == 0 && ok && !(p.inject_stall && tcount == 0)) {
+        if (issuer && !(p.inject_stall && tcount == 0)) {
           if constexpr (PAIR)
             umma_commit_pair(&tfull[buf], BOTH);
           else
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
         }
         ++tcount;
       }
-      if (lane == 0) {
+      if (issuer) {
         if constexpr (PAIR)
           umma_commit_pair(drain, BOTH);
         else
@@ -488,8 +495,40 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
       }
     }
     // every MMA that writes this CTA's tensor memory is done before it is freed
-    if (lane == 0) wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
+    wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
     __syncwarp();
+  } else if (WG && warp == 2 + EW) {
+    // ---------------------------------------------- foreign rows (WGRAD)
+    // Ahead of the MMA by the depth of the ring: waits for the copies of an
+    // expert's last k-block in this CTA, zeroes the foreign rows of its last
+    // step and counts the stage in for the MMA.
+    if constexpr (WG) {
+      uint32_t it = 0, phases = 0;  // one phase bit per stage
+      bool ok = true;
+      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
+      GroupedTile w;
+      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+        it += static_cast<uint32_t>((w.rows + kBK - 1) / kBK);
+        if ((w.rows & 15) == 0) continue;
+        const uint32_t s = (it - 1) % STAGES;
+        ok = wait_bounded(&tailbar[s], (phases >> s) & 1u, wp, abort_flag, 9);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        phases ^= 1u << s;
+        const int tail = w.rows & (kBK - 1);
+        const int r1 = (tail + 15) & ~15;
+        zero_rows(smem_u32(sA) + s * L::A_BYTES, 2, tail, r1);
+        zero_rows(smem_u32(sB) + s * L::B_BYTES, ((PAIR ? w.n / 2 : w.n) + 63) / 64, tail, r1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_cluster(full0 + s * 8);
+          else
+            mbar_arrive(&full[s]);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const uint32_t ew = warp & 3u;         // TMEM lane quarter
@@ -535,24 +574,16 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
       if (ok) {
         const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TR;
         const int64_t orow = WG ? static_cast<int64_t>(w.e) * p.K + w.c0 : static_cast<int64_t>(w.c0);
-#pragma unroll 1
-        for (int c = static_cast<int>(eh); c * 32 < w.n; c += EW / 4) {
+        constexpr int STEP = EW / 4;  // the quarter's warps take chunks of 32 columns in turn
+        const auto finish = [&](const uint32_t (&acc)[32], int c) {
           float v[32];
-          if (empty_tile) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-          } else {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tbase + c * 32, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          }
+          for (int j = 0; j < 32; ++j) v[j] = empty_tile ? 0.f : __uint_as_float(acc[j]);
           const int rows = w.cols - c * 32;
           const int64_t at = (orow + c * 32) * p.N + fw;
           if constexpr (EPI == EPI_DRELU_BGRAD) {
             const uint32_t mine = mnext;
-            if ((c + EW / 4) * 32 < w.n) mnext = mask_word(c + EW / 4);
+            if ((c + STEP) * 32 < w.n) mnext = mask_word(c + STEP);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const uint32_t m = __shfl_sync(0xffffffffu, mine, j);
@@ -588,16 +619,30 @@ __global__ void __launch_bounds__(64 + 32 * GroupedEpiWarps<TR>::value, 1)
             store_cols32(v, reinterpret_cast<float*>(p.out) + at, p.N, rows, nvalid);
           else
             store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.out) + at, p.N, rows, nvalid);
-        }
-        if (!empty_tile) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              mbar_arrive_cluster(tempty0 + buf * 8);
-            else
-              mbar_arrive(&tempty[buf]);
+        };
+        // two chunks are read together, and the accumulator is handed back as
+        // soon as the last of them is in registers, before it is stored
+#pragma unroll 1
+        for (int c = static_cast<int>(eh); c * 32 < w.n || c == static_cast<int>(eh); c += 2 * STEP) {
+          const bool one = c * 32 < w.n, two = (c + STEP) * 32 < w.n;
+          uint32_t r0[32], r1[32];
+          if (!empty_tile) {
+            if (one) tmem_ld_32x32b_x32(tbase + c * 32, r0);
+            if (two) tmem_ld_32x32b_x32(tbase + (c + STEP) * 32, r1);
+            tmem_wait_ld();
+            if ((c + 2 * STEP) * 32 >= w.n) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (PAIR)
+                  mbar_arrive_peer(tempty0 + buf * 8);
+                else
+                  mbar_arrive(&tempty[buf]);
+              }
+            }
           }
+          if (one) finish(r0, c);
+          if (two) finish(r1, c + STEP);
         }
       }
       if (!empty_tile) ++tcount;

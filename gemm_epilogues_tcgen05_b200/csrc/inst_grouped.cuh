@@ -10,7 +10,7 @@ namespace ge_inst {
 template <bool PAIR, int TR, int KPS, int EPI, bool BF, bool WK>
 GroupedInstance grouped_one() {
   using L = ge::GroupedSmem<PAIR, TR, KPS>;
-  return {ge::grouped_kernel<PAIR, TR, KPS, EPI, BF, WK>, L::BYTES, 64 + 32 * ge::GroupedEpiWarps<TR>::value, L::STAGES,
+  return {ge::grouped_kernel<PAIR, TR, KPS, EPI, BF, WK>, L::BYTES, ge::GroupedThreads<EPI, TR>::value, L::STAGES,
           L::BK};
 }
 

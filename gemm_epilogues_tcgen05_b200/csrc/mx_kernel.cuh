@@ -210,112 +210,125 @@ __global__ void __launch_bounds__(320, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
-      MxTile w;
-      for (int tile = unit; ok && mx_tile<TR, FM>(p, offs, start, stile, tile, w); tile += units) {
-        const int f0 = w.f0 + static_cast<int>(rank) * 128;
-        const int nloc = PAIR ? w.n / 2 : w.n;
-        const int c0 = w.c0 + static_cast<int>(rank) * nloc;
-        const int boxes = (nloc + BXR - 1) / BXR;
-        const int ra = (w.cols + 127) / 128;  // scale tiles along the rows; both CTAs of a pair need all of them
-        // a peer whose features are all past N loads its scales at a tile past the last (zeros)
-        const int wtile = f0 < p.N ? w.e * mp.wt + f0 / 128 : p.E * mp.wt;
-        const uint32_t tx = (PAIR ? 2u : 1u) * (L::A_BYTES + static_cast<uint32_t>(boxes) * BXR * 128 +
-                                                static_cast<uint32_t>(1 + ra) * L::SF_TILE);
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const uint32_t s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!wait_bounded(&empty[s], ph ^ 1u, wp, abort_flag, 1)) {
-            ok = false;
-            break;
-          }
+    // (the whole warp walks the tiles, one elected lane issues: elect_one)
+    const bool issuer = elect_one();
+    uint32_t it = 0, s = 0, ph = 1;
+    bool ok = true;
+    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
+    MxTile w;
+    for (int tile = unit; ok && mx_tile<TR, FM>(p, offs, start, stile, tile, w); tile += units) {
+      const int f0 = w.f0 + static_cast<int>(rank) * 128;
+      const int nloc = PAIR ? w.n / 2 : w.n;
+      const int c0 = w.c0 + static_cast<int>(rank) * nloc;
+      const int boxes = (nloc + BXR - 1) / BXR;
+      const int ra = (w.cols + 127) / 128;  // scale tiles along the rows; both CTAs of a pair need all of them
+      // a peer whose features are all past N loads its scales at a tile past the last (zeros)
+      const int wtile = f0 < p.N ? w.e * mp.wt + f0 / 128 : p.E * mp.wt;
+      const uint32_t tx = (PAIR ? 2u : 1u) * (L::A_BYTES + static_cast<uint32_t>(boxes) * BXR * 128 +
+                                              static_cast<uint32_t>(1 + ra) * L::SF_TILE);
+      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        ok = wait_bounded(&empty[s], ph, wp, abort_flag, 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (issuer) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
           const uint32_t bar = full0 + s * 8;
+          uint8_t* sf = sSF + s * L::SF_BYTES;
           tma_load_3d<PAIR>(sA + s * L::A_BYTES, &tmA, bar, kb * 128, f0, w.e);
           for (int i = 0; i < boxes; ++i)
             tma_load_3d<PAIR>(sB + s * L::B_BYTES + i * (BXR * 128), &tmB, bar, kb * 128, c0 + i * BXR, 0);
-          uint8_t* sf = sSF + s * L::SF_BYTES;
           tma_load_3d<PAIR>(sf, &tmSA, bar, 0, kb * 2, wtile);
-          for (int i = 0; i < ra; ++i)
-            tma_load_3d<PAIR>(sf + (1 + i) * L::SF_TILE, &tmSB, bar, 0, kb * 2, w.srow + i);
+          tma_load_3d<PAIR>(sf + L::SF_TILE, &tmSB, bar, 0, kb * 2, w.srow);
+          if (L::RA == 2 && ra == 2) tma_load_3d<PAIR>(sf + 2 * L::SF_TILE, &tmSB, bar, 0, kb * 2, w.srow + 1);
+        }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-      const uint32_t inflight = it < STAGES ? it : STAGES;
-      for (uint32_t i = it - inflight; i < it; ++i)
-        wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
-                     /*honour_abort=*/false);
     }
+    const uint32_t inflight = it < STAGES ? it : STAGES;
+    for (uint32_t i = it - inflight; i < it; ++i)
+      wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
+                   /*honour_abort=*/false);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      if (rank == 0) {
-        uint32_t it = 0, tcount = 0;
-        bool ok = true;
-        MxTile w;
-        for (int tile = unit; ok && mx_tile<TR, FM>(p, offs, start, stile, tile, w); tile += units, ++tcount) {
-          const uint32_t buf = tcount % DBUF;
-          const uint32_t tph = (tcount / DBUF) & 1u;
-          if (!wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3)) break;
+    // the whole warp walks the tiles, one elected lane issues
+    const bool issuer = elect_one();
+    if (rank == 0) {
+      uint32_t it = 0, tcount = 0, s = 0, ph = 0;
+      bool ok = true;
+      MxTile w;
+      for (int tile = unit; ok && mx_tile<TR, FM>(p, offs, start, stile, tile, w); tile += units, ++tcount) {
+        const uint32_t buf = tcount % DBUF;
+        const uint32_t tph = (tcount / DBUF) & 1u;
+        ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * TR;
+        const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
+        const bool all_scales = w.cols > 128 * (L::RA - 1);  // every scale tile along the rows is in use
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * TR;
-          const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
-          const int ra = (w.cols + 127) / 128;
-          for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-            const uint32_t s = it % STAGES;
-            const uint32_t ph = (it / STAGES) & 1u;
-            if (!wait_bounded(&full[s], ph, wp, abort_flag, 4)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
-            const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
-            const uint32_t f0 = smem_u32(sSF + s * L::SF_BYTES);
-            // scale columns of this stage: A's two tiles, then per k tile the rows' tiles side by side
-            const uint32_t sfa = tmem_base + SF_COL + (it & 1u) * SF_SET;
-            const uint32_t sfb = sfa + 8;
-            const int steps = min(4, (p.K - kb * L::BK + 63) / 64);
+          const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
+          const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
+          const uint32_t f0 = smem_u32(sSF + s * L::SF_BYTES);
+          // scale columns of this stage: A's two tiles, then per k tile the rows' tiles side by side
+          const uint32_t sfa = tmem_base + SF_COL + (it & 1u) * SF_SET;
+          const uint32_t sfb = sfa + 8;
+          const int steps = min(4, (p.K - kb * L::BK + 63) / 64);
+          if (issuer) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (2 * h >= steps) break;
-              copy_scales<PAIR>(sfa + h * 4, f0 + h * 512);
-              for (int i = 0; i < ra; ++i)
-                copy_scales<PAIR>(sfb + h * (4 * L::RA) + i * 4, f0 + (1 + i) * L::SF_TILE + h * 512);
+              if (2 * h < steps) {
+                copy_scales<PAIR>(sfa + h * 4, f0 + h * 512);
+                copy_scales<PAIR>(sfb + h * (4 * L::RA), f0 + L::SF_TILE + h * 512);
+                if (L::RA == 2 && all_scales)
+                  copy_scales<PAIR>(sfb + h * (4 * L::RA) + 4, f0 + 2 * L::SF_TILE + h * 512);
+              }
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (kk >= steps) break;
-              const uint32_t id = static_cast<uint32_t>(kk & 1) * 2u;  // which byte pair of the scale column
-              umma_mxf4<PAIR>(d_tmem, smem_desc_sw128(a0 + kk * 32, 16, 1024), smem_desc_sw128(b0 + kk * 32, 16, 1024),
-                              idesc | (id << 4) | (id << 29), sfa + (kk >> 1) * 4, sfb + (kk >> 1) * (4 * L::RA),
-                              (kb > 0 || kk > 0) ? 1u : 0u);
+              if (kk < steps) {
+                const uint32_t id = static_cast<uint32_t>(kk & 1) * 2u;  // which byte pair of the scale column
+                umma_mxf4<PAIR>(d_tmem, smem_desc_sw128(a0 + kk * 32, 16, 1024), smem_desc_sw128(b0 + kk * 32, 16, 1024),
+                                idesc | (id << 4) | (id << 29), sfa + (kk >> 1) * 4, sfb + (kk >> 1) * (4 * L::RA),
+                                (kb > 0 || kk > 0) ? 1u : 0u);
+              }
             }
             if constexpr (PAIR)
               umma_commit_pair(&empty[s], BOTH);
             else
               umma_commit(&empty[s]);
           }
-          if (!ok) break;
-          // (fault injection: the epilogue then waits on a barrier nothing arrives on)
-          if (!(p.inject_stall && tcount == 0)) {
-            if constexpr (PAIR)
-              umma_commit_pair(&tfull[buf], BOTH);
-            else
-              umma_commit(&tfull[buf]);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
           }
         }
+        if (!ok) break;
+        // (fault injection: the epilogue then waits on a barrier nothing arrives on)
+        if (issuer && !(p.inject_stall && tcount == 0)) {
+          if constexpr (PAIR)
+            umma_commit_pair(&tfull[buf], BOTH);
+          else
+            umma_commit(&tfull[buf]);
+        }
+      }
+      if (issuer) {
         if constexpr (PAIR)
           umma_commit_pair(drain, BOTH);
         else
           umma_commit(drain);
       }
-      // every MMA that writes this CTA's tensor memory is done before it is freed
-      wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
     }
+    // every MMA that writes this CTA's tensor memory is done before it is freed
+    wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(320, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          mbar_arrive_cluster(tempty0 + buf * 8);
+          mbar_arrive_peer(tempty0 + buf * 8);
         else
           mbar_arrive(&tempty[buf]);
       }

@@ -22,6 +22,19 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 
+// True in one lane of the (converged) warp. Code under it keeps its addresses
+// in uniform registers, which tcgen05 instructions take their operands from; a
+// branch on the lane index made the compiler move every operand there one by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -234,6 +247,15 @@ __device__ __forceinline__ void cluster_sync() {
 // arrive on an mbarrier given by its shared::cluster address (possibly the peer's)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same for a signal that hands back tensor memory which this warp has read
+// (tcgen05.wait::ld, then tcgen05.fence::before_thread_sync): nothing written
+// to global memory needs to be visible with it, and a release at cluster scope
+// made the epilogue wait for its outstanding stores first (microscaled product,
+// T = 4096, N = 11008, K = 4096: 129.8 us with, 120.4 us without).
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 2-D tiled load into this CTA's shared memory whose completion is counted on
