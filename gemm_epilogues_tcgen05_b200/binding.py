@@ -341,6 +341,24 @@ class Plan:
         return (dW, dbias) if with_dbias else dW
 
 
+def _raw_stream(index: int, stream) -> int:
+    """The stream's handle; without one, the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_ptr(stream)
+
+
+def _ptr_on(index: int, t, shape, dtype, name) -> int:
+    """_ptr of a tensor that must be on CUDA device ``index``: one test for the
+    tensor that is right (these checks are most of a small call's host time);
+    _ptr says what is wrong with another."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, shape, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
 class _DevicePlan(Plan):
     """What plans bound to one device share: tensors are checked to be on it,
     and the default stream is its current one."""
@@ -349,16 +367,15 @@ class _DevicePlan(Plan):
         self.handle = handle
         if not handle:
             raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = torch.cuda.current_device()
 
     def _p(self, t, shape, dtype, name):
-        ptr = _ptr(t, shape, dtype, name)
-        if t is not None and t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
-        return ptr
+        if t is None:
+            return None
+        return _ptr_on(self.index, t, shape, dtype, name)
 
     def _s(self, stream) -> int:
-        return _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+        return _raw_stream(self.index, stream)
 
 
 class GroupedPlan(_DevicePlan):
@@ -380,6 +397,7 @@ class GroupedPlan(_DevicePlan):
         self.dtype = self.bias_dtype = dtype
         self.epilog = EPILOGS[epilog] if isinstance(epilog, str) else epilog
         self.aux_words = (N + 31) // 32
+        self._shapes = ((T, K), (E, N), (E + 1,), (T, N), (T, self.aux_words), (E, K, N), (E, K))
         self._own(lib().gemm_epi_grouped_plan(E, T, N, K, DTYPES[dtype], self.epilog,
                                               (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0)))
 
@@ -388,26 +406,26 @@ class GroupedPlan(_DevicePlan):
         return self._p(aux, spec[0], spec[1], "aux")
 
     def gemm_epi_grouped_execute(self, X, W, bias, offsets, Y, aux=None, stream=None):
-        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        i, dt, (xs, bs, os, ys, *_) = self.index, self.dtype, self._shapes
         _check(lib().gemm_epi_grouped_execute(
-            self.handle, self._p(X, (T, K), dt, "X"), self._p(W, self.w_shape, dt, "W"),
-            self._p(bias, (E, N), self.bias_dtype, "bias"), self._p(offsets, (E + 1,), torch.int32, "offsets"),
-            self._p(Y, (T, N), self.out_dtype, "Y"), self._aux(aux), self._s(stream)))
+            self.handle, _ptr_on(i, X, xs, dt, "X"), _ptr_on(i, W, self.w_shape, dt, "W"),
+            None if bias is None else _ptr_on(i, bias, bs, self.bias_dtype, "bias"),
+            _ptr_on(i, offsets, os, torch.int32, "offsets"), _ptr_on(i, Y, ys, self.out_dtype, "Y"),
+            None if aux is None else self._aux(aux), self._s(stream)))
 
     def gemm_epi_grouped_drelu_bgrad_execute(self, dY2, W2, aux, offsets, dZ, dbias, stream=None):
-        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        i, dt, (xs, bs, os, ys, ms, *_) = self.index, self.dtype, self._shapes
         _check(lib().gemm_epi_grouped_drelu_bgrad_execute(
-            self.handle, self._p(dY2, (T, K), dt, "dY2"), self._p(W2, self.w_shape, dt, "W2"),
-            self._p(aux, (T, self.aux_words), torch.int32, "aux"),
-            self._p(offsets, (E + 1,), torch.int32, "offsets"), self._p(dZ, (T, N), self.out_dtype, "dZ"),
-            self._p(dbias, (E, N), torch.float32, "dbias"), self._s(stream)))
+            self.handle, _ptr_on(i, dY2, xs, dt, "dY2"), _ptr_on(i, W2, self.w_shape, dt, "W2"),
+            _ptr_on(i, aux, ms, torch.int32, "aux"), _ptr_on(i, offsets, os, torch.int32, "offsets"),
+            _ptr_on(i, dZ, ys, self.out_dtype, "dZ"), _ptr_on(i, dbias, bs, torch.float32, "dbias"), self._s(stream)))
 
     def gemm_epi_grouped_wgrad_execute(self, X, dZ, offsets, dW, dbias=None, stream=None):
-        E, T, N, K, dt = self.E, self.T, self.N, self.K, self.dtype
+        i, dt, (xs, _, os, ys, _, ws, db) = self.index, self.dtype, self._shapes
         _check(lib().gemm_epi_grouped_wgrad_execute(
-            self.handle, self._p(X, (T, K), dt, "X"), self._p(dZ, (T, N), dt, "dZ"),
-            self._p(offsets, (E + 1,), torch.int32, "offsets"), self._p(dW, (E, K, N), self.out_dtype, "dW"),
-            self._p(dbias, (E, K), torch.float32, "dbias"), self._s(stream)))
+            self.handle, _ptr_on(i, X, xs, dt, "X"), _ptr_on(i, dZ, ys, dt, "dZ"),
+            _ptr_on(i, offsets, os, torch.int32, "offsets"), _ptr_on(i, dW, ws, self.out_dtype, "dW"),
+            None if dbias is None else _ptr_on(i, dbias, db, torch.float32, "dbias"), self._s(stream)))
 
     # conveniences that allocate their outputs (rows outside every expert: zeros)
     def forward(self, X, W, bias, offsets, stream=None):
@@ -438,47 +456,63 @@ def mx_scales_bytes(rows: int, cols: int, batch: int = 1, groups: int | None = N
     return n
 
 
-def _mx_args(values, q, scales, offsets, transposed, names):
-    """Checked shapes of one quantisation call: (batch, rows, cols, pointers...)."""
-    if values.dim() not in (2, 3):
-        raise ValueError(f"{names[0]} must have 2 or 3 dimensions")
-    batch = values.shape[0] if values.dim() == 3 else 1
-    rows, cols = values.shape[-2:]
-    if transposed:
-        rows, cols = cols, rows
-    groups = 0 if offsets is None else offsets.numel() - 1
-    dev = values.device
-    for t, name in ((q, "q"), (scales, "scales"), (offsets, "offsets")):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {names[0]} on {dev}")
-    shape = (batch, rows, cols // 2) if values.dim() == 3 else (rows, cols // 2)
-    return batch, rows, cols, (
-        _ptr(values, tuple(values.shape), values.dtype, names[0]), _ptr(q, shape, torch.uint8, "q"),
-        _ptr(scales, (mx_scales_bytes(rows, cols, batch, groups),), torch.uint8, "scales"),
-        _ptr(offsets, (groups + 1,), torch.int32, "offsets"), groups)
+def _mx_args(values, name, q, scales, offsets, transposed):
+    """Check one quantisation call's tensors (``values``: the 16-bit or fp32
+    side): device, batch, rows, cols, groups and the four pointers."""
+    if not isinstance(values, torch.Tensor) or values.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a tensor of 2 or 3 dimensions")
+    if not values.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    shape = values.shape
+    flat = len(shape) == 2
+    batch = 1 if flat else shape[0]
+    rows, cols = (shape[-1], shape[-2]) if transposed else (shape[-2], shape[-1])
+    if rows < 1 or cols < 32 or cols % 32 or batch < 1:
+        raise ValueError(f"bad shape {tuple(shape)} of {name}: rows >= 1 and a multiple of 32 columns")
+    index = values.get_device()
+    if offsets is None:
+        groups, tiles, po = 0, batch * ((rows + 127) // 128), None
+    else:
+        groups = offsets.numel() - 1
+        tiles = rows // 128 + min(groups, rows)
+        po = _ptr_on(index, offsets, (groups + 1,), torch.int32, "offsets")
+        if groups < 1:
+            raise ValueError("offsets must have at least 2 entries")
+    pq = _ptr_on(index, q, (rows, cols // 2) if flat else (batch, rows, cols // 2), torch.uint8, "q")
+    ps = _ptr_on(index, scales, (tiles * ((cols + 127) // 128) * 512,), torch.uint8, "scales")
+    return index, batch, rows, cols, groups, _ptr_on(index, values, shape, values.dtype, name), pq, ps, po
+
+
+def _on_device(index, fn, *args):
+    """One call with device ``index`` current (the quantisation entry points run on the current device)."""
+    if index == torch.cuda.current_device():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args))
 
 
 def gemm_epi_mx_quantize(src, q, scales, offsets=None, transposed=False, stream=None):
     """Quantise src (rows x cols, or batch x rows x cols; 16-bit) to microscaled
     4 bits: q (... x cols / 2, uint8) and scales (uint8, ``mx_scales_bytes``).
     transposed: src is (batch x) cols x rows. offsets: int32, rows in groups."""
-    if src.dtype not in DTYPES:
+    index, batch, rows, cols, groups, px, pq, ps, po = _mx_args(src, "src", q, scales, offsets, transposed)
+    dtype = DTYPES.get(src.dtype)
+    if dtype is None:
         raise ValueError(f"src has dtype {src.dtype}, expected float16 or bfloat16")
-    batch, rows, cols, (ps, pq, pc, po, groups) = _mx_args(src, q, scales, offsets, transposed, ("src",))
-    with torch.cuda.device(src.device):
-        _check(lib().gemm_epi_mx_quantize(batch, rows, cols, DTYPES[src.dtype], MX_TRANSPOSED if transposed else 0, ps,
-                                          po, groups, pq, pc, _stream_ptr(stream)))
+    _on_device(index, lib().gemm_epi_mx_quantize, batch, rows, cols, dtype, MX_TRANSPOSED if transposed else 0, px, po,
+               groups, pq, ps, _raw_stream(index, stream))
 
 
 def gemm_epi_mx_dequantize(q, scales, out, offsets=None, stream=None):
     """The values that q and scales stand for, into out (float16, bfloat16 or float32)."""
-    f32 = out.dtype == torch.float32
-    if not f32 and out.dtype not in DTYPES:
+    index, batch, rows, cols, groups, px, pq, ps, po = _mx_args(out, "out", q, scales, offsets, False)
+    f32 = out.dtype is torch.float32
+    dtype = BF16 if f32 else DTYPES.get(out.dtype)
+    if dtype is None:
         raise ValueError(f"out has dtype {out.dtype}, expected float16, bfloat16 or float32")
-    batch, rows, cols, (ps, pq, pc, po, groups) = _mx_args(out, q, scales, offsets, False, ("out",))
-    with torch.cuda.device(out.device):
-        _check(lib().gemm_epi_mx_dequantize(batch, rows, cols, BF16 if f32 else DTYPES[out.dtype],
-                                            FLAG_OUT_F32 if f32 else 0, pq, pc, po, groups, ps, _stream_ptr(stream)))
+    _on_device(index, lib().gemm_epi_mx_dequantize, batch, rows, cols, dtype, FLAG_OUT_F32 if f32 else 0, pq, ps, po,
+               groups, px, _raw_stream(index, stream))
 
 
 def mx_quantize(src, offsets=None, transposed=False, stream=None):

@@ -758,7 +758,7 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->split_k = 1;
     info->grid = p->grid;
     info->launches = p->gr.launches;
-    info->workspace_bytes = p->partial_bytes + sizeof(int) * (size_t)p->n_tickets;
+    info->workspace_bytes = p->partial_bytes + p->split_bytes + sizeof(int) * (size_t)p->n_tickets;
   } else if (p->kernel == 1) {
     info->tile_m = 128;  // features per tile (the MMA's M)
     info->tile_n = p->sk.TP;  // padded rows (the MMA's N)

@@ -8,20 +8,49 @@ using namespace ge_host;
 namespace {
 
 // Rows per tile, from the mean number of rows per expert (the plan knows no
-// offsets; any division of the rows is computed right by each).
-int choose_tr(int64_t E, int64_t T, int epilog) {
+// offsets; any division of the rows is computed right by each): the least of
+// rounds of tiles x time per tile. A tile of 64 k takes about 0.25 us on one
+// SM while all of them load (32-row tiles less when few are busy), 0.33 us on a
+// CTA pair. Measured (us, 32 / 128 / 256 rows): one expert of 1000 rows, K =
+// 4096, N = 256: 16.4 / 20.9 / 24.5; four of 100, K = 2048, N = 512: 11.2 /
+// 13.5 / 12.1. WGRAD is bound by its stores where experts are short: E = 32 of
+// 125 rows, K = 1024, N = 2048, fp32: 56.8 (128) and 60 (256); E = 8 of 1024,
+// K = 4096, N = 11008: 738 and 577.
+int choose_tr(int64_t E, int64_t T, int64_t N, int64_t K, int epilog, bool out_f32, int sms) {
+  const bool wgrad = epilog == GEMM_EPI_WGRAD;
   if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
     const int v = atoi(f);
-    if (v == 128 || v == 256 || (v == 32 && epilog != GEMM_EPI_WGRAD)) return v;
+    if (v == 128 || v == 256 || (v == 32 && !wgrad)) return v;
   }
-  const int64_t mean = (T + E - 1) / E;
-  if (epilog == GEMM_EPI_WGRAD) return 256;
-  return mean <= 32 ? 32 : mean <= 128 ? 128 : 256;
+  const int64_t active = E < T ? E : T, mean = (T + active - 1) / active;
+  int best = 0;
+  double best_us = 0;
+  for (int tr : {32, 128, 256}) {
+    if (wgrad && tr == 32) continue;
+    const int units = tr == 256 ? sms / 2 : sms;
+    const int64_t n_ft = (N + (tr == 256 ? 255 : 127)) / (tr == 256 ? 256 : 128);
+    const int64_t tiles = (wgrad ? E * ((K + tr - 1) / tr) : active * ((mean + tr - 1) / tr)) * n_ft;
+    const double busy = tiles < units ? double(tiles) / units : 1.0;
+    const double stage = tr == 256 ? 0.33 : tr == 128 ? (busy < 0.8 ? 0.2 : 0.25 * busy) : (busy < 0.58 ? 0.145 : 0.25 * busy);
+    double tile_us = double(((wgrad ? mean : K) + 63) / 64) * stage;
+    if (wgrad) {  // storing a tile
+      const double store = (tr == 256 ? 2.8 : 1.4) * (out_f32 ? 1.35 : 1.0);
+      if (tile_us < store) tile_us = store;
+    }
+    const double us = double((tiles + units - 1) / units) * tile_us + (tr == 256 ? 4.0 : tr == 128 ? 3.0 : 2.0);
+    if (best == 0 || us < best_us * 0.999) {
+      best = tr;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 void release(gemm_epi_plan_s* p) {
   if (p->partials) cudaFree(p->partials);
   if (p->col_tickets) cudaFree(p->col_tickets);
+  if (p->sk_partials) cudaFree(p->sk_partials);
+  if (p->sk_tickets) cudaFree(p->sk_tickets);
   if (p->status_host) cudaFreeHost(p->status_host);
   delete p;
 }
@@ -44,6 +73,10 @@ ge::GroupedParams params(const gemm_epi_plan_s* p, const int32_t* offsets) {
   k.bias_f32 = p->bias_f32;
   k.out_f32 = p->out_f32;
   k.inject_stall = p->inject_stall;
+  k.max_items = p->split_items;
+  k.force_splits = p->force_splits;
+  k.split_slots = p->sk_partials;
+  k.split_tickets = p->sk_tickets;
   return k;
 }
 
@@ -100,7 +133,9 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     return nullptr;
   }
   const bool wgrad = epilog == GEMM_EPI_WGRAD;
-  const int tr = choose_tr(E, T, (int)epilog);
+  int dev = 0, sms = 0;
+  if (require_b200(&dev, &sms)) return nullptr;
+  const int tr = choose_tr(E, T, N, K, (int)epilog, (flags & GEMM_EPI_FLAG_OUT_F32) != 0, sms);
   const int64_t n_ft = (N + (tr == 256 ? 255 : 127)) / (tr == 256 ? 256 : 128);
   const int64_t row_tiles = T / tr + (E < T ? E : T);  // at most: every expert may end in a part of a tile
   const int64_t tiles = wgrad ? E * n_ft * ((K + tr - 1) / tr) : row_tiles * n_ft;
@@ -108,8 +143,6 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
     return nullptr;
   }
-  int dev = 0, sms = 0;
-  if (require_b200(&dev, &sms)) return nullptr;
   auto* p = new gemm_epi_plan_s();
   p->kind = 1;
   p->uT = p->T = T;
@@ -123,9 +156,21 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
   p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
   p->aux_words = ceil_div(N, 32);
   const bool bf16 = dtype == GEMM_EPI_BF16;
-  const ge_inst::GroupedInstance inst =
-      bf16 ? (w_nk ? ge_inst::grouped_bf16_nk(tr, (int)epilog) : ge_inst::grouped_bf16_mn(tr, (int)epilog))
-           : (w_nk ? ge_inst::grouped_f16_nk(tr, (int)epilog) : ge_inst::grouped_f16_mn(tr, (int)epilog));
+  // Few tiles (as far as the plan can tell) with a long contraction: the
+  // instance that may share a tile among CTAs. Below about 20 stages joining the
+  // parts costs what it saves (T = 8, K = 2048, N = 512, 16 stages: 9.5 us whole,
+  // 11.6 us in four parts).
+  const int64_t stages = wgrad ? (T + 63) / 64 : (K + (tr == 32 ? 127 : 63)) / (tr == 32 ? 128 : 64);
+  const int64_t active = E < T ? E : T, mean = (T + active - 1) / active;
+  const int64_t expected = wgrad ? tiles : active * ((mean + tr - 1) / tr) * n_ft;
+  bool split = tr != 256 && stages >= 20 && 2 * expected <= sms;
+  if (const char* f = getenv("GEMM_EPI_FORCE_SPLIT")) {  // tuning override
+    p->force_splits = atoi(f) > 0 ? atoi(f) : 0;
+    if (p->force_splits) split = tr != 256 && p->force_splits > 1;
+  }
+  const auto pick = bf16 ? (w_nk ? ge_inst::grouped_bf16_nk : ge_inst::grouped_bf16_mn)
+                         : (w_nk ? ge_inst::grouped_f16_nk : ge_inst::grouped_f16_mn);
+  const ge_inst::GroupedInstance inst = pick(tr, (int)epilog, split);
   GroupedCfg& g = p->gr;
   g.fn = inst.fn;
   g.smem = inst.smem;
@@ -164,7 +209,7 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     const int pairs = resident_pairs((const void*)g.fn, g.threads, g.smem, sms);
     p->grid = 2 * (int)(tiles < pairs ? tiles : pairs);
   } else {
-    p->grid = (int)(tiles < sms ? tiles : sms);
+    p->grid = (int)(split || tiles > sms ? sms : tiles);  // (idle CTAs cost about 1 us)
   }
   e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
   if (e != cudaSuccess) {
@@ -187,6 +232,30 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     e = cudaMalloc((void**)&p->partials, p->partial_bytes);
     if (e == cudaSuccess) e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
     if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+  }
+  if (e == cudaSuccess && split) {
+    p->split_items = 2 * sms;  // room for two work items an SM
+    p->split_bytes = (size_t)p->split_items * tr * 128 * sizeof(float) + sizeof(int) * (size_t)p->split_items;
+    e = cudaMalloc((void**)&p->sk_partials, (size_t)p->split_items * tr * 128 * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * (size_t)p->split_items);
+    if (e == cudaSuccess) e = cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)p->split_items);
+  }
+  if (e == cudaSuccess && wgrad) {
+    // the optional bias gradient: row slices for about eight blocks an SM (one
+    // expert may hold all the rows: E = 32, K = 1024, 4000 rows, 631 of them in
+    // one expert, took 18.5 us with two slices)
+    const int64_t blocks = E * ceil_div(K, 256);
+    int64_t s = 8 * (int64_t)sms / blocks;
+    const int64_t most = (T + 63) / 64;
+    s = s > most ? most : s;
+    g.slices = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    if (g.slices > 1) {
+      p->partial_bytes = (size_t)g.slices * (size_t)E * (size_t)K * sizeof(float);
+      p->n_tickets = (int)blocks;
+      e = cudaMalloc((void**)&p->partials, p->partial_bytes);
+      if (e == cudaSuccess) e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
+      if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+    }
   }
   if (e != cudaSuccess) {
     cuda_fail(e, "grouped plan workspace");
@@ -300,14 +369,11 @@ int gemm_epi_grouped_wgrad_execute(gemm_epi_plan_t plan, const void* X, const vo
   k.out = dW;
   rc = launch(p, a, b, k, stream);
   if (rc || !dbias) return rc;
-  const dim3 grid((unsigned)ceil_div(p->uK, 64), (unsigned)p->gr.E);
-  if (p->dtype == GEMM_EPI_BF16)
-    ge::grouped_colsum_kernel<true><<<grid, 256, 0, stream>>>((const uint16_t*)X, offsets, (int)p->uT, p->gr.E,
-                                                              (int)p->uK, dbias);
-  else
-    ge::grouped_colsum_kernel<false><<<grid, 256, 0, stream>>>((const uint16_t*)X, offsets, (int)p->uT, p->gr.E,
-                                                               (int)p->uK, dbias);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)ceil_div(p->uK, 256), (unsigned)p->gr.E, (unsigned)p->gr.slices);
+  const auto kernel = p->dtype == GEMM_EPI_BF16 ? ge::grouped_colsum_kernel<true> : ge::grouped_colsum_kernel<false>;
+  Launch l(grid, 256, 0, false, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, (const uint16_t*)X, offsets, (int)p->uT, p->gr.E, (int)p->uK,
+                                           p->gr.slices, p->partials, p->col_tickets, dbias);
   if (e != cudaSuccess) return cuda_fail(e, "grouped bias-gradient launch");
   return GEMM_EPI_OK;
 }

@@ -54,6 +54,11 @@ struct GroupedParams {
   uint64_t timeout_ns;
   int32_t bias_f32, out_f32;
   int32_t inject_stall;
+  // one-CTA tiles, few of them: k split over several CTAs (grouped_splits)
+  int32_t max_items;        // slots; 0: no split
+  int32_t force_splits;     // override of grouped_splits' choice (0: none)
+  float* split_slots;       // [max_items][TR][128]
+  int* split_tickets;       // [max_items], zero between launches
 };
 
 // Shared memory: a ring of stages (W: 128 features x 64·KPS k; X: this CTA's
@@ -136,6 +141,40 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* offs,
   for (int i = a; i < b; ++i) offs[i] = max(offs[i], before);
   __syncwarp();
   grouped_prefix<TR>(p, offs, start, tiles_per_mt, a, b);
+}
+
+// How many CTAs share a tile's contraction when there are few tiles (few
+// rows, few or narrow experts): the S up to 16 with the least estimated time,
+//   rounds of tiles x S work items x (stages / S x stage time + joining),
+// where a stage's time is what one SM takes to stream it and joining is the
+// partials' trip through L2 (write, ticket, read by the last to arrive),
+// which grows with the parts and the rows. The constants (ns) are fitted to
+// measurements: T = 4, K = 8192, N = 512 takes 26.0 us unsplit and 19.0, 14.2,
+// 14.3, 17.8 with 2, 4, 8, 16 parts; T = 32, K = 4096, N = 1024 15.5 and 14.5,
+// 12.5, 13.8, 19.1; WGRAD of 8192 rows, K = N = 64 32.3 and 25.1, 20.9, 22.0
+// with 2, 4, 8, K = N = 256 33.2 and 30.0, 28.3, 34.6. Every CTA computes the
+// same from the same table.
+template <int TR>
+__device__ __forceinline__ int grouped_splits(const GroupedParams& p, int tiles, int stages, int units, int rows) {
+  constexpr int kStage = TR == 32 ? 290 : 240;
+  const int s = static_cast<int>(lane_id()) + 1;
+  const int64_t items = static_cast<int64_t>(tiles) * s;
+  uint64_t cost = ~0ull;
+  if (p.force_splits > 0) {
+    if (s <= 16 && (s == 1 || items <= p.max_items)) cost = static_cast<uint64_t>(abs(s - p.force_splits)) << 5 | static_cast<uint64_t>(s);
+  } else if (s <= 16 && (s == 1 || (items <= p.max_items && 2 * s <= stages && stages >= 16))) {
+    const int64_t rounds = (items + units - 1) / units;
+    const int r = min(rows, TR);
+    const int64_t join = s == 1 ? 0 : TR == 32 ? 1400 + s * (500 + r * 6) : 2400 + (1 + s) * r * 25;
+    cost = static_cast<uint64_t>(rounds * (static_cast<int64_t>((stages + s - 1) / s) * kStage + join)) << 5 |
+           static_cast<uint64_t>(s);
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, cost, d);
+    cost = o < cost ? o : cost;
+  }
+  return static_cast<int>(cost & 31u);
 }
 
 // One output tile: features f0.., and `n` columns of the MMA's N slot of
@@ -269,12 +308,16 @@ struct GroupedThreads {
   static constexpr int value = 64 + 32 * GroupedEpiWarps<TR>::value + (EPI == EPI_WGRAD ? 32 : 0);
 };
 
-template <bool PAIR, int TR, int KPS, int EPI, bool BF16, bool WK>
+// SPLIT: an instance of its own for plans that may have few tiles (the joining
+// code took registers from the epilogue of the others: WGRAD of 32 experts, K =
+// 1024, N = 2048, 57 us without, 99 us with).
+template <bool PAIR, int TR, int KPS, int EPI, bool BF16, bool WK, bool SPLIT = false>
 __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const GroupedParams p) {
   using L = GroupedSmem<PAIR, TR, KPS>;
   constexpr bool WG = EPI == EPI_WGRAD;
+  static_assert(!SPLIT || !PAIR, "only one-CTA tiles are split");
   static_assert(!WG || (KPS == 1 && !WK && TR >= 128), "WGRAD stages one k-block of 64 rows");
   constexpr int STAGES = L::STAGES;
   constexpr int EW = GroupedEpiWarps<TR>::value;
@@ -298,6 +341,8 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
+  volatile int* split_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 12);
+  int* split_count = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);
   float* half_sum = reinterpret_cast<float*>(smem + L::OFF_SUM);
   int* offs = reinterpret_cast<int*>(smem + L::OFF_TABLE);
   int* start = offs + kMaxExperts + 1;
@@ -338,7 +383,22 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       tmem_relinquish();
     }
   }
-  if (warp == 2) grouped_table<TR>(p, offs, start, p.n_ft);
+  wait_for_inputs();
+  if (warp == 2) {
+    grouped_table<TR>(p, offs, start, p.n_ft);
+    if constexpr (SPLIT) {
+      __syncwarp();
+      int most = 0;  // the longest expert
+      for (int e = static_cast<int>(lane); e < p.E; e += 32) most = max(most, offs[e + 1] - offs[e]);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+      const int tiles = WG ? p.E * p.n_ft * p.n_kt : start[p.E];
+      const int n = p.max_items > 0 && tiles > 0
+                        ? grouped_splits<TR>(p, tiles, WG ? (most + kBK - 1) / kBK : p.k_blocks, units, WG ? p.K : most)
+                        : 1;
+      if (lane == 0) *split_count = n;
+    }
+  }
   tc_fence_before();
   if constexpr (PAIR)
     cluster_sync();  // both CTAs' barriers exist before either side signals the other
@@ -346,6 +406,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  const int S = SPLIT ? *split_count : 1;  // work item i: part i % S of tile i / S
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -355,15 +416,24 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     bool ok = true;
     const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
     GroupedTile w;
-    for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+    for (int item = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units) {
       const int f0 = w.f0 + static_cast<int>(rank) * 128;
       const int nloc = PAIR ? w.n / 2 : w.n;
       const int c0 = w.c0 + static_cast<int>(rank) * nloc;
       const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
       const bool cut = WG && (w.rows & 15) != 0;  // the last k-block holds foreign rows within a step of 16
+      const int part = SPLIT ? item % S : 0;
+      const int kb0 = SPLIT ? kbs * part / S : 0, kb1 = SPLIT ? kbs * (part + 1) / S : kbs;
+      // One-CTA forward tiles start at different k: started together, all CTAs
+      // read the same columns of their weights at a time, which for rows of a
+      // power-of-two length fall on few memory channels (E = 64, K = 1024, N =
+      // 5000, N x K weights: 118.9 us with all at 0, 115.4 us; E = 8, K = 4096,
+      // N = 11008: 112.5 and 109.7)
+      const int rot = WG || PAIR || (SPLIT && S > 1) ? 0 : static_cast<int>(static_cast<uint32_t>(w.f0 / FM * 5 + w.e * 3) %
+                                                               static_cast<uint32_t>(kbs));
       const int boxes = (nloc + (WG ? 64 : BXR) - 1) / (WG ? 64 : BXR);
       const uint32_t tx = L::A_BYTES + static_cast<uint32_t>(boxes) * (WG ? 64 * kBK * 2 : KPS * BXR * kBK * 2);
-      for (int kb = 0; kb < kbs; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         ok = wait_bounded(&empty[s], ph, wp, abort_flag, 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -392,7 +462,8 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], PAIR ? 2 * tx : tx);
             const uint32_t bar = full0 + s * 8;
-            const int k = kb * L::BK;
+            const int kr = kb + rot;
+            const int k = (kr >= kbs ? kr - kbs : kr) * L::BK;
             if constexpr (WK) {
 #pragma unroll
               for (int j = 0; j < KPS; ++j) tma_load_3d<PAIR>(a + j * L::A_SUB_K, &tmA, bar, k + j * kBK, f0, w.e);
@@ -426,9 +497,11 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       uint32_t tcount = 0, s = 0, ph = 0;
       bool ok = true;
       GroupedTile w;
-      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+      for (int item = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units) {
         const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
-        if (WG && kbs == 0) continue;  // an expert without rows: the epilogue stores zeros
+        const int part = SPLIT ? item % S : 0;
+        const int kb0 = SPLIT ? kbs * part / S : 0, kb1 = SPLIT ? kbs * (part + 1) / S : kbs;
+        if (kb0 == kb1) continue;  // nothing to contract (an expert without rows): the epilogue takes zeros
         const uint32_t buf = tcount & 1u;
         const uint32_t tph = (tcount >> 1) & 1u;
         ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
@@ -438,7 +511,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         const int tail = WG ? w.rows - (kbs - 1) * kBK : 0;  // rows in the last k-block
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
         const uint32_t d_tmem = tmem_base + buf * TR;
-        for (int kb = 0; kb < kbs; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -458,7 +531,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
                                        : smem_desc_sw128(a0 + j * L::A_SUB_MN + kk * 2048, L::A_CHUNK, 1024);
                 const uint64_t bd = WG ? smem_desc_sw128(b0 + kk * 2048, 64 * kBK * 2, 1024)
                                        : smem_desc_sw128(b0 + j * L::B_SUB + kk * 32, 16, 1024);
-                const uint32_t acc = (kb > 0 || j > 0 || kk > 0) ? 1u : 0u;
+                const uint32_t acc = (kb > kb0 || j > 0 || kk > 0) ? 1u : 0u;
                 if (!WG || kk < steps) {
                   if constexpr (PAIR)
                     umma_f16_pair(d_tmem, ad, bd, idesc, acc);
@@ -507,9 +580,12 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       bool ok = true;
       const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
       GroupedTile w;
-      for (int tile = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
-        it += static_cast<uint32_t>((w.rows + kBK - 1) / kBK);
-        if ((w.rows & 15) == 0) continue;
+      for (int item = unit; ok && grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units) {
+        const int kbs = (w.rows + kBK - 1) / kBK;
+        const int part = SPLIT ? item % S : 0;
+        const int kb0 = SPLIT ? kbs * part / S : 0, kb1 = SPLIT ? kbs * (part + 1) / S : kbs;
+        it += static_cast<uint32_t>(kb1 - kb0);
+        if ((w.rows & 15) == 0 || kb1 == kb0 || kb1 < kbs) continue;
         const uint32_t s = (it - 1) % STAGES;
         ok = wait_bounded(&tailbar[s], (phases >> s) & 1u, wp, abort_flag, 9);
         ok = __all_sync(0xffffffffu, ok);
@@ -544,13 +620,16 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           for (int n = static_cast<int>(et); n < p.N; n += ET) p.dbias[static_cast<int64_t>(e) * p.N + n] = 0.f;
     }
     GroupedTile w;
-    for (int tile = unit; grouped_tile<EPI, TR, FM>(p, offs, start, tile, w); tile += units) {
+    for (int item = unit; grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units) {
       const int fw = w.f0 + static_cast<int>(rank * 128u + ew * 32u);  // the warp's first feature
       const int n = fw + static_cast<int>(lane);
       const bool n_ok = n < p.N;
       const int nvalid = max(0, min(32, p.N - fw));
       const int word = fw >> 5;
-      const bool empty_tile = WG && w.rows == 0;
+      const int kbs = WG ? (w.rows + kBK - 1) / kBK : p.k_blocks;
+      const int part = SPLIT ? item % S : 0;
+      const bool empty_tile = SPLIT ? kbs * part / S == kbs * (part + 1) / S : kbs == 0;
+      bool finisher = true;  // of a split tile, the CTA that takes its last ticket
       const uint32_t buf = tcount & 1u;
       const uint32_t tph = (tcount >> 1) & 1u;
       float bias_n = 0.f;
@@ -565,7 +644,8 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
                    ? __ldg(p.aux_in + static_cast<int64_t>(w.c0 + r) * p.aux_words + word)
                    : 0u;
       };
-      if constexpr (EPI == EPI_DRELU_BGRAD) mnext = mask_word(static_cast<int>(eh));
+      if constexpr (EPI == EPI_DRELU_BGRAD)
+        if (!SPLIT || S == 1) mnext = mask_word(static_cast<int>(eh));
       if (!empty_tile) {
         if (ok) ok = wait_bounded(&tfull[buf], tph, wp, abort_flag, 6);
         ok = __all_sync(0xffffffffu, ok);
@@ -575,10 +655,10 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TR;
         const int64_t orow = WG ? static_cast<int64_t>(w.e) * p.K + w.c0 : static_cast<int64_t>(w.c0);
         constexpr int STEP = EW / 4;  // the quarter's warps take chunks of 32 columns in turn
-        const auto finish = [&](const uint32_t (&acc)[32], int c) {
+        const auto finish = [&](const uint32_t (&acc)[32], int c, bool joined = false) {
           float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = empty_tile ? 0.f : __uint_as_float(acc[j]);
+          for (int j = 0; j < 32; ++j) v[j] = empty_tile && !joined ? 0.f : __uint_as_float(acc[j]);
           const int rows = w.cols - c * 32;
           const int64_t at = (orow + c * 32) * p.N + fw;
           if constexpr (EPI == EPI_DRELU_BGRAD) {
@@ -620,10 +700,30 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           else
             store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.out) + at, p.N, rows, nvalid);
         };
+        if (SPLIT && S > 1) {
+          // a part of a split tile: leave the fp32 accumulator in this item's slot
+          float* slot = p.split_slots + static_cast<int64_t>(item) * (TR * 128) + ew * 32 + lane;
+#pragma unroll 1
+          for (int c = static_cast<int>(eh); c * 32 < w.cols; c += STEP) {
+            uint32_t r[32];
+            if (!empty_tile) {
+              tmem_ld_32x32b_x32(tbase + c * 32, r);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j < w.cols) slot[(c * 32 + j) * 128] = empty_tile ? 0.f : __uint_as_float(r[j]);
+          }
+          if (!empty_tile) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+          }
+        }
         // two chunks are read together, and the accumulator is handed back as
         // soon as the last of them is in registers, before it is stored
 #pragma unroll 1
-        for (int c = static_cast<int>(eh); c * 32 < w.n || c == static_cast<int>(eh); c += 2 * STEP) {
+        for (int c = static_cast<int>(eh); (!SPLIT || S == 1) && (c * 32 < w.n || c == static_cast<int>(eh)); c += 2 * STEP) {
           const bool one = c * 32 < w.n, two = (c + STEP) * 32 < w.n;
           uint32_t r0[32], r1[32];
           if (!empty_tile) {
@@ -644,9 +744,54 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           if (one) finish(r0, c);
           if (two) finish(r1, c + STEP);
         }
+        if (SPLIT && S > 1) {
+          const int tile = item / S;
+          __threadfence();
+          named_bar_sync(1, ET);
+          if (et == 0) {
+            const int last = atomicAdd(p.split_tickets + tile, 1) == S - 1;
+            if (last) p.split_tickets[tile] = 0;  // ready for the next launch
+            *split_flag = last;
+          }
+          named_bar_sync(1, ET);
+          finisher = *split_flag != 0;
+          if (finisher) {
+            // the parts in order, so the sum does not depend on who came last;
+            // SB parts' loads of a chunk are in flight together
+            __threadfence();
+            constexpr int SB = EW == 4 ? 4 : 2;
+            const float* base = p.split_slots + static_cast<int64_t>(tile) * S * (TR * 128) + ew * 32 + lane;
+            if constexpr (EPI == EPI_DRELU_BGRAD) mnext = mask_word(static_cast<int>(eh));
+#pragma unroll 1
+            for (int c = static_cast<int>(eh); c * 32 < w.cols; c += STEP) {
+              float sum[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+#pragma unroll 1
+              for (int s0 = 0; s0 < S; s0 += SB) {
+                float x[SB][32];
+#pragma unroll
+                for (int s = 0; s < SB; ++s)
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    x[s][j] = s0 + s < S && c * 32 + j < w.cols
+                                  ? __ldcg(base + static_cast<int64_t>(s0 + s) * (TR * 128) + (c * 32 + j) * 128)
+                                  : 0.f;
+#pragma unroll
+                for (int s = 0; s < SB; ++s)
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) sum[j] += x[s][j];
+              }
+              uint32_t r[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[j]);
+              finish(r, c, true);
+            }
+          }
+        }
       }
       if (!empty_tile) ++tcount;
-      if constexpr (EPI == EPI_DRELU_BGRAD) {
+      if (EPI == EPI_DRELU_BGRAD && finisher) {
         // column sums: the quarter's two warps in order, then (more than one
         // row tile) one partial row per tile, summed in tile order by the
         // block of features' last tile, so the result does not depend on timing
@@ -702,19 +847,25 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
   }
 }
 
-// Column sums of X per expert (WGRAD's optional bias gradient): a block takes
-// one expert and 64 columns; 8 row lanes stride over the expert's rows and are
-// added in lane order. Bound by one read of X.
+// Column sums of X per expert (WGRAD's optional bias gradient), one read of X.
+// A block takes 256 columns of one expert and one of `slices` equal parts of
+// its rows (more than one where experts x columns alone would not fill the
+// GPU); its 8 warps stride over the rows, 16 bytes a lane. Warps are added in
+// order, and the block that takes a (columns, expert)'s last ticket adds the
+// slices in order, so the sum does not depend on timing.
 template <bool BF16>
 __global__ void __launch_bounds__(256) grouped_colsum_kernel(const uint16_t* __restrict__ X, const int32_t* offsets, int T,
-                                                             int E, int K, float* __restrict__ dbias) {
-  __shared__ float2 part[8][32];
+                                                             int E, int K, int slices, float* partials, int* tickets,
+                                                             float* __restrict__ dbias) {
+  __shared__ float part[8][256];
   __shared__ int span[2];
-  const int e = blockIdx.y;
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  __shared__ int last;
+  wait_for_inputs();
+  const int e = blockIdx.y, z = blockIdx.z;
+  const int lane = static_cast<int>(lane_id()), r = static_cast<int>(threadIdx.x >> 5);
   if (threadIdx.x < 32) {  // offsets as the products read them: the running maximum cut to [0, T]
     int m = 0, at_e = 0;
-    for (int i = static_cast<int>(threadIdx.x); i <= e + 1; i += 32) {
+    for (int i = lane; i <= e + 1; i += 32) {
       m = max(m, min(offsets[i], T));
       if (i <= e) at_e = m;
     }
@@ -723,38 +874,66 @@ __global__ void __launch_bounds__(256) grouped_colsum_kernel(const uint16_t* __r
       m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       at_e = max(at_e, __shfl_xor_sync(0xffffffffu, at_e, d));
     }
-    if (threadIdx.x == 0) {
-      span[0] = at_e;
-      span[1] = m;
+    if (lane == 0) {
+      const int64_t n = m - at_e;
+      span[0] = at_e + static_cast<int>(n * z / slices);
+      span[1] = at_e + static_cast<int>(n * (z + 1) / slices);
     }
   }
   __syncthreads();
-  const int k = blockIdx.x * 64 + c * 2;
-  float2 s = make_float2(0.f, 0.f);
-  if (k < K)
-    for (int t = span[0] + r; t < span[1]; t += 8) {
-      const uint32_t u = *reinterpret_cast<const uint32_t*>(X + static_cast<int64_t>(t) * K + k);
-      if constexpr (BF16) {
-        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&u);
-        s.x += __low2float(h);
-        s.y += __high2float(h);
-      } else {
-        const __half2 h = *reinterpret_cast<const __half2*>(&u);
-        s.x += __low2float(h);
-        s.y += __high2float(h);
-      }
-    }
-  part[r][c] = s;
-  __syncthreads();
-  if (r == 0 && k < K) {
+  const int k = blockIdx.x * 256 + lane * 8;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (k < K) {
+    const auto add = [&](uint4 v) {
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      s.x += part[i][c].x;
-      s.y += part[i][c].y;
+      for (int i = 0; i < 4; ++i) {
+        float2 f;
+        if constexpr (BF16)
+          f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+        else
+          f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        s[2 * i] += f.x;
+        s[2 * i + 1] += f.y;
+      }
+    };
+    int t = span[0] + r;
+    for (; t + 24 < span[1]; t += 32) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(X + static_cast<int64_t>(t + 8 * i) * K + k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add(v[i]);
     }
-    float* d = dbias + static_cast<int64_t>(e) * K + k;
-    d[0] = s.x;
-    d[1] = s.y;
+    for (; t < span[1]; t += 8) add(*reinterpret_cast<const uint4*>(X + static_cast<int64_t>(t) * K + k));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[r][lane * 8 + i] = s[i];
+  __syncthreads();
+  const int kc = blockIdx.x * 256 + static_cast<int>(threadIdx.x);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += part[i][threadIdx.x];
+  const int64_t at = static_cast<int64_t>(e) * K + kc;
+  if (slices == 1) {
+    if (kc < K) dbias[at] = sum;
+    return;
+  }
+  const int64_t stride = static_cast<int64_t>(E) * K;
+  if (kc < K) partials[z * stride + at] = sum;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int* tk = tickets + static_cast<int64_t>(e) * gridDim.x + blockIdx.x;
+    last = atomicAdd(tk, 1) == slices - 1;
+    if (last) *tk = 0;  // ready for the next launch
+  }
+  __syncthreads();
+  if (last && kc < K) {
+    __threadfence();
+    float t = 0.f;
+    for (int i = 0; i < slices; ++i) t += __ldcg(partials + i * stride + at);
+    dbias[at] = t;
   }
 }
 

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -118,6 +119,7 @@ struct GroupedCfg {
   bool pair = false;
   int launches = 1;
   int E = 0 /* 0: no groups (kind 2) */, n_ft = 0, n_kt = 0, group = 1;
+  int slices = 1;  // WGRAD: row slices of the optional bias gradient
 };
 
 // Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`
@@ -139,36 +141,54 @@ inline int encode_3d(CUtensorMap* map, CUtensorMapDataType type, const void* bas
   return GEMM_EPI_OK;
 }
 
-// The current device's number and SM count; an error unless it is a B200.
+// The current device's number and SM count; an error unless it is a B200. The
+// device's properties are asked for once (they never change).
 inline int require_b200(int* dev, int* sms) {
+  constexpr int kMax = 64;
+  static std::atomic<int> known[kMax];  // 0: not asked yet; else 1 + SM count, negative if no B200
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
-  cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  if (major != 10 || minor != 0)
+  int v = *dev >= 0 && *dev < kMax ? known[*dev].load(std::memory_order_relaxed) : 0;
+  if (v == 0) {
+    int major = 0, minor = 0, n = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+    v = major == 10 && minor == 0 && n > 0 ? 1 + n : -(major * 16 + minor) - 1;
+    if (*dev >= 0 && *dev < kMax) known[*dev].store(v, std::memory_order_relaxed);
+  }
+  if (v < 0)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.0 (sm_100a)", *dev,
-                major, minor);
+                (-v - 1) / 16, (-v - 1) % 16);
+  *sms = v - 1;
   return GEMM_EPI_OK;
 }
 
-// A launch configuration with clusters of two for CTA pairs.
+// A launch configuration: clusters of two for CTA pairs, and programmatic
+// serialization, so that a kernel's set-up (barriers, tensor memory) overlaps
+// the end of the kernel before it; the kernels wait for it before they touch
+// global memory (ge::wait_for_inputs).
 struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  Launch(int grid, int threads, uint32_t smem, bool pair, cudaStream_t s) {
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cudaLaunchAttribute attr[2];
+  Launch(dim3 grid, int threads, size_t smem, bool pair, cudaStream_t s) {
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = pair ? 2 : 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pair ? 2 : 1;
   }
+  Launch(int grid, int threads, size_t smem, bool pair, cudaStream_t s)
+      : Launch(dim3((unsigned)grid, 1, 1), threads, smem, pair, s) {}
+  Launch(const Launch&) = delete;
+  Launch& operator=(const Launch&) = delete;
 };
 
 // CTA pairs of this kernel that the device holds at once; one per two SMs if
@@ -252,6 +272,9 @@ struct gemm_epi_plan_s {
   const void* ws_ptr = nullptr;
   CUtensorMap tmWs;  // the weight operand with a 64·KPS-row box
   ge_host::GroupedCfg gr;  // kind 1 and 2
+  int force_splits = 0;    // GEMM_EPI_FORCE_SPLIT
+  int split_items = 0;     // kind 1, one-CTA tiles: slots of the k split (sk_partials, sk_tickets)
+  size_t split_bytes = 0;
 };
 
 namespace ge_host {
@@ -290,7 +313,8 @@ inline int take_status(gemm_epi_plan_s* p) {
   if (v != 0) {
     *s = 0;
     // an interrupted launch may have left split-tile tickets counted
-    if (p->sk_tickets) cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)ceil_div(p->N, 128));
+    if (p->sk_tickets)
+      cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)(p->kind == 0 ? ceil_div(p->N, 128) : p->split_items));
     if (p->col_tickets) cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
     if (p->pair_flags) cudaMemset(p->pair_flags, 0, sizeof(int) * (size_t)p->n_pair_flags);
     return fail(GEMM_EPI_ERR_TIMEOUT, "a kernel of this plan gave up waiting (watchdog code 0x%x)", v);

@@ -2,5 +2,5 @@
 #include "inst_grouped.cuh"
 
 namespace ge_inst {
-GroupedInstance grouped_bf16_mn(int tr, int epi) { return grouped_any<true, false>(tr, epi); }
+GroupedInstance grouped_bf16_mn(int tr, int epi, bool split) { return grouped_any<true, false>(tr, epi, split); }
 }  // namespace ge_inst

@@ -2,5 +2,5 @@
 #include "inst_grouped.cuh"
 
 namespace ge_inst {
-GroupedInstance grouped_f16_mn(int tr, int epi) { return grouped_any<false, false>(tr, epi); }
+GroupedInstance grouped_f16_mn(int tr, int epi, bool split) { return grouped_any<false, false>(tr, epi, split); }
 }  // namespace ge_inst

@@ -2,5 +2,5 @@
 #include "inst_grouped.cuh"
 
 namespace ge_inst {
-GroupedInstance grouped_f16_nk(int tr, int epi) { return grouped_any<false, true>(tr, epi); }
+GroupedInstance grouped_f16_nk(int tr, int epi, bool split) { return grouped_any<false, true>(tr, epi, split); }
 }  // namespace ge_inst

@@ -44,16 +44,17 @@ SkinnyKernelFn skinny_bf16_kps2(int tp, int epi);
 
 // Products grouped by expert: tiles of at most tr = 32 or 128 rows (one CTA,
 // 128 features) or 256 (CTA pair, 256 features); wk: the weights are N x K.
-// WGRAD has no tr = 32 and no wk instance (nullptr).
+// WGRAD has no tr = 32 and no wk instance (nullptr). split: the one-CTA tiles' k
+// may be shared by several CTAs.
 struct GroupedInstance {
   GroupedKernelFn fn;
   uint32_t smem;
   int threads, stages, bk;
 };
-GroupedInstance grouped_f16_mn(int tr, int epi);
-GroupedInstance grouped_f16_nk(int tr, int epi);
-GroupedInstance grouped_bf16_mn(int tr, int epi);
-GroupedInstance grouped_bf16_nk(int tr, int epi);
+GroupedInstance grouped_f16_mn(int tr, int epi, bool split);
+GroupedInstance grouped_f16_nk(int tr, int epi, bool split);
+GroupedInstance grouped_bf16_mn(int tr, int epi, bool split);
+GroupedInstance grouped_bf16_nk(int tr, int epi, bool split);
 
 // Microscaled product: tiles of 128 rows (one CTA) or 256 (CTA pair); BIAS,
 // RELU_BIAS, GELU_BIAS and STORE.

@@ -15,8 +15,8 @@ int64_t row_tiles(int64_t rows, int64_t groups) {
 
 // the shape checks that quantisation and its inverse share
 int check_shape(const char* call, int64_t batch, int64_t rows, int64_t cols, gemm_epi_dtype dtype, int64_t groups) {
-  if (batch < 1 || rows < 1 || cols < 32 || cols % 32 != 0 || rows > (int64_t)1 << 30 || cols > (int64_t)1 << 24 ||
-      batch > (int64_t)1 << 24 || batch * rows > (int64_t)1 << 40 || batch * rows * cols > (int64_t)1 << 46)
+  if (batch < 1 || rows < 1 || cols < 32 || cols % 32 != 0 || rows > (int64_t)1 << 30 || cols > (int64_t)1 << 22 ||
+      batch > (int64_t)1 << 24 || batch * rows > (int64_t)1 << 36)
     return fail(GEMM_EPI_ERR_INVALID_ARG,
                 "%s: bad shape batch=%lld rows=%lld cols=%lld (need all >= 1, cols a multiple of 32)", call, (long long)batch,
                 (long long)rows, (long long)cols);
@@ -35,13 +35,27 @@ ge::MxQuantParams quant_params(int64_t batch, int64_t rows, int64_t cols, int64_
   k.kt = ceil_div(cols, 128);
   k.rt = ceil_div(rows, 128);
   k.groups = (int32_t)groups;
+  k.flat = batch == 1 || rows % 128 == 0;
   k.offsets = offsets;
   return k;
 }
 
-unsigned blocks_for(int64_t items, int per_block, int sms, int blocks_per_sm) {
-  const int64_t want = (items + per_block - 1) / per_block, most = (int64_t)sms * blocks_per_sm;
-  return (unsigned)(want < most ? want : most);
+// Blocks along x for `items` of `per_block` each, `columns` blocks along y, and
+// about `per_sm` blocks an SM in all.
+dim3 grid_for(int64_t items, int per_block, int64_t columns, int sms, int per_sm) {
+  const int64_t want = (items + per_block - 1) / per_block;
+  int64_t most = ((int64_t)sms * per_sm + columns - 1) / columns;
+  if (most < 1) most = 1;
+  return dim3((unsigned)(want < most ? want : most), (unsigned)columns, 1);
+}
+
+size_t table_bytes(int64_t groups) { return groups > 0 ? 2 * (size_t)(groups + 1) * sizeof(int) : 0; }
+
+int run(void (*kernel)(ge::MxQuantParams), dim3 grid, int threads, size_t smem, const ge::MxQuantParams& k,
+        cudaStream_t stream) {
+  Launch l(grid, threads, smem, false, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, k);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "quantisation launch");
 }
 
 void release(gemm_epi_plan_s* p) {
@@ -182,21 +196,11 @@ int gemm_epi_mx_quantize(int64_t batch, int64_t rows, int64_t cols, gemm_epi_dty
   k.scales = scales;
   const bool bf16 = dtype == GEMM_EPI_BF16;
   if (t) {
-    const unsigned blocks = blocks_for(batch * ((rows + 63) / 64) * k.kt, 4, sms, 16);
-    if (bf16)
-      ge::mx_quantize_t_kernel<true><<<blocks, 128, 0, stream>>>(k);
-    else
-      ge::mx_quantize_t_kernel<false><<<blocks, 128, 0, stream>>>(k);
-  } else {
-    const unsigned blocks = blocks_for(batch * rows * ((cols + 1023) / 1024), 8, sms, 8);
-    const size_t table = groups > 0 ? 2 * (size_t)(groups + 1) * sizeof(int) : 0;
-    if (bf16)
-      ge::mx_quantize_kernel<true><<<blocks, 256, table, stream>>>(k);
-    else
-      ge::mx_quantize_kernel<false><<<blocks, 256, table, stream>>>(k);
+    const dim3 blocks = grid_for(batch * ((rows + 63) / 64), 4, k.kt, sms, 32);
+    return run(bf16 ? ge::mx_quantize_t_kernel<true> : ge::mx_quantize_t_kernel<false>, blocks, 128, 0, k, stream);
   }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "quantisation launch");
+  const dim3 blocks = grid_for(batch * rows, 8, (cols + 1023) / 1024, sms, 32);
+  return run(bf16 ? ge::mx_quantize_kernel<true> : ge::mx_quantize_kernel<false>, blocks, 256, table_bytes(groups), k, stream);
 }
 
 int gemm_epi_mx_dequantize(int64_t batch, int64_t rows, int64_t cols, gemm_epi_dtype dtype, uint32_t flags,
@@ -218,14 +222,9 @@ int gemm_epi_mx_dequantize(int64_t batch, int64_t rows, int64_t cols, gemm_epi_d
   k.scales = const_cast<uint8_t*>(scales);
   k.out = out;
   k.out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
-  const unsigned blocks = blocks_for(batch * rows * ((cols + 1023) / 1024), 8, sms, 8);
-  const size_t table = groups > 0 ? 2 * (size_t)(groups + 1) * sizeof(int) : 0;
-  if (dtype == GEMM_EPI_BF16)
-    ge::mx_dequantize_kernel<true><<<blocks, 256, table, stream>>>(k);
-  else
-    ge::mx_dequantize_kernel<false><<<blocks, 256, table, stream>>>(k);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "dequantisation launch");
+  const dim3 blocks = grid_for(batch * rows, 8, (cols + 1023) / 1024, sms, 32);
+  return run(dtype == GEMM_EPI_BF16 ? ge::mx_dequantize_kernel<true> : ge::mx_dequantize_kernel<false>, blocks, 256,
+             table_bytes(groups), k, stream);
 }
 
 gemm_epi_plan_t gemm_epi_mx_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype, gemm_epi_epilog epilog,

@@ -101,6 +101,14 @@ struct MxTile {
   int srow;  // scale tile of the first row
 };
 
+// One-CTA tiles start at different k, as the grouped kernel's do: with all
+// CTAs at the same columns of rows of K / 2 bytes, few memory channels are
+// asked at a time.
+template <bool PAIR>
+__device__ __forceinline__ int mx_first_k(const MxTile& w, int k_blocks) {
+  return PAIR ? 0 : static_cast<int>(static_cast<uint32_t>(w.f0 / 128 * 5 + w.e * 3) % static_cast<uint32_t>(k_blocks));
+}
+
 template <int TR, int FM>
 __device__ __forceinline__ bool mx_tile(const GroupedParams& p, const int* offs, const int* start, const int* stile,
                                         int tile, MxTile& w) {
@@ -194,6 +202,7 @@ __global__ void __launch_bounds__(320, 1)
       tmem_relinquish();
     }
   }
+  wait_for_inputs();
   if (warp == 2) {
     grouped_table<TR>(p, offs, start, p.n_ft);
     const int per = (p.E + 1 + 31) / 32;
@@ -226,7 +235,8 @@ __global__ void __launch_bounds__(320, 1)
       const int wtile = f0 < p.N ? w.e * mp.wt + f0 / 128 : p.E * mp.wt;
       const uint32_t tx = (PAIR ? 2u : 1u) * (L::A_BYTES + static_cast<uint32_t>(boxes) * BXR * 128 +
                                               static_cast<uint32_t>(1 + ra) * L::SF_TILE);
-      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+      int kb = mx_first_k<PAIR>(w, p.k_blocks);
+      for (int i_k = 0; i_k < p.k_blocks; ++i_k, ++it, kb = kb + 1 == p.k_blocks ? 0 : kb + 1) {
         ok = wait_bounded(&empty[s], ph, wp, abort_flag, 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -270,7 +280,8 @@ __global__ void __launch_bounds__(320, 1)
         const uint32_t d_tmem = tmem_base + buf * TR;
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w.n >> 3) << 17);
         const bool all_scales = w.cols > 128 * (L::RA - 1);  // every scale tile along the rows is in use
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        int kb = mx_first_k<PAIR>(w, p.k_blocks);
+        for (int i_k = 0; i_k < p.k_blocks; ++i_k, ++it, kb = kb + 1 == p.k_blocks ? 0 : kb + 1) {
           ok = wait_bounded(&full[s], ph, wp, abort_flag, 4);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -298,7 +309,7 @@ __global__ void __launch_bounds__(320, 1)
                 const uint32_t id = static_cast<uint32_t>(kk & 1) * 2u;  // which byte pair of the scale column
                 umma_mxf4<PAIR>(d_tmem, smem_desc_sw128(a0 + kk * 32, 16, 1024), smem_desc_sw128(b0 + kk * 32, 16, 1024),
                                 idesc | (id << 4) | (id << 29), sfa + (kk >> 1) * 4, sfb + (kk >> 1) * (4 * L::RA),
-                                (kb > 0 || kk > 0) ? 1u : 0u);
+                                (i_k > 0 || kk > 0) ? 1u : 0u);
               }
             }
             if constexpr (PAIR)

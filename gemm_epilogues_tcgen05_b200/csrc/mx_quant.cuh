@@ -32,6 +32,7 @@ struct MxQuantParams {
   int32_t kt;            // scale tiles along a row: ceil(cols / 128)
   int32_t rt;            // scale tiles along the rows of one matrix (no groups)
   int32_t groups;        // row groups (0: none)
+  int32_t flat;          // a row's place among the scales is its index (one matrix, or whole scale tiles)
   const int32_t* offsets;
   const void* src;
   uint8_t* q;
@@ -40,25 +41,43 @@ struct MxQuantParams {
   int32_t out_f32;
 };
 
-// scale byte of a block whose largest magnitude is `top`
-__device__ __forceinline__ uint32_t mx_scale_byte(float top) {
-  const int e = static_cast<int>(__float_as_uint(top) >> 23);  // top >= 0, or NaN
-  return top != top || e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
+// Scale byte of a block from its largest magnitude, given by the bits of the
+// 16-bit values with their signs off: as unsigned integers these are ordered
+// as the magnitudes are, infinity above every number and NaN above infinity.
+template <bool BF16>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+  float f;
+  if constexpr (BF16)
+    f = __uint_as_float(top << 16);
+  else
+    f = __half2float(__ushort_as_half(static_cast<unsigned short>(top)));
+  const int e = static_cast<int>(__float_as_uint(f) >> 23);
+  return e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
 }
+__device__ __forceinline__ uint32_t mx_abs2(uint32_t u) { return u & 0x7fff7fffu; }
 // 2^(127 - byte), exact for bytes up to 253 (255 stands for NaN; its values are not read)
 __device__ __forceinline__ float mx_inverse_scale(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
 // 2^(byte - 127)
 __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
 }
-// |a| or |b|, whichever is larger; NaN if either is
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+// eight values to e2m1, the first in the lowest four bits
+__device__ __forceinline__ uint32_t mx_pack8(float a, float b, float c, float d, float e, float f, float g, float h) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 p, q, s, t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, s, t};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h));
   return r;
 }
-__device__ __forceinline__ uint32_t mx_pack2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// two packed values
+__device__ __forceinline__ float2 mx_unpack2(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+  return __half22float2(__half2(h));
 }
 
 template <bool BF16>
@@ -73,7 +92,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 // The row's place among the scale tiles (rows counted with the padding of
 // whole tiles), or -1 for a row of no group.
 __device__ __forceinline__ int64_t mx_scale_row(const MxQuantParams& p, const int* offs, const int* start, int64_t row) {
-  if (p.groups == 0) return (row / p.rows) * (static_cast<int64_t>(p.rt) * 128) + row % p.rows;
+  if (p.groups == 0) {
+    if (p.flat) return row;
+    const int64_t b = row / p.rows;
+    return b * (static_cast<int64_t>(p.rt) * 128) + (row - b * p.rows);
+  }
   const int r = static_cast<int>(row);
   if (r < offs[0] || r >= offs[p.groups]) return -1;
   int lo = 0, hi = p.groups;  // offs[lo] <= r < offs[hi]
@@ -106,17 +129,15 @@ __device__ __forceinline__ void mx_table(const MxQuantParams& p, int* offs, int*
 // bytes a lane (8 elements; four lanes make a block), all in flight together.
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p) {
+  wait_for_inputs();
   extern __shared__ int table[];
   int* offs = table;
   int* start = table + p.groups + 1;
   mx_table(p, offs, start);
   const int lane = static_cast<int>(lane_id());
-  const int chunks = (p.cols + 1023) / 1024;
-  const int64_t items = p.batch * p.rows * chunks;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t row = it / chunks;
-    const int c0 = static_cast<int>(it - row * chunks) * 1024 + lane * 8;
+  const int c0 = static_cast<int>(blockIdx.y) * 1024 + lane * 8;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < p.batch * p.rows;
+       row += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t srow = mx_scale_row(p, offs, start, row);
     if (srow < 0) continue;
     const uint16_t* src = reinterpret_cast<const uint16_t*>(p.src) + row * p.cols;
@@ -127,16 +148,14 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = c0 + i * 256;
+      uint32_t top = __vmaxu2(__vmaxu2(mx_abs2(x[i].x), mx_abs2(x[i].y)), __vmaxu2(mx_abs2(x[i].z), mx_abs2(x[i].w)));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t byte = mx_scale_byte<BF16>(max(top & 0xffffu, top >> 16));
+      const float s = mx_inverse_scale(byte);
       const float2 a = unpack2<BF16>(x[i].x), b = unpack2<BF16>(x[i].y), d = unpack2<BF16>(x[i].z),
                    e = unpack2<BF16>(x[i].w);
-      float top = max_abs_nan(max_abs_nan(max_abs_nan(a.x, a.y), max_abs_nan(b.x, b.y)),
-                              max_abs_nan(max_abs_nan(d.x, d.y), max_abs_nan(e.x, e.y)));
-      top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t byte = mx_scale_byte(top);
-      const float s = mx_inverse_scale(byte);
-      const uint32_t w = mx_pack2(a.x * s, a.y * s) | mx_pack2(b.x * s, b.y * s) << 8 | mx_pack2(d.x * s, d.y * s) << 16 |
-                         mx_pack2(e.x * s, e.y * s) << 24;
+      const uint32_t w = mx_pack8(a.x * s, a.y * s, b.x * s, b.y * s, d.x * s, d.y * s, e.x * s, e.y * s);
       // four blocks' bytes make the word of this row in a scale tile
       uint32_t word = byte << ((lane >> 2 & 3) * 8);
       if (c >= p.cols) word = 0u;
@@ -154,15 +173,14 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
 // load, so a warp reads 128 contiguous bytes of every source row.
 template <bool BF16>
 __global__ void __launch_bounds__(128) mx_quantize_t_kernel(const MxQuantParams p) {
+  wait_for_inputs();
   const int lane = static_cast<int>(lane_id());
+  const int kt = static_cast<int>(blockIdx.y);
   const int64_t rchunks = (p.rows + 63) / 64;
-  const int64_t items = p.batch * rchunks * p.kt;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); it < items;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); it < p.batch * rchunks;
        it += static_cast<int64_t>(gridDim.x) * 4) {
-    const int64_t b = it / (rchunks * p.kt);
-    const int64_t in = it - b * rchunks * p.kt;
-    const int kt = static_cast<int>(in / rchunks);
-    const int64_t r = (in - kt * rchunks) * 64 + lane * 2;
+    const int64_t b = p.batch == 1 ? 0 : it / rchunks;
+    const int64_t r = (it - b * rchunks) * 64 + lane * 2;
     if (r >= p.rows) continue;  // no exchange between lanes below
     const uint16_t* src = reinterpret_cast<const uint16_t*>(p.src) + b * p.rows * p.cols + r;
     uint32_t word0 = 0u, word1 = 0u;
@@ -173,25 +191,21 @@ __global__ void __launch_bounds__(128) mx_quantize_t_kernel(const MxQuantParams 
       uint32_t x[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] = *reinterpret_cast<const uint32_t*>(src + (static_cast<int64_t>(c) + j) * p.rows);
-      float t0 = 0.f, t1 = 0.f;
+      uint32_t top = 0u;  // both rows' largest magnitudes
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float2 v = unpack2<BF16>(x[j]);
-        t0 = max_abs_nan(t0, v.x);
-        t1 = max_abs_nan(t1, v.y);
-      }
-      const uint32_t b0 = mx_scale_byte(t0), b1 = mx_scale_byte(t1);
+      for (int j = 0; j < 32; ++j) top = __vmaxu2(top, mx_abs2(x[j]));
+      const uint32_t b0 = mx_scale_byte<BF16>(top & 0xffffu), b1 = mx_scale_byte<BF16>(top >> 16);
       const float s0 = mx_inverse_scale(b0), s1 = mx_inverse_scale(b1);
       uint32_t q0[4], q1[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        q0[g] = q1[g] = 0u;
+        float2 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = unpack2<BF16>(x[g * 8 + 2 * j]), v = unpack2<BF16>(x[g * 8 + 2 * j + 1]);
-          q0[g] |= mx_pack2(u.x * s0, v.x * s0) << (8 * j);
-          q1[g] |= mx_pack2(u.y * s1, v.y * s1) << (8 * j);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = unpack2<BF16>(x[g * 8 + j]);
+        q0[g] = mx_pack8(v[0].x * s0, v[1].x * s0, v[2].x * s0, v[3].x * s0, v[4].x * s0, v[5].x * s0, v[6].x * s0,
+                         v[7].x * s0);
+        q1[g] = mx_pack8(v[0].y * s1, v[1].y * s1, v[2].y * s1, v[3].y * s1, v[4].y * s1, v[5].y * s1, v[6].y * s1,
+                         v[7].y * s1);
       }
       uint8_t* dst = p.q + ((b * p.rows + r) * p.cols + c) / 2;
       *reinterpret_cast<uint4*>(dst) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
@@ -209,17 +223,15 @@ __global__ void __launch_bounds__(128) mx_quantize_t_kernel(const MxQuantParams 
 // steps in flight.
 template <bool BF16>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxQuantParams p) {
+  wait_for_inputs();
   extern __shared__ int table[];
   int* offs = table;
   int* start = table + p.groups + 1;
   mx_table(p, offs, start);
   const int lane = static_cast<int>(lane_id());
-  const int chunks = (p.cols + 1023) / 1024;
-  const int64_t items = p.batch * p.rows * chunks;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t row = it / chunks;
-    const int c0 = static_cast<int>(it - row * chunks) * 1024 + lane * 8;
+  const int c0 = static_cast<int>(blockIdx.y) * 1024 + lane * 8;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < p.batch * p.rows;
+       row += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t srow = mx_scale_row(p, offs, start, row);
     if (srow < 0) continue;
     uint32_t x[4], sb[4];
@@ -232,23 +244,26 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxQuantParams 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = c0 + i * 256;
-      if (c >= p.cols) break;
-      const float s = mx_scale_value(sb[i]);
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(x[i] >> (8 * j)), __NV_E2M1);
-        const float2 f = __half22float2(__half2(h));
-        v[2 * j] = f.x * s;
-        v[2 * j + 1] = f.y * s;
-      }
       if (p.out_f32) {
-        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + row * p.cols + c);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
+        // neighbouring lanes (one block's, so one scale) share both words, so
+        // that each store instruction covers 512 contiguous bytes
+        const uint32_t even = __shfl_sync(0xffffffffu, x[i], lane & ~1), odd = __shfl_sync(0xffffffffu, x[i], lane | 1);
+        if (c >= p.cols) continue;
+        const float s = mx_scale_value(sb[i]);
+        const int h = (lane & 1) * 16;
+        const float2 a = mx_unpack2(even >> h & 0xffu), b = mx_unpack2(even >> (h + 8) & 0xffu);
+        const float2 d = mx_unpack2(odd >> h & 0xffu), e = mx_unpack2(odd >> (h + 8) & 0xffu);
+        float* dst = reinterpret_cast<float*>(p.out) + row * p.cols + (c & ~15) + (lane & 1) * 4;
+        *reinterpret_cast<float4*>(dst) = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+        *reinterpret_cast<float4*>(dst + 8) = make_float4(d.x * s, d.y * s, e.x * s, e.y * s);
+      } else if (c < p.cols) {
+        const float s = mx_scale_value(sb[i]);
+        float2 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mx_unpack2(x[i] >> (8 * j) & 0xffu);
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + row * p.cols + c) =
-            make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]), pack2<BF16>(v[6], v[7]));
+            make_uint4(pack2<BF16>(v[0].x * s, v[0].y * s), pack2<BF16>(v[1].x * s, v[1].y * s),
+                       pack2<BF16>(v[2].x * s, v[2].y * s), pack2<BF16>(v[3].x * s, v[3].y * s));
       }
     }
   }

@@ -35,6 +35,14 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Launches that may overlap the end of the kernel before them (the host sets
+// the programmatic-serialization attribute): returns when every kernel before
+// this one has finished and its writes are visible. Every thread calls it
+// before its first access to global memory other than the parameters. (Letting
+// the next kernel in earlier, with griddepcontrol.launch_dependents at the
+// start, gained nothing more: its blocks took slots from this one's.)
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

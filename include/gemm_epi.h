@@ -46,6 +46,7 @@
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
  *   GEMM_EPI_SKINNY_PREFETCH, GEMM_EPI_TAIL_SPLIT=0|1, GEMM_EPI_CACHE_HINTS=0|1,
  *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped and microscaled plans),
+ *   GEMM_EPI_FORCE_SPLIT=1..16 (CTAs that share a grouped tile's contraction, as far as there is room),
  *   GEMM_EPI_PAIR_SPLIT=0|1 (stream-K CTA pairs; off by default),
  *   GEMM_EPI_PAIR_SK_FIRST=0|1 (with stream-K: its tiles before the whole tiles, the
  *   default, or after them)

@@ -233,6 +233,42 @@ def test_wgrad_layouts(monkeypatch, layout, N, K, tr):
     check_wgrad(layout, N, K, torch.bfloat16, with_dbias=layout != "large")
 
 
+@pytest.mark.parametrize("split", [1, 2, 5, 16])
+@pytest.mark.parametrize("tr", [32, 128])
+@pytest.mark.parametrize("layout", ["mixed", "single", "empty", "large"])
+def test_split_contraction(monkeypatch, layout, tr, split):
+    """Tiles whose contraction several CTAs share, more parts than k-blocks among them."""
+    force(monkeypatch, tr)
+    monkeypatch.setenv("GEMM_EPI_FORCE_SPLIT", str(split))
+    for epilog in ("RELU_AUX_BIAS", "GELU_AUX_BIAS", "NONE"):
+        check_forward(layout, 72, 264, torch.bfloat16, epilog, w_nk=split == 2, out_f32=split == 5)
+    check_backward(layout, 200, 520, torch.bfloat16)
+    if tr == 128:
+        check_wgrad(layout, 72, 136, torch.bfloat16, out_f32=split == 5)
+
+
+def test_few_tiles_over_a_long_contraction():
+    """The kernel's own choice of the split: one narrow expert, and one long one beside a short one."""
+    g = gen(21)
+    T, N, K = 5, 64, 4096
+    X, W = ints((T, K), -1, 1, g, torch.bfloat16), ints((1, K, N), -1, 1, g, torch.bfloat16)
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    aux = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    with GroupedPlan(1, T, N, K, torch.bfloat16, "DRELU_BGRAD", out_f32=True) as p:
+        for _ in range(3):
+            dZ, db = p.backward(X, W, aux, offsets)
+            ref = X.double() @ W[0].double()
+            assert torch.equal(dZ.double(), ref) and torch.equal(db[0].double(), ref.sum(0))
+    X, dZ = ints((3005, 40), -1, 1, g, torch.bfloat16), ints((3005, 72), -1, 1, g, torch.bfloat16)
+    offsets = torch.tensor([0, 2999, 2999, 3005], dtype=torch.int32, device="cuda")
+    with GroupedPlan(3, 3005, 72, 40, torch.bfloat16, "WGRAD", out_f32=True) as p:
+        for _ in range(2):
+            dW, db = p.wgrad(X, dZ, offsets, with_dbias=True)
+            for e, (a, b) in enumerate(((0, 2999), (2999, 2999), (2999, 3005))):
+                assert torch.equal(dW[e].double(), X[a:b].double().t() @ dZ[a:b].double())
+                assert torch.equal(db[e].double(), X[a:b].double().sum(0))
+
+
 @pytest.mark.parametrize("tail", list(range(1, 17)) + [47, 48, 49, 63, 64, 65])
 def test_wgrad_row_tails_keep_foreign_rows_out(monkeypatch, tail):
     """Every length of an expert's last k-block, with NaN right behind it."""
