@@ -234,7 +234,7 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
   }
   if (e == cudaSuccess && split) {
-    p->split_items = 2 * sms;  // room for two work items an SM
+    p->split_items = sms;  // one work item an SM: more parts never paid
     p->split_bytes = (size_t)p->split_items * tr * 128 * sizeof(float) + sizeof(int) * (size_t)p->split_items;
     e = cudaMalloc((void**)&p->sk_partials, (size_t)p->split_items * tr * 128 * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * (size_t)p->split_items);

@@ -64,6 +64,6 @@ struct MxInstance {
   uint32_t smem;
   int threads, stages, bk;
 };
-MxInstance mx_any(int tr, int epi, bool bf16);
+MxInstance mx_any(int tr, int epi, bool bf16, bool f32);  // f32: fp32 output
 
 }  // namespace ge_inst

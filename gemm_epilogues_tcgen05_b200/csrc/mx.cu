@@ -119,7 +119,7 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
   p->device = dev;
   p->num_sms = sms;
   p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
-  const ge_inst::MxInstance inst = ge_inst::mx_any(tr, (int)epilog, dtype == GEMM_EPI_BF16);
+  const ge_inst::MxInstance inst = ge_inst::mx_any(tr, (int)epilog, dtype == GEMM_EPI_BF16, p->out_f32 != 0);
   GroupedCfg& g = p->gr;
   g.mx_fn = inst.fn;
   g.smem = inst.smem;

@@ -18,8 +18,9 @@
 //     columns.
 //   * CTA pairs compute 256 x 256, whose accumulator and the scales do not fit
 //     twice in the 512 columns. One accumulator, then: eight epilogue warps
-//     bring it to registers (128 values a thread) and hand it back at once, so
-//     the next tile's MMAs wait for that drain only, not for the stores.
+//     bring it to registers (rounded and packed to 16 bits as they read it) and
+//     hand it back, so the next tile's MMAs wait for that drain only, not for
+//     the stores.
 #pragma once
 
 #include "grouped_kernel.cuh"
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool mx_tile(const GroupedParams& p, const int* offs,
   return true;
 }
 
-template <bool PAIR, int TR, int EPI, bool BF16>
+template <bool PAIR, int TR, int EPI, bool BF16, bool F32>
 __global__ void __launch_bounds__(320, 1)
     mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const MxParams mp) {
@@ -365,35 +366,69 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TR;
       const int c_first = static_cast<int>(eh) * NCH;
-      uint32_t acc[NCH][32];
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if ((c_first + i) * 32 < w.n) tmem_ld_32x32b_x32(tbase + (c_first + i) * 32, acc[i]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_peer(tempty0 + buf * 8);
-        else
-          mbar_arrive(&tempty[buf]);
-      }
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const int r0 = (c_first + i) * 32;
-        if (r0 >= w.cols) break;
-        float v[32];
+      const auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_peer(tempty0 + buf * 8);
+          else
+            mbar_arrive(&tempty[buf]);
+        }
+      };
+      const auto apply = [&](const uint32_t (&acc)[32], float (&v)[32]) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          v[j] = __uint_as_float(acc[i][j]) + bias_n;
-          if constexpr (AppliesGelu<EPI>::value) v[j] = gelu_erf(v[j]);
+          v[j] = __uint_as_float(acc[j]) + bias_n;
           if constexpr (EPI == EPI_RELU_BIAS) v[j] = v[j] > 0.f ? v[j] : 0.f;
         }
-        const int64_t at = static_cast<int64_t>(w.c0 + r0) * p.N + fw;
-        if (p.out_f32)
-          store_cols32(v, reinterpret_cast<float*>(p.out) + at, p.N, w.cols - r0, nvalid);
-        else
-          store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.out) + at, p.N, w.cols - r0, nvalid);
+        if constexpr (AppliesGelu<EPI>::value) gelu32(v);
+      };
+      const int64_t at0 = static_cast<int64_t>(w.c0) * p.N + fw;
+      if constexpr (F32) {
+        uint32_t acc[NCH][32];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+          if ((c_first + i) * 32 < w.n) tmem_ld_32x32b_x32(tbase + (c_first + i) * 32, acc[i]);
+        tmem_wait_ld();
+        hand_back();
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const int r0 = (c_first + i) * 32;
+          if (r0 < w.cols) {
+            float v[32];
+            apply(acc[i], v);
+            store_cols32(v, reinterpret_cast<float*>(p.out) + at0 + static_cast<int64_t>(r0) * p.N, p.N, w.cols - r0, nvalid);
+          }
+        }
+      } else {
+        // rounded and packed as they are read, two chunks at a time, so that a
+        // tile takes 64 registers until it is stored
+        uint32_t pk[NCH][16];
+#pragma unroll
+        for (int i = 0; i < NCH; i += 2) {
+          uint32_t acc[2][32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((c_first + i + h) * 32 < w.n) tmem_ld_32x32b_x32(tbase + (c_first + i + h) * 32, acc[h]);
+          tmem_wait_ld();
+          if (i + 2 == NCH) hand_back();
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((c_first + i + h) * 32 < w.n) {
+              float v[32];
+              apply(acc[h], v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pk[i + h][j] = pack2<BF16>(v[2 * j], v[2 * j + 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const int r0 = (c_first + i) * 32;
+          if (r0 < w.cols)
+            store_packed16(pk[i], reinterpret_cast<uint16_t*>(p.out) + at0 + static_cast<int64_t>(r0) * p.N, p.N,
+                           w.cols - r0, nvalid);
+        }
       }
     }
   }
