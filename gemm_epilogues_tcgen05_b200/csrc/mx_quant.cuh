@@ -16,8 +16,14 @@
 // (zero values) stays zero. With row groups, every group starts a new row
 // tile, so a tile of the grouped product always starts at a tile of scales.
 //
-// Both kernels are bound by memory: 2 bytes read and 17/32 written an element
-// (the inverse the other way round).
+// The kernels are bound by memory: 2 bytes read and 17/32 written an element
+// (the inverse the other way round). What is read once (the source) and what is
+// large and not read back soon (fp32 values) passes L2 with an evict-first
+// hint, which leaves the packed values there for the kernel that reads them
+// next: 4096 x 11008, transposed source, quantised and back to fp32, 72 us
+// without and 60.6 us with (294 MB; 45 us at the copy rate). Alone: 1000 x 4096
+// 3.7 us and 4.4 us (launch-bound), 4096 x 4096 9.0 us (4.7 TB/s), 11008 x 4096
+// transposed 20 us (5.7 TB/s), to fp32 29.9 us (6.8 TB/s).
 #pragma once
 
 #include <cuda_fp4.h>
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
     uint4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      x[i] = c0 + i * 256 < p.cols ? *reinterpret_cast<const uint4*>(src + c0 + i * 256) : make_uint4(0u, 0u, 0u, 0u);
+      x[i] = c0 + i * 256 < p.cols ? __ldcs(reinterpret_cast<const uint4*>(src + c0 + i * 256)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = c0 + i * 256;
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(128) mx_quantize_t_kernel(const MxQuantParams 
       if (c >= p.cols) break;
       uint32_t x[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = *reinterpret_cast<const uint32_t*>(src + (static_cast<int64_t>(c) + j) * p.rows);
+      for (int j = 0; j < 32; ++j) x[j] = __ldcs(reinterpret_cast<const uint32_t*>(src + (static_cast<int64_t>(c) + j) * p.rows));
       uint32_t top = 0u;  // both rows' largest magnitudes
 #pragma unroll
       for (int j = 0; j < 32; ++j) top = __vmaxu2(top, mx_abs2(x[j]));
@@ -254,8 +260,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxQuantParams 
         const float2 a = mx_unpack2(even >> h & 0xffu), b = mx_unpack2(even >> (h + 8) & 0xffu);
         const float2 d = mx_unpack2(odd >> h & 0xffu), e = mx_unpack2(odd >> (h + 8) & 0xffu);
         float* dst = reinterpret_cast<float*>(p.out) + row * p.cols + (c & ~15) + (lane & 1) * 4;
-        *reinterpret_cast<float4*>(dst) = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
-        *reinterpret_cast<float4*>(dst + 8) = make_float4(d.x * s, d.y * s, e.x * s, e.y * s);
+        __stcs(reinterpret_cast<float4*>(dst), make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
+        __stcs(reinterpret_cast<float4*>(dst + 8), make_float4(d.x * s, d.y * s, e.x * s, e.y * s));
       } else if (c < p.cols) {
         const float s = mx_scale_value(sb[i]);
         float2 v[4];

@@ -475,9 +475,62 @@ def test_refusals_on_a_live_plan():
 
 
 @pytest.mark.parametrize("tr", [32, 256])
-def test_watchdog(monkeypatch, tr):
+def test_a_thousand_experts(monkeypatch, tr):
+    force(monkeypatch, tr)
+    g = gen(31)
+    E, N, K = 1000, 40, 24
+    sizes = torch.randint(0, 3, (E,), generator=g, device="cuda").tolist()
+    sizes[517] = 300
+    off = offsets_of(sizes, 0)
+    T = off[-1]
+    X, W = ints((T, K), -3, 3, g, torch.bfloat16), ints((E, K, N), -3, 3, g, torch.bfloat16)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    e = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(sizes, device="cuda"))
+    ref = torch.bmm(X.double()[:, None], W.double()[e])[:, 0]
+    with GroupedPlan(E, T, N, K, torch.bfloat16, "NONE") as p:
+        Y, _ = p.forward(X, W, None, offsets)
+    assert torch.equal(Y, ref.to(torch.bfloat16))
+    dZ = ints((T, N), -3, 3, g, torch.bfloat16)
+    with GroupedPlan(E, T, N, K, torch.bfloat16, "WGRAD", out_f32=True) as p:
+        dW, db = p.wgrad(X, dZ, offsets, with_dbias=True)
+    outer = torch.zeros((E, K, N), dtype=torch.float64, device="cuda").index_add_(0, e, X.double()[:, :, None] * dZ.double()[:, None])
+    assert torch.equal(dW.double(), outer)
+    assert torch.equal(db.double(), torch.zeros((E, K), dtype=torch.float64, device="cuda").index_add_(0, e, X.double()))
+
+
+def test_outputs_past_32_bit_offsets():
+    """More than 2^31 elements of Y, of the mask's rows, and of dW."""
+    g = gen(32)
+    T, N, K = 270000, 8192, 8
+    X, W = ints((T, K), -3, 3, g, torch.bfloat16), ints((2, K, N), -3, 3, g, torch.bfloat16)
+    b = ints((2, N), -3, 3, g, torch.bfloat16)
+    offsets = torch.tensor([0, 5, T - 3], dtype=torch.int32, device="cuda")
+    with GroupedPlan(2, T, N, K, torch.bfloat16, "RELU_AUX_BIAS") as p:
+        Y, aux = p.forward(X, W, b, offsets)
+        torch.cuda.synchronize()
+        assert p.status() == 0
+    for rows in (slice(5, 9), slice(T - 400, T - 3)):
+        Z = X[rows].double() @ W[1].double() + b[1].double()
+        assert torch.equal(Y[rows], Z.clamp(min=0).to(torch.bfloat16)) and torch.equal(bits_of(aux[rows], N), Z > 0)
+    assert bool((Y[T - 3:] == 0).all())
+    del Y, aux, X, W
+    E, K = 34, 8192
+    X, dZ = ints((E * 3, K), -3, 3, g, torch.bfloat16), ints((E * 3, N), -3, 3, g, torch.bfloat16)
+    offsets = torch.arange(E + 1, device="cuda", dtype=torch.int32) * 3
+    with GroupedPlan(E, E * 3, N, K, torch.bfloat16, "WGRAD") as p:
+        dW = p.wgrad(X, dZ, offsets)
+        torch.cuda.synchronize()
+        assert p.status() == 0
+    for e in (0, 32, 33):
+        assert torch.equal(dW[e], (X[3 * e:3 * e + 3].double().t() @ dZ[3 * e:3 * e + 3].double()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("tr", [32, 256])
+@pytest.mark.parametrize("split", [1, 4])
+def test_watchdog(monkeypatch, tr, split):
     """A withheld completion signal ends the wait in time and is reported; the plan works again afterwards."""
     force(monkeypatch, tr)
+    monkeypatch.setenv("GEMM_EPI_FORCE_SPLIT", str(split))
     monkeypatch.setenv("GEMM_EPI_TEST_HOOKS", "1")
     monkeypatch.setenv("GEMM_EPI_INJECT_STALL", "1")
     monkeypatch.setenv("GEMM_EPI_WAIT_TIMEOUT_MS", "50")
@@ -489,3 +542,7 @@ def test_watchdog(monkeypatch, tr):
         torch.cuda.synchronize()
         assert p.status() == binding.ERR_TIMEOUT
         assert p.status() == 0
+        with pytest.raises(GemmEpiError):  # the next call reports the run-out of the one before
+            p.forward(X, W, None, offsets)
+            torch.cuda.synchronize()
+            p.forward(X, W, None, offsets)

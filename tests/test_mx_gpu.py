@@ -351,6 +351,32 @@ def test_captured_and_other_stream():
             assert bool(((Y.double() - ref).abs() <= 2 * K * 2.0 ** -24 * S + U[torch.bfloat16] * ref.abs()).all())
 
 
+def test_sizes_past_32_bit_offsets():
+    """More than 2^31 elements quantised, given back, and written by the product."""
+    R, C = 33000, 65536
+    x = torch.zeros((R, C), dtype=torch.bfloat16, device="cuda")
+    x[:3] = spread((3, C), gen(1), torch.bfloat16)
+    x[-2:] = spread((2, C), gen(2), torch.bfloat16)
+    q, s = mx_quantize(x)
+    val = ref_quantize(x[-2:])
+    assert torch.equal(torch.stack([q[-2:] & 7, q[-2:] >> 4 & 7], -1).view(2, C).long(), val[1] & 7)
+    out = torch.empty((R, C), dtype=torch.bfloat16, device="cuda")
+    gemm_epi_mx_dequantize(q, s, out)
+    assert torch.equal(out[-2:], val[0].to(torch.bfloat16)) and torch.equal(out[:3], ref_quantize(x[:3])[0].to(torch.bfloat16))
+    assert bool((out[3:-2] == 0).all())
+    del x, q, s, out
+    T, N, K = 270000, 8192, 32
+    g = gen(3)
+    Xq, Xs, X = random_mx((1, T, K), g)
+    Wq, Ws, W = random_mx((1, N, K), g)
+    with MxPlan(T, N, K, torch.bfloat16, "NONE") as p:
+        Y = p.forward(Xq[0], Xs, Wq[0], Ws, None)
+        torch.cuda.synchronize()
+        assert p.status() == 0
+    for rows in (slice(0, 5), slice(T - 300, T)):
+        assert torch.equal(Y[rows], (X[0, rows] @ W[0].t()).to(torch.bfloat16))
+
+
 def test_refusals_on_a_live_plan():
     L = binding.lib()
     x = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
