@@ -13,9 +13,10 @@ namespace {
 // SM while all of them load (32-row tiles less when few are busy), 0.33 us on a
 // CTA pair. Measured (us, 32 / 128 / 256 rows): one expert of 1000 rows, K =
 // 4096, N = 256: 16.4 / 20.9 / 24.5; four of 100, K = 2048, N = 512: 11.2 /
-// 13.5 / 12.1. WGRAD is bound by its stores where experts are short: E = 32 of
+// 13.5 / 12.1; one of 3932, K = 192, N = 5824, DRELU_BGRAD: 338 / 45 / 28. WGRAD is
+// bound by its stores where experts are short: E = 32 of
 // 125 rows, K = 1024, N = 2048, fp32: 56.8 (128) and 60 (256); E = 8 of 1024,
-// K = 4096, N = 11008: 738 and 577.
+// K = 4096, N = 11008: 738 and 577; E = 6 of 3, K = 3320, N = 9336: 160 and 116.
 int choose_tr(int64_t E, int64_t T, int64_t N, int64_t K, int epilog, bool out_f32, int sms) {
   const bool wgrad = epilog == GEMM_EPI_WGRAD;
   if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
@@ -33,10 +34,10 @@ int choose_tr(int64_t E, int64_t T, int64_t N, int64_t K, int epilog, bool out_f
     const double busy = tiles < units ? double(tiles) / units : 1.0;
     const double stage = tr == 256 ? 0.33 : tr == 128 ? (busy < 0.8 ? 0.2 : 0.25 * busy) : (busy < 0.58 ? 0.145 : 0.25 * busy);
     double tile_us = double(((wgrad ? mean : K) + 63) / 64) * stage;
-    if (wgrad) {  // storing a tile
-      const double store = (tr == 256 ? 2.8 : 1.4) * (out_f32 ? 1.35 : 1.0);
-      if (tile_us < store) tile_us = store;
-    }
+    // storing a tile, which the next tile's products overlap
+    double store = tr == 256 ? (out_f32 ? 3.5 : 2.4) : tr == 128 ? (out_f32 ? 1.7 : 1.4) : 1.2;
+    if (epilog == GEMM_EPI_DRELU_BGRAD && mean > tr) store += tr == 32 ? 6.0 : 0.6;  // joining the column sums
+    if (tile_us < store) tile_us = store;
     const double us = double((tiles + units - 1) / units) * tile_us + (tr == 256 ? 4.0 : tr == 128 ? 3.0 : 2.0);
     if (best == 0 || us < best_us * 0.999) {
       best = tr;

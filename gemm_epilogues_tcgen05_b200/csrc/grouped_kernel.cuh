@@ -75,15 +75,15 @@ struct GroupedSmem {
   static constexpr uint32_t B_BYTES = KPS * B_SUB;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
   static constexpr uint32_t TABLE = 2 * (kMaxExperts + 1) * 4;
-  static constexpr uint32_t FIXED = TABLE + 40 * 8 + 128 * 4 + 64 + 1024;
+  static constexpr uint32_t FIXED = TABLE + 40 * 8 + 4 * 128 * 4 + 64 + 1024;
   static constexpr int STAGES = (232448 - FIXED) / STAGE > 10 ? 10 : (232448 - FIXED) / STAGE;
   static constexpr uint32_t OFF_A = 0;
   static constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_B + STAGES * B_BYTES;
   static constexpr uint32_t N_BARS = 3 * STAGES + 5;   // full, empty, tail, tfull[2], tempty[2], drain
   static constexpr uint32_t OFF_MISC = OFF_BAR + 40 * 8;
-  static constexpr uint32_t OFF_SUM = OFF_MISC + 64;   // column sums of the second half of the epilogue warps
-  static constexpr uint32_t OFF_TABLE = OFF_SUM + 128 * 4;
+  static constexpr uint32_t OFF_SUM = OFF_MISC + 64;   // DRELU_BGRAD: [2][warps per quarter][128] column sums
+  static constexpr uint32_t OFF_TABLE = OFF_SUM + 4 * 128 * 4;
   static constexpr uint32_t BYTES = OFF_TABLE + TABLE + 1024;
   static_assert(N_BARS <= 40, "barrier space");
   static_assert(STAGES >= 3 && BYTES <= 232448, "grouped shared memory above the per-CTA limit");
@@ -229,6 +229,22 @@ __device__ __forceinline__ bool grouped_tile(const GroupedParams& p, const int* 
   return true;
 }
 
+// 32 x 32 bits across the warp, transposed: lane l's bit j becomes lane j's bit
+// l. Mask words are one per row, a lane of the epilogue holds one feature of 32
+// rows. (One ballot or shuffle per row instead is a chain of 32 round trips:
+// T = 3932, K = 192, N = 5824 took 36.5 us with the mask written so, 16.9 us
+// without a mask.)
+__device__ __forceinline__ uint32_t warp_transpose_bits(uint32_t x) {
+  const uint32_t lane = lane_id();
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    const uint32_t low = d == 16 ? 0x0000ffffu : d == 8 ? 0x00ff00ffu : d == 4 ? 0x0f0f0f0fu : d == 2 ? 0x33333333u : 0x55555555u;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, d);
+    x = (lane & d) ? (x & ~low) | ((y >> d) & low) : (x & low) | ((y & low) << d);
+  }
+  return x;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
@@ -358,10 +374,10 @@ __device__ __forceinline__ void zero_rows(uint32_t addr, int chunks, int r0, int
 }
 
 // Threads: producer and MMA warps, the epilogue's, and for WGRAD the warp that
-// zeroes foreign rows.
+// zeroes foreign rows, for DRELU_BGRAD the one that joins the column sums.
 template <int EPI, int TR>
 struct GroupedThreads {
-  static constexpr int value = 64 + 32 * GroupedEpiWarps<TR>::value + (EPI == EPI_WGRAD ? 32 : 0);
+  static constexpr int value = 64 + 32 * GroupedEpiWarps<TR>::value + (EPI == EPI_WGRAD || EPI == EPI_DRELU_BGRAD ? 32 : 0);
 };
 
 // SPLIT: an instance of its own for plans that may have few tiles (the joining
@@ -396,10 +412,10 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
+  volatile int* sum_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 20);  // [2]
   volatile int* split_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 12);
   int* split_count = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);
-  float* half_sum = reinterpret_cast<float*>(smem + L::OFF_SUM);
+  float* sums = reinterpret_cast<float*>(smem + L::OFF_SUM);
   int* offs = reinterpret_cast<int*>(smem + L::OFF_TABLE);
   int* start = offs + kMaxExperts + 1;
 
@@ -425,7 +441,6 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *last_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
@@ -661,12 +676,74 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         }
       }
     }
+  } else if (EPI == EPI_DRELU_BGRAD && warp == 2 + EW) {
+    // ------------------------------------------------- column sums (DRELU_BGRAD)
+    // A tile's sums over its rows, the quarter's warps in order, straight to
+    // dbias or (an expert of several row tiles) to one partial row per tile;
+    // the block of features' last tile adds those in tile order, so the result
+    // does not depend on timing. In a warp of its own: the fence before the
+    // ticket waits for its few stores only, not for the epilogue's.
+    if constexpr (EPI == EPI_DRELU_BGRAD) {
+      uint32_t dcount = 0;
+      GroupedTile w;
+      for (int item = unit; grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units, ++dcount) {
+        const uint32_t b = dcount & 1u;
+        named_bar_sync(2 + b, ET + 32);
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i] = sums[b * (EW / 4) * 128 + i * 32 + lane];
+          if constexpr (EW == 8) s[i] += sums[(b * 2 + 1) * 128 + i * 32 + lane];
+        }
+        // (after an abort the sums are not whole; one lane's view, so that all agree)
+        const bool use = __shfl_sync(0xffffffffu, sum_flag[b] != 0 && *abort_flag == 0 ? 1 : 0, 0) != 0;
+        named_bar_arrive(4 + b, ET + 32);
+        const int n0 = w.f0 + static_cast<int>(rank * 128u + lane);
+        if (!use || w.f0 + static_cast<int>(rank) * 128 >= p.N) continue;  // warp-uniform
+        float* out = p.dbias + static_cast<int64_t>(w.e) * p.N;
+        if (w.mt > 1) {
+          const int64_t mrow = start[w.e] / p.n_ft;
+          float* row = p.partials + (mrow + w.mb) * p.N;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n0 + i * 32 < p.N) row[n0 + i * 32] = s[i];
+          __threadfence();
+          __syncwarp();
+          int last = 0;
+          if (lane == 0) {
+            int* tk = p.tickets + static_cast<int64_t>(w.e) * p.nfb + (w.f0 >> 7) + static_cast<int>(rank);
+            last = atomicAdd(tk, 1) == w.mt - 1;
+            if (last) *tk = 0;  // ready for the next launch
+          }
+          if (__shfl_sync(0xffffffffu, last, 0) == 0) continue;
+          __threadfence();
+          const float* src = p.partials + mrow * p.N;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = 0.f;
+          for (int m0 = 0; m0 < w.mt; m0 += 8) {
+            float x[8][4];
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[m][i] = m0 + m < w.mt && n0 + i * 32 < p.N ? __ldcg(src + static_cast<int64_t>(m0 + m) * p.N + n0 + i * 32) : 0.f;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[i] += x[m][i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + i * 32 < p.N) out[n0 + i * 32] = s[i];
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const uint32_t ew = warp & 3u;         // TMEM lane quarter
     const uint32_t eh = (warp - 2u) >> 2;  // which of the quarter's warps
     const uint32_t et = threadIdx.x - 64;
-    uint32_t tcount = 0;
+    uint32_t tcount = 0, dcount = 0;
     bool ok = true;
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : smem_u32(&tempty[0]);
     if constexpr (EPI == EPI_DRELU_BGRAD) {
@@ -718,14 +795,15 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           const int rows = w.cols - c * 32;
           const int64_t at = (orow + c * 32) * p.N + fw;
           if constexpr (EPI == EPI_DRELU_BGRAD) {
-            const uint32_t mine = mnext;
+            const uint32_t mine = warp_transpose_bits(mnext);  // bit j: this feature of row j
             if ((c + STEP) * 32 < w.n) mnext = mask_word(c + STEP);
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const uint32_t m = __shfl_sync(0xffffffffu, mine, j);
-              v[j] = ((m >> lane) & 1u) ? v[j] : 0.f;
-              dsum += v[j];  // rows past the tile have no mask bit set
+              v[j] = (mine >> j) & 1u ? v[j] : 0.f;
+              part[j & 3] += v[j];  // rows past the tile have no mask bit set
             }
+            dsum += (part[0] + part[1]) + (part[2] + part[3]);
           } else if constexpr (!PlainStore<EPI>::value) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += bias_n;
@@ -733,19 +811,18 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
               store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.aux_out) + at, p.N, rows, nvalid);
             if constexpr (AppliesGelu<EPI>::value) gelu32(v);
             if constexpr (EPI == EPI_RELU_BIAS || EPI == EPI_RELU_AUX_BIAS) {
-              uint32_t myword = 0u;
+              uint32_t bits = 0u;  // of this feature, by row
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const bool pos = v[j] > 0.f;
-                if constexpr (EPI == EPI_RELU_AUX_BIAS) {
-                  const uint32_t b = __ballot_sync(0xffffffffu, pos && n_ok);
-                  if (lane == static_cast<uint32_t>(j)) myword = b;
-                }
+                if constexpr (EPI == EPI_RELU_AUX_BIAS) bits |= (pos ? 1u : 0u) << j;
                 v[j] = pos ? v[j] : 0.f;
               }
-              if constexpr (EPI == EPI_RELU_AUX_BIAS)
+              if constexpr (EPI == EPI_RELU_AUX_BIAS) {
+                const uint32_t mine = warp_transpose_bits(n_ok ? bits : 0u);
                 if (static_cast<int>(lane) < rows && word < p.aux_words)
-                  p.aux_out[(orow + c * 32 + static_cast<int>(lane)) * p.aux_words + word] = myword;
+                  p.aux_out[(orow + c * 32 + static_cast<int>(lane)) * p.aux_words + word] = mine;
+              }
             }
           }
           if (p.out_f32)
@@ -844,46 +921,18 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         }
       }
       if (!empty_tile) ++tcount;
-      if (EPI == EPI_DRELU_BGRAD && finisher) {
-        // column sums: the quarter's two warps in order, then (more than one
-        // row tile) one partial row per tile, summed in tile order by the
-        // block of features' last tile, so the result does not depend on timing
-        const int fl = static_cast<int>(ew * 32u + lane);
-        if constexpr (EW == 8) {
-          if (eh == 1) half_sum[fl] = dsum;
-          named_bar_sync(1, ET);
-          if (eh == 0) dsum += half_sum[fl];
-        }
-        if (w.mt == 1) {
-          if (eh == 0 && n_ok && ok) p.dbias[static_cast<int64_t>(w.e) * p.N + n] = dsum;
-          if constexpr (EW == 8) named_bar_sync(1, ET);  // half_sum is reused by the next tile
-        } else {
-          const int64_t mrow = start[w.e] / p.n_ft;
-          if (eh == 0 && n_ok && ok) p.partials[(mrow + w.mb) * p.N + n] = dsum;
-          __threadfence();
-          named_bar_sync(1, ET);
-          if (et == 0) {
-            int last = 0;
-            const int fb = (w.f0 >> 7) + static_cast<int>(rank);
-            if (ok && fb < p.nfb) {
-              int* t = p.tickets + static_cast<int64_t>(w.e) * p.nfb + fb;
-              last = atomicAdd(t, 1) == w.mt - 1;
-              if (last) *t = 0;  // ready for the next launch
-            }
-            *last_flag = last;
-          }
-          named_bar_sync(1, ET);
-          if (*last_flag && eh == 0 && n_ok) {
-            __threadfence();
-            const float* src = p.partials + mrow * p.N + n;
-            float s = 0.f;
-            for (int m = 0; m < w.mt; ++m) s += __ldcg(src + static_cast<int64_t>(m) * p.N);
-            p.dbias[static_cast<int64_t>(w.e) * p.N + n] = s;
-          }
-          named_bar_sync(1, ET);  // last_flag and half_sum are reused by the next tile
-        }
+      if constexpr (EPI == EPI_DRELU_BGRAD) {
+        // this tile's column sums to the joining warp, two tiles deep
+        const uint32_t b = dcount & 1u;
+        if (dcount >= 2) named_bar_sync(4 + b, ET + 32);  // it has read the ones before
+        sums[(b * (EW / 4) + eh) * 128 + ew * 32 + lane] = dsum;
+        if (et == 0) sum_flag[b] = finisher ? 1 : 0;
+        named_bar_arrive(2 + b, ET + 32);
+        ++dcount;
       }
     }
+    if constexpr (EPI == EPI_DRELU_BGRAD)
+      for (uint32_t i = dcount < 2 ? 0 : dcount - 2; i < dcount; ++i) named_bar_sync(4 + (i & 1u), ET + 32);
   }
 
   tc_fence_before();

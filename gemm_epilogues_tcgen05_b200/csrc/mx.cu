@@ -63,6 +63,32 @@ void release(gemm_epi_plan_s* p) {
   delete p;
 }
 
+// Rows per tile, as for grouped plans: rounds of tiles x (stages of 256 k x
+// time per stage + what a tile costs beside them). Measured (us, 128 / 256 rows):
+// T = 4096, N = 11008, K = 4096: 106 / 73; E = 16, T = 1003, N = 5000, K = 2048:
+// 20.8 / 23.8.
+int choose_tr(int64_t groups, int64_t T, int64_t N, int64_t K, int sms) {
+  if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
+    const int v = atoi(f);
+    if (v == 128 || v == 256) return v;
+  }
+  const int64_t active = groups < T ? groups : T, mean = (T + active - 1) / active;
+  int best = 0;
+  double best_us = 0;
+  for (int tr : {128, 256}) {
+    const int units = tr == 256 ? sms / 2 : sms;
+    const int64_t tiles = active * ((mean + tr - 1) / tr) * ((N + (tr == 256 ? 255 : 127)) / (tr == 256 ? 256 : 128));
+    const double busy = tiles < units ? double(tiles) / units : 1.0;
+    const double stage = tr == 256 ? (busy < 0.7 ? 0.28 : 0.4 * busy) : (busy < 0.6 ? 0.15 : 0.25 * busy);
+    const double us = double((tiles + units - 1) / units) * (double((K + 255) / 256) * stage + (tr == 256 ? 1.5 : 0.8));
+    if (best == 0 || us < best_us * 0.999) {
+      best = tr;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
 gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype, gemm_epi_epilog epilog,
                           uint32_t flags) {
   if ((flags & ~(uint32_t)GEMM_EPI_FLAG_OUT_F32) != 0) {
@@ -94,12 +120,9 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     return nullptr;
   }
   const int64_t groups = E > 0 ? E : 1;
-  const int64_t mean = (T + groups - 1) / groups;
-  int tr = mean <= 128 ? 128 : 256;
-  if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
-    const int v = atoi(f);
-    if (v == 128 || v == 256) tr = v;
-  }
+  int dev = 0, sms = 0;
+  if (require_b200(&dev, &sms)) return nullptr;
+  const int tr = choose_tr(groups, T, N, K, sms);
   const int fm = tr == 256 ? 256 : 128;
   const int64_t n_ft = (N + fm - 1) / fm;
   const int64_t tiles = (E > 0 ? T / tr + (E < T ? E : T) : (T + tr - 1) / tr) * n_ft;
@@ -107,8 +130,6 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
     return nullptr;
   }
-  int dev = 0, sms = 0;
-  if (require_b200(&dev, &sms)) return nullptr;
   auto* p = new gemm_epi_plan_s();
   p->kind = 2;
   p->uT = p->T = T;
