@@ -35,7 +35,7 @@ int choose_tr(int64_t E, int64_t T, int64_t N, int64_t K, int epilog, bool out_f
     const double stage = tr == 256 ? 0.33 : tr == 128 ? (busy < 0.8 ? 0.2 : 0.25 * busy) : (busy < 0.58 ? 0.145 : 0.25 * busy);
     double tile_us = double(((wgrad ? mean : K) + 63) / 64) * stage;
     // storing a tile, which the next tile's products overlap
-    double store = tr == 256 ? (out_f32 ? 3.5 : 2.4) : tr == 128 ? (out_f32 ? 1.7 : 1.4) : 1.2;
+    double store = tr == 256 ? (out_f32 ? 3.4 : 2.3) : tr == 128 ? (out_f32 ? 1.7 : 1.4) : 1.2;
     if (epilog == GEMM_EPI_DRELU_BGRAD && mean > tr) store += tr == 32 ? 6.0 : 0.6;  // joining the column sums
     if (tile_us < store) tile_us = store;
     const double us = double((tiles + units - 1) / units) * tile_us + (tr == 256 ? 4.0 : tr == 128 ? 3.0 : 2.0);
