@@ -120,7 +120,10 @@ typedef struct {
   int64_t T, N, K;
   int dtype, epilog;
   int kernel;          /* 0 = tile kernel (one CTA per tile), 1 = few-row kernel (swap-AB,
-                          stream-K), 2 = tile kernel on CTA pairs (256-row tiles) */
+                          stream-K), 2 = tile kernel on CTA pairs (256-row tiles); grouped
+                          plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
+                          (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs).
+                          For 3 to 7 tile_m counts features and tile_n rows */
   int tile_m, tile_n, tile_k, stages;
   int split_k;         /* K slices per output tile (1 = none) */
   int grid;            /* CTAs launched by the main kernel */
@@ -339,10 +342,14 @@ GEMM_EPI_API int drelu_bgrad_execute_noalloc(int64_t T, int64_t N, int64_t K, ge
  * are used as their running maximum, cut to [0, T]: decreasing or larger
  * values cannot reach outside the tensors, and name the rows that this gives.
  * Results, rounding, the 16-bit types, epilogs, flags, error codes, watchdog,
- * streams and ownership are those of one product; sums are in a fixed order,
- * so equal calls give equal bits. A call runs on the plan's device whichever
- * is current. gemm_epi_free, _query, _status, _last_error and _set_bias_f32
+ * streams and ownership are those of one product, with two exceptions: these
+ * kernels evaluate GELU as max(z, 0) - |z| erfc(|z| / sqrt(2)) / 2 by a
+ * polynomial (absolute error at most 1.8e-7 |z|), and a call runs on the plan's
+ * device whichever is current. Sums are in a fixed order, so equal calls give
+ * equal bits. gemm_epi_free, _query, _status, _last_error and _set_bias_f32
  * take these plans too; the other calls return GEMM_EPI_ERR_EPILOG_MISMATCH.
+ * Launches are programmatic: a kernel may be set up while the one before it on
+ * the stream ends, and touches global memory only after that one has finished.
  */
 
 /*
