@@ -354,9 +354,19 @@ def _ptr_on(index: int, t, shape, dtype, name) -> int:
         if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
-        pass
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     _ptr(t, shape, dtype, name)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _zeros(shape, dtype, device, stream):
+    """Zeros written on the stream that the call will use (a fill on another
+    stream could come after the call's own stores)."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.zeros(shape, dtype=dtype, device=device)
 
 
 class _DevicePlan(Plan):
@@ -429,14 +439,14 @@ class GroupedPlan(_DevicePlan):
 
     # conveniences that allocate their outputs (rows outside every expert: zeros)
     def forward(self, X, W, bias, offsets, stream=None):
-        Y = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=X.device)
+        Y = _zeros((self.T, self.N), self.out_dtype, X.device, stream)
         spec = self.aux_spec()
-        aux = torch.zeros(spec[0], dtype=spec[1], device=X.device) if spec else None
+        aux = _zeros(*spec, X.device, stream) if spec else None
         self.gemm_epi_grouped_execute(X, W, bias, offsets, Y, aux, stream)
         return Y, aux
 
     def backward(self, dY2, W2, aux, offsets, stream=None):
-        dZ = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=dY2.device)
+        dZ = _zeros((self.T, self.N), self.out_dtype, dY2.device, stream)
         dbias = torch.empty((self.E, self.N), dtype=torch.float32, device=dY2.device)
         self.gemm_epi_grouped_drelu_bgrad_execute(dY2, W2, aux, offsets, dZ, dbias, stream)
         return dZ, dbias
@@ -518,9 +528,9 @@ def gemm_epi_mx_dequantize(q, scales, out, offsets=None, stream=None):
 def mx_quantize(src, offsets=None, transposed=False, stream=None):
     """gemm_epi_mx_quantize with allocated outputs: (q, scales)."""
     rows, cols = (src.shape[-1], src.shape[-2]) if transposed else src.shape[-2:]
-    q = torch.zeros((*src.shape[:-2], rows, cols // 2), dtype=torch.uint8, device=src.device)
+    q = _zeros((*src.shape[:-2], rows, cols // 2), torch.uint8, src.device, stream)
     n = mx_scales_bytes(rows, cols, src.shape[0] if src.dim() == 3 else 1, None if offsets is None else offsets.numel() - 1)
-    scales = torch.zeros(n, dtype=torch.uint8, device=src.device)
+    scales = _zeros((n,), torch.uint8, src.device, stream)
     gemm_epi_mx_quantize(src, q, scales, offsets, transposed, stream)
     return q, scales
 
@@ -553,6 +563,6 @@ class MxPlan(_DevicePlan):
             self._p(Y, (T, N), self.out_dtype, "Y"), self._s(stream)))
 
     def forward(self, Xq, Xs, Wq, Ws, bias, offsets=None, stream=None):
-        Y = torch.zeros((self.T, self.N), dtype=self.out_dtype, device=Xq.device)
+        Y = _zeros((self.T, self.N), self.out_dtype, Xq.device, stream)
         self.gemm_epi_mx_execute(Xq, Xs, Wq, Ws, bias, Y, offsets, stream)
         return Y

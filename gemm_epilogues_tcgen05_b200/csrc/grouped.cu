@@ -201,6 +201,9 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     return nullptr;
   }
   cudaError_t e = cudaFuncSetAttribute(g.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
+  // DRELU_BGRAD also clears dbias of experts without rows, a CTA at a time: as
+  // many CTAs as that takes where the tiles are few (1000 experts, one row)
+  const int64_t clearing = epilog == GEMM_EPI_DRELU_BGRAD ? E * N / 16384 : 0;
   if (e != cudaSuccess) {
     cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
     release(p);
@@ -208,9 +211,11 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
   }
   if (g.pair) {
     const int pairs = resident_pairs((const void*)g.fn, g.threads, g.smem, sms);
-    p->grid = 2 * (int)(tiles < pairs ? tiles : pairs);
+    const int64_t want = tiles > clearing ? tiles : clearing;
+    p->grid = 2 * (int)(want < pairs ? want : pairs);
   } else {
-    p->grid = (int)(split || tiles > sms ? sms : tiles);  // (idle CTAs cost about 1 us)
+    const int64_t want = tiles > clearing ? tiles : clearing;
+    p->grid = (int)(split || want > sms ? sms : want);  // (idle CTAs cost about 1 us)
   }
   e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
   if (e != cudaSuccess) {

@@ -447,6 +447,90 @@ def test_other_stream_and_repeatability():
         assert torch.equal(dZ, got[0][0]) and torch.equal(db, got[0][1])
 
 
+def test_gelu_of_special_values():
+    """One term a product, so Z is the weight itself: infinities, NaN, far and near values."""
+    z = torch.tensor([float("inf"), float("-inf"), NAN, 60000.0, -60000.0, 5.25, -5.25, 5.0, -5.0, 1.0, -1.0, 0.0, -0.0, 2.0 ** -24,
+                      -(2.0 ** -24), 0.5], device="cuda").half()
+    X = torch.zeros((3, 8), dtype=torch.float16, device="cuda")
+    X[:, 0] = 1
+    W = torch.zeros((1, 8, 16), dtype=torch.float16, device="cuda")
+    W[0, 0] = z
+    b = torch.zeros((1, 16), dtype=torch.float16, device="cuda")
+    offsets = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    with GroupedPlan(1, 3, 16, 8, torch.float16, "GELU_BIAS", out_f32=True) as p:
+        Y, _ = p.forward(X, W, b, offsets)
+    d = z.double()
+    ref = torch.where(d == float("-inf"), 0.0, d * torch.special.ndtr(d))
+    assert bool((torch.isnan(Y) == torch.isnan(ref)).all()) and bool(torch.isinf(Y[:, 0]).all())
+    fine = torch.isfinite(ref)
+    assert bool(((Y[:, fine].double() - ref[fine]).abs() <= 2e-7 * d[fine].abs()).all())
+    assert bool((Y[:, 1] == 0).all()) and bool((Y[:, 4] == 0).all())
+
+
+def test_conveniences_on_another_stream():
+    """The zeros that forward and backward start from are written on the call's stream."""
+    g = gen(41)
+    T, N, K = 4000, 1024, 64
+    X, W = ints((T, K), -3, 3, g, torch.bfloat16), ints((2, K, N), -3, 3, g, torch.bfloat16)
+    offsets = torch.tensor([0, 1500, T - 7], dtype=torch.int32, device="cuda")
+    aux = torch.full((T, N // 32), -1, dtype=torch.int32, device="cuda")
+    ref = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    ref[:1500], ref[1500:T - 7] = X[:1500].double() @ W[0].double(), X[1500:T - 7].double() @ W[1].double()
+    busy = torch.randn((4096, 4096), device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with GroupedPlan(2, T, N, K, torch.bfloat16, "NONE") as p, GroupedPlan(2, T, N, K, torch.bfloat16, "DRELU_BGRAD") as q:
+        for stream in (s, s.cuda_stream):
+            for _ in range(8):
+                busy = busy @ busy * 1e-3  # the current stream is behind
+            Y, _ = p.forward(X, W, None, offsets, stream=stream)
+            dZ, _ = q.backward(X, W, aux, offsets, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(Y, ref.to(torch.bfloat16)) and torch.equal(dZ, Y)
+
+
+def test_two_plans_at_once():
+    """Two plans on two streams, each with tickets and partials of its own, over and over."""
+    g = gen(42)
+    cases = []
+    for T, N, K, E in ((3000, 520, 72, 3), (5, 64, 4096, 1)):
+        X, W = ints((T, K), -1, 1, g, torch.bfloat16), ints((E, K, N), -1, 1, g, torch.bfloat16)
+        offsets = torch.linspace(0, T, E + 1, device="cuda").to(torch.int32)
+        off = offsets.tolist()
+        aux = torch.full((T, (N + 31) // 32), -1, dtype=torch.int32, device="cuda")
+        G = torch.cat([X[off[e]:off[e + 1]].double() @ W[e].double() for e in range(E)])
+        db = torch.stack([G[off[e]:off[e + 1]].sum(0) for e in range(E)])
+        p = GroupedPlan(E, T, N, K, torch.bfloat16, "DRELU_BGRAD", out_f32=True)
+        out = torch.zeros((T, N), device="cuda"), torch.zeros((E, N), device="cuda")
+        cases.append((p, X, W, aux, offsets, out, G, db, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, X, W, aux, offsets, out, _, _, s in cases:
+            p.gemm_epi_grouped_drelu_bgrad_execute(X, W, aux, offsets, *out, s)
+    torch.cuda.synchronize()
+    for p, *_, out, G, db, _ in cases:
+        assert p.status() == 0 and torch.equal(out[0].double(), G) and torch.equal(out[1].double(), db)
+        p.free()
+
+
+def test_bias_gradient_of_many_experts_without_rows(monkeypatch):
+    E, T, N, K = 1000, 2, 2056, 16
+    g = gen(43)
+    X, W = ints((T, K), -3, 3, g, torch.bfloat16), ints((E, K, N), -3, 3, g, torch.bfloat16)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[501:] = 2
+    aux = torch.full((T, (N + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    for tr in (32, 256):
+        force(monkeypatch, tr)
+        with GroupedPlan(E, T, N, K, torch.bfloat16, "DRELU_BGRAD") as p:
+            db = torch.full((E, N), NAN, device="cuda")
+            dZ = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+            p.gemm_epi_grouped_drelu_bgrad_execute(X, W, aux, off, dZ, db)
+            ref = torch.zeros((E, N), dtype=torch.float64, device="cuda")
+            ref[500] = (X.double() @ W[500].double()).sum(0)
+            assert torch.equal(db.double(), ref) and p.info()["grid"] > 100
+
+
 def test_refusals_on_a_live_plan():
     L = binding.lib()
     x = torch.zeros(64 * 64, dtype=torch.bfloat16, device="cuda")
@@ -468,6 +552,11 @@ def test_refusals_on_a_live_plan():
         assert L.drelu_bgrad_execute(bw.handle, q, q, q, q, q, None) == binding.ERR_EPILOG_MISMATCH
         with pytest.raises(ValueError):
             p.gemm_epi_grouped_execute(x.view(64, 64), x, x, o, x)
+        with pytest.raises(TypeError):
+            p.gemm_epi_grouped_execute(None, x, x, o, x)
+        with pytest.raises(GemmEpiError):  # a bias is missing
+            p.gemm_epi_grouped_execute(x.view(64, 64), torch.zeros((2, 64, 64), dtype=torch.bfloat16, device="cuda"), None, o,
+                                       x.view(64, 64), torch.zeros((64, 2), dtype=torch.int32, device="cuda"))
         info = p.info()
         assert (info["T"], info["N"], info["K"], info["kernel"], info["tile_n"]) == (64, 64, 64, 3, 32)
     with pytest.raises(GemmEpiError):
