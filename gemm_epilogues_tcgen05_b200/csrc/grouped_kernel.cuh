@@ -57,7 +57,7 @@ struct GroupedParams {
   // one-CTA tiles, few of them: k split over several CTAs (grouped_splits)
   int32_t max_items;        // slots; 0: no split
   int32_t force_splits;     // override of grouped_splits' choice (0: none)
-  float* split_slots;       // [max_items][TR][128]
+  float* split_slots;       // [max_items][TR / 4][128][4]
   int* split_tickets;       // [max_items], zero between launches
 };
 
@@ -864,8 +864,9 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
             store_cols16<BF16>(v, reinterpret_cast<uint16_t*>(p.out) + at, p.N, rows, nvalid);
         };
         if (SPLIT && S > 1 && ok) {
-          // a part of a split tile: leave the fp32 accumulator in this item's slot
-          float* slot = p.split_slots + static_cast<int64_t>(item) * (TR * 128) + ew * 32 + lane;
+          // a part of a split tile: leave the fp32 accumulator in this item's slot,
+          // four rows of a feature together (16-byte stores and loads)
+          float4* slot = reinterpret_cast<float4*>(p.split_slots) + static_cast<int64_t>(item) * (TR * 32) + ew * 32 + lane;
 #pragma unroll 1
           for (int c = static_cast<int>(eh); c * 32 < w.cols; c += STEP) {
             uint32_t r[32];
@@ -874,8 +875,11 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
               tmem_wait_ld();
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c * 32 + j < w.cols) slot[(c * 32 + j) * 128] = empty_tile ? 0.f : __uint_as_float(r[j]);
+            for (int q = 0; q < 8; ++q)
+              if (c * 32 + 4 * q < w.cols)
+                slot[(c * 8 + q) * 128] = empty_tile ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                     : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                                                   __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
           }
           if (!empty_tile) {
             tc_fence_before();
@@ -923,7 +927,8 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
             // SB parts' loads of a chunk are in flight together
             __threadfence();
             constexpr int SB = EW == 4 ? 4 : 2;
-            const float* base = p.split_slots + static_cast<int64_t>(tile) * S * (TR * 128) + ew * 32 + lane;
+            const float4* base = reinterpret_cast<const float4*>(p.split_slots) +
+                                 static_cast<int64_t>(tile) * S * (TR * 32) + ew * 32 + lane;
             if constexpr (EPI == EPI_DRELU_BGRAD) mnext = mask_word(static_cast<int>(eh));
 #pragma unroll 1
             for (int c = static_cast<int>(eh); c * 32 < w.cols; c += STEP) {
@@ -932,18 +937,23 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
               for (int j = 0; j < 32; ++j) sum[j] = 0.f;
 #pragma unroll 1
               for (int s0 = 0; s0 < S; s0 += SB) {
-                float x[SB][32];
+                float4 x[SB][8];
 #pragma unroll
                 for (int s = 0; s < SB; ++s)
 #pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    x[s][j] = s0 + s < S && c * 32 + j < w.cols
-                                  ? __ldcg(base + static_cast<int64_t>(s0 + s) * (TR * 128) + (c * 32 + j) * 128)
-                                  : 0.f;
+                  for (int q = 0; q < 8; ++q)
+                    x[s][q] = s0 + s < S && c * 32 + 4 * q < w.cols
+                                  ? __ldcg(base + static_cast<int64_t>(s0 + s) * (TR * 32) + (c * 8 + q) * 128)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int s = 0; s < SB; ++s)
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) sum[j] += x[s][j];
+                  for (int q = 0; q < 8; ++q) {
+                    sum[4 * q] += x[s][q].x;
+                    sum[4 * q + 1] += x[s][q].y;
+                    sum[4 * q + 2] += x[s][q].z;
+                    sum[4 * q + 3] += x[s][q].w;
+                  }
               }
               uint32_t r[32];
 #pragma unroll
