@@ -158,13 +158,23 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
   p->aux_words = ceil_div(N, 32);
   const bool bf16 = dtype == GEMM_EPI_BF16;
   // Few tiles (as far as the plan can tell) with a long contraction: the
-  // instance that may share a tile among CTAs. Below about 20 stages joining the
-  // parts costs what it saves (T = 8, K = 2048, N = 512, 16 stages: 9.5 us whole,
-  // 11.6 us in four parts).
-  const int64_t stages = wgrad ? (T + 63) / 64 : (K + (tr == 32 ? 127 : 63)) / (tr == 32 ? 128 : 64);
+  // instance that may share a tile among CTAs, where the estimate gains at least
+  // the 2 us that this instance takes longer over whole tiles (WGRAD of 2678
+  // rows, K = 864, N = 208: 14.9 us, 16.6 in this instance unsplit, 15.7 in four
+  // parts; forward of 2777 rows, K = 3856, N = 232: 26.4 us, 18.5 in three).
   const int64_t active = E < T ? E : T, mean = (T + active - 1) / active;
+  // (WGRAD contracts over an expert's rows: one of twice the mean)
+  const int64_t longest = 2 * mean < T ? 2 * mean : T;
+  const int64_t stages = wgrad ? (longest + 63) / 64 : (K + (tr == 32 ? 127 : 63)) / (tr == 32 ? 128 : 64);
   const int64_t expected = wgrad ? tiles : active * ((mean + tr - 1) / tr) * n_ft;
-  bool split = tr != 256 && stages >= 20 && 2 * expected <= sms;
+  bool split = false;
+  if (tr != 256 && expected <= sms) {
+    const int rows = (int)(wgrad ? K : mean);
+    const int64_t whole = ge::grouped_split_ns(tr, expected, 1, (int)stages, sms, rows);
+    for (int s = 2; s <= 16; ++s)
+      split = split || (ge::grouped_split_allowed(expected, s, (int)stages, sms) &&
+                        ge::grouped_split_ns(tr, expected, s, (int)stages, sms, rows) + 2000 <= whole);
+  }
   if (const char* f = getenv("GEMM_EPI_FORCE_SPLIT")) {  // tuning override
     p->force_splits = atoi(f) > 0 ? atoi(f) : 0;
     if (p->force_splits) split = tr != 256 && p->force_splits > 1;

@@ -172,31 +172,41 @@ __device__ __forceinline__ void grouped_table(const GroupedParams& p, int* offs,
   grouped_prefix<TR>(p, offs, start, tiles_per_mt, a, b);
 }
 
-// How many CTAs share a tile's contraction when there are few tiles (few
-// rows, few or narrow experts): the S up to 16 with the least estimated time,
-//   rounds of tiles x S work items x (stages / S x stage time + joining),
+// The estimated time (ns) of `tiles` tiles of `stages` stages, `rows` rows in
+// the longest, each shared by s CTAs:
+//   rounds of tiles x s work items x (stages / s x stage time + joining),
 // where a stage's time is what one SM takes to stream it and joining is the
 // partials' trip through L2 (write, ticket, read by the last to arrive),
-// which grows with the parts and the rows. The constants (ns) are fitted to
-// measurements: T = 4, K = 8192, N = 512 takes 26.0 us unsplit and 19.0, 14.2,
-// 14.3, 17.8 with 2, 4, 8, 16 parts; T = 32, K = 4096, N = 1024 15.5 and 14.5,
-// 12.5, 13.8, 19.1; WGRAD of 8192 rows, K = N = 64 32.3 and 25.1, 20.9, 22.0
-// with 2, 4, 8, K = N = 256 33.2 and 30.0, 28.3, 34.6. Every CTA computes the
-// same from the same table.
+// which grows with the parts and the rows. Fitted to measurements: T = 4, K =
+// 8192, N = 512 takes 24.8 us unsplit and 16.7, 11.6, 9.7, 9.7 with 2, 4, 8, 16
+// parts; T = 32, K = 4096, N = 1024 14.1 and 11.8, 9.6, 9.4, 11.0; WGRAD of 8192
+// rows, K = N = 64 31.7 and 21.8, 15.9, 14.1, 15.6, K = N = 256 32.4 and 24.3,
+// 19.4, 19.6, 32.0.
+__host__ __device__ __forceinline__ int64_t grouped_split_ns(int tr, int64_t tiles, int s, int stages, int units, int rows) {
+  const int64_t rounds = (tiles * s + units - 1) / units;
+  const int r = rows < tr ? rows : tr;
+  const int64_t join = s == 1 ? 0 : tr == 32 ? 2000 + s * (50 + r * 5) : 2600 + s * r * 8;
+  return rounds * (static_cast<int64_t>((stages + s - 1) / s) * (tr == 32 ? 300 : 215) + join);
+}
+
+// May s CTAs share each tile? One item an SM at most (max_items slots), two
+// stages each, and a contraction that is worth it at all.
+__host__ __device__ __forceinline__ bool grouped_split_allowed(int64_t tiles, int s, int stages, int max_items) {
+  return s == 1 || (tiles * s <= max_items && 2 * s <= stages && stages >= 16);
+}
+
+// How many CTAs share a tile's contraction when there are few tiles (few
+// rows, few or narrow experts): the S up to 16 with the least estimated time.
+// Every CTA computes the same from the same table.
 template <int TR>
 __device__ __forceinline__ int grouped_splits(const GroupedParams& p, int tiles, int stages, int units, int rows) {
-  constexpr int kStage = TR == 32 ? 290 : 240;
   const int s = static_cast<int>(lane_id()) + 1;
-  const int64_t items = static_cast<int64_t>(tiles) * s;
   uint64_t cost = ~0ull;
   if (p.force_splits > 0) {
-    if (s <= 16 && (s == 1 || items <= p.max_items)) cost = static_cast<uint64_t>(abs(s - p.force_splits)) << 5 | static_cast<uint64_t>(s);
-  } else if (s <= 16 && (s == 1 || (items <= p.max_items && 2 * s <= stages && stages >= 16))) {
-    const int64_t rounds = (items + units - 1) / units;
-    const int r = min(rows, TR);
-    const int64_t join = s == 1 ? 0 : TR == 32 ? 1400 + s * (500 + r * 6) : 2400 + (1 + s) * r * 25;
-    cost = static_cast<uint64_t>(rounds * (static_cast<int64_t>((stages + s - 1) / s) * kStage + join)) << 5 |
-           static_cast<uint64_t>(s);
+    if (s <= 16 && (s == 1 || static_cast<int64_t>(tiles) * s <= p.max_items))
+      cost = static_cast<uint64_t>(abs(s - p.force_splits)) << 5 | static_cast<uint64_t>(s);
+  } else if (s <= 16 && grouped_split_allowed(tiles, s, stages, p.max_items)) {
+    cost = static_cast<uint64_t>(grouped_split_ns(TR, tiles, s, stages, units, rows)) << 5 | static_cast<uint64_t>(s);
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
