@@ -7,6 +7,7 @@ kernels; if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -146,6 +147,27 @@ def _ptr(t, shape, dtype, name) -> int | None:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _on_stream(stream, device):
+    """The stream that a call will use, as the current one: outputs that a
+    convenience allocates belong to it. (Memory from another stream's pool may
+    still be read or written by work that waits on that stream.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    with _on_stream(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _zeros(shape, dtype, device, stream):
+    with _on_stream(stream, device):
+        return torch.zeros(shape, dtype=dtype, device=device)
 
 
 def gemm_epi_plan(T: int, N: int, K: int, dtype, epilog, flags: int = 0) -> int:
@@ -319,24 +341,24 @@ class Plan:
                 _ptr(dZ, (T, N), self.out_dtype, "dZ"), _ptr(dbias, (N,), torch.float32, "dbias"), _stream_ptr(stream))
         return lib().drelu_bgrad_unfused_execute, args
 
-    # conveniences that allocate their outputs (allocation happens in torch,
-    # outside the library; the library call itself allocates nothing)
+    # conveniences that allocate their outputs on the call's stream (allocation
+    # happens in torch, outside the library; the library call allocates nothing)
     def forward(self, X, W, bias, stream=None):
-        Y = torch.empty((self.T, self.N), dtype=self.out_dtype, device=X.device)
+        Y = _empty((self.T, self.N), self.out_dtype, X.device, stream)
         spec = self.aux_spec()
-        aux = torch.empty(spec[0], dtype=spec[1], device=X.device) if spec else None
+        aux = _empty(*spec, X.device, stream) if spec else None
         self.gemm_epi_execute(X, W, bias, Y, aux, stream)
         return Y, aux
 
     def backward(self, dY2, W2, aux, stream=None):
-        dZ = torch.empty((self.T, self.N), dtype=self.out_dtype, device=dY2.device)
-        dbias = torch.empty((self.N,), dtype=torch.float32, device=dY2.device)
+        dZ = _empty((self.T, self.N), self.out_dtype, dY2.device, stream)
+        dbias = _empty((self.N,), torch.float32, dY2.device, stream)
         self.drelu_bgrad_execute(dY2, W2, aux, dZ, dbias, stream)
         return dZ, dbias
 
     def wgrad(self, X, dZ, with_dbias=False, stream=None):
-        dW = torch.empty((self.K, self.N), dtype=self.out_dtype, device=X.device)
-        dbias = torch.empty((self.K,), dtype=torch.float32, device=X.device) if with_dbias else None
+        dW = _empty((self.K, self.N), self.out_dtype, X.device, stream)
+        dbias = _empty((self.K,), torch.float32, X.device, stream) if with_dbias else None
         self.gemm_epi_wgrad_execute(X, dZ, dW, dbias, stream)
         return (dW, dbias) if with_dbias else dW
 
@@ -357,16 +379,6 @@ def _ptr_on(index: int, t, shape, dtype, name) -> int:
         raise TypeError(f"{name} must be a torch.Tensor") from None
     _ptr(t, shape, dtype, name)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-
-
-def _zeros(shape, dtype, device, stream):
-    """Zeros written on the stream that the call will use (a fill on another
-    stream could come after the call's own stores)."""
-    if stream is None:
-        return torch.zeros(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
-    with torch.cuda.stream(s):
-        return torch.zeros(shape, dtype=dtype, device=device)
 
 
 class _DevicePlan(Plan):
@@ -447,13 +459,13 @@ class GroupedPlan(_DevicePlan):
 
     def backward(self, dY2, W2, aux, offsets, stream=None):
         dZ = _zeros((self.T, self.N), self.out_dtype, dY2.device, stream)
-        dbias = torch.empty((self.E, self.N), dtype=torch.float32, device=dY2.device)
+        dbias = _empty((self.E, self.N), torch.float32, dY2.device, stream)
         self.gemm_epi_grouped_drelu_bgrad_execute(dY2, W2, aux, offsets, dZ, dbias, stream)
         return dZ, dbias
 
     def wgrad(self, X, dZ, offsets, with_dbias=False, stream=None):
-        dW = torch.empty((self.E, self.K, self.N), dtype=self.out_dtype, device=X.device)
-        dbias = torch.empty((self.E, self.K), dtype=torch.float32, device=X.device) if with_dbias else None
+        dW = _empty((self.E, self.K, self.N), self.out_dtype, X.device, stream)
+        dbias = _empty((self.E, self.K), torch.float32, X.device, stream) if with_dbias else None
         self.gemm_epi_grouped_wgrad_execute(X, dZ, offsets, dW, dbias, stream)
         return (dW, dbias) if with_dbias else dW
 
