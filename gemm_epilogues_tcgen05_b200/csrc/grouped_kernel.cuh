@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   volatile int* sum_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 20);  // [2]
+  volatile uint64_t* last_step = reinterpret_cast<volatile uint64_t*>(smem + L::OFF_MISC + 32);  // see wait_steps
   volatile int* split_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 12);
   int* split_count = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);
   float* sums = reinterpret_cast<float*>(smem + L::OFF_SUM);
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *last_step = globaltimer_ns();
     fence_barrier_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
@@ -545,12 +547,13 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       const int boxes = (nloc + (WG ? 64 : BXR) - 1) / (WG ? 64 : BXR);
       const uint32_t tx = L::A_BYTES + static_cast<uint32_t>(boxes) * (WG ? 64 * kBK * 2 : KPS * BXR * kBK * 2);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        ok = wait_bounded(&empty[s], ph, wp, abort_flag, 1);
+        ok = wait_steps(&empty[s], ph, wp, abort_flag, last_step, 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* a = sA + s * L::A_BYTES;
         uint8_t* b = sB + s * L::B_BYTES;
         if (issuer) {
+          if (it % kStepStages == 0) *last_step = globaltimer_ns();
           if constexpr (WG) {
             const int t = w.row0 + kb * kBK;
             if (cut && kb == kbs - 1) {
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     // leader's barriers count them: there the release by the MMA shows it)
     const uint32_t inflight = it < STAGES ? it : STAGES;
     for (uint32_t i = it - inflight; i < it; ++i)
-      wait_bounded(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 2,
+      wait_steps(PAIR ? &empty[i % STAGES] : &full[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, last_step, 2,
                    /*honour_abort=*/false);
     __syncwarp();
   } else if (warp == 1) {
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         if (kb0 == kb1) continue;  // nothing to contract (an expert without rows): the epilogue takes zeros
         const uint32_t buf = tcount & 1u;
         const uint32_t tph = (tcount >> 1) & 1u;
-        ok = wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3);
+        ok = wait_steps(&tempty[buf], tph ^ 1u, wp, abort_flag, last_step, 3);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       }
     }
     // every MMA that writes this CTA's tensor memory is done before it is freed
-    wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
+    wait_steps(drain, 0, wp, abort_flag, last_step, 5, /*honour_abort=*/false);
     __syncwarp();
   } else if (WG && warp == 2 + EW) {
     // ---------------------------------------------- foreign rows (WGRAD)
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         it += static_cast<uint32_t>(kb1 - kb0);
         if ((w.rows & 15) == 0 || kb1 == kb0 || kb1 < kbs) continue;
         const uint32_t s = (it - 1) % STAGES;
-        ok = wait_bounded(&tailbar[s], (phases >> s) & 1u, wp, abort_flag, 9);
+        ok = wait_steps(&tailbar[s], (phases >> s) & 1u, wp, abort_flag, last_step, 9);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         phases ^= 1u << s;
@@ -792,8 +795,10 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
     if constexpr (EPI == EPI_DRELU_BGRAD) {
       // experts without rows: no tile of theirs exists, and their bias gradient is zero
       for (int e = static_cast<int>(blockIdx.x); e < p.E; e += static_cast<int>(gridDim.x))
-        if (offs[e] == offs[e + 1])
+        if (offs[e] == offs[e + 1]) {
           for (int n = static_cast<int>(et); n < p.N; n += ET) p.dbias[static_cast<int64_t>(e) * p.N + n] = 0.f;
+          if (et == 0) *last_step = globaltimer_ns();
+        }
     }
     GroupedTile w;
     for (int item = unit; grouped_tile<EPI, TR, FM>(p, offs, start, SPLIT ? item / S : item, w); item += units) {
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
       if constexpr (EPI == EPI_DRELU_BGRAD)
         if (!SPLIT || S == 1) mnext = mask_word(static_cast<int>(eh));
       if (!empty_tile) {
-        if (ok) ok = wait_bounded(&tfull[buf], tph, wp, abort_flag, 6);
+        if (ok) ok = wait_steps(&tfull[buf], tph, wp, abort_flag, last_step, 6);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
@@ -973,7 +978,10 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
           }
         }
       }
-      if (!empty_tile) ++tcount;
+      if (!empty_tile)
+        ++tcount;
+      else if (et == 0)
+        *last_step = globaltimer_ns();
       if constexpr (EPI == EPI_DRELU_BGRAD) {
         // this tile's column sums to the joining warp, two tiles deep
         const uint32_t b = dcount & 1u;

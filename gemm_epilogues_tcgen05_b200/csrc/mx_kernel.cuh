@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(320, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  volatile uint64_t* last_step = reinterpret_cast<volatile uint64_t*>(smem + L::OFF_MISC + 8);  // see wait_steps
   int* offs = reinterpret_cast<int*>(smem + L::OFF_TABLE);
   int* start = offs + kMaxExperts + 1;
   int* stile = start + kMaxExperts + 1;  // first scale tile (128 rows) of each expert
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(320, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *last_step = globaltimer_ns();
     fence_barrier_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(320, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (issuer) {
+          if (PAIR && it % kStepStages == 0) *last_step = globaltimer_ns();
           if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
           const uint32_t bar = full0 + s * 8;
           uint8_t* sf = sSF + s * L::SF_BYTES;
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(320, 1)
       }
     }
     // every MMA that writes this CTA's tensor memory is done before it is freed
-    wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);
+    wait_steps(drain, 0, wp, abort_flag, last_step, 5, /*honour_abort=*/false);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue

@@ -194,6 +194,30 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
   }
 }
 
+// The same for a wait that can span most of a healthy launch (until a CTA
+// pair's last tile, an expert's last rows, an epilogue with many tiles to
+// clear): it runs out only if this CTA made no step within the limit either.
+// `last` is when it last did: the producer writes it every kStepStages stages,
+// an epilogue with each tile that it only clears. Steps are finite, so it ends.
+// (Read after the limit has passed, the polling loop stays as it is: counting
+// steps in it, and writing one a stage, cost small grouped launches 0.9 us.)
+constexpr uint32_t kStepStages = 64;
+__device__ __forceinline__ bool wait_steps(uint64_t* bar, uint32_t parity, const TileParams& p, volatile int* abort_flag,
+                                           volatile uint64_t* last, int site, bool honour_abort = true) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (honour_abort && *abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    // (signed: a step made meanwhile is later than now)
+    if (now - t0 > p.timeout_ns && static_cast<int64_t>(now - *last) > static_cast<int64_t>(p.timeout_ns)) {
+      report_timeout(p.status, abort_flag, site);
+      return false;
+    }
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ float load_16(const void* base, int64_t i) {
   if constexpr (BF16)

@@ -40,7 +40,9 @@
  * Environment variables, read when a plan is created (and by every call of
  * drelu_bgrad_execute_noalloc); none is needed in normal use:
  *   GEMM_EPI_WAIT_TIMEOUT_MS      limit of each bounded wait inside a kernel
- *                                 (default 2000 ms; see GEMM_EPI_ERR_TIMEOUT)
+ *                                 (default 2000 ms; see GEMM_EPI_ERR_TIMEOUT).
+ *                                 A wait that spans many tiles counts from the
+ *                                 last progress, so a launch may last longer
  *   tuning overrides of the plan's choices, for measurement and tests:
  *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny, GEMM_EPI_FORCE_BN=64|128|192|256,
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
