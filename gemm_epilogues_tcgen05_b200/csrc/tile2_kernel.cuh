@@ -67,7 +67,7 @@ struct Tile2Smem {
   static constexpr uint32_t OFF_BAR = OFF_B + STAGES * B_BYTES;
   static constexpr uint32_t N_BARS = 2 * STAGES + 6;  // full, empty, tfull[2], tempty[2], drain, stream-K fixup
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;
-  static constexpr uint32_t OFF_BIAS = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr uint32_t OFF_BIAS = (OFF_MISC + 24 + 15) / 16 * 16;
   static constexpr uint32_t OFF_COLP = OFF_BIAS + 2 * BN * 4;
   static constexpr uint32_t OFF_STG = (OFF_COLP + 2 * 4 * BN * 4 + 1023) / 1024 * 1024;
   static constexpr uint32_t OFF_AUXSTG = OFF_STG + kStageBytesPerWarp * EW;
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
   uint8_t* auxstg_s = smem + L::OFF_AUXSTG;                       // [EW warps][1 KB]
   volatile int* dflag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
   volatile int* sflag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 12);  // stream-K wait result
+  volatile uint64_t* last_step = reinterpret_cast<volatile uint64_t*>(smem + L::OFF_MISC + 16);  // see wait_steps
 
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = lane_id();
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     mbar_init(drain, 1);
     mbar_init(fixbar, 1);
     *abort_flag = 0;
+    *last_step = globaltimer_ns();
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -302,6 +304,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
             ok = false;
             break;
           }
+          if (it % kStepStages == 0) *last_step = globaltimer_ns();
           if (rank == 0) mbar_arrive_expect_tx(&full[s], w.half < 0 ? PAIR_TX : PAIR_TX_HALF);
           const uint32_t fbar = full0 + s * 8;  // the leader's full[s]
           if constexpr (A_MN) {
@@ -364,7 +367,8 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         umma_commit_pair(drain, BOTH);
       }
       // both CTAs: the leader's MMAs write this CTA's TMEM; they must be done
-      wait_bounded(drain, 0, p, abort_flag, 5, /*honour_abort=*/false);
+      // (the other CTA waits here from its start)
+      wait_steps(drain, 0, p, abort_flag, last_step, 5, /*honour_abort=*/false);
     }
     __syncwarp();
   } else {

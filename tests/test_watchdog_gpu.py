@@ -9,7 +9,7 @@ are exact.
 import pytest
 import torch
 
-from gemm_epilogues_tcgen05_b200 import GroupedPlan, MxPlan
+from gemm_epilogues_tcgen05_b200 import GroupedPlan, MxPlan, Plan
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -37,6 +37,19 @@ def run_long(p, call):
     torch.cuda.synchronize()
     assert p.status() == 0
     assert a.elapsed_time(b) > 2 * LIMIT_MS
+
+
+def test_one_product_on_cta_pairs(monkeypatch):
+    limit(monkeypatch)
+    monkeypatch.setenv("GEMM_EPI_FORCE_KERNEL", "pair")
+    T, N, K = 32768, 16384, 16384
+    X, W = signs((T, K), 1), signs((K, N), 2)
+    Y = torch.zeros((T, N), dtype=BF, device="cuda")
+    with Plan(T, N, K, BF, "NONE") as p:
+        assert p.info()["kernel"] == 2
+        run_long(p, lambda: p.gemm_epi_execute(X, W, None, Y))
+    for r in (slice(0, 3), slice(T - 3, T)):
+        assert torch.equal(Y[r], (X[r].double() @ W.double()).to(BF))
 
 
 @pytest.mark.parametrize("tr", [128, 256])
