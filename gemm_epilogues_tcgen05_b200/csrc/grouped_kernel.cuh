@@ -296,35 +296,47 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   return r;
 }
 
-// GELU(z) = z Phi(z) = max(z, 0) - |z| h(|z|) with h(a) = erfc(a / sqrt 2) / 2.
-// Without cancellation on either side: an error e of h costs e |z|. h is a
-// polynomial of degree 15 in u = 2 a / 5.25 - 1, a least-maximum fit on [0, 5.25]
-// with h(5.25) = 0 (where the true value is 7.6e-8); beyond, a is held there, so
-// infinities give inf and 0, and max.NaN keeps NaN. |error| <= 1.8e-7 |z| with
-// fp32 Horner (checked over 4 million points). All multiply-adds, two values an
-// instruction: with erff (an exponential and its branches) a 256 x 256 tile's
-// epilogue outlasted its products. Microscaled T = 4096, N = 11008, K = 4096:
-// 150 us with erff against 74 without an activation; E = 16, T = 1003, K = 2048,
-// N = 5000: 28.3 and 21.3 us.
+// GELU(z) = z Phi(z) = max(z, 0) - |z| h(|z|) with h(a) = Phi(-a) = 2^q(a), so
+// that the negative tail keeps its relative accuracy (an approximation of h
+// itself, off by 2e-7 everywhere, was 0.2 % off at z = -4 and of the wrong sign
+// at -5.2). q(a) = -1 + a (s(a) - a / (2 ln 2)): the Gaussian's exponent apart, s
+// stays between -1.2 and -0.3, a polynomial of degree 14 in u = 2 a / 13 - 1
+// (a weighted least-maximum fit on [0, 13], off by less than 2e-8 max(1, |q| / 2) /
+// max(a, 0.3)), and the form is exact at a = 0. Measured over half a million
+// points: |error| <= 9.3e-8 |z|, and relative to the result of a negative z at
+// most 8e-7 down to -4, 2e-6 down to -6, 9e-6 down to -12.9, where h leaves the
+// normal numbers and becomes 0 (ex2's flush); a is held at 13 beyond, so
+// infinities give inf and 0, and max.NaN keeps NaN. Multiply-adds on two values an
+// instruction and one ex2 each: with erff (an exponential and its branches) a 256
+// x 256 tile's epilogue outlasted its products (microscaled T = 4096, N = 11008, K
+// = 4096: 150 us, 96.5 with this, 74 without an activation; a polynomial for h
+// took 92.3. E = 16, T = 1003, K = 2048, N = 5000: 23 us with either, 20.4 without).
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ void gelu32(float (&v)[32]) {
-  constexpr float kA = 5.25f, kS = 2.0f / 5.25f;
-  constexpr float kC[16] = {4.332505e-03f,  -3.3400327e-02f, 1.1507147e-01f,  -2.2597559e-01f,
-                            2.5717223e-01f, -1.2065171e-01f, -9.799971e-02f,  1.951371e-01f,
-                            -9.483086e-02f, -5.943329e-02f,  9.744846e-02f,   -2.165498e-02f,
-                            -3.6828823e-02f, 2.0791065e-02f, 5.6347707e-03f,  -4.812312e-03f};
+  constexpr float kA = 13.0f, kS = 2.0f / 13.0f, kHalfLog2e = 0.72134752f;
+  constexpr float kC[15] = {-0.47054109f, 0.258029431f, -0.160296753f, 0.102642007f, -0.0657589659f,
+                            0.0410890728f, -0.0249870718f, 0.0165973958f, -0.00968039781f, -0.000120837707f,
+                            0.00111253548f, 0.00610661181f, -0.00311078061f, -0.00396853918f, 0.00253350381f};
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     const float a0 = fminf(fabsf(v[j]), kA), a1 = fminf(fabsf(v[j + 1]), kA);
-    const uint64_t u = fma_f32x2(pack_f32x2(a0, a1), pack_f32x2(kS, kS), pack_f32x2(-1.f, -1.f));
-    uint64_t h = pack_f32x2(kC[15], kC[15]);
+    const uint64_t a = pack_f32x2(a0, a1);
+    const uint64_t u = fma_f32x2(a, pack_f32x2(kS, kS), pack_f32x2(-1.f, -1.f));
+    uint64_t s = pack_f32x2(kC[14], kC[14]);
 #pragma unroll
-    for (int k = 14; k >= 0; --k) h = fma_f32x2(h, u, pack_f32x2(kC[k], kC[k]));
-    float h0, h1, r0, r1;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(h0), "=f"(h1) : "l"(h));
+    for (int k = 13; k >= 0; --k) s = fma_f32x2(s, u, pack_f32x2(kC[k], kC[k]));
+    s = fma_f32x2(a, pack_f32x2(-kHalfLog2e, -kHalfLog2e), s);
+    const uint64_t q = fma_f32x2(a, s, pack_f32x2(-1.f, -1.f));
+    float q0, q1, r0, r1;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q0), "=f"(q1) : "l"(q));
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r0) : "f"(v[j]));
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r1) : "f"(v[j + 1]));
-    v[j] = fmaf(-a0, h0, r0);
-    v[j + 1] = fmaf(-a1, h1, r1);
+    v[j] = fmaf(-a0, exp2_ftz(q0), r0);
+    v[j + 1] = fmaf(-a1, exp2_ftz(q1), r1);
   }
 }
 

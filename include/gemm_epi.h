@@ -345,8 +345,9 @@ GEMM_EPI_API int drelu_bgrad_execute_noalloc(int64_t T, int64_t N, int64_t K, ge
  * values cannot reach outside the tensors, and name the rows that this gives.
  * Results, rounding, the 16-bit types, epilogs, flags, error codes, watchdog,
  * streams and ownership are those of one product, with two exceptions: these
- * kernels evaluate GELU as max(z, 0) - |z| erfc(|z| / sqrt(2)) / 2 by a
- * polynomial (absolute error at most 1.8e-7 |z|), and a call runs on the plan's
+ * kernels evaluate GELU as max(z, 0) - |z| Phi(-|z|) with Phi(-a) as a power of
+ * two (error at most 1e-7 |z|, and of a negative z at most 1e-5 of the result,
+ * 1e-6 down to z = -4; below z = -12.9 the result is 0), and a call runs on the plan's
  * device whichever is current. Sums are in a fixed order, so equal calls give
  * equal bits. gemm_epi_free, _query, _status, _last_error and _set_bias_f32
  * take these plans too; the other calls return GEMM_EPI_ERR_EPILOG_MISMATCH.
