@@ -807,7 +807,7 @@ int gemm_epi_execute(gemm_epi_plan_t plan, const void* X, const void* W, const v
       (p->epilog == GEMM_EPI_RELU_AUX_BIAS && !aligned(aux, 4)) || (gelu_aux && !aligned(aux, 16)))
     return fail(GEMM_EPI_ERR_MISALIGNED,
                 "gemm_epi_execute: X, W, Y need 16-byte, bias 2-byte, aux 4-byte (GELU_AUX_BIAS: 16-byte) alignment");
-  int rc = take_status(p);
+  int rc = begin_call(p, stream);
   if (rc) return rc;
   if (p->kernel == 1) {
     rc = prepare_skinny_maps(p, X, W);
@@ -839,7 +839,7 @@ int drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, const void* W2, c
   if (!aligned(dY2, 16) || !aligned(W2, 16) || !aligned(dZ, 16) || !aligned(aux, 4) || !aligned(dbias, 4))
     return fail(GEMM_EPI_ERR_MISALIGNED,
                 "drelu_bgrad_execute: dY2, W2, dZ need 16-byte, aux and dbias 4-byte alignment");
-  int rc = take_status(p);
+  int rc = begin_call(p, stream);
   if (rc) return rc;
   if (p->kernel == 1) {
     rc = prepare_skinny_maps(p, dY2, W2);
@@ -878,7 +878,7 @@ int gemm_epi_unfused_execute(gemm_epi_plan_t plan, const void* X, const void* W,
   if (!aligned(X, 16) || !aligned(W, 16) || !aligned(T1, 16) || !aligned(T2, 16) || !aligned(Y, 16) ||
       !aligned(bias, p->bias_f32 ? 4 : 2) || (aux && !aligned(aux, 4)))
     return fail(GEMM_EPI_ERR_MISALIGNED, "unfused: misaligned pointer");
-  int rc = take_status(p);
+  int rc = begin_call(p, stream);
   if (rc) return rc;
   rc = prepare_maps(p, X, W);
   if (rc) return rc;
@@ -940,7 +940,7 @@ int gemm_epi_wgrad_execute(gemm_epi_plan_t plan, const void* X, const void* dZ, 
   if (!X || !dZ || !dW) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_wgrad_execute: NULL X, dZ or dW");
   if (!aligned(X, 16) || !aligned(dZ, 16) || !aligned(dW, 16) || (dbias && !aligned(dbias, 4)))
     return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_wgrad_execute: X, dZ, dW need 16-byte, dbias 4-byte alignment");
-  int rc = take_status(p);
+  int rc = begin_call(p, stream);
   if (rc) return rc;
   rc = prepare_maps(p, X, dZ);
   if (rc) return rc;
@@ -974,7 +974,7 @@ int drelu_bgrad_unfused_execute(gemm_epi_plan_t plan, const void* dY2, const voi
   if (!aligned(dY2, 16) || !aligned(W2, 16) || !aligned(G, 16) || !aligned(dZ, 16) || !aligned(aux, 4) ||
       !aligned(dbias, 4))
     return fail(GEMM_EPI_ERR_MISALIGNED, "unfused: misaligned pointer");
-  int rc = take_status(p);
+  int rc = begin_call(p, stream);
   if (rc) return rc;
   rc = prepare_maps(p, dY2, W2);
   if (rc) return rc;

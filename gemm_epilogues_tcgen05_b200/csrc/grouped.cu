@@ -81,11 +81,12 @@ ge::GroupedParams params(const gemm_epi_plan_s* p, const int32_t* offsets) {
   return k;
 }
 
-int launch(const gemm_epi_plan_s* p, const CUtensorMap& a, const CUtensorMap& b, const ge::GroupedParams& k,
+int launch(gemm_epi_plan_s* p, const CUtensorMap& a, const CUtensorMap& b, const ge::GroupedParams& k,
            cudaStream_t s) {
   Launch l(p->grid, p->gr.threads, p->gr.smem, p->gr.pair, s);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, p->gr.fn, a, b, k);
   if (e != cudaSuccess) return cuda_fail(e, "grouped kernel launch");
+  if (p->inject_stall == 2) p->inject_stall = 0;
   return GEMM_EPI_OK;
 }
 
@@ -319,7 +320,7 @@ int gemm_epi_grouped_execute(gemm_epi_plan_t plan, const void* X, const void* W,
                 "gemm_epi_grouped_execute: X, W, Y need 16-byte, offsets and aux 4-byte (GELU_AUX_BIAS: 16-byte), bias "
                 "2-byte (fp32: 4-byte) alignment");
   DeviceScope scope(p->device);
-  rc = take_status(p);
+  rc = begin_call(p, stream);
   if (rc) return rc;
   CUtensorMap a, b;
   rc = forward_maps(p, X, W, &a, &b);
@@ -346,7 +347,7 @@ int gemm_epi_grouped_drelu_bgrad_execute(gemm_epi_plan_t plan, const void* dY2, 
     return fail(GEMM_EPI_ERR_MISALIGNED,
                 "gemm_epi_grouped_drelu_bgrad_execute: dY2, W2, dZ need 16-byte, aux, offsets, dbias 4-byte alignment");
   DeviceScope scope(p->device);
-  rc = take_status(p);
+  rc = begin_call(p, stream);
   if (rc) return rc;
   CUtensorMap a, b;
   rc = forward_maps(p, dY2, W2, &a, &b);
@@ -373,7 +374,7 @@ int gemm_epi_grouped_wgrad_execute(gemm_epi_plan_t plan, const void* X, const vo
     return fail(GEMM_EPI_ERR_MISALIGNED,
                 "gemm_epi_grouped_wgrad_execute: X, dZ, dW need 16-byte, offsets and dbias 4-byte alignment");
   DeviceScope scope(p->device);
-  rc = take_status(p);
+  rc = begin_call(p, stream);
   if (rc) return rc;
   const auto u16 = CU_TENSOR_MAP_DATA_TYPE_UINT16;
   CUtensorMap a, b;

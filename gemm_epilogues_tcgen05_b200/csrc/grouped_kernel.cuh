@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(GroupedThreads<EPI, TR>::value, 1)
         }
         if (!ok) break;
         // (fault injection: the epilogue then waits on a barrier nothing arrives on)
-        if (issuer && !(p.inject_stall && tcount == 0)) {
+        if (issuer && !(p.inject_stall && tcount == 0 && (p.inject_stall == 1 || unit == 0))) {
           if constexpr (PAIR)
             umma_commit_pair(&tfull[buf], BOTH);
           else

@@ -61,8 +61,9 @@ inline bool inject_encode_failure() { return test_hook("GEMM_EPI_INJECT_ENCODE_F
 // (2 s; GEMM_EPI_WAIT_TIMEOUT_MS overrides) and, for the watchdog tests,
 // GEMM_EPI_INJECT_STALL -- the MMA issuer withholds its first tile's
 // completion signal, so the epilogue's wait runs out and the kernel reports
-// ERR_TIMEOUT. Read when a plan is created and on every call of the
-// allocation-free entry point.
+// ERR_TIMEOUT (2, grouped and microscaled plans: one CTA of the first launch
+// only). Read when a plan is created and on every call of the allocation-free
+// entry point.
 struct WatchdogEnv {
   uint64_t timeout_ns = 2000000000ull;
   int inject_stall = 0;
@@ -73,7 +74,7 @@ inline WatchdogEnv watchdog_env() {
     const long long ms = atoll(t);
     if (ms > 0) w.timeout_ns = (uint64_t)ms * 1000000ull;
   }
-  w.inject_stall = test_hook("GEMM_EPI_INJECT_STALL") ? 1 : 0;
+  if (test_hook("GEMM_EPI_INJECT_STALL")) w.inject_stall = atoi(getenv("GEMM_EPI_INJECT_STALL")) == 2 ? 2 : 1;
   return w;
 }
 
@@ -249,6 +250,7 @@ struct gemm_epi_plan_s {
   int* status_dev = nullptr;
   uint64_t timeout_ns = 0;
   int inject_stall = 0;  // GEMM_EPI_INJECT_STALL at plan time (watchdog tests)
+  bool counts_stale = false;  // an interrupted launch may have left counters of this workspace above zero
   int tail_split = 1;    // GEMM_EPI_TAIL_SPLIT=0 keeps whole tiles in the pair kernel's last round
   int bias_f32 = 0;      // gemm_epi_set_bias_f32: the forward bias is fp32
   int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
@@ -312,13 +314,30 @@ inline int take_status(gemm_epi_plan_s* p) {
   const int v = *s;
   if (v != 0) {
     *s = 0;
-    // an interrupted launch may have left split-tile tickets counted
-    if (p->sk_tickets)
-      cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)(p->kind == 0 ? ceil_div(p->N, 128) : p->split_items));
-    if (p->col_tickets) cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
-    if (p->pair_flags) cudaMemset(p->pair_flags, 0, sizeof(int) * (size_t)p->n_pair_flags);
+    p->counts_stale = true;
     return fail(GEMM_EPI_ERR_TIMEOUT, "a kernel of this plan gave up waiting (watchdog code 0x%x)", v);
   }
+  return GEMM_EPI_OK;
+}
+
+// Before a call launches: the report of an earlier run-out, and the counters
+// that it left cleared on the call's own stream (the legacy stream orders
+// nothing for a stream that does not block on it). While a stream is being
+// captured the clearing becomes part of the graph, so it stays due until a call
+// that runs.
+inline int begin_call(gemm_epi_plan_s* p, cudaStream_t stream) {
+  const int rc = take_status(p);
+  if (rc || !p->counts_stale) return rc;
+  const auto clear = [stream](int* counts, int n) {
+    return counts ? cudaMemsetAsync(counts, 0, sizeof(int) * (size_t)n, stream) : cudaSuccess;
+  };
+  cudaError_t e = clear(p->sk_tickets, p->kind == 0 ? ceil_div(p->N, 128) : p->split_items);
+  if (e == cudaSuccess) e = clear(p->col_tickets, p->n_tickets);
+  if (e == cudaSuccess) e = clear(p->pair_flags, p->n_pair_flags);
+  if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace of an interrupted launch");
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capture) == cudaSuccess && capture == cudaStreamCaptureStatusNone)
+    p->counts_stale = false;
   return GEMM_EPI_OK;
 }
 

@@ -272,7 +272,7 @@ int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, const uint8_t* 
     return fail(GEMM_EPI_ERR_MISALIGNED,
                 "gemm_epi_mx_execute: values, scales and Y need 16-byte, offsets 4-byte, bias 2-byte (fp32: 4-byte) alignment");
   DeviceScope scope(p->device);
-  rc = take_status(p);
+  rc = begin_call(p, stream);
   if (rc) return rc;
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   const auto plain = CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -303,7 +303,9 @@ int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, const uint8_t* 
   k.g.inject_stall = p->inject_stall;
   Launch l(p->grid, p->gr.threads, p->gr.smem, p->gr.pair, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, p->gr.mx_fn, a, b, sa, sb, k);
-  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "microscaled product launch");
+  if (e != cudaSuccess) return cuda_fail(e, "microscaled product launch");
+  if (p->inject_stall == 2) p->inject_stall = 0;
+  return GEMM_EPI_OK;
 }
 
 }  // extern "C"
