@@ -32,7 +32,9 @@ inline int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+// The error stays with this call: the runtime would hand it to the next launch that asks for the last one.
 inline int cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   return fail(GEMM_EPI_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
