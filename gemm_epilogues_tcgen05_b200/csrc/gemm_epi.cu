@@ -625,7 +625,7 @@ gemm_epi_plan_t gemm_epi_plan_ex(int64_t T, int64_t N, int64_t K, gemm_epi_dtype
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(stream-K partials)"));
       e = cudaMalloc((void**)&p->pair_flags, sizeof(int) * 2 * (size_t)pairs);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(stream-K flags)"));
-      e = cudaMemset(p->pair_flags, 0, sizeof(int) * 2 * (size_t)pairs);
+      e = zero_counts(p->pair_flags, 2 * (size_t)pairs);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMemset(stream-K flags)"));
       p->n_pair_flags = 2 * pairs;
       p->pair_bytes += sizeof(int) * 2 * (size_t)pairs;
@@ -680,7 +680,7 @@ gemm_epi_plan_t gemm_epi_plan_ex(int64_t T, int64_t N, int64_t K, gemm_epi_dtype
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(split-tile partials)"));
       e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * (size_t)n_tiles);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(tickets)"));
-      e = cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)n_tiles);
+      e = zero_counts(p->sk_tickets, (size_t)n_tiles);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMemset(tickets)"));
       p->sk_bytes += sizeof(int) * (size_t)n_tiles;
     }
@@ -701,7 +701,7 @@ gemm_epi_plan_t gemm_epi_plan_ex(int64_t T, int64_t N, int64_t K, gemm_epi_dtype
       p->n_tickets = p->kernel == 2 ? 2 * p->n_tiles : p->n_tiles;  // pair kernel: 128-column half blocks
       e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMalloc(column tickets)"));
-      e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+      e = zero_counts(p->col_tickets, (size_t)p->n_tickets);
       if (e != cudaSuccess) return cleanup(cuda_fail(e, "cudaMemset(column tickets)"));
     }
   } else if (epilog == GEMM_EPI_WGRAD) {  // partials of the optional bias gradient (sum of X over its rows)

@@ -248,14 +248,14 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     p->n_tickets = (int)(E * ceil_div(N, 128));
     e = cudaMalloc((void**)&p->partials, p->partial_bytes);
     if (e == cudaSuccess) e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
-    if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+    if (e == cudaSuccess) e = zero_counts(p->col_tickets, (size_t)p->n_tickets);
   }
   if (e == cudaSuccess && split) {
     p->split_items = sms;  // one work item an SM: more parts never paid
     p->split_bytes = (size_t)p->split_items * tr * 128 * sizeof(float) + sizeof(int) * (size_t)p->split_items;
     e = cudaMalloc((void**)&p->sk_partials, (size_t)p->split_items * tr * 128 * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * (size_t)p->split_items);
-    if (e == cudaSuccess) e = cudaMemset(p->sk_tickets, 0, sizeof(int) * (size_t)p->split_items);
+    if (e == cudaSuccess) e = zero_counts(p->sk_tickets, (size_t)p->split_items);
   }
   if (e == cudaSuccess && wgrad) {
     // the optional bias gradient: row slices for about eight blocks an SM (one
@@ -271,7 +271,7 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
       p->n_tickets = (int)blocks;
       e = cudaMalloc((void**)&p->partials, p->partial_bytes);
       if (e == cudaSuccess) e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
-      if (e == cudaSuccess) e = cudaMemset(p->col_tickets, 0, sizeof(int) * (size_t)p->n_tickets);
+      if (e == cudaSuccess) e = zero_counts(p->col_tickets, (size_t)p->n_tickets);
     }
   }
   if (e != cudaSuccess) {

@@ -144,6 +144,19 @@ inline int encode_3d(CUtensorMap* map, CUtensorMapDataType type, const void* bas
   return GEMM_EPI_OK;
 }
 
+// Counters of a new workspace set to zero, and done with when this returns:
+// the plan's first call may run on any stream, and a memset on the legacy
+// stream, which could be behind, is not waited for by all of them.
+inline cudaError_t zero_counts(int* counts, size_t n) {
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(counts, 0, sizeof(int) * n, s);
+  const cudaError_t done = cudaStreamSynchronize(s);
+  cudaStreamDestroy(s);
+  return e != cudaSuccess ? e : done;
+}
+
 // The current device's number and SM count; an error unless it is a B200. The
 // device's properties are asked for once (they never change).
 inline int require_b200(int* dev, int* sms) {

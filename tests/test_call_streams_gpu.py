@@ -5,7 +5,11 @@ still to be written by work that waits there. A convenience called on another
 stream must not take that memory for an output: its kernel ends first, and the
 late writes would land in a finished result. Integer inputs, so every result is
 exact.
+
+A plan's counters are zero before its first call, whatever stream that runs on.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -120,3 +124,58 @@ def test_microscaled():
             Y = p.forward(xq, xs, wq, ws, None, stream=s)
             torch.cuda.synchronize()
             assert torch.equal(Y.double(), x.double() @ w.double().t())
+
+
+def dirty_small_blocks():
+    """Device memory that small allocations are likely to get next, filled with ones."""
+    rt = ctypes.CDLL("libcudart.so.12")
+    blocks = [ctypes.c_void_p() for _ in range(256)]
+    for b in blocks:
+        assert rt.cudaMalloc(ctypes.byref(b), ctypes.c_size_t(4096)) == 0
+        assert rt.cudaMemset(b, 0xFF, ctypes.c_size_t(4096)) == 0
+    torch.cuda.synchronize()
+    for b in blocks:
+        assert rt.cudaFree(b) == 0
+
+
+def test_a_new_plan_on_a_stream_of_its_own(monkeypatch):
+    """Made while the legacy stream is behind, and run at once on a stream that does not wait for it."""
+    s = torch.cuda.Stream()
+    R, K1, N1 = 300, 2048, 264
+    X, W = ints((R, K1), 1), ints((1, K1, N1), 2)
+    Y = torch.zeros((R, N1), device="cuda")
+    G = X.double() @ W[0].double()
+    aux = torch.full((R, (N1 + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    db = torch.zeros((1, N1), device="cuda")
+    few, Yf = ints((40, K1), 3), torch.zeros((40, N1), device="cuda")
+    monkeypatch.setenv("GEMM_EPI_FORCE_GROUPED", "128")
+    monkeypatch.setenv("GEMM_EPI_FORCE_SPLIT", "4")
+
+    def grouped():
+        with GroupedPlan(1, R, N1, K1, BF, "DRELU_BGRAD", out_f32=True) as p:
+            p.gemm_epi_grouped_drelu_bgrad_execute(X, W, aux, offsets, Y, db, stream=s)
+            s.synchronize()
+        assert torch.equal(Y.double(), G) and torch.equal(db[0].double(), G.sum(0))
+
+    def one():
+        with Plan(R, N1, K1, BF, "DRELU_BGRAD", out_f32=True) as p:
+            p.drelu_bgrad_execute(X, W[0], aux, Y, db[0], stream=s)
+            s.synchronize()
+        assert torch.equal(Y.double(), G) and torch.equal(db[0].double(), G.sum(0))
+
+    def few_rows():
+        with Plan(40, N1, K1, BF, "NONE", out_f32=True) as p:
+            assert p.info()["split_k"] > 1
+            p.gemm_epi_execute(few, W[0], None, Yf, stream=s)
+            s.synchronize()
+        assert torch.equal(Yf.double(), few.double() @ W[0].double())
+
+    for run in (grouped, one, few_rows):
+        Y.zero_()
+        db.zero_()
+        dirty_small_blocks()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)
+        run()
+        torch.cuda.synchronize()
