@@ -755,9 +755,9 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->tile_n = p->gr.TR;                // rows per tile at most (the MMA's N)
     info->tile_k = p->gr.BK;
     info->stages = p->gr.stages;
-    info->split_k = 1;
+    info->split_k = p->split_k;
     info->grid = p->grid;
-    info->launches = p->gr.launches;
+    info->launches = 1;
     info->workspace_bytes = p->partial_bytes + p->split_bytes + sizeof(int) * (size_t)p->n_tickets;
   } else if (p->kernel == 1) {
     info->tile_m = 128;  // features per tile (the MMA's M)

@@ -169,17 +169,31 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
   const int64_t stages = wgrad ? (longest + 63) / 64 : (K + (tr == 32 ? 127 : 63)) / (tr == 32 ? 128 : 64);
   const int64_t expected = wgrad ? tiles : active * ((mean + tr - 1) / tr) * n_ft;
   bool split = false;
+  int parts = 1;  // with the least estimate, as the kernel would choose for these rows
   if (tr != 256 && expected <= sms) {
     const int rows = (int)(wgrad ? K : mean);
     const int64_t whole = ge::grouped_split_ns(tr, expected, 1, (int)stages, sms, rows);
-    for (int s = 2; s <= 16; ++s)
-      split = split || (ge::grouped_split_allowed(expected, s, (int)stages, sms) &&
-                        ge::grouped_split_ns(tr, expected, s, (int)stages, sms, rows) + 2000 <= whole);
+    int64_t least = whole;
+    for (int s = 2; s <= 16; ++s) {
+      if (!ge::grouped_split_allowed(expected, s, (int)stages, sms)) continue;
+      const int64_t ns = ge::grouped_split_ns(tr, expected, s, (int)stages, sms, rows);
+      if (ns < least) {
+        least = ns;
+        parts = s;
+      }
+    }
+    split = least + 2000 <= whole;
   }
   if (const char* f = getenv("GEMM_EPI_FORCE_SPLIT")) {  // tuning override
     p->force_splits = atoi(f) > 0 ? atoi(f) : 0;
-    if (p->force_splits) split = tr != 256 && p->force_splits > 1;
+    if (p->force_splits) {
+      split = tr != 256 && p->force_splits > 1;
+      const int64_t room = sms / expected;
+      parts = p->force_splits < 16 ? p->force_splits : 16;
+      if (parts > room) parts = room > 1 ? (int)room : 1;
+    }
   }
+  p->split_k = split ? parts : 1;
   const auto pick = bf16 ? (w_nk ? ge_inst::grouped_bf16_nk : ge_inst::grouped_bf16_mn)
                          : (w_nk ? ge_inst::grouped_f16_nk : ge_inst::grouped_f16_mn);
   const ge_inst::GroupedInstance inst = pick(tr, (int)epilog, split);

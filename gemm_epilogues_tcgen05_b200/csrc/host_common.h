@@ -120,7 +120,6 @@ struct GroupedCfg {
   int threads = 0, stages = 0;
   int TR = 0, BK = 64;  // rows of a tile; k per stage
   bool pair = false;
-  int launches = 1;
   int E = 0 /* 0: no groups (kind 2) */, n_ft = 0, n_kt = 0, group = 1;
   int slices = 1;  // WGRAD: row slices of the optional bias gradient
 };
@@ -292,6 +291,7 @@ struct gemm_epi_plan_s {
   int force_splits = 0;    // GEMM_EPI_FORCE_SPLIT
   int split_items = 0;     // kind 1, one-CTA tiles: slots of the k split (sk_partials, sk_tickets)
   size_t split_bytes = 0;
+  int split_k = 1;         // kind 1: the parts of a tile where every expert has the mean number of rows
 };
 
 namespace ge_host {
