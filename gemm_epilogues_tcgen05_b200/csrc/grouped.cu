@@ -12,11 +12,15 @@ namespace {
 // rounds of tiles x time per tile. A tile of 64 k takes about 0.25 us on one
 // SM while all of them load (32-row tiles less when few are busy), 0.33 us on a
 // CTA pair. Measured (us, 32 / 128 / 256 rows): one expert of 1000 rows, K =
-// 4096, N = 256: 16.4 / 20.9 / 24.5; four of 100, K = 2048, N = 512: 11.2 /
-// 13.5 / 12.1; one of 3932, K = 192, N = 5824, DRELU_BGRAD: 338 / 45 / 28. WGRAD is
+// 4096, N = 256: 12.9 / 15.3 / 23.9; four of 100, K = 2048, N = 512: 9.2 /
+// 11.6 / 11.4; one of 3932, K = 192, N = 5824, DRELU_BGRAD: 334 / 47 / 27. WGRAD is
 // bound by its stores where experts are short: E = 32 of
-// 125 rows, K = 1024, N = 2048, fp32: 56.8 (128) and 60 (256); E = 8 of 1024,
-// K = 4096, N = 11008: 738 and 577; E = 6 of 3, K = 3320, N = 9336: 160 and 116.
+// 125 rows, K = 1024, N = 2048, fp32: 53.5 (128) and 53.8 (256); E = 8 of 1024,
+// K = 4096, N = 11008: 732 and 519; E = 6 of 3, K = 3320, N = 9336: 181 and 132.
+// What the mean cannot see: T = 8192 planned, 64 rows there (8 experts, K = 4096,
+// N = 11008): 110 us in the plan's 256-row tiles, 112 planned for 64; T = 4096
+// planned, 16 there (K = 2048, N = 512): 11.4 (128) and 9.8 (32). One expert of
+// 4033 rows beside 63 of one, K = 1024, N = 4096: 129 (128, chosen) and 111 (256).
 int choose_tr(int64_t E, int64_t T, int64_t N, int64_t K, int epilog, bool out_f32, int sms) {
   const bool wgrad = epilog == GEMM_EPI_WGRAD;
   if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override

@@ -65,8 +65,8 @@ void release(gemm_epi_plan_s* p) {
 
 // Rows per tile, as for grouped plans: rounds of tiles x (stages of 256 k x
 // time per stage + what a tile costs beside them). Measured (us, 128 / 256 rows):
-// T = 4096, N = 11008, K = 4096: 106 / 73; E = 16, T = 1003, N = 5000, K = 2048:
-// 20.8 / 23.8.
+// T = 4096, N = 11008, K = 4096: 137 / 74; E = 16, T = 1000, N = 5000, K = 2048:
+// 21.5 / 24.1; T = 4, N = 11008, K = 4096: 8.6 / 10.2.
 int choose_tr(int64_t groups, int64_t T, int64_t N, int64_t K, int sms) {
   if (const char* f = getenv("GEMM_EPI_FORCE_GROUPED")) {  // tuning override
     const int v = atoi(f);
