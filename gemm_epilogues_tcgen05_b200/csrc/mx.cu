@@ -8,6 +8,8 @@ using namespace ge_host;
 
 namespace {
 
+constexpr int64_t kMaxCols = (int64_t)1 << 22;  // of a row: a launch has a block row per scale tile
+
 int64_t row_tiles(int64_t rows, int64_t groups) {
   // groups: each may end in a part of a tile
   return groups > 0 ? rows / 128 + (groups < rows ? groups : rows) : (rows + 127) / 128;
@@ -15,11 +17,11 @@ int64_t row_tiles(int64_t rows, int64_t groups) {
 
 // the shape checks that quantisation and its inverse share
 int check_shape(const char* call, int64_t batch, int64_t rows, int64_t cols, gemm_epi_dtype dtype, int64_t groups) {
-  if (batch < 1 || rows < 1 || cols < 32 || cols % 32 != 0 || rows > (int64_t)1 << 30 || cols > (int64_t)1 << 22 ||
+  if (batch < 1 || rows < 1 || cols < 32 || cols % 32 != 0 || rows > (int64_t)1 << 30 || cols > kMaxCols ||
       batch > (int64_t)1 << 24 || batch * rows > (int64_t)1 << 36)
     return fail(GEMM_EPI_ERR_INVALID_ARG,
-                "%s: bad shape batch=%lld rows=%lld cols=%lld (need all >= 1, cols a multiple of 32)", call, (long long)batch,
-                (long long)rows, (long long)cols);
+                "%s: bad shape batch=%lld rows=%lld cols=%lld (need all >= 1, cols a multiple of 32 and at most %lld)", call,
+                (long long)batch, (long long)rows, (long long)cols, (long long)kMaxCols);
   if (dtype != GEMM_EPI_F16 && dtype != GEMM_EPI_BF16) return fail(GEMM_EPI_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
   if (groups < 0 || groups > ge::kMaxExperts || (groups > 0 && batch != 1))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "%s: bad number of groups %lld (0 to %d, with one matrix)", call,
@@ -99,13 +101,13 @@ gemm_epi_plan_t make_plan(int64_t E, int64_t T, int64_t N, int64_t K, gemm_epi_d
     fail(GEMM_EPI_ERR_INVALID_ARG, "bad number of experts %lld (need 0 to %d)", (long long)E, ge::kMaxExperts);
     return nullptr;
   }
-  if (T < 1 || N < 8 || K < 32 || (N % 8) != 0 || (K % 32) != 0) {
+  if (T < 1 || N < 8 || K < 32 || (N % 8) != 0 || (K % 32) != 0 || K > kMaxCols) {
     fail(GEMM_EPI_ERR_INVALID_ARG,
-         "bad shape T=%lld N=%lld K=%lld (need T>=1, N a multiple of 8, K a multiple of 32)", (long long)T, (long long)N,
-         (long long)K);
+         "bad shape T=%lld N=%lld K=%lld (need T>=1, N a multiple of 8, K a multiple of 32 and at most %lld)", (long long)T,
+         (long long)N, (long long)K, (long long)kMaxCols);
     return nullptr;
   }
-  if (T > (int64_t)1 << 30 || N > (int64_t)1 << 24 || K > (int64_t)1 << 24 || T * N > ((int64_t)1 << 40) ||
+  if (T > (int64_t)1 << 30 || N > (int64_t)1 << 24 || T * N > ((int64_t)1 << 40) ||
       K * N > ((int64_t)1 << 37)) {
     fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
     return nullptr;

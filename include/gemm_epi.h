@@ -412,7 +412,7 @@ GEMM_EPI_API int64_t gemm_epi_mx_scales_bytes(int64_t batch, int64_t rows, int64
  * gemm_epi_mx_quantize: `batch` matrices of rows x cols (dtype; row-major, or
  * cols x rows with GEMM_EPI_MX_TRANSPOSED, which needs rows a multiple of 8 and
  * no groups) to q (batch x rows x cols / 2 bytes) and scales. cols is a
- * multiple of 32. With groups > 0 (1 to 1024, batch 1) offsets are groups + 1
+ * multiple of 32, at most 2^22. With groups > 0 (1 to 1024, batch 1) offsets are groups + 1
  * int32 on the device, and rows of no group are not read or written. src, q,
  * scales 16-byte, offsets 4-byte aligned. Asynchronous on `stream`, one launch
  * on the current device, no workspace.
@@ -430,7 +430,7 @@ GEMM_EPI_API int gemm_epi_mx_dequantize(int64_t batch, int64_t rows, int64_t col
 /*
  * gemm_epi_mx_plan: Y = epilog(X . W^T) of microscaled operands, X T x K and W
  * N x K, accumulated in fp32. E = 0: one weight; E = 1 to 1024: grouped by
- * expert, as gemm_epi_grouped_plan. K a multiple of 32, N of 8; epilog BIAS,
+ * expert, as gemm_epi_grouped_plan. K a multiple of 32, at most 2^22, N of 8; epilog BIAS,
  * RELU_BIAS, GELU_BIAS or NONE; dtype is Y's and the bias's; flags
  * GEMM_EPI_FLAG_OUT_F32 or 0. gemm_epi_free, _query, _status and _set_bias_f32
  * take the plan too.
