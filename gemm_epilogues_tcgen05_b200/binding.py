@@ -7,7 +7,6 @@ kernels; if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -153,19 +152,21 @@ def _on_stream(stream, device):
     """The stream that a call will use, as the current one: outputs that a
     convenience allocates belong to it. (Memory from another stream's pool may
     still be read or written by work that waits on that stream.)"""
-    if stream is None:
-        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
     return torch.cuda.stream(stream)
 
 
 def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with _on_stream(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _zeros(shape, dtype, device, stream):
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
     with _on_stream(stream, device):
         return torch.zeros(shape, dtype=dtype, device=device)
 
@@ -538,7 +539,8 @@ def gemm_epi_mx_dequantize(q, scales, out, offsets=None, stream=None):
 
 
 def mx_quantize(src, offsets=None, transposed=False, stream=None):
-    """gemm_epi_mx_quantize with allocated outputs: (q, scales)."""
+    """gemm_epi_mx_quantize with allocated outputs, cleared first: (q, scales).
+    A loop that keeps its buffers calls gemm_epi_mx_quantize itself."""
     rows, cols = (src.shape[-1], src.shape[-2]) if transposed else src.shape[-2:]
     q = _zeros((*src.shape[:-2], rows, cols // 2), torch.uint8, src.device, stream)
     n = mx_scales_bytes(rows, cols, src.shape[0] if src.dim() == 3 else 1, None if offsets is None else offsets.numel() - 1)
