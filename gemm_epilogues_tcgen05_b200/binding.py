@@ -153,7 +153,9 @@ def _on_stream(stream, device):
     convenience allocates belong to it. (Memory from another stream's pool may
     still be read or written by work that waits on that stream.)"""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+        handle = _stream_ptr(stream)
+        # (ExternalStream takes 0 for no handle at all, and gives a new stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 

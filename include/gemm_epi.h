@@ -130,7 +130,7 @@ typedef struct {
   int tile_m, tile_n, tile_k, stages;
   int split_k;         /* K slices per output tile (1 = none). Grouped plans: for experts of the mean
                           number of rows; a call that finds others may share a tile among fewer or
-                          more CTAs (at most 16), a plan that reports 1 never does */
+                          more CTAs (at most 16) */
   int grid;            /* CTAs launched by the main kernel */
   int launches;        /* kernel launches per execute call (a WGRAD call with dbias: 2 more, grouped 1 more) */
   int num_sms;

@@ -13,7 +13,7 @@ import ctypes
 import pytest
 import torch
 
-from gemm_epilogues_tcgen05_b200 import GroupedPlan, MxPlan, Plan, mx_quantize
+from gemm_epilogues_tcgen05_b200 import GroupedPlan, MxPlan, Plan, binding, mx_quantize
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -124,6 +124,21 @@ def test_microscaled():
             Y = p.forward(xq, xs, wq, ws, None, stream=s)
             torch.cuda.synchronize()
             assert torch.equal(Y.double(), x.double() @ w.double().t())
+
+
+def test_handle_zero_is_the_legacy_stream():
+    """The outputs of a call on stream handle 0 belong to the legacy stream, which that handle means."""
+    X, W = ints((T, K), 1), ints((1, K, N), 2)
+    offsets = torch.tensor([0, T - 9], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with binding._on_stream(0, X.device):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        with GroupedPlan(1, T, N, K, BF, "NONE") as p:
+            torch.cuda._sleep(100_000_000)
+            Y, _ = p.forward(X, W, None, offsets, stream=0)
+            torch.cuda.synchronize()
+    assert torch.equal(Y[:T - 9], (X[:T - 9].double() @ W[0].double()).to(BF)) and not bool(Y[T - 9:].any())
 
 
 def dirty_small_blocks():
