@@ -33,7 +33,10 @@ EXPORTED = ["gemm_epi_plan", "gemm_epi_execute", "drelu_bgrad_execute", "gemm_ep
             "drelu_bgrad_execute_noalloc", "gemm_epi_wgrad_execute", "gemm_epi_set_bias_f32", "gemm_epi_plan_ex",
             "gemm_epi_grouped_plan", "gemm_epi_grouped_execute", "gemm_epi_grouped_drelu_bgrad_execute",
             "gemm_epi_grouped_wgrad_execute", "gemm_epi_mx_scales_bytes", "gemm_epi_mx_quantize",
-            "gemm_epi_mx_dequantize", "gemm_epi_mx_plan", "gemm_epi_mx_execute"]
+            "gemm_epi_mx_dequantize", "gemm_epi_mx_plan", "gemm_epi_mx_execute", "gemm_epi_gated_plan",
+            "gemm_epi_gated_execute", "gemm_epi_dgated_execute"]
+GATED_EPILOGS = {"GATED": 8, "DGATED": 9, "GATED_AUX": 10}  # gemm_epi_gated_epilog
+ACTS = {"SILU": 0, "GELU": 1, "RELU": 2}  # gemm_epi_act
 MX_TRANSPOSED = 1  # GEMM_EPI_MX_TRANSPOSED
 FLAG_W_NK = 1  # GEMM_EPI_FLAG_W_NK
 FLAG_OUT_F32 = 2  # GEMM_EPI_FLAG_OUT_F32
@@ -113,6 +116,12 @@ def lib() -> ctypes.CDLL:
         L.gemm_epi_mx_plan.argtypes = [i64, i64, i64, i64, ci, ci, ctypes.c_uint32]
         L.gemm_epi_mx_execute.restype = ci
         L.gemm_epi_mx_execute.argtypes = [vp] * 9
+        L.gemm_epi_gated_plan.restype = vp
+        L.gemm_epi_gated_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.c_uint32]
+        L.gemm_epi_gated_execute.restype = ci
+        L.gemm_epi_gated_execute.argtypes = [vp] * 7
+        L.gemm_epi_dgated_execute.restype = ci
+        L.gemm_epi_dgated_execute.argtypes = [vp] * 7
         _lib = L
     return _lib
 
@@ -582,3 +591,58 @@ class MxPlan(_DevicePlan):
         Y = _zeros((self.T, self.N), self.out_dtype, Xq.device, stream)
         self.gemm_epi_mx_execute(Xq, Xs, Wq, Ws, bias, Y, offsets, stream)
         return Y
+
+
+class GatedPlan(_DevicePlan):
+    """A plan for a gated layer: Z = X . W + bias (2N columns, the gate's first),
+    H = act(Z[:, :N]) * Z[:, N:], with act "SILU", "GELU" or "RELU".
+
+    epilog "GATED": H. "GATED_AUX": H and Z (T x 2N, 16-bit), which the backward
+    reads. "DGATED": dZ (T x 2N) from dY (T x K), W2 (K x N) and Z, and the bias
+    gradient (2N). W is K x 2N (``w_nk``: 2N x K; W2: N x K); ``out_f32``: H or dZ
+    is fp32. bias may be None. Tensors must be on the device that was current
+    when the plan was made; the default stream is that device's current one."""
+
+    def __init__(self, T: int, N: int, K: int, dtype: torch.dtype, epilog: str = "GATED", act: str = "SILU",
+                 w_nk: bool = False, out_f32: bool = False):
+        self.T, self.N, self.K = T, N, K
+        self.out_dtype = torch.float32 if out_f32 else dtype
+        self.dtype = self.bias_dtype = dtype
+        self.epilog = GATED_EPILOGS[epilog] if isinstance(epilog, str) else epilog
+        cols = N if self.epilog == GATED_EPILOGS["DGATED"] else 2 * N
+        self.w_shape = (cols, K) if w_nk else (K, cols)
+        self._shapes = ((T, K), (T, N), (T, 2 * N), (2 * N,))
+        self._own(lib().gemm_epi_gated_plan(T, N, K, DTYPES[dtype], self.epilog, ACTS[act] if isinstance(act, str) else act,
+                                            (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0)))
+
+    def aux_spec(self):
+        return (self._shapes[2], self.dtype) if self.epilog == GATED_EPILOGS["GATED_AUX"] else None
+
+    def gemm_epi_gated_execute(self, X, W, bias, H, aux=None, stream=None):
+        i, dt, (xs, hs, zs, bs) = self.index, self.dtype, self._shapes
+        _check(lib().gemm_epi_gated_execute(
+            self.handle, _ptr_on(i, X, xs, dt, "X"), _ptr_on(i, W, self.w_shape, dt, "W"),
+            None if bias is None else _ptr_on(i, bias, bs, self.bias_dtype, "bias"),
+            _ptr_on(i, H, hs, self.out_dtype, "H"), None if aux is None else _ptr_on(i, aux, zs, dt, "aux"),
+            self._s(stream)))
+
+    def gemm_epi_dgated_execute(self, dY, W2, aux, dZ, dbias=None, stream=None):
+        i, dt, (xs, _, zs, bs) = self.index, self.dtype, self._shapes
+        _check(lib().gemm_epi_dgated_execute(
+            self.handle, _ptr_on(i, dY, xs, dt, "dY"), _ptr_on(i, W2, self.w_shape, dt, "W2"),
+            _ptr_on(i, aux, zs, dt, "aux"), _ptr_on(i, dZ, zs, self.out_dtype, "dZ"),
+            None if dbias is None else _ptr_on(i, dbias, bs, torch.float32, "dbias"), self._s(stream)))
+
+    # conveniences that allocate their outputs on the call's stream
+    def forward(self, X, W, bias=None, stream=None):
+        H = _empty((self.T, self.N), self.out_dtype, X.device, stream)
+        spec = self.aux_spec()
+        aux = _empty(*spec, X.device, stream) if spec else None
+        self.gemm_epi_gated_execute(X, W, bias, H, aux, stream)
+        return H, aux
+
+    def backward(self, dY, W2, aux, with_dbias=False, stream=None):
+        dZ = _empty((self.T, 2 * self.N), self.out_dtype, dY.device, stream)
+        dbias = _empty((2 * self.N,), torch.float32, dY.device, stream) if with_dbias else None
+        self.gemm_epi_dgated_execute(dY, W2, aux, dZ, dbias, stream)
+        return (dZ, dbias) if with_dbias else dZ

@@ -250,7 +250,7 @@ class DeviceScope {
 }  // namespace ge_host
 
 struct gemm_epi_plan_s {
-  int kind = 0;      // 0: one product; 1: products grouped by expert (grouped.cu); 2: microscaled (mx.cu)
+  int kind = 0;      // 0: one product; 1: products grouped by expert (grouped.cu); 2: microscaled (mx.cu); 3: gated (gated.cu)
   int64_t T, N, K;   // the kernels' rows, columns and contraction length
   int64_t uT, uK;    // the caller's T and K (WGRAD: rows = uK, contraction = uT)
   int dtype, epilog;
@@ -279,6 +279,7 @@ struct gemm_epi_plan_s {
   int bias_f32 = 0;      // gemm_epi_set_bias_f32: the forward bias is fp32
   int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
   int out_f32 = 0;       // GEMM_EPI_FLAG_OUT_F32: Y / dZ / dW written as fp32
+  int act = 0;           // kind 3: gemm_epi_act
   int cache_hints = 0;   // few-row kernel: L2 eviction policies on the operand loads (GEMM_EPI_CACHE_HINTS)
   // tensor-map cache
   const void* a_ptr = nullptr;
@@ -299,7 +300,7 @@ struct gemm_epi_plan_s {
   CUtensorMap tmWs;  // the weight operand with a 64·KPS-row box
   ge_host::GroupedCfg gr;  // kind 1 and 2
   int force_splits = 0;    // GEMM_EPI_FORCE_SPLIT
-  int split_items = 0;     // kind 1, one-CTA tiles: slots of the k split (sk_partials, sk_tickets)
+  int split_items = 0;     // counters in sk_tickets (kind 1, one-CTA tiles: slots of the k split)
   size_t split_bytes = 0;
   int split_k = 1;         // kind 1: the parts of a tile where every expert has the mean number of rows
 };
@@ -327,7 +328,7 @@ inline gemm_epi_plan_s* lookup_kind(gemm_epi_plan_t plan, int kind, const char* 
   if (!p) {
     *code = fail(GEMM_EPI_ERR_INVALID_ARG, "%s: unknown plan", call);
   } else if (p->kind != kind) {
-    const char* what[] = {"of one product", "of products grouped by expert", "of a microscaled product"};
+    const char* what[] = {"of one product", "of products grouped by expert", "of a microscaled product", "of a gated layer"};
     *code = fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "%s called on a plan %s", call, what[p->kind]);
     p = nullptr;
   }

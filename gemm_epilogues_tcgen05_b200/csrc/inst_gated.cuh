@@ -1,0 +1,45 @@
+// inst_gated.cuh -- kernel instances of gated layers for one operand type and
+// weight layout (included by inst_gated_*.cu).
+#pragma once
+
+#include "kernel_table.h"
+#include "skinny_kernel.cuh"
+#include "tile2_kernel.cuh"
+
+namespace ge_inst {
+
+template <int BN, int ST, int EPI, bool BF, bool BK>
+GatedInstance gated_tile() {
+  static_assert(ge::TileSmem<BN, ST, ge::StageBlocks<EPI, BN, false>::value>::BYTES <= 232448, "above the per-CTA limit");
+  return {ge::tile_kernel<BN, ST, EPI, BF, BK>, ge::TileSmem<BN, ST, ge::StageBlocks<EPI, BN, false>::value>::BYTES, ge::kThreads, ST};
+}
+
+template <bool BF, bool BK>
+GatedInstance gated_any(int bn, bool pair, int epi) {
+  constexpr int F = ge::EPI_GATED, B = ge::EPI_DGATED;
+  if (pair) {
+    constexpr uint32_t smem = ge::Tile2Smem<256, 5, 8, ge::StageBlocks<F, 256, true>::value>::BYTES;
+    static_assert(smem <= 232448, "above the per-CTA limit");
+    return {epi == F ? ge::tile2_kernel<256, 5, F, BF, BK> : ge::tile2_kernel<256, 5, B, BF, BK>, smem, 64 + 32 * 8, 5};
+  }
+  if (bn == 256) return epi == F ? gated_tile<256, 4, F, BF, BK>() : gated_tile<256, 4, B, BF, BK>();
+  if (bn == 128) return epi == F ? gated_tile<128, 6, F, BF, BK>() : gated_tile<128, 6, B, BF, BK>();
+  if (bn == 64 && epi == B) return gated_tile<64, 8, B, BF, BK>();
+  return {};
+}
+
+template <int TP, bool BF, bool BK>
+GatedSkinnyInstance gated_skinny_tp() {
+  using L = ge::SkinnySmem<TP, 2, true>;
+  return {ge::skinny_kernel<TP, 2, ge::EPI_GATED, BF, BK>, L::BYTES, L::STAGES};
+}
+
+template <bool BF, bool BK>
+GatedSkinnyInstance gated_skinny_any(int tp) {
+  return tp == 16   ? gated_skinny_tp<16, BF, BK>()
+         : tp == 32 ? gated_skinny_tp<32, BF, BK>()
+         : tp == 64 ? gated_skinny_tp<64, BF, BK>()
+                    : gated_skinny_tp<128, BF, BK>();
+}
+
+}  // namespace ge_inst

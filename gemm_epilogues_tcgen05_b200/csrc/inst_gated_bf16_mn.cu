@@ -1,0 +1,7 @@
+// inst_gated_bf16_mn.cu -- gated layers, bf16 operands, K x N weight.
+#include "inst_gated.cuh"
+
+namespace ge_inst {
+GatedInstance gated_bf16_mn(int bn, bool pair, int epi) { return gated_any<true, false>(bn, pair, epi); }
+GatedSkinnyInstance gated_skinny_bf16_mn(int tp) { return gated_skinny_any<true, false>(tp); }
+}  // namespace ge_inst

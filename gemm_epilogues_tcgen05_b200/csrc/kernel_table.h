@@ -66,4 +66,28 @@ struct MxInstance {
 };
 MxInstance mx_any(int tr, int epi, bool bf16, bool f32);  // f32: fp32 output
 
+// Gated layers: EPI_GATED on tiles of bn = 128 or 256 accumulator columns (one
+// CTA) or 256 (CTA pair), EPI_DGATED also on 64; _nk: the weight is N x K.
+struct GatedInstance {
+  TileKernelFn fn;
+  uint32_t smem;
+  int threads, stages;
+};
+GatedInstance gated_f16_mn(int bn, bool pair, int epi);
+GatedInstance gated_f16_nk(int bn, bool pair, int epi);
+GatedInstance gated_bf16_mn(int bn, bool pair, int epi);
+GatedInstance gated_bf16_nk(int bn, bool pair, int epi);
+
+// The few-row kernel for EPI_GATED: tp = 16, 32, 64 or 128 padded rows, two
+// k-blocks a stage.
+struct GatedSkinnyInstance {
+  SkinnyKernelFn fn;
+  uint32_t smem;
+  int stages;
+};
+GatedSkinnyInstance gated_skinny_f16_mn(int tp);
+GatedSkinnyInstance gated_skinny_f16_nk(int tp);
+GatedSkinnyInstance gated_skinny_bf16_mn(int tp);
+GatedSkinnyInstance gated_skinny_bf16_nk(int tp);
+
 }  // namespace ge_inst

@@ -43,6 +43,7 @@ struct SkinnyParams {
   int32_t out_f32;                 // the output is fp32 (else the 16-bit type)
   int32_t cache_hints;             // W streamed once: evict_first; X read by every CTA: evict_last
   int32_t inject_stall;            // fault injection for tests: withhold the first segment's tfull commit
+  int32_t act;                     // gated layers: an ActKind
 };
 
 // A stage holds KPS consecutive 64-deep k-blocks: W as one box of 64 features
@@ -50,7 +51,12 @@ struct SkinnyParams {
 // Stages of 32 KB or more kept one SM's TMA stream up to 1.5x faster than
 // 16 KB stages with the same bytes in flight (a load-only stream of W, 4096 x
 // 11008, over 86 CTAs).
-template <int TP, int KPS>
+//
+// GATED (a gated layer's forward): the 128 lanes are the gate's pre-activations
+// of 64 features and the up projection's of the same 64, one 64-feature chunk of
+// A from each half of the weight. The epilogue warps of the two halves exchange
+// through shared memory (XCHG), 16 rows at a time, and each finishes 8 of them.
+template <int TP, int KPS, bool GATED = false>
 struct SkinnySmem {
   static constexpr int BK = kBK * KPS;                 // k per stage
   static constexpr uint32_t A_CHUNK = 64 * BK * 2;     // one 64-feature chunk x BK k-rows
@@ -59,13 +65,15 @@ struct SkinnySmem {
   static constexpr uint32_t B_SUB = TP * kBK * 2;      // TP rows x 128 B (one 64-k block of X)
   static constexpr uint32_t B_BYTES = KPS * B_SUB;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = (230400 / STAGE) > 12 ? 12 : (230400 / STAGE);
+  static constexpr uint32_t XCHG = GATED ? 2 * 16 * 64 * 4 : 0;
+  static constexpr int STAGES = ((230400 - XCHG) / STAGE) > 12 ? 12 : ((230400 - XCHG) / STAGE);
   static constexpr uint32_t OFF_A = 0;
   static constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_B + STAGES * B_BYTES;
   static constexpr uint32_t N_BARS = 2 * STAGES + 5;
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;  // tmem slot, abort flag, last flag
-  static constexpr uint32_t END = OFF_MISC + 16;
+  static constexpr uint32_t OFF_XCHG = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr uint32_t END = OFF_XCHG + XCHG;
   static constexpr uint32_t BYTES = END + 1024;
   static_assert(STAGES >= 2, "few-row stage too large");
   static_assert(BYTES <= 232448, "few-row shared memory above the per-CTA limit");
@@ -222,13 +230,51 @@ __device__ __forceinline__ void skinny_finish16(const SkinnyParams& p, float (&v
   }
 }
 
+// GATED: 16 rows t0 .. t0 + 15 of this thread's pre-activation (v, the bias not
+// yet added) -- feature n of half `half` (0: the gate). Rows 8 (1 - half) .. + 7 go to the
+// thread of the other half through xchg ([16][64] floats), the other 8 are
+// finished here. Called by the 128 epilogue threads alike; `turn` picks one of
+// two buffers, so that one barrier a call is enough (a buffer is written again
+// only after the barrier of the call between, which its readers have passed).
+template <bool BF16>
+__device__ __forceinline__ void skinny_gated16(const SkinnyParams& p, float (&v)[16], int t0, int n, bool n_ok, int half,
+                                               float bias_n, float* xchg, uint32_t& turn) {
+  float* buf = xchg + (turn & 1u) * (16 * 64) + (n & 63);
+  turn ^= 1u;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    v[j] += bias_n;
+    const int t = t0 + j;
+    if (p.aux_out && n_ok && t < p.T)
+      store_16<BF16>(p.aux_out, (static_cast<int64_t>(t) * 2 + half) * p.N + n, v[j]);
+  }
+  // (static indices: v stays in registers)
+#pragma unroll
+  for (int j = 0; j < 8; ++j) buf[(half ? j : 8 + j) * 64] = half ? v[j] : v[8 + j];
+  named_bar_sync(2, 128);
+  float g[8], u[8], none[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float mine = half ? v[8 + j] : v[j], other = buf[(half ? 8 + j : j) * 64];
+    g[j] = half ? other : mine;
+    u[j] = half ? mine : other;
+  }
+  act_values<8, false>(p.act, g, g, none);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int t = t0 + 8 * half + j;
+    if (n_ok && t < p.T) store_out<BF16, 2>(p, static_cast<int64_t>(t) * p.N + n, g[j] * u[j]);
+  }
+}
+
 // Sum the segments' partials of one tile, 32 rows at a time, in segment
 // order, and finish those rows. With S > 0 the segment loop is unrolled so
 // that all S x 32 loads of a batch are in flight together (the reads are
 // L2 round trips; issued one by one they would dominate the kernel).
 template <int S, int TP, int EPI, bool BF16>
 __device__ __forceinline__ void skinny_fixup(const SkinnyParams& p, const float* base, int nsegs, int n, bool n_ok,
-                                             int word, float bias_n, float& dbias_acc) {
+                                             int word, float bias_n, float& dbias_acc, int half, float* xchg,
+                                             uint32_t& turn) {
   constexpr int SEG = TP * 128;
   constexpr int RB = TP < 32 ? TP : 32;  // rows per batch
 #pragma unroll 1
@@ -266,20 +312,28 @@ __device__ __forceinline__ void skinny_fixup(const SkinnyParams& p, const float*
       float w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = v[h * 16 + j];
-      skinny_finish16_rows<EPI, BF16, 2, false>(p, w, t0 + h * 16, n, n_ok, word, bias_n, dbias_acc, mk[h]);
+      if constexpr (EPI == EPI_GATED)
+        skinny_gated16<BF16>(p, w, t0 + h * 16, n, n_ok, half, bias_n, xchg, turn);
+      else
+        skinny_finish16_rows<EPI, BF16, 2, false>(p, w, t0 + h * 16, n, n_ok, word, bias_n, dbias_acc, mk[h]);
     }
   }
 }
 
-template <int TP, int KPS, int EPI, bool BF16>
+// BK (gated layers only): the weight is given N x K, its chunks of 64 features
+// are staged K-major, one box of 64 k each.
+template <int TP, int KPS, int EPI, bool BF16, bool BK = false>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const SkinnyParams p) {
-  using L = SkinnySmem<TP, KPS>;
+  constexpr bool GATED = EPI == EPI_GATED;
+  using L = SkinnySmem<TP, KPS, GATED>;
   constexpr int STAGES = L::STAGES;
+  constexpr int TN = GATED ? 64 : 128;  // output features of a tile
+  static_assert(GATED || !BK, "N x K weights: gated layers only");
   static_assert(TP == 16 || TP == 32 || TP == 64 || TP == 128 || TP == 256, "TP must be a power of two in [16, 256]");
   constexpr uint32_t TMEM_COLS = 2 * TP < 32 ? 32 : 2 * TP;
-  constexpr uint32_t IDESC = idesc_f16(BF16, /*A MN-major*/ true, /*B MN-major*/ false, 128, TP);
+  constexpr uint32_t IDESC = idesc_f16(BF16, /*A MN-major*/ !BK, /*B MN-major*/ false, 128, TP);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -330,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (GATED) wait_for_inputs();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -352,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t gk = lo;  // global k-block index of the next load
       const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
       while (ok && skinny_segment(p, hi, g, s)) {
-        const int n0 = s.tile * 128;
+        const int n0 = s.tile * TN;
+        const int n1 = GATED ? p.N + n0 : n0 + 64;  // the second chunk of 64 features
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++it, ++gk) {
           if (p.prefetch > 0) prefetch_upto(gk + static_cast<uint32_t>(p.prefetch));
           const uint32_t st = it % STAGES;
@@ -362,15 +418,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[st], L::STAGE);
-          if (p.cache_hints) {
+          if constexpr (BK) {  // per 64 k: 64 features of the gate, then 64 of the up projection, 8 KB each
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) {
+              uint8_t* a = sA + st * L::A_BYTES + j * 2 * L::A_SUB;
+              tma_load_2d_hint(a, &tmW, &full[st], kb * L::BK + j * kBK, n0, pol_w);
+              tma_load_2d_hint(a + L::A_SUB, &tmW, &full[st], kb * L::BK + j * kBK, n1, pol_w);
+              tma_load_2d_hint(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0, pol_x);
+            }
+          } else if (p.cache_hints) {
             tma_load_2d_hint(sA + st * L::A_BYTES, &tmW, &full[st], n0, kb * L::BK, pol_w);
-            tma_load_2d_hint(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n0 + 64, kb * L::BK, pol_w);
+            tma_load_2d_hint(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n1, kb * L::BK, pol_w);
 #pragma unroll
             for (int j = 0; j < KPS; ++j)
               tma_load_2d_hint(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0, pol_x);
           } else {
             tma_load_2d(sA + st * L::A_BYTES, &tmW, &full[st], n0, kb * L::BK);
-            tma_load_2d(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n0 + 64, kb * L::BK);
+            tma_load_2d(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n1, kb * L::BK);
 #pragma unroll
             for (int j = 0; j < KPS; ++j)
               tma_load_2d(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0);
@@ -411,7 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
               // A = W^T: feature-major, 64-feature chunks A_CHUNK apart (LBO), 8 k-rows 1 KB apart (SBO)
-              const uint64_t adesc = smem_desc_sw128(a0 + j * L::A_SUB + kk * 2048, L::A_CHUNK, 1024);
+              // (BK: K-major 128-byte rows, 8-feature groups 1 KB apart, 128 features per 64 k)
+              const uint64_t adesc = BK ? smem_desc_sw128(a0 + j * 2 * L::A_SUB + kk * 32, 16, 1024)
+                                        : smem_desc_sw128(a0 + j * L::A_SUB + kk * 2048, L::A_CHUNK, 1024);
               // B = X: K-major 128-byte rows, 8-row groups 1 KB apart, one TP-row block per 64 k
               const uint64_t bdesc = smem_desc_sw128(b0 + j * L::B_SUB + kk * 32, 16, 1024);
               umma_f16(d_tmem, adesc, bdesc, IDESC, (kb > s.kb0 || j > 0 || kk > 0) ? 1u : 0u);
@@ -431,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const uint32_t ew = warp & 3u;
     const uint32_t et = threadIdx.x - 64;
+    float* xchg = reinterpret_cast<float*>(smem + L::OFF_XCHG);  // GATED
+    uint32_t turn = 0;
     uint32_t scount = 0;
     bool ok = true;
     uint32_t g = lo;
@@ -440,13 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tph = (scount >> 1) & 1u;
       ++scount;
       const int n_local = static_cast<int>(ew * 32 + lane);
-      const int n = s.tile * 128 + n_local;
+      const int half = GATED ? n_local >> 6 : 0;  // 1: the up projection
+      const int n = s.tile * TN + (GATED ? n_local & 63 : n_local);
       const bool n_ok = n < p.N;
       const bool warp_ok = __all_sync(0xffffffffu, n_ok);  // all 32 features of this warp in range
       const int word = (s.tile * 128 + static_cast<int>(ew) * 32) >> 5;
       float bias_n = 0.f;
       if constexpr (AddsBias<EPI>::value)
         bias_n = n_ok ? load_bias<BF16>(p.bias, p.bias_f32, n) : 0.f;
+      if constexpr (GATED)
+        if (p.bias && n_ok) bias_n = load_bias<BF16>(p.bias, p.bias_f32, static_cast<int64_t>(half) * p.N + n);
       float dbias_acc = 0.f;
       const bool whole = s.kb0 == 0 && s.kb1 == p.kbt;
       // DRELU_BGRAD, whole tile: every mask word the tile needs, loaded before
@@ -465,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       if (ok) ok = wait_bounded(&tfull[buf], tph, wp, abort_flag, 6);
       ok = __all_sync(0xffffffffu, ok);
+      if constexpr (GATED) ok = named_bar_and(2, 128, ok);  // the rows' exchange needs all four warps
       const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TP;
       float* slot = p.partials + (static_cast<int64_t>(s.tile) * p.max_segs + s.seg) * (TP * 128);
       if (ok) {
@@ -487,7 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-          if (whole) {
+          if (GATED && whole) {
+            skinny_gated16<BF16>(p, v, c * 16, n, n_ok, half, bias_n, xchg, turn);
+          } else if (whole) {
             skinny_finish16<EPI, BF16, (TP > 16)>(p, v, c * 16, n, n_ok, warp_ok, word, bias_n, dbias_acc, mk);
           } else if (TP > 16 && c * 16 + 16 <= p.T) {
 #pragma unroll
@@ -524,10 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
           const float* base = p.partials + static_cast<int64_t>(s.tile) * p.max_segs * (TP * 128) + n_local;
           switch (s.nsegs) {
-            case 2: skinny_fixup<2, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
-            case 3: skinny_fixup<3, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
-            case 4: skinny_fixup<4, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
-            default: skinny_fixup<0, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
+            case 2: skinny_fixup<2, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
+            case 3: skinny_fixup<3, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
+            case 4: skinny_fixup<4, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
+            default: skinny_fixup<0, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
           }
           if constexpr (EPI == EPI_DRELU_BGRAD)
             if (n_ok) p.dbias[n] = dbias_acc;

@@ -45,7 +45,7 @@
 namespace ge {
 
 // Epilogue warps of the pair kernel: one per TMEM lane quarter, or two for
-// the GELU epilogs (each with half of a tile's columns). A warp reaches only
+// the GELU epilogs and gated layers (each with half of a tile's columns). A warp reaches only
 // its own quarter of the TMEM lanes, so the four quarters sit on the four
 // SM sub-partitions, one warp each; with one warp per sub-partition a GELU
 // epilogue (erff per element, a chain of dependent operations) ran about
@@ -54,10 +54,10 @@ namespace ge {
 // four (their partial slots are laid out per quarter).
 template <int EPI, bool SPLIT>
 struct PairEpiWarps {
-  static constexpr int value = AppliesGelu<EPI>::value && !SPLIT ? 8 : 4;
+  static constexpr int value = (AppliesGelu<EPI>::value || IsGated<EPI>::value) && !SPLIT ? 8 : 4;
 };
 
-template <int BN, int STAGES, int EW = 4>
+template <int BN, int STAGES, int EW = 4, int BLOCKS = 2>
 struct Tile2Smem {
   static constexpr uint32_t A_BYTES = kBM * kBK * 2;          // this CTA's 128 rows x 64 k
   static constexpr uint32_t B_CHUNK = kBK * 64 * 2;           // 64 k x 64 n
@@ -70,8 +70,8 @@ struct Tile2Smem {
   static constexpr uint32_t OFF_BIAS = (OFF_MISC + 24 + 15) / 16 * 16;
   static constexpr uint32_t OFF_COLP = OFF_BIAS + 2 * BN * 4;
   static constexpr uint32_t OFF_STG = (OFF_COLP + 2 * 4 * BN * 4 + 1023) / 1024 * 1024;
-  static constexpr uint32_t OFF_AUXSTG = OFF_STG + kStageBytesPerWarp * EW;
-  static constexpr uint32_t END = OFF_AUXSTG + kAuxStageBytesPerWarp * EW;
+  static constexpr uint32_t OFF_AUXSTG = OFF_STG + BLOCKS * 2048 * EW;
+  static constexpr uint32_t END = OFF_AUXSTG + (BLOCKS == 2 ? kAuxStageBytesPerWarp * EW : 0);
   static constexpr uint32_t BYTES = END + 1024;
 };
 
@@ -213,7 +213,11 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
                  const TileParams p) {
   constexpr int EW = PairEpiWarps<EPI, SPLIT>::value;  // epilogue warps
   constexpr int ET = 32 * EW;                          // epilogue threads
-  using L = Tile2Smem<BN, STAGES, EW>;
+  constexpr int SB = StageBlocks<EPI, BN, true>::value;
+  using L = Tile2Smem<BN, STAGES, EW, SB>;
+  constexpr bool GATED = EPI == EPI_GATED;  // rank 0 loads the gate's weight, rank 1 the up projection's
+  static_assert(!(SPLIT && IsGated<EPI>::value), "gated layers run on whole tiles");
+  constexpr int BNO = GATED ? BN / 2 : BN;  // output columns of a tile
   static_assert(BN == 128 || BN == 256, "the pair kernel splits BN in 64-column chunks per CTA");
   constexpr uint32_t TMEM_COLS = 2 * BN;
   static_assert(BN == 256, "the tail split halves 256-column tiles");
@@ -279,6 +283,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
   cluster_sync();  // both CTAs' barriers exist before either side signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (IsGated<EPI>::value) wait_for_inputs();
   const int m2_tiles = (p.m_tiles + 1) / 2;  // 256-row tiles
   // half units would need a 64-row box of a K-major W: with BK every unit is a whole tile
   TileParams pw = p;
@@ -296,7 +301,8 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         const int m0 = w.mb * 2 * kBM + static_cast<int>(rank) * kBM;
         // this CTA's columns: half of the tile (two 64-wide chunks), or half of a half (one chunk)
         const int nchunks = w.half < 0 ? BN / 128 : 1;
-        const int nh0 = w.nb * BN + (w.half < 0 ? 0 : w.half * (BN / 2)) + static_cast<int>(rank) * nchunks * 64;
+        const int nh0 = GATED ? w.nb * BNO + (w.half < 0 ? 0 : w.half * (BNO / 2)) + static_cast<int>(rank) * p.N
+                              : w.nb * BN + (w.half < 0 ? 0 : w.half * (BN / 2)) + static_cast<int>(rank) * nchunks * 64;
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     const uint32_t ew = warp & 3u;             // TMEM lane quarter
     const uint32_t eh = (warp - 2u) >> 2;      // column half (EW == 8), else 0
     const uint32_t et = threadIdx.x - 64;      // 0 .. ET - 1
-    uint8_t* stg = stg_s + (warp - 2u) * kStageBytesPerWarp;
+    uint8_t* stg = stg_s + (warp - 2u) * (SB * 2048);
     uint32_t scount = 0;
     uint32_t tcount = 0;
     bool ok = true;
@@ -386,13 +392,17 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     for (; work.next(w); ++tcount) {
       const int prow = w.mb * 2 + static_cast<int>(rank);  // this CTA's 128-row block
       const int m0 = prow * kBM;
-      const int n0 = w.nb * BN + (w.half < 0 ? 0 : w.half * (BN / 2));
-      const int ncols = w.half < 0 ? BN : BN / 2;
+      const int n0 = w.nb * BNO + (w.half < 0 ? 0 : w.half * (BNO / 2));
+      const int ncols = w.half < 0 ? BNO : BNO / 2;
       const uint32_t buf = tcount & 1u;
       const uint32_t tph = (tcount >> 1) & 1u;
       float* bs = bias_s + buf * BN;
       float* cp = colp_s + buf * 4 * BN;
       epi_stage_bias<BN, EPI, BF16, ET>(p, n0, bs, et, ncols);
+      if constexpr (GATED) gated_stage_bias<BN, BF16, ET>(p, n0, bs, et, ncols);
+      DGatedInput gin{};
+      if constexpr (EPI == EPI_DGATED)
+        gin = dgated_load(p, m0 + static_cast<int>(ew * 32 + lane), n0 + static_cast<int>(eh) * (ncols / 2));
       MaskWords<BN> mw{};
       if constexpr (EPI == EPI_DRELU_BGRAD) mw = load_mask_words<BN>(p, m0 + static_cast<int>(ew * 32 + lane), n0);
       named_bar_sync(1, ET);
@@ -499,7 +509,15 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
       }
       if (ok) {
         tc_fence_after();
-        if constexpr (EW == 8) {
+        if constexpr (GATED) {
+          const int hc = ncols / 2, c0 = static_cast<int>(eh) * hc;
+          gated_rows<BF16, SB>(p, trow + c0, trow + ncols + c0, n0 + c0, hc, bs + c0, bs + BN / 2 + c0, &tmY, &tmAux, stg,
+                              scount, m0 + static_cast<int>(ew * 32));
+        } else if constexpr (EPI == EPI_DGATED) {
+          const int hc = ncols / 2, c0 = static_cast<int>(eh) * hc;
+          dgated_rows<BF16, SB>(p, trow + c0, m0 + r, n0 + c0, hc, gin, colp_s + ew * (2 * BN) + c0, BN, &tmY, stg, scount,
+                               m0 + static_cast<int>(ew * 32));
+        } else if constexpr (EW == 8) {
           // this warp's half of the columns (the GELU epilogs: no mask words,
           // no column sums, no stream-K addends)
           const int hc = ncols / 2, c0 = static_cast<int>(eh) * hc;
@@ -513,6 +531,15 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8);
+      }
+      if constexpr (EPI == EPI_DGATED) {
+        if (p.dbias) {
+          named_bar_sync(1, ET);
+          const bool has_row = prow < p.m_tiles;
+          if (ok && has_row) dgated_write_partials<BN, ET>(p, prow, n0, colp_s, et, ncols);
+          const int rows = (ok && has_row) ? 1 : 0;
+          dgated_finish_dbias<ET>(p, 2 * w.nb + (w.half < 0 ? 0 : w.half), n0, rows, et, dflag, BN / 2, w.half < 0 ? 2 : 1);
+        }
       }
       if constexpr (EPI == EPI_DRELU_BGRAD) {
         named_bar_sync(1, ET);

@@ -22,6 +22,7 @@
 // copies and MMAs finish, frees its tensor memory and returns.
 #pragma once
 
+#include "activation.cuh"
 #include "ptx.cuh"
 
 namespace ge {
@@ -36,7 +37,15 @@ enum EpiKind : int {
   EPI_GELU_BIAS = 4,
   EPI_WGRAD = 5,
   EPI_STORE = 6,
-  EPI_GELU_AUX_BIAS = 7  // GELU_BIAS, and the pre-activation Z stored (16-bit) as the auxiliary output
+  EPI_GELU_AUX_BIAS = 7,  // GELU_BIAS, and the pre-activation Z stored (16-bit) as the auxiliary output
+  // gated layers (gated_epilogue.cuh); the public values are gemm_epi_gated_epilog's
+  EPI_GATED = 8,   // H = act(Z_gate) Z_up; a tile's columns are one half gate, one half up projection
+  EPI_DGATED = 9   // dZ = [dH U act'(G) | dH act(G)]
+};
+
+template <int EPI>
+struct IsGated {
+  static constexpr bool value = EPI == EPI_GATED || EPI == EPI_DGATED;
 };
 
 // Epilogs that apply GELU.
@@ -118,6 +127,7 @@ struct TileParams {
   int* sk_flags;            // [pairs][2 ranks]: segments in for the tile the pair finishes; zero between launches
   int32_t sk_max_segs;
   int32_t sk_first;         // stream-K tiles before the whole tiles (else after them)
+  int32_t act;              // gated layers: an ActKind
 };
 
 constexpr int kBM = 128;
@@ -129,7 +139,15 @@ constexpr uint32_t kStageBytesPerWarp = 2 * 2048;
 // mask-word staging: each epilogue warp's 32 rows x (BN / 32) words of a tile
 constexpr uint32_t kAuxStageBytesPerWarp = 1024;
 
-template <int BN, int STAGES>
+// Output blocks (2 KB) that each epilogue warp cycles through. A gated layer's
+// chunk of 32 columns gives up to three (H and both halves of Z); the one-CTA
+// kernel's 256-column tiles leave room for two.
+template <int EPI, int BN, bool PAIR>
+struct StageBlocks {
+  static constexpr int value = IsGated<EPI>::value && (PAIR || BN < 256) ? 3 : 2;
+};
+
+template <int BN, int STAGES, int BLOCKS = 2>
 struct TileSmem {
   static constexpr uint32_t A_BYTES = kBM * kBK * 2;          // 16 KB
   static constexpr uint32_t B_CHUNK = kBK * 64 * 2;           // 8 KB: 64 K-rows x 64 N
@@ -142,8 +160,8 @@ struct TileSmem {
   static constexpr uint32_t OFF_BIAS = (OFF_MISC + 16 + 15) / 16 * 16;
   static constexpr uint32_t OFF_COLP = OFF_BIAS + 2 * BN * 4;
   static constexpr uint32_t OFF_STG = (OFF_COLP + 2 * 4 * BN * 4 + 1023) / 1024 * 1024;
-  static constexpr uint32_t OFF_AUXSTG = OFF_STG + kStageBytesPerWarp * 4;
-  static constexpr uint32_t END = OFF_AUXSTG + kAuxStageBytesPerWarp * 4;
+  static constexpr uint32_t OFF_AUXSTG = OFF_STG + BLOCKS * 2048 * 4;
+  static constexpr uint32_t END = OFF_AUXSTG + (BLOCKS == 2 ? kAuxStageBytesPerWarp * 4 : 0);
   static constexpr uint32_t BYTES = END + 1024;               // + alignment slack
 };
 
@@ -580,6 +598,12 @@ __device__ __forceinline__ void epi_finish_dbias(const TileParams& p, int nb, in
   named_bar_sync(1, 128);  // the flag word is reused by the next tile
 }
 
+}  // namespace ge
+
+#include "gated_epilogue.cuh"
+
+namespace ge {
+
 // BK: the weight is N x K (K contiguous) and B is staged K-major; a template
 // parameter, not a runtime flag -- a branch on it in the producer and MMA
 // loops cost 3-4 % on the FFN shape (their issue path is latency-critical)
@@ -588,7 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmAux,
                 const TileParams p) {
-  using L = TileSmem<BN, STAGES>;
+  constexpr int SB = StageBlocks<EPI, BN, false>::value;
+  using L = TileSmem<BN, STAGES, SB>;
+  constexpr bool GATED = EPI == EPI_GATED;
+  static_assert(!GATED || BN % 128 == 0, "a gated tile's halves are whole 64-column chunks");
+  constexpr int BNO = GATED ? BN / 2 : BN;  // output columns of a tile
   static_assert(BN % 64 == 0 && BN >= 64 && BN <= 256, "BN must be 64, 128, 192 or 256");
   constexpr uint32_t TMEM_COLS = (2 * BN <= 32) ? 32 : (2 * BN <= 64) ? 64 : (2 * BN <= 128) ? 128
                                  : (2 * BN <= 256) ? 256 : 512;
@@ -643,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (IsGated<EPI>::value) wait_for_inputs();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -652,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = blockIdx.x; ok && tile < p.num_tiles; tile += gridDim.x) {
         int mb, nb;
         tile_coords(tile, p.m_tiles, p.n_tiles, p.group_m, p.raster_n, mb, nb);
-        const int m0 = mb * kBM, n0 = nb * BN;
+        const int m0 = mb * kBM, n0 = nb * BNO;
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
@@ -667,12 +696,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d(sA + s * L::A_BYTES, &tmA, &full[s], kb * kBK, m0);
           }
-          if constexpr (BK) {
+          if constexpr (BK && GATED) {  // a box of BN / 2 features from each half of the weight
+            tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
+            tma_load_2d(sB + s * L::B_BYTES + L::B_BYTES / 2, &tmB, &full[s], kb * kBK, p.N + n0);
+          } else if constexpr (BK) {
             tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
           } else {
 #pragma unroll
             for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, &full[s], n0 + j * 64, kb * kBK);
+              tma_load_2d(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, &full[s],
+                          (GATED && j >= BN / 128 ? p.N - BNO : 0) + n0 + j * 64, kb * kBK);
           }
         }
       }
@@ -725,19 +758,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const uint32_t ew = warp & 3u;        // TMEM lane quarter this warp may access
     const uint32_t et = threadIdx.x - 64;  // 0..127
-    uint8_t* stg = stg_s + ew * kStageBytesPerWarp;
+    uint8_t* stg = stg_s + ew * (SB * 2048);
     uint32_t scount = 0;
     uint32_t tcount = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++tcount) {
       int mb, nb;
       tile_coords(tile, p.m_tiles, p.n_tiles, p.group_m, p.raster_n, mb, nb);
-      const int m0 = mb * kBM, n0 = nb * BN;
+      const int m0 = mb * kBM, n0 = nb * BNO;
       const uint32_t buf = tcount & 1u;
       const uint32_t tph = (tcount >> 1) & 1u;
       float* bs = bias_s + buf * BN;
       float* cp = colp_s + buf * 4 * BN;
       epi_stage_bias<BN, EPI, BF16>(p, n0, bs, et);
+      if constexpr (GATED) gated_stage_bias<BN, BF16, 128>(p, n0, bs, et, BNO);
+      const int row = m0 + static_cast<int>(ew * 32 + lane);
+      DGatedInput gin{};
+      if constexpr (EPI == EPI_DGATED) gin = dgated_load(p, row, n0);
       MaskWords<BN> mw{};
       if constexpr (EPI == EPI_DRELU_BGRAD) mw = load_mask_words<BN>(p, m0 + static_cast<int>(ew * 32 + lane), n0);
       named_bar_sync(1, 128);
@@ -745,9 +782,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
-        epi_rows<BN, EPI, BF16>(p, tmem_base + ((ew * 32u) << 16) + buf * BN, m0 + static_cast<int>(ew * 32 + lane), n0,
-                                bs, cp + ew * BN, &tmY, stg, scount, m0 + static_cast<int>(ew * 32), &tmAux,
-                                auxstg_s + ew * kAuxStageBytesPerWarp, mw);
+        const uint32_t trow = tmem_base + ((ew * 32u) << 16) + buf * BN;
+        if constexpr (GATED)
+          gated_rows<BF16, SB>(p, trow, trow + BNO, n0, BNO, bs, bs + BNO, &tmY, &tmAux, stg, scount,
+                              m0 + static_cast<int>(ew * 32));
+        else if constexpr (EPI == EPI_DGATED)
+          dgated_rows<BF16, SB>(p, trow, row, n0, BN, gin, colp_s + ew * (2 * BN), BN, &tmY, stg, scount,
+                               m0 + static_cast<int>(ew * 32));
+        else
+          epi_rows<BN, EPI, BF16>(p, trow, row, n0, bs, cp + ew * BN, &tmY, stg, scount, m0 + static_cast<int>(ew * 32),
+                                  &tmAux, auxstg_s + ew * kAuxStageBytesPerWarp, mw);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[buf]);
@@ -756,6 +800,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(1, 128);
         if (ok) epi_write_partials<BN>(p, mb, n0, cp, et);
         if (p.col_tickets) epi_finish_dbias<BN>(p, nb, n0, ok ? 1 : 0, et, dflag);
+      }
+      if constexpr (EPI == EPI_DGATED) {
+        if (p.dbias) {
+          named_bar_sync(1, 128);
+          if (ok) dgated_write_partials<BN, 128>(p, mb, n0, colp_s, et, BN);
+          dgated_finish_dbias<128>(p, nb, n0, ok ? 1 : 0, et, dflag, BN, 1);
+        }
       }
     }
     if (lane == 0) bulk_wait_group_all();  // this warp's output stores are complete

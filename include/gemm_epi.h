@@ -127,7 +127,7 @@ typedef struct {
                           plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
                           (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs).
                           For 3 to 7 tile_m counts features and tile_n rows */
-  int tile_m, tile_n, tile_k, stages;
+  int tile_m, tile_n, tile_k, stages;  /* a gated layer's tiles count gate and up features alike */
   int split_k;         /* K slices per output tile (1 = none). Grouped plans: for experts of the mean
                           number of rows; a call that finds others may share a tile among fewer or
                           more CTAs (at most 16) */
@@ -448,6 +448,61 @@ GEMM_EPI_API gemm_epi_plan_t gemm_epi_mx_plan(int64_t E, int64_t T, int64_t N, i
 GEMM_EPI_API int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                                      const uint8_t* Ws, const void* bias, const int32_t* offsets, void* Y,
                                      cudaStream_t stream);
+
+/*
+ * Gated layers (the feed-forward block in which an activated gate multiplies a
+ * second projection): both projections, the activation and the product in one
+ * kernel, and its backward.
+ *   X     T x K        activations
+ *   W     K x 2N       the gate's N features, then the up projection's
+ *                      (GEMM_EPI_FLAG_W_NK: 2N x K)
+ *   bias  2N           or NULL
+ *   Z = X.W + bias (T x 2N; G = its first N columns, U = its last N)
+ *   H     T x N        act(G) * U
+ *   aux   T x 2N       Z in the plan's 16-bit type (GATED_AUX), for the backward
+ *   dY    T x K        gradient of the block's output; dH = dY.W2
+ *   W2    K x N        (GEMM_EPI_FLAG_W_NK: N x K) the weight that follows the layer,
+ *                      as DRELU_BGRAD's
+ *   dZ    T x 2N       dG = dH U act'(G), then dU = dH act(G), of G and U as in aux
+ *   dbias 2N           sum over t of dZ before its rounding, fp32; or NULL
+ * The rest of the backward pass are plans that exist: dX = dZ.W^T is NONE with K =
+ * 2N (a 2N x K weight is its K x N operand as it stands), dW is WGRAD with N = 2N.
+ * Arithmetic, outputs, rounding, the 16-bit types, flags, error codes, watchdog,
+ * streams and ownership are those of one product; H is computed from Z before Z
+ * is rounded. dbias is summed in a fixed order. GELU is z Phi(z) as grouped
+ * products evaluate it; SILU's exponential and quotient are CUDA's fast ones
+ * (error of H about 1e-6 of it). An activation of -infinity is NaN for SILU and 0
+ * for GELU and RELU; RELU of NaN is 0, and RELU's derivative at 0 is 0. A call runs
+ * on the plan's device whichever is current, and launches are programmatic, as
+ * those of grouped products. gemm_epi_free, _query, _status, _last_error and
+ * _set_bias_f32 (forward) take these plans; the other calls return
+ * GEMM_EPI_ERR_EPILOG_MISMATCH.
+ */
+typedef enum { GEMM_EPI_SILU = 0, GEMM_EPI_GELU = 1, GEMM_EPI_RELU = 2 } gemm_epi_act;
+typedef enum {
+  GEMM_EPI_GATED = 8,      /* H                    */
+  GEMM_EPI_DGATED = 9,     /* dZ, and dbias        */
+  GEMM_EPI_GATED_AUX = 10  /* H, and aux           */
+} gemm_epi_gated_epilog;
+
+/*
+ * gemm_epi_gated_plan: T >= 1; N and K multiples of 8, N at most 2^23, the rest as
+ * gemm_epi_plan_ex. N is the number of columns of H, also for DGATED, where K is
+ * the contraction length of dY.W2. Flags GEMM_EPI_FLAG_W_NK (W or W2) and
+ * GEMM_EPI_FLAG_OUT_F32 (H or dZ; aux stays 16-bit). gemm_epi_query reports
+ * kernels 0 to 2. Both weight layouts have a few-row kernel (forward, T <= 128).
+ */
+GEMM_EPI_API gemm_epi_plan_t gemm_epi_gated_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
+                                                 gemm_epi_gated_epilog epilog, gemm_epi_act act, uint32_t flags);
+
+/* GATED and GATED_AUX. X, W, H and aux 16-byte, bias 2-byte (fp32: 4-byte)
+ * aligned; aux is ignored (may be NULL) for GATED. Returns as gemm_epi_execute. */
+GEMM_EPI_API int gemm_epi_gated_execute(gemm_epi_plan_t plan, const void* X, const void* W, const void* bias, void* H,
+                                        void* aux, cudaStream_t stream);
+
+/* DGATED. dY, W2, aux and dZ 16-byte, dbias 4-byte aligned. Returns as gemm_epi_execute. */
+GEMM_EPI_API int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, const void* W2, const void* aux, void* dZ,
+                                         float* dbias, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
