@@ -66,27 +66,26 @@ bool use_skinny(int64_t T) {
   return T <= 128;
 }
 
-// A T x 2N matrix as rows of two matrices of N columns, in blocks of 32 rows and
-// 64 bytes: what is stored past column N of one half is cut off.
-int encode_halves(CUtensorMap* map, const void* base, int64_t T, int64_t N, bool f32, const char* name) {
+// The pre-activations, T x 2N, as rows of two matrices of N columns, in blocks of 32
+// rows and 64 bytes: what is stored past column N of one half is cut off.
+int encode_halves(CUtensorMap* map, const void* base, int64_t T, int64_t N) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(GEMM_EPI_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   if (inject_encode_failure()) return fail(GEMM_EPI_ERR_CUDA, "injected tensor map encode failure");
-  const cuuint64_t size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)N, 2, (cuuint64_t)T};
-  const cuuint64_t strides[2] = {(cuuint64_t)N * size, 2 * (cuuint64_t)N * size};
-  const cuuint32_t box[3] = {f32 ? 16u : 32u, 1, 32};
+  const cuuint64_t strides[2] = {(cuuint64_t)N * 2, (cuuint64_t)N * 4};
+  const cuuint32_t box[3] = {32, 1, 32};
   const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(GEMM_EPI_ERR_CUDA, "tensor map encode for %s failed (CUresult %d)", name, (int)r);
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(GEMM_EPI_ERR_CUDA, "tensor map encode for the pre-activations failed (CUresult %d)", (int)r);
   return GEMM_EPI_OK;
 }
 
 void release(gemm_epi_plan_s* p) {
   if (p->partials) cudaFree(p->partials);
-  if (p->col_tickets) cudaFree(p->col_tickets);
   if (p->sk_partials) cudaFree(p->sk_partials);
   if (p->sk_tickets) cudaFree(p->sk_tickets);
   if (p->status_host) cudaFreeHost(p->status_host);
@@ -166,14 +165,10 @@ cudaError_t plan_tiles(gemm_epi_plan_s* p, bool bf16, bool forward, int sms) {
     p->grid = p->num_tiles < sms ? p->num_tiles : sms;
   }
   if (forward) return cudaSuccess;
-  // the bias gradient's partial rows, and a counter per column block (pairs: per 128 columns)
-  p->partial_bytes = (size_t)p->m_tiles * 2 * (size_t)p->N * sizeof(float);
+  // the bias gradient's partial sums, a row for each 32 of T
+  p->partial_bytes = (size_t)ceil_div(p->T, 32) * 2 * (size_t)p->N * sizeof(float);
   if (test_hook("GEMM_EPI_INJECT_PLAN_ALLOC_FAILURE")) return cudaErrorMemoryAllocation;
-  e = cudaMalloc((void**)&p->partials, p->partial_bytes);
-  if (e != cudaSuccess) return e;
-  p->n_tickets = pair ? 2 * p->n_tiles : p->n_tiles;
-  e = cudaMalloc((void**)&p->col_tickets, sizeof(int) * (size_t)p->n_tickets);
-  return e == cudaSuccess ? zero_counts(p->col_tickets, (size_t)p->n_tickets) : e;
+  return cudaMalloc((void**)&p->partials, p->partial_bytes);
 }
 
 gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype, gemm_epi_gated_epilog epilog,
@@ -339,7 +334,7 @@ int gemm_epi_gated_execute(gemm_epi_plan_t plan, const void* X, const void* W, c
   rc = encode_2d(&a, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, ge::kBM, "the row operand");
   if (!rc) rc = encode_weight(&b, p, W, 2 * p->N, ge::kBK, p->cfg.pair ? 128u : (uint32_t)p->cfg.BN / 2);
   if (!rc) rc = p->out_f32 ? encode_out_f32(&y, H, p->T, p->N) : encode_out(&y, H, p->T, p->N);
-  if (!rc && aux) rc = encode_halves(&z, aux, p->T, p->N, false, "the pre-activations");
+  if (!rc && aux) rc = encode_halves(&z, aux, p->T, p->N);
   if (rc) return rc;
   ge::TileParams k{};
   k.bias = bias;
@@ -361,18 +356,21 @@ int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, const void* W2
   DeviceScope scope(p->device);
   rc = begin_call(p, stream);
   if (rc) return rc;
-  CUtensorMap a, b, y;
+  CUtensorMap a, b;
   rc = encode_2d(&a, dY, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, ge::kBM, "dY");
   if (!rc) rc = encode_weight(&b, p, W2, p->N, ge::kBK, p->cfg.pair ? 128u : (uint32_t)p->cfg.BN);
-  if (!rc) rc = encode_halves(&y, dZ, p->T, p->N, p->out_f32 != 0, "dZ");
   if (rc) return rc;
   ge::TileParams k{};
   k.out = dZ;
   k.aux_in = static_cast<const uint32_t*>(aux);
   k.partials = p->partials;
-  k.col_tickets = p->col_tickets;
   k.dbias = dbias;
-  return launch_tiles(p, a, b, y, y, k, stream);
+  rc = launch_tiles(p, a, b, a, a, k, stream);  // (outputs go out without a map)
+  if (rc || !dbias) return rc;
+  Launch l(ceil_div(2 * p->N, 32), 256, 0, false, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, ge::dgated_dbias_kernel, static_cast<const float*>(p->partials),
+                                           ceil_div(p->T, 32), (int)(2 * p->N), dbias);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "bias gradient launch");
 }
 
 }  // extern "C"

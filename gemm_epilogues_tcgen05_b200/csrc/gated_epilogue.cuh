@@ -105,21 +105,89 @@ __device__ __forceinline__ void gated_rows(const TileParams& p, uint32_t tgate, 
   }
 }
 
-// Backward: 32 columns of G and of U of one row, 16-bit.
-struct DGatedInput {
-  uint4 g[4], u[4];
+// The tiles of a CTA as a warp's DGatedStream walks them.
+template <int BN>
+struct TileSource {
+  int tile, row;  // row: the warp's first of a tile
+  __device__ __forceinline__ bool next(const TileParams& p, int& n0, int& ncols, int& row0) {
+    if (tile >= p.num_tiles) return false;
+    int mb, nb;
+    tile_coords(tile, p.m_tiles, p.n_tiles, p.group_m, p.raster_n, mb, nb);
+    tile += gridDim.x;
+    n0 = nb * BN;
+    ncols = BN;
+    row0 = mb * kBM + row;
+    return true;
+  }
 };
 
-__device__ __forceinline__ DGatedInput dgated_load(const TileParams& p, int row, int nc0) {
-  DGatedInput r;
-  const uint16_t* z = reinterpret_cast<const uint16_t*>(p.aux_in) + static_cast<int64_t>(row) * 2 * p.N + nc0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const bool in = row < p.T && nc0 + 8 * q < p.N;  // N is a multiple of 8
-    r.g[q] = in ? __ldg(reinterpret_cast<const uint4*>(z + 8 * q)) : make_uint4(0, 0, 0, 0);
-    r.u[q] = in ? __ldg(reinterpret_cast<const uint4*>(z + p.N + 8 * q)) : make_uint4(0, 0, 0, 0);
+// Backward: an epilogue warp's own stream of G and U, in chunks of 32 rows x 32
+// columns of both, in the order in which the warp will work on them and a slot or
+// two before it does, across tiles: while a tile's products are still running its
+// first chunks have come in. A slot holds [G, U][32 rows][64 bytes], 16-byte piece q of
+// row r at q ^ ((r >> 1) & 3), so that a lane's own row and eight lanes' two rows
+// are both free of bank conflicts; dG and dU take the places of G and U, and go out as
+// 64 contiguous bytes of eight rows an instruction.
+//
+// Neither direction uses TMA: its rows of 64 bytes are as many requests as the
+// operands' of 128, a quarter more in all, and the operands come late for them.
+// T = K = 4096, N = 11008 (us): threads loading their own row's 64 bytes one chunk
+// ahead and TMA stores 315; TMA both ways 294 (263 with the loads left out, 272
+// without the stores).
+template <class Source>
+struct DGatedStream {
+  const TileParams& p;
+  uint32_t slots;   // shared address
+  Source source;
+  int n0 = 0, ncols = 0, row0 = 0, c = 0;  // the next chunk to be loaded
+  bool live = true;
+  uint32_t next_in = 0, next_out = 0;      // slots
+
+  __device__ __forceinline__ DGatedStream(const TileParams& p_, const uint8_t* s, Source src)
+      : p(p_), slots(smem_u32(s)), source(src) {}
+  // piece lane % 4 of row 8 i + lane / 4
+  static __device__ __forceinline__ uint32_t piece(int i) {
+    const uint32_t row = 8 * i + (lane_id() >> 2);
+    return row * 64 + (((lane_id() & 3u) ^ ((row >> 1) & 3u)) * 16);
   }
-  return r;
+  __device__ __forceinline__ void issue() {
+    while (live && (c >= ncols || n0 + c >= p.N)) {
+      live = source.next(p, n0, ncols, row0);
+      c = 0;
+    }
+    if (live) {
+      const int col = n0 + c + 8 * static_cast<int>(lane_id() & 3u);
+      const uint32_t dst = slots + next_in * 4096;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = row0 + 8 * i + static_cast<int>(lane_id() >> 2);
+        const bool in = row < p.T && col < p.N;  // N is a multiple of 8
+        const uint16_t* z = reinterpret_cast<const uint16_t*>(p.aux_in) + (in ? static_cast<int64_t>(row) * 2 * p.N + col : 0);
+        cp_async_16(dst + piece(i), z, in);
+        cp_async_16(dst + 2048 + piece(i), in ? z + p.N : z, in);
+      }
+      c += 32;
+      next_in = next_in + 1 == kDGatedSlots ? 0 : next_in + 1;
+    }
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void start() {
+    for (int i = 0; i < kDGatedSlots; ++i) issue();
+  }
+  // the next chunk's slot, when it has come
+  __device__ __forceinline__ uint32_t take() {
+    cp_async_wait<kDGatedSlots - 1>();
+    __syncwarp();
+    const uint32_t at = slots + next_out * 4096;
+    next_out = next_out + 1 == kDGatedSlots ? 0 : next_out + 1;
+    return at;
+  }
+};
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
+  return v;
 }
 
 template <bool BF16>
@@ -134,13 +202,34 @@ __device__ __forceinline__ void unpack_2x(uint32_t w, float& lo, float& hi) {
   }
 }
 
-// This warp's 32 rows (row = this lane's), columns n0 .. n0 + ncols - 1, of which `in`
-// holds the first 32 of G and U: each next 32 are loaded while the last are
-// worked on. colp (fp32, this lane quarter's): the column sums, dG's and, `gap` later, dU's.
-template <bool BF16, int NB>
-__device__ __forceinline__ void dgated_rows(const TileParams& p, uint32_t tbase, int row, int n0, int ncols,
-                                            DGatedInput in, float* colp, int gap, const CUtensorMap* tmY, uint8_t* stg,
-                                            uint32_t& scount, int wrow0) {
+// fp32 outputs: 32 columns of one half through the slot, 128 bytes a row (piece q of
+// row r at q ^ (r & 7)), 128 contiguous bytes of four rows an instruction.
+__device__ __forceinline__ void dgated_store_f32(const TileParams& p, uint32_t slot, const float (&v)[32], int half,
+                                                 int wrow0, int nc0) {
+  const uint32_t lane = lane_id();
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    st_shared_v4(slot + lane * 128 + ((q ^ (lane & 7u)) * 16),
+                 make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                            __float_as_uint(v[4 * q + 3])));
+  __syncwarp();
+  const int col = nc0 + 4 * static_cast<int>(lane & 7u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t r = 4 * i + (lane >> 3);
+    const int row = wrow0 + static_cast<int>(r);
+    if (row < p.T && col < p.N)
+      *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + (static_cast<int64_t>(row) * 2 + half) * p.N + col) =
+          ld_shared_v4(slot + r * 128 + (((lane & 7u) ^ (r & 7u)) * 16));
+  }
+}
+
+// This warp's 32 rows from wrow0 on, columns n0 .. n0 + ncols - 1. With dbias, the
+// column sums of the 32 rows go into a row of the partials of their own (2N
+// columns), which dgated_dbias_kernel adds up.
+template <bool BF16, class Stream>
+__device__ __forceinline__ void dgated_rows(const TileParams& p, uint32_t tbase, int wrow0, int n0, int ncols, Stream& in) {
   const uint32_t lane = lane_id();
 #pragma unroll 1
   for (int c = 0; c < ncols; c += 32) {
@@ -148,12 +237,15 @@ __device__ __forceinline__ void dgated_rows(const TileParams& p, uint32_t tbase,
     if (nc0 >= p.N) break;  // warp-uniform
     uint32_t r[32];
     tmem_ld_32x32b_x32(tbase + c, r);
+    const uint32_t slot = in.take();
+    const uint32_t own = slot + lane * 64, swz = ((lane >> 1) & 3u) * 16;
     tmem_wait_ld();
     float dg[32], du[32];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t wg[4] = {in.g[q].x, in.g[q].y, in.g[q].z, in.g[q].w};
-      const uint32_t wu[4] = {in.u[q].x, in.u[q].y, in.u[q].z, in.u[q].w};
+      const uint4 ig = ld_shared_v4(own + ((q * 16) ^ swz)), iu = ld_shared_v4(own + 2048 + ((q * 16) ^ swz));
+      const uint32_t wg[4] = {ig.x, ig.y, ig.z, ig.w};
+      const uint32_t wu[4] = {iu.x, iu.y, iu.z, iu.w};
       float g[8], a[8], d[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack_2x<BF16>(wg[j], g[2 * j], g[2 * j + 1]);
@@ -169,77 +261,75 @@ __device__ __forceinline__ void dgated_rows(const TileParams& p, uint32_t tbase,
         du[8 * q + 2 * j + 1] = h1 * a[2 * j + 1];
       }
     }
-    if (c + 32 < ncols) in = dgated_load(p, row, nc0 + 32);
-    gated_store<BF16, NB, true>(dg, tmY, stg, scount, nc0, 0, wrow0, p.out_f32 != 0, p.N);
-    gated_store<BF16, NB, true>(du, tmY, stg, scount, nc0, 1, wrow0, p.out_f32 != 0, p.N);
-    if (p.dbias) {
-      if (row >= p.T) {  // (0 x an infinite weight is no zero)
+    if (p.out_f32) {
+      dgated_store_f32(p, slot, dg, 0, wrow0, nc0);
+      dgated_store_f32(p, slot, du, 1, wrow0, nc0);
+    } else {
+      // (a lane's row is read by that lane alone before it is replaced)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        st_shared_v4(own + ((q * 16) ^ swz),
+                     make_uint4(pack2<BF16>(dg[8 * q], dg[8 * q + 1]), pack2<BF16>(dg[8 * q + 2], dg[8 * q + 3]),
+                                pack2<BF16>(dg[8 * q + 4], dg[8 * q + 5]), pack2<BF16>(dg[8 * q + 6], dg[8 * q + 7])));
+        st_shared_v4(own + 2048 + ((q * 16) ^ swz),
+                     make_uint4(pack2<BF16>(du[8 * q], du[8 * q + 1]), pack2<BF16>(du[8 * q + 2], du[8 * q + 3]),
+                                pack2<BF16>(du[8 * q + 4], du[8 * q + 5]), pack2<BF16>(du[8 * q + 6], du[8 * q + 7])));
+      }
+      __syncwarp();
+      const int col = nc0 + 8 * static_cast<int>(lane & 3u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = wrow0 + 8 * i + static_cast<int>(lane >> 2);
+        if (row < p.T && col < p.N) {
+          uint16_t* z = reinterpret_cast<uint16_t*>(p.out) + static_cast<int64_t>(row) * 2 * p.N + col;
+          *reinterpret_cast<uint4*>(z) = ld_shared_v4(slot + Stream::piece(i));
+          *reinterpret_cast<uint4*>(z + p.N) = ld_shared_v4(slot + 2048 + Stream::piece(i));
+        }
+      }
+    }
+    __syncwarp();
+    in.issue();
+    if (p.dbias && wrow0 < p.T) {
+      if (wrow0 + static_cast<int>(lane) >= p.T) {  // (0 x an infinite weight is no zero)
 #pragma unroll
         for (int j = 0; j < 32; ++j) dg[j] = du[j] = 0.f;
       }
       warp_transpose_reduce32(dg);
-      colp[c + lane] = dg[0];
       warp_transpose_reduce32(du);
-      colp[gap + c + lane] = du[0];
+      if (nc0 + static_cast<int>(lane) < p.N) {
+        float* to = p.partials + static_cast<int64_t>(wrow0 >> 5) * 2 * p.N + nc0 + lane;
+        to[0] = dg[0];
+        to[p.N] = du[0];
+      }
     }
   }
 }
 
-// Column sums of a tile's 128 rows, the four lane quarters in order, into row
-// `prow` of the partials (2N columns). cp: four times [dG: BN][dU: BN].
-template <int BN, int NT>
-__device__ __forceinline__ void dgated_write_partials(const TileParams& p, int prow, int n0, const float* cp, uint32_t et,
-                                                      int ncols) {
-  for (int c = et; c < 2 * ncols; c += NT) {
-    const int half = c >= ncols ? 1 : 0, cc = c - half * ncols, n = n0 + cc;
-    if (n >= p.N) continue;
-    const float* s = cp + half * BN + cc;
-    p.partials[(static_cast<int64_t>(prow) * 2 + half) * p.N + n] = ((s[0] + s[2 * BN]) + s[4 * BN]) + s[6 * BN];
-  }
-}
-
-// As epi_finish_dbias, for both halves: the tile that takes a column block's
-// last ticket adds the block's partial rows in ascending order (sixteen loads
-// in flight) and resets the counter.
-template <int NT>
-__device__ __forceinline__ void dgated_finish_dbias(const TileParams& p, int nb, int n0, int rows, uint32_t et,
-                                                    volatile int* flag, int ncols, int nblocks) {
-  __threadfence();
-  named_bar_sync(1, NT);
-  if (et == 0) {
-    int bits = 0;
-    for (int b = 0; b < nblocks; ++b) {
-      const int prev = atomicAdd(p.col_tickets + nb + b, rows);
-      if (prev + rows == p.m_tiles) {
-        p.col_tickets[nb + b] = 0;
-        bits |= 1 << b;
-      }
-    }
-    *flag = bits;
-  }
-  named_bar_sync(1, NT);
-  const int bits = *flag;
-  if (bits) {
-    __threadfence();
-    const int total = nblocks * ncols;
-    for (int c = et; c < 2 * total; c += NT) {
-      const int half = c >= total ? 1 : 0, cc = c - half * total, n = n0 + cc;
-      if (!((bits >> (cc / ncols)) & 1) || n >= p.N) continue;
-      const float* col = p.partials + static_cast<int64_t>(half) * p.N + n;
-      const int64_t stride = 2 * static_cast<int64_t>(p.N);
-      float s = 0.f;
-      for (int m0 = 0; m0 < p.m_tiles; m0 += 16) {
-        float x[16];
+// The bias gradient: the partial sums' `rows` rows, in 8 runs of rows, each in
+// ascending order, then the runs in order. 32 columns a block.
+static __global__ void __launch_bounds__(256) dgated_dbias_kernel(const float* partials, int rows, int cols, float* dbias) {
+  __shared__ float run[8][32];
+  wait_for_inputs();
+  const int n = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  const int per = (rows + 7) / 8, r0 = y * per, r1 = min(rows, r0 + per);
+  float s = 0.f;
+  if (n < cols) {
+    const float* at = partials + n;
+    for (int r = r0; r < r1; r += 16) {
+      float x[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = m0 + j < p.m_tiles ? __ldcg(col + (m0 + j) * stride) : 0.f;
+      for (int j = 0; j < 16; ++j) x[j] = r + j < r1 ? __ldcg(at + static_cast<int64_t>(r + j) * cols) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (m0 + j < p.m_tiles) s += x[j];
-      }
-      p.dbias[static_cast<int64_t>(half) * p.N + n] = s;
+      for (int j = 0; j < 16; ++j) s += x[j];
     }
   }
-  named_bar_sync(1, NT);  // the flag word is reused by the next tile
+  run[y][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (y == 0 && n < cols) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s += run[j][threadIdx.x];
+    dbias[n] = s;
+  }
 }
 
 }  // namespace ge

@@ -661,7 +661,7 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->launches = 1;
     info->workspace_bytes = p->pair_bytes +
                             (p->epilog == GEMM_EPI_DRELU_BGRAD || p->epilog == GEMM_EPI_DGATED
-                                 ? p->partial_bytes + sizeof(int) * (size_t)p->n_tickets
+                                 ? p->partial_bytes + sizeof(int) * (size_t)p->n_tickets  // (DGATED has none)
                              : p->epilog == GEMM_EPI_WGRAD     ? p->partial_bytes
                                                                : 0);
   }

@@ -10,18 +10,21 @@ namespace ge_inst {
 
 template <int BN, int ST, int EPI, bool BF, bool BK>
 GatedInstance gated_tile() {
-  static_assert(ge::TileSmem<BN, ST, ge::StageBlocks<EPI, BN, false>::value>::BYTES <= 232448, "above the per-CTA limit");
-  return {ge::tile_kernel<BN, ST, EPI, BF, BK>, ge::TileSmem<BN, ST, ge::StageBlocks<EPI, BN, false>::value>::BYTES, ge::kThreads, ST};
+  static_assert(ge::TileSmem<BN, ST, EPI>::BYTES <= 232448, "above the per-CTA limit");
+  return {ge::tile_kernel<BN, ST, EPI, BF, BK>, ge::TileSmem<BN, ST, EPI>::BYTES, ge::kThreads, ST};
+}
+
+template <int ST, int EPI, bool BF, bool BK>
+GatedInstance gated_pair() {
+  using L = ge::Tile2Smem<256, ST, 8, EPI>;
+  static_assert(L::BYTES <= 232448, "above the per-CTA limit");
+  return {ge::tile2_kernel<256, ST, EPI, BF, BK>, L::BYTES, 64 + 32 * 8, ST};
 }
 
 template <bool BF, bool BK>
 GatedInstance gated_any(int bn, bool pair, int epi) {
   constexpr int F = ge::EPI_GATED, B = ge::EPI_DGATED;
-  if (pair) {
-    constexpr uint32_t smem = ge::Tile2Smem<256, 5, 8, ge::StageBlocks<F, 256, true>::value>::BYTES;
-    static_assert(smem <= 232448, "above the per-CTA limit");
-    return {epi == F ? ge::tile2_kernel<256, 5, F, BF, BK> : ge::tile2_kernel<256, 5, B, BF, BK>, smem, 64 + 32 * 8, 5};
-  }
+  if (pair) return epi == F ? gated_pair<5, F, BF, BK>() : gated_pair<5, B, BF, BK>();
   if (bn == 256) return epi == F ? gated_tile<256, 4, F, BF, BK>() : gated_tile<256, 4, B, BF, BK>();
   if (bn == 128) return epi == F ? gated_tile<128, 6, F, BF, BK>() : gated_tile<128, 6, B, BF, BK>();
   if (bn == 64 && epi == B) return gated_tile<64, 8, B, BF, BK>();

@@ -147,6 +147,18 @@ __device__ __forceinline__ void bulk_load_g2s(void* dst, const void* src, uint32
       : "memory");
 }
 
+// 16 bytes global -> shared by this thread (through L2 only; zeros where `in` is
+// false), counted in its groups
+__device__ __forceinline__ void cp_async_16(uint32_t saddr, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// wait until at most N of this thread's groups are under way
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Prefetch a 2-D tile into L2 only (no shared memory, no completion signal).
 __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap* map, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(

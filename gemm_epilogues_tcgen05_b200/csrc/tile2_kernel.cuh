@@ -57,8 +57,10 @@ struct PairEpiWarps {
   static constexpr int value = (AppliesGelu<EPI>::value || IsGated<EPI>::value) && !SPLIT ? 8 : 4;
 };
 
-template <int BN, int STAGES, int EW = 4, int BLOCKS = 2>
+template <int BN, int STAGES, int EW = 4, int EPI = -1>
 struct Tile2Smem {
+  static constexpr bool LEAN = EPI == EPI_DGATED;             // no bias, column sums or mask words
+  static constexpr int BLOCKS = StageBlocks<EPI, BN, true>::value;
   static constexpr uint32_t A_BYTES = kBM * kBK * 2;          // this CTA's 128 rows x 64 k
   static constexpr uint32_t B_CHUNK = kBK * 64 * 2;           // 64 k x 64 n
   static constexpr uint32_t B_BYTES = (BN / 128) * B_CHUNK;   // this CTA's BN/2 columns
@@ -68,10 +70,10 @@ struct Tile2Smem {
   static constexpr uint32_t N_BARS = 2 * STAGES + 6;  // full, empty, tfull[2], tempty[2], drain, stream-K fixup
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr uint32_t OFF_BIAS = (OFF_MISC + 24 + 15) / 16 * 16;
-  static constexpr uint32_t OFF_COLP = OFF_BIAS + 2 * BN * 4;
-  static constexpr uint32_t OFF_STG = (OFF_COLP + 2 * 4 * BN * 4 + 1023) / 1024 * 1024;
+  static constexpr uint32_t OFF_COLP = OFF_BIAS + (LEAN ? 0 : 2 * BN * 4);
+  static constexpr uint32_t OFF_STG = (OFF_COLP + (LEAN ? 0 : 2 * 4 * BN * 4) + 1023) / 1024 * 1024;
   static constexpr uint32_t OFF_AUXSTG = OFF_STG + BLOCKS * 2048 * EW;
-  static constexpr uint32_t END = OFF_AUXSTG + (BLOCKS == 2 ? kAuxStageBytesPerWarp * EW : 0);
+  static constexpr uint32_t END = OFF_AUXSTG + (EPI == EPI_GATED || LEAN ? 0 : kAuxStageBytesPerWarp * EW);
   static constexpr uint32_t BYTES = END + 1024;
 };
 
@@ -206,6 +208,21 @@ struct PairWork {
   }
 };
 
+// The units of a pair as a warp's DGatedStream walks them.
+template <int BN>
+struct PairSource {
+  PairWork<false> work;
+  int row, eh;  // the warp's first row of a unit, its half of the unit's columns
+  __device__ __forceinline__ bool next(const TileParams&, int& n0, int& ncols, int& row0) {
+    PairUnit w;
+    if (!work.next(w)) return false;
+    ncols = (w.half < 0 ? BN : BN / 2) / 2;
+    n0 = w.nb * BN + (w.half < 0 ? 0 : w.half * (BN / 2)) + eh * ncols;
+    row0 = w.mb * 2 * kBM + row;
+    return true;
+  }
+};
+
 template <int BN, int STAGES, int EPI, bool BF16, bool BK = false, bool SPLIT = false>
 __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     tile2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -213,8 +230,12 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
                  const TileParams p) {
   constexpr int EW = PairEpiWarps<EPI, SPLIT>::value;  // epilogue warps
   constexpr int ET = 32 * EW;                          // epilogue threads
-  constexpr int SB = StageBlocks<EPI, BN, true>::value;
-  using L = Tile2Smem<BN, STAGES, EW, SB>;
+  using L = Tile2Smem<BN, STAGES, EW, EPI>;
+  constexpr int SB = L::BLOCKS;
+  // gated layers: the producer and MMA warps walk their loops whole and one
+  // elected lane issues (elect_one); under a branch on the lane, between the
+  // instructions of a long epilogue, the MMAs were issued too late
+  constexpr bool WARP_ISSUE = IsGated<EPI>::value;
   constexpr bool GATED = EPI == EPI_GATED;  // rank 0 loads the gate's weight, rank 1 the up projection's
   static_assert(!(SPLIT && IsGated<EPI>::value), "gated layers run on whole tiles");
   constexpr int BNO = GATED ? BN / 2 : BN;  // output columns of a tile
@@ -291,7 +312,8 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (WARP_ISSUE || lane == 0) {
+      const bool issuer = !WARP_ISSUE || elect_one();
       uint32_t it = 0;
       bool ok = true;
       const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
@@ -306,24 +328,28 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
-          if (!wait_bounded(&empty[s], ph ^ 1u, p, abort_flag, 1)) {
+          bool got = wait_bounded(&empty[s], ph ^ 1u, p, abort_flag, 1);
+          if constexpr (WARP_ISSUE) got = __all_sync(0xffffffffu, got);
+          if (!got) {
             ok = false;
             break;
           }
-          if (it % kStepStages == 0) *last_step = globaltimer_ns();
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], w.half < 0 ? PAIR_TX : PAIR_TX_HALF);
-          const uint32_t fbar = full0 + s * 8;  // the leader's full[s]
-          if constexpr (A_MN) {
-            tma_load_2d_pair(sA + s * L::A_BYTES, &tmA, fbar, m0, kb * kBK);
-            tma_load_2d_pair(sA + s * L::A_BYTES + kAChunkMN, &tmA, fbar, m0 + 64, kb * kBK);
-          } else {
-            tma_load_2d_pair(sA + s * L::A_BYTES, &tmA, fbar, kb * kBK, m0);
-          }
-          if constexpr (BK) {  // this CTA's 128 rows of the N x K weight in one box
-            tma_load_2d_pair(sB + s * L::B_BYTES, &tmB, fbar, kb * kBK, nh0);
-          } else {
-            for (int j = 0; j < nchunks; ++j)
-              tma_load_2d_pair(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, fbar, nh0 + j * 64, kb * kBK);
+          if (issuer) {
+            if (it % kStepStages == 0) *last_step = globaltimer_ns();
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], w.half < 0 ? PAIR_TX : PAIR_TX_HALF);
+            const uint32_t fbar = full0 + s * 8;  // the leader's full[s]
+            if constexpr (A_MN) {
+              tma_load_2d_pair(sA + s * L::A_BYTES, &tmA, fbar, m0, kb * kBK);
+              tma_load_2d_pair(sA + s * L::A_BYTES + kAChunkMN, &tmA, fbar, m0 + 64, kb * kBK);
+            } else {
+              tma_load_2d_pair(sA + s * L::A_BYTES, &tmA, fbar, kb * kBK, m0);
+            }
+            if constexpr (BK) {  // this CTA's 128 rows of the N x K weight in one box
+              tma_load_2d_pair(sB + s * L::B_BYTES, &tmB, fbar, kb * kBK, nh0);
+            } else {
+              for (int j = 0; j < nchunks; ++j)
+                tma_load_2d_pair(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, fbar, nh0 + j * 64, kb * kBK);
+            }
           }
         }
       }
@@ -335,7 +361,8 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
+    if (WARP_ISSUE || lane == 0) {
+      const bool issuer = !WARP_ISSUE || elect_one();
       if (rank == 0) {
         uint32_t it = 0, tcount = 0;
         bool ok = true;
@@ -345,32 +372,38 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
           const uint32_t idesc = BK ? IDESC_BK : w.half < 0 ? IDESC : IDESC_HALF;
           const uint32_t buf = tcount & 1u;
           const uint32_t tph = (tcount >> 1) & 1u;
-          if (!wait_bounded(&tempty[buf], tph ^ 1u, p, abort_flag, 3)) break;
+          bool room = wait_bounded(&tempty[buf], tph ^ 1u, p, abort_flag, 3);
+          if constexpr (WARP_ISSUE) room = __all_sync(0xffffffffu, room);
+          if (!room) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
           for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
             const uint32_t s = it % STAGES;
             const uint32_t ph = (it / STAGES) & 1u;
-            if (!wait_bounded(&full[s], ph, p, abort_flag, 4)) {
+            bool got = wait_bounded(&full[s], ph, p, abort_flag, 4);
+            if constexpr (WARP_ISSUE) got = __all_sync(0xffffffffu, got);
+            if (!got) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
-            const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
+            if (issuer) {
+              const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
+              const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t adesc = a_desc<A_MN>(a0, kk);
-              const uint64_t bdesc = b_desc(b0, kk, BK, L::B_CHUNK);
-              umma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb > w.kb0 || kk != 0) ? 1u : 0u);
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                const uint64_t adesc = a_desc<A_MN>(a0, kk);
+                const uint64_t bdesc = b_desc(b0, kk, BK, L::B_CHUNK);
+                umma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb > w.kb0 || kk != 0) ? 1u : 0u);
+              }
+              umma_commit_pair(&empty[s], BOTH);
             }
-            umma_commit_pair(&empty[s], BOTH);
           }
           if (!ok) break;
           // (fault injection: both CTAs' epilogues then wait on a barrier nothing arrives on)
-          if (!(p.inject_stall && tcount == 0)) umma_commit_pair(&tfull[buf], BOTH);
+          if (issuer && !(p.inject_stall && tcount == 0)) umma_commit_pair(&tfull[buf], BOTH);
         }
-        umma_commit_pair(drain, BOTH);
+        if (issuer) umma_commit_pair(drain, BOTH);
       }
       // both CTAs: the leader's MMAs write this CTA's TMEM; they must be done
       // (the other CTA waits here from its start)
@@ -389,6 +422,9 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     PairWork<SPLIT> work(pw, pair, npairs, m2_tiles);
     PairUnit w;
+    DGatedStream<PairSource<BN>> gin(p, stg, PairSource<BN>{PairWork<false>(pw, pair, npairs, m2_tiles),
+                                                            static_cast<int>(rank * kBM + ew * 32), static_cast<int>(eh)});
+    if constexpr (EPI == EPI_DGATED) gin.start();
     for (; work.next(w); ++tcount) {
       const int prow = w.mb * 2 + static_cast<int>(rank);  // this CTA's 128-row block
       const int m0 = prow * kBM;
@@ -400,9 +436,6 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
       float* cp = colp_s + buf * 4 * BN;
       epi_stage_bias<BN, EPI, BF16, ET>(p, n0, bs, et, ncols);
       if constexpr (GATED) gated_stage_bias<BN, BF16, ET>(p, n0, bs, et, ncols);
-      DGatedInput gin{};
-      if constexpr (EPI == EPI_DGATED)
-        gin = dgated_load(p, m0 + static_cast<int>(ew * 32 + lane), n0 + static_cast<int>(eh) * (ncols / 2));
       MaskWords<BN> mw{};
       if constexpr (EPI == EPI_DRELU_BGRAD) mw = load_mask_words<BN>(p, m0 + static_cast<int>(ew * 32 + lane), n0);
       named_bar_sync(1, ET);
@@ -515,8 +548,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
                               scount, m0 + static_cast<int>(ew * 32));
         } else if constexpr (EPI == EPI_DGATED) {
           const int hc = ncols / 2, c0 = static_cast<int>(eh) * hc;
-          dgated_rows<BF16, SB>(p, trow + c0, m0 + r, n0 + c0, hc, gin, colp_s + ew * (2 * BN) + c0, BN, &tmY, stg, scount,
-                               m0 + static_cast<int>(ew * 32));
+          dgated_rows<BF16>(p, trow + c0, m0 + static_cast<int>(ew * 32), n0 + c0, hc, gin);
         } else if constexpr (EW == 8) {
           // this warp's half of the columns (the GELU epilogs: no mask words,
           // no column sums, no stream-K addends)
@@ -532,15 +564,6 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8);
       }
-      if constexpr (EPI == EPI_DGATED) {
-        if (p.dbias) {
-          named_bar_sync(1, ET);
-          const bool has_row = prow < p.m_tiles;
-          if (ok && has_row) dgated_write_partials<BN, ET>(p, prow, n0, colp_s, et, ncols);
-          const int rows = (ok && has_row) ? 1 : 0;
-          dgated_finish_dbias<ET>(p, 2 * w.nb + (w.half < 0 ? 0 : w.half), n0, rows, et, dflag, BN / 2, w.half < 0 ? 2 : 1);
-        }
-      }
       if constexpr (EPI == EPI_DRELU_BGRAD) {
         named_bar_sync(1, ET);
         const bool has_row = prow < p.m_tiles;
@@ -555,6 +578,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         }
       }
     }
+    if constexpr (EPI == EPI_DGATED) cp_async_wait<0>();
     if (lane == 0) bulk_wait_group_all();  // this warp's output stores are complete
     __syncwarp();
   }

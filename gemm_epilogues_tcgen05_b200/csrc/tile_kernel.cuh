@@ -138,17 +138,21 @@ constexpr int kThreads = 192;
 constexpr uint32_t kStageBytesPerWarp = 2 * 2048;
 // mask-word staging: each epilogue warp's 32 rows x (BN / 32) words of a tile
 constexpr uint32_t kAuxStageBytesPerWarp = 1024;
+// DGATED: slots of an epilogue warp, each 32 rows x 32 columns of G and of U
+constexpr int kDGatedSlots = 2;
 
-// Output blocks (2 KB) that each epilogue warp cycles through. A gated layer's
+// Blocks of 2 KB that each epilogue warp stages its outputs in. A gated layer's
 // chunk of 32 columns gives up to three (H and both halves of Z); the one-CTA
-// kernel's 256-column tiles leave room for two.
+// kernel's 256-column tiles leave room for two. DGATED: the slots of DGatedStream.
 template <int EPI, int BN, bool PAIR>
 struct StageBlocks {
-  static constexpr int value = IsGated<EPI>::value && (PAIR || BN < 256) ? 3 : 2;
+  static constexpr int value = EPI == EPI_DGATED ? 2 * kDGatedSlots : EPI == EPI_GATED && (PAIR || BN < 256) ? 3 : 2;
 };
 
-template <int BN, int STAGES, int BLOCKS = 2>
+template <int BN, int STAGES, int EPI = -1>
 struct TileSmem {
+  static constexpr bool LEAN = EPI == EPI_DGATED;             // no bias, column sums or mask words
+  static constexpr int BLOCKS = StageBlocks<EPI, BN, false>::value;
   static constexpr uint32_t A_BYTES = kBM * kBK * 2;          // 16 KB
   static constexpr uint32_t B_CHUNK = kBK * 64 * 2;           // 8 KB: 64 K-rows x 64 N
   static constexpr uint32_t B_BYTES = (BN / 64) * B_CHUNK;
@@ -158,10 +162,10 @@ struct TileSmem {
   static constexpr uint32_t N_BARS = 2 * STAGES + 5;          // full, empty, tfull[2], tempty[2], drain
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;  // tmem slot, abort flag
   static constexpr uint32_t OFF_BIAS = (OFF_MISC + 16 + 15) / 16 * 16;
-  static constexpr uint32_t OFF_COLP = OFF_BIAS + 2 * BN * 4;
-  static constexpr uint32_t OFF_STG = (OFF_COLP + 2 * 4 * BN * 4 + 1023) / 1024 * 1024;
+  static constexpr uint32_t OFF_COLP = OFF_BIAS + (LEAN ? 0 : 2 * BN * 4);
+  static constexpr uint32_t OFF_STG = (OFF_COLP + (LEAN ? 0 : 2 * 4 * BN * 4) + 1023) / 1024 * 1024;
   static constexpr uint32_t OFF_AUXSTG = OFF_STG + BLOCKS * 2048 * 4;
-  static constexpr uint32_t END = OFF_AUXSTG + (BLOCKS == 2 ? kAuxStageBytesPerWarp * 4 : 0);
+  static constexpr uint32_t END = OFF_AUXSTG + (EPI == EPI_GATED || LEAN ? 0 : kAuxStageBytesPerWarp * 4);
   static constexpr uint32_t BYTES = END + 1024;               // + alignment slack
 };
 
@@ -612,8 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmAux,
                 const TileParams p) {
-  constexpr int SB = StageBlocks<EPI, BN, false>::value;
-  using L = TileSmem<BN, STAGES, SB>;
+  using L = TileSmem<BN, STAGES, EPI>;
+  constexpr int SB = L::BLOCKS;
+  // gated layers: the producer and MMA warps walk their loops whole and one
+  // elected lane issues (elect_one); under a branch on the lane, between the
+  // instructions of a long epilogue, the MMAs were issued too late
+  constexpr bool WARP_ISSUE = IsGated<EPI>::value;
   constexpr bool GATED = EPI == EPI_GATED;
   static_assert(!GATED || BN % 128 == 0, "a gated tile's halves are whole 64-column chunks");
   constexpr int BNO = GATED ? BN / 2 : BN;  // output columns of a tile
@@ -675,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (WARP_ISSUE || lane == 0) {
+      const bool issuer = !WARP_ISSUE || elect_one();
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < p.num_tiles; tile += gridDim.x) {
@@ -685,27 +694,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
-          if (!wait_bounded(&empty[s], ph ^ 1u, p, abort_flag, 1)) {
+          bool got = wait_bounded(&empty[s], ph ^ 1u, p, abort_flag, 1);
+          if constexpr (WARP_ISSUE) got = __all_sync(0xffffffffu, got);
+          if (!got) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], STAGE_TX);
-          if constexpr (A_MN) {
-            tma_load_2d(sA + s * L::A_BYTES, &tmA, &full[s], m0, kb * kBK);
-            tma_load_2d(sA + s * L::A_BYTES + kAChunkMN, &tmA, &full[s], m0 + 64, kb * kBK);
-          } else {
-            tma_load_2d(sA + s * L::A_BYTES, &tmA, &full[s], kb * kBK, m0);
-          }
-          if constexpr (BK && GATED) {  // a box of BN / 2 features from each half of the weight
-            tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
-            tma_load_2d(sB + s * L::B_BYTES + L::B_BYTES / 2, &tmB, &full[s], kb * kBK, p.N + n0);
-          } else if constexpr (BK) {
-            tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
-          } else {
+          if (issuer) {
+            mbar_arrive_expect_tx(&full[s], STAGE_TX);
+            if constexpr (A_MN) {
+              tma_load_2d(sA + s * L::A_BYTES, &tmA, &full[s], m0, kb * kBK);
+              tma_load_2d(sA + s * L::A_BYTES + kAChunkMN, &tmA, &full[s], m0 + 64, kb * kBK);
+            } else {
+              tma_load_2d(sA + s * L::A_BYTES, &tmA, &full[s], kb * kBK, m0);
+            }
+            if constexpr (BK && GATED) {  // a box of BN / 2 features from each half of the weight
+              tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
+              tma_load_2d(sB + s * L::B_BYTES + L::B_BYTES / 2, &tmB, &full[s], kb * kBK, p.N + n0);
+            } else if constexpr (BK) {
+              tma_load_2d(sB + s * L::B_BYTES, &tmB, &full[s], kb * kBK, n0);
+            } else {
 #pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, &full[s],
-                          (GATED && j >= BN / 128 ? p.N - BNO : 0) + n0 + j * 64, kb * kBK);
+              for (int j = 0; j < BN / 64; ++j)
+                tma_load_2d(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, &full[s],
+                            (GATED && j >= BN / 128 ? p.N - BNO : 0) + n0 + j * 64, kb * kBK);
+            }
           }
         }
       }
@@ -717,40 +730,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
+    if (WARP_ISSUE || lane == 0) {
+      const bool issuer = !WARP_ISSUE || elect_one();
       uint32_t it = 0, tcount = 0;
       bool ok = true;
       constexpr uint32_t idesc = BK ? IDESC_BK : IDESC;
       for (int tile = blockIdx.x; ok && tile < p.num_tiles; tile += gridDim.x, ++tcount) {
         const uint32_t buf = tcount & 1u;
         const uint32_t tph = (tcount >> 1) & 1u;
-        if (!wait_bounded(&tempty[buf], tph ^ 1u, p, abort_flag, 3)) break;
+        bool room = wait_bounded(&tempty[buf], tph ^ 1u, p, abort_flag, 3);
+        if constexpr (WARP_ISSUE) room = __all_sync(0xffffffffu, room);
+        if (!room) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * BN;
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
-          if (!wait_bounded(&full[s], ph, p, abort_flag, 4)) {
+          bool got = wait_bounded(&full[s], ph, p, abort_flag, 4);
+          if constexpr (WARP_ISSUE) got = __all_sync(0xffffffffu, got);
+          if (!got) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
-          const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
+          if (issuer) {
+            const uint32_t a0 = smem_u32(sA + s * L::A_BYTES);
+            const uint32_t b0 = smem_u32(sB + s * L::B_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint64_t adesc = a_desc<A_MN>(a0, kk);
-            const uint64_t bdesc = b_desc(b0, kk, BK, L::B_CHUNK);
-            umma_f16(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              const uint64_t adesc = a_desc<A_MN>(a0, kk);
+              const uint64_t bdesc = b_desc(b0, kk, BK, L::B_CHUNK);
+              umma_f16(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+            umma_commit(&empty[s]);
           }
-          umma_commit(&empty[s]);
         }
         if (!ok) break;
         // (fault injection: the epilogue then waits on a barrier nothing arrives on)
-        if (!(p.inject_stall && tcount == 0)) umma_commit(&tfull[buf]);
+        if (issuer && !(p.inject_stall && tcount == 0)) umma_commit(&tfull[buf]);
       }
       // every MMA issued above must finish before tensor memory is freed
-      umma_commit(drain);
+      if (issuer) umma_commit(drain);
       wait_bounded(drain, 0, p, abort_flag, 5, /*honour_abort=*/false);
     }
     __syncwarp();
@@ -762,6 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t scount = 0;
     uint32_t tcount = 0;
     bool ok = true;
+    DGatedStream<TileSource<BN>> gin(p, stg, TileSource<BN>{static_cast<int>(blockIdx.x), static_cast<int>(ew * 32)});
+    if constexpr (EPI == EPI_DGATED) gin.start();
     for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++tcount) {
       int mb, nb;
       tile_coords(tile, p.m_tiles, p.n_tiles, p.group_m, p.raster_n, mb, nb);
@@ -773,8 +795,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       epi_stage_bias<BN, EPI, BF16>(p, n0, bs, et);
       if constexpr (GATED) gated_stage_bias<BN, BF16, 128>(p, n0, bs, et, BNO);
       const int row = m0 + static_cast<int>(ew * 32 + lane);
-      DGatedInput gin{};
-      if constexpr (EPI == EPI_DGATED) gin = dgated_load(p, row, n0);
       MaskWords<BN> mw{};
       if constexpr (EPI == EPI_DRELU_BGRAD) mw = load_mask_words<BN>(p, m0 + static_cast<int>(ew * 32 + lane), n0);
       named_bar_sync(1, 128);
@@ -787,8 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           gated_rows<BF16, SB>(p, trow, trow + BNO, n0, BNO, bs, bs + BNO, &tmY, &tmAux, stg, scount,
                               m0 + static_cast<int>(ew * 32));
         else if constexpr (EPI == EPI_DGATED)
-          dgated_rows<BF16, SB>(p, trow, row, n0, BN, gin, colp_s + ew * (2 * BN), BN, &tmY, stg, scount,
-                               m0 + static_cast<int>(ew * 32));
+          dgated_rows<BF16>(p, trow, m0 + static_cast<int>(ew * 32), n0, BN, gin);
         else
           epi_rows<BN, EPI, BF16>(p, trow, row, n0, bs, cp + ew * BN, &tmY, stg, scount, m0 + static_cast<int>(ew * 32),
                                   &tmAux, auxstg_s + ew * kAuxStageBytesPerWarp, mw);
@@ -801,14 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) epi_write_partials<BN>(p, mb, n0, cp, et);
         if (p.col_tickets) epi_finish_dbias<BN>(p, nb, n0, ok ? 1 : 0, et, dflag);
       }
-      if constexpr (EPI == EPI_DGATED) {
-        if (p.dbias) {
-          named_bar_sync(1, 128);
-          if (ok) dgated_write_partials<BN, 128>(p, mb, n0, colp_s, et, BN);
-          dgated_finish_dbias<128>(p, nb, n0, ok ? 1 : 0, et, dflag, BN, 1);
-        }
-      }
     }
+    if constexpr (EPI == EPI_DGATED) cp_async_wait<0>();
     if (lane == 0) bulk_wait_group_all();  // this warp's output stores are complete
     __syncwarp();
   }

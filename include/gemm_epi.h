@@ -132,7 +132,7 @@ typedef struct {
                           number of rows; a call that finds others may share a tile among fewer or
                           more CTAs (at most 16) */
   int grid;            /* CTAs launched by the main kernel */
-  int launches;        /* kernel launches per execute call (a WGRAD call with dbias: 2 more, grouped 1 more) */
+  int launches;        /* kernel launches per execute call (a WGRAD call with dbias: 2 more, grouped 1 more; DGATED with dbias 1 more) */
   int num_sms;
   size_t workspace_bytes;
 } gemm_epi_info;
