@@ -83,7 +83,7 @@ enum ActKind : int { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU = 2 };
 //   SILU  a = z p, p = 1 / (1 + e^-z);  d = p (1 + z (1 - p)) = p + a (1 - p)
 //   GELU  a = max(z, 0) - |z| h(|z|);   d = Phi(z) + z phi(z), Phi(z) = h(-z) or 1 - h(z)
 //   RELU  a = max(z, 0), of NaN 0;      d = 1 where z > 0
-// The exponential is off by 2 + 1.2 |z| ulp, the reciprocal by 1: p's 1e-6 at |z| =
+// The exponential is off by 2 ulp and its rounded argument's |z| ulp, the reciprocal by 1: p's 1e-6 at |z| =
 // 10 is far below the 16 bits that the inputs of d and nearly all outputs are
 // rounded to. p is 0 from z = -88.7 on, where e^-z leaves fp32; -inf gives NaN, as
 // -inf x 0 does.
@@ -97,7 +97,7 @@ __device__ __forceinline__ void act_values(int act, const float (&z)[M], float (
   if (act == ACT_SILU) {
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const float p = reciprocal(1.f + __expf(-z[j]));
+      const float p = reciprocal(1.f + exp2_ftz(-1.44269504f * z[j]));
       a[j] = z[j] * p;
       if constexpr (DERIV) d[j] = fmaf(a[j], 1.f - p, p);
     }

@@ -17,9 +17,9 @@ ge_inst::GatedInstance instance(bool bf16, bool w_nk, int bn, bool pair, int epi
   return w_nk ? ge_inst::gated_f16_nk(bn, pair, epi) : ge_inst::gated_f16_mn(bn, pair, epi);
 }
 
-ge_inst::GatedSkinnyInstance skinny_instance(bool bf16, bool w_nk, int tp) {
-  if (bf16) return w_nk ? ge_inst::gated_skinny_bf16_nk(tp) : ge_inst::gated_skinny_bf16_mn(tp);
-  return w_nk ? ge_inst::gated_skinny_f16_nk(tp) : ge_inst::gated_skinny_f16_mn(tp);
+ge_inst::GatedSkinnyInstance skinny_instance(bool bf16, bool w_nk, int tp, int gn) {
+  if (bf16) return w_nk ? ge_inst::gated_skinny_bf16_nk(tp, gn) : ge_inst::gated_skinny_bf16_mn(tp, gn);
+  return w_nk ? ge_inst::gated_skinny_f16_nk(tp, gn) : ge_inst::gated_skinny_f16_mn(tp, gn);
 }
 
 // Accumulator columns that tiles of bn cover: a gated tile is half gate, half up.
@@ -27,9 +27,11 @@ int64_t columns(int64_t N, bool forward, int bn) {
   return forward ? (N + bn / 2 - 1) / (bn / 2) * bn : N;
 }
 
-// Tiles as the dense plans choose them (GEMM_EPI_FORCE_BN and _FORCE_KERNEL
-// override where there is such an instance): the least estimate, CTA pairs when
-// there is a wave of their tiles, X at most 1 GiB, and they are estimated no slower.
+// Tiles by the dense plans' estimates (GEMM_EPI_FORCE_BN and _FORCE_KERNEL override
+// where there is such an instance): CTA pairs for X of at most 1 GiB where they
+// are estimated no slower, also with less than a wave of their tiles (DGATED, fp16,
+// us, tiles / pairs: T = 160, K = 4096, N = 11008 40 / 35; T = 1024, K = N = 4096 38.5 /
+// 35.5; GATED, T = 300, K = 2048, N = 4096 17.6 / 17.9).
 int choose_bn(int64_t T, int64_t N, int64_t K, bool forward, int sms) {
   if (const char* f = getenv("GEMM_EPI_FORCE_BN")) {
     const int v = atoi(f);
@@ -51,19 +53,20 @@ int choose_bn(int64_t T, int64_t N, int64_t K, bool forward, int sms) {
 bool use_pair(int64_t T, int64_t N, int64_t K, bool forward, int bn, int sms) {
   if (const char* f = getenv("GEMM_EPI_FORCE_KERNEL")) {
     if (!strcmp(f, "tile") || !strcmp(f, "skinny")) return false;
-    if (!strcmp(f, "pair")) return T > 128;
+    if (!strcmp(f, "pair")) return T > 32;
   }
   if (T <= 128 || T * K * 2 > ((int64_t)1 << 30)) return false;
-  const int64_t cols = columns(N, forward, 256), tiles = ((T + 255) / 256) * ((cols + 255) / 256);
-  return tiles >= sms / 2 && est_pair_us(T, cols, K, sms / 2) <= est_tile_us(T, columns(N, forward, bn), K, bn, sms);
+  return est_pair_us(T, columns(N, forward, 256), K, sms / 2) <= est_tile_us(T, columns(N, forward, bn), K, bn, sms);
 }
 
+// The few-row kernel for T <= 32. Measured (us, few-row / tiles): K = 4096, N =
+// 11008, T = 32 31.3 / 35, T = 64 41.8 / 35.2, T = 128 47.9 / 35.5; K = 2048, N = 5632,
+// T = 64 25.8 / 13.8.
 bool use_skinny(int64_t T) {
   if (const char* f = getenv("GEMM_EPI_FORCE_KERNEL")) {
     if (!strcmp(f, "tile")) return false;
-    if (!strcmp(f, "pair")) return T <= 128;
   }
-  return T <= 128;
+  return T <= 32;
 }
 
 // The pre-activations, T x 2N, as rows of two matrices of N columns, in blocks of 32
@@ -92,25 +95,27 @@ void release(gemm_epi_plan_s* p) {
   delete p;
 }
 
-// The few-row kernel's schedule, as the dense plans lay it out (64 features of H
-// a tile): whole tiles where there are between half as many as SMs and as many,
-// else equal shares of all k-blocks, at least four stages of 128 k each.
+// The few-row kernel's schedule: whole tiles where there are between half as many
+// as SMs and as many -- of 128 features of H if there are that many, else of 64 -- and
+// otherwise equal shares of all k-blocks, at least 256 k each.
 cudaError_t plan_skinny(gemm_epi_plan_s* p, bool bf16, int sms) {
-  const int tp = p->T <= 16 ? 16 : p->T <= 32 ? 32 : p->T <= 64 ? 64 : 128;
-  const ge_inst::GatedSkinnyInstance inst = skinny_instance(bf16, p->w_nk != 0, tp);
+  const int tp = p->T <= 16 ? 16 : 32;
+  const int gn = 2 * ceil_div(p->N, 128) >= sms ? 128 : 64;
+  const ge_inst::GatedSkinnyInstance inst = skinny_instance(bf16, p->w_nk != 0, tp, gn);
   p->kernel = 1;
   p->sk.TP = tp;
   p->sk.KPS = 2;
   p->sk.fn = inst.fn;
   p->sk.smem = inst.smem;
   p->sk.stages = inst.stages;
-  const int n_tiles = ceil_div(p->N, 64);
+  p->sk_features = gn;
+  const int n_tiles = ceil_div(p->N, gn);
   p->sk_kbt = ceil_div(p->K, (int64_t)ge::kBK * 2);
   p->sk_total = n_tiles * p->sk_kbt;
   if (n_tiles * 2 >= sms && n_tiles <= sms) {
     p->sk_grid = n_tiles;
   } else {
-    const int g = p->sk_total / 4;
+    const int g = p->sk_total / 2;
     p->sk_grid = g < 1 ? 1 : g < sms ? g : sms;
   }
   if (const char* f = getenv("GEMM_EPI_SKINNY_GRID")) {  // tuning override
@@ -124,7 +129,7 @@ cudaError_t plan_skinny(gemm_epi_plan_s* p, bool bf16, int sms) {
   }
   cudaError_t e = cudaFuncSetAttribute(p->sk.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p->sk.smem);
   if (e != cudaSuccess || p->sk_max_segs == 1) return e;
-  p->sk_bytes = (size_t)n_tiles * p->sk_max_segs * tp * 128 * sizeof(float);
+  p->sk_bytes = (size_t)n_tiles * p->sk_max_segs * (gn / 64) * tp * 128 * sizeof(float);
   e = cudaMalloc((void**)&p->sk_partials, p->sk_bytes);
   if (e != cudaSuccess) return e;
   e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * (size_t)n_tiles);
@@ -160,7 +165,8 @@ cudaError_t plan_tiles(gemm_epi_plan_s* p, bool bf16, bool forward, int sms) {
   if (pair) {
     const int tiles = ceil_div(p->T, 256) * p->n_tiles;
     const int pairs = resident_pairs((const void*)p->cfg.fn, p->cfg.threads, p->cfg.smem, sms);
-    p->grid = 2 * (tiles < pairs ? tiles : pairs);
+    // (at most half as many tiles as pairs: a pair for each half of a tile)
+    p->grid = 2 * (p->tail_split && 2 * tiles <= pairs ? 2 * tiles : tiles < pairs ? tiles : pairs);
   } else {
     p->grid = p->num_tiles < sms ? p->num_tiles : sms;
   }
@@ -271,14 +277,14 @@ int launch_tiles(gemm_epi_plan_s* p, const CUtensorMap& a, const CUtensorMap& b,
 int run_skinny(gemm_epi_plan_s* p, const void* X, const void* W, const void* bias, void* H, void* aux,
                cudaStream_t stream) {
   CUtensorMap w, x;
-  int rc = encode_weight(&w, p, W, 2 * p->N, 2 * ge::kBK, 64);
+  int rc = encode_weight(&w, p, W, 2 * p->N, 2 * ge::kBK, (uint32_t)p->sk_features);
   if (!rc) rc = encode_2d(&x, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, (uint32_t)p->sk.TP, "the row operand");
   if (rc) return rc;
   ge::SkinnyParams k{};
   k.T = (int32_t)p->T;
   k.N = (int32_t)p->N;
   k.K = (int32_t)p->K;
-  k.n_tiles = ceil_div(p->N, 64);
+  k.n_tiles = ceil_div(p->N, p->sk_features);
   k.kbt = p->sk_kbt;
   k.total_kb = p->sk_total;
   k.max_segs = p->sk_max_segs;
@@ -332,7 +338,7 @@ int gemm_epi_gated_execute(gemm_epi_plan_t plan, const void* X, const void* W, c
   if (p->kernel == 1) return run_skinny(p, X, W, bias, H, aux, stream);
   CUtensorMap a, b, y, z;
   rc = encode_2d(&a, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, ge::kBM, "the row operand");
-  if (!rc) rc = encode_weight(&b, p, W, 2 * p->N, ge::kBK, p->cfg.pair ? 128u : (uint32_t)p->cfg.BN / 2);
+  if (!rc) rc = encode_weight(&b, p, W, 2 * p->N, ge::kBK, p->cfg.pair ? 64u : (uint32_t)p->cfg.BN / 2);
   if (!rc) rc = p->out_f32 ? encode_out_f32(&y, H, p->T, p->N) : encode_out(&y, H, p->T, p->N);
   if (!rc && aux) rc = encode_halves(&z, aux, p->T, p->N);
   if (rc) return rc;
@@ -358,7 +364,7 @@ int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, const void* W2
   if (rc) return rc;
   CUtensorMap a, b;
   rc = encode_2d(&a, dY, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, ge::kBM, "dY");
-  if (!rc) rc = encode_weight(&b, p, W2, p->N, ge::kBK, p->cfg.pair ? 128u : (uint32_t)p->cfg.BN);
+  if (!rc) rc = encode_weight(&b, p, W2, p->N, ge::kBK, p->cfg.pair ? 64u : (uint32_t)p->cfg.BN);
   if (rc) return rc;
   ge::TileParams k{};
   k.out = dZ;

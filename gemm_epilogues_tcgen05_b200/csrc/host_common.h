@@ -290,6 +290,7 @@ struct gemm_epi_plan_s {
   // few-row kernel (kernel == 1)
   int kernel = 0;
   ge_host::SkinnyCfg sk;
+  int sk_features = 128;  // gated: features of H in a tile
   int sk_grid = 0, sk_kbt = 0, sk_total = 0, sk_max_segs = 1, sk_prefetch = 0;
   float* sk_partials = nullptr;
   int* sk_tickets = nullptr;

@@ -31,18 +31,16 @@ GatedInstance gated_any(int bn, bool pair, int epi) {
   return {};
 }
 
-template <int TP, bool BF, bool BK>
+template <int TP, int GN, bool BF, bool BK>
 GatedSkinnyInstance gated_skinny_tp() {
-  using L = ge::SkinnySmem<TP, 2, true>;
-  return {ge::skinny_kernel<TP, 2, ge::EPI_GATED, BF, BK>, L::BYTES, L::STAGES};
+  using L = ge::SkinnySmem<TP, 2, GN>;
+  return {ge::skinny_kernel<TP, 2, ge::EPI_GATED, BF, BK, GN>, L::BYTES, L::STAGES};
 }
 
 template <bool BF, bool BK>
-GatedSkinnyInstance gated_skinny_any(int tp) {
-  return tp == 16   ? gated_skinny_tp<16, BF, BK>()
-         : tp == 32 ? gated_skinny_tp<32, BF, BK>()
-         : tp == 64 ? gated_skinny_tp<64, BF, BK>()
-                    : gated_skinny_tp<128, BF, BK>();
+GatedSkinnyInstance gated_skinny_any(int tp, int gn) {
+  if (tp == 16) return gn == 128 ? gated_skinny_tp<16, 128, BF, BK>() : gated_skinny_tp<16, 64, BF, BK>();
+  return gn == 128 ? gated_skinny_tp<32, 128, BF, BK>() : gated_skinny_tp<32, 64, BF, BK>();
 }
 
 }  // namespace ge_inst

@@ -3,5 +3,5 @@
 
 namespace ge_inst {
 GatedInstance gated_bf16_mn(int bn, bool pair, int epi) { return gated_any<true, false>(bn, pair, epi); }
-GatedSkinnyInstance gated_skinny_bf16_mn(int tp) { return gated_skinny_any<true, false>(tp); }
+GatedSkinnyInstance gated_skinny_bf16_mn(int tp, int gn) { return gated_skinny_any<true, false>(tp, gn); }
 }  // namespace ge_inst

@@ -3,5 +3,5 @@
 
 namespace ge_inst {
 GatedInstance gated_bf16_nk(int bn, bool pair, int epi) { return gated_any<true, true>(bn, pair, epi); }
-GatedSkinnyInstance gated_skinny_bf16_nk(int tp) { return gated_skinny_any<true, true>(tp); }
+GatedSkinnyInstance gated_skinny_bf16_nk(int tp, int gn) { return gated_skinny_any<true, true>(tp, gn); }
 }  // namespace ge_inst

@@ -3,5 +3,5 @@
 
 namespace ge_inst {
 GatedInstance gated_f16_nk(int bn, bool pair, int epi) { return gated_any<false, true>(bn, pair, epi); }
-GatedSkinnyInstance gated_skinny_f16_nk(int tp) { return gated_skinny_any<false, true>(tp); }
+GatedSkinnyInstance gated_skinny_f16_nk(int tp, int gn) { return gated_skinny_any<false, true>(tp, gn); }
 }  // namespace ge_inst

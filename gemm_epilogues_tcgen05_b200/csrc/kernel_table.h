@@ -78,16 +78,16 @@ GatedInstance gated_f16_nk(int bn, bool pair, int epi);
 GatedInstance gated_bf16_mn(int bn, bool pair, int epi);
 GatedInstance gated_bf16_nk(int bn, bool pair, int epi);
 
-// The few-row kernel for EPI_GATED: tp = 16, 32, 64 or 128 padded rows, two
-// k-blocks a stage.
+// The few-row kernel for EPI_GATED: tp = 16 or 32 padded rows, tiles of
+// gn = 64 or 128 features of H, two k-blocks a stage.
 struct GatedSkinnyInstance {
   SkinnyKernelFn fn;
   uint32_t smem;
   int stages;
 };
-GatedSkinnyInstance gated_skinny_f16_mn(int tp);
-GatedSkinnyInstance gated_skinny_f16_nk(int tp);
-GatedSkinnyInstance gated_skinny_bf16_mn(int tp);
-GatedSkinnyInstance gated_skinny_bf16_nk(int tp);
+GatedSkinnyInstance gated_skinny_f16_mn(int tp, int gn);
+GatedSkinnyInstance gated_skinny_f16_nk(int tp, int gn);
+GatedSkinnyInstance gated_skinny_bf16_mn(int tp, int gn);
+GatedSkinnyInstance gated_skinny_bf16_nk(int tp, int gn);
 
 }  // namespace ge_inst

@@ -52,20 +52,26 @@ struct SkinnyParams {
 // 16 KB stages with the same bytes in flight (a load-only stream of W, 4096 x
 // 11008, over 86 CTAs).
 //
-// GATED (a gated layer's forward): the 128 lanes are the gate's pre-activations
-// of 64 features and the up projection's of the same 64, one 64-feature chunk of
-// A from each half of the weight. The epilogue warps of the two halves exchange
-// through shared memory (XCHG), 16 rows at a time, and each finishes 8 of them.
-template <int TP, int KPS, bool GATED = false>
+// GN (a gated layer's forward; 0 otherwise) is the features of H in a tile:
+//   128  the gate's and the up projection's weights are two A operands with an
+//        accumulator each, so that a thread finds both pre-activations of its
+//        feature in its own lane, and W comes in runs of 256 bytes;
+//   64   both in one operand and one accumulator, the gate's in lanes 0..63: half
+//        as much weight a tile, for weights with few tiles. The two halves of the
+//        epilogue warps exchange pre-activations through shared memory (XCHG).
+// Measured (T = 8, us, 64 / 128): K = 4096, N = 11008 37 / 29.7 (K x N), 31.7 / 32.4
+// (N x K); K = 2048, N = 5632 11.2 / 14.5; K = 1024, N = 2048 6.4 / 8.5.
+template <int TP, int KPS, int GN = 0>
 struct SkinnySmem {
   static constexpr int BK = kBK * KPS;                 // k per stage
   static constexpr uint32_t A_CHUNK = 64 * BK * 2;     // one 64-feature chunk x BK k-rows
-  static constexpr uint32_t A_BYTES = 2 * A_CHUNK;     // 128 features
+  static constexpr uint32_t A_OP = 2 * A_CHUNK;        // 128 features
+  static constexpr uint32_t A_BYTES = (GN == 128 ? 2 : 1) * A_OP;
   static constexpr uint32_t A_SUB = 64 * kBK * 2;      // 64 k-rows of one chunk (8 KB)
   static constexpr uint32_t B_SUB = TP * kBK * 2;      // TP rows x 128 B (one 64-k block of X)
   static constexpr uint32_t B_BYTES = KPS * B_SUB;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-  static constexpr uint32_t XCHG = GATED ? 2 * 16 * 64 * 4 : 0;
+  static constexpr uint32_t XCHG = GN == 64 ? 2 * 16 * 64 * 4 : 0;
   static constexpr int STAGES = ((230400 - XCHG) / STAGE) > 12 ? 12 : ((230400 - XCHG) / STAGE);
   static constexpr uint32_t OFF_A = 0;
   static constexpr uint32_t OFF_B = OFF_A + STAGES * A_BYTES;
@@ -230,40 +236,99 @@ __device__ __forceinline__ void skinny_finish16(const SkinnyParams& p, float (&v
   }
 }
 
-// GATED: 16 rows t0 .. t0 + 15 of this thread's pre-activation (v, the bias not
-// yet added) -- feature n of half `half` (0: the gate). Rows 8 (1 - half) .. + 7 go to the
-// thread of the other half through xchg ([16][64] floats), the other 8 are
-// finished here. Called by the 128 epilogue threads alike; `turn` picks one of
-// two buffers, so that one barrier a call is enough (a buffer is written again
-// only after the barrier of the call between, which its readers have passed).
-template <bool BF16>
-__device__ __forceinline__ void skinny_gated16(const SkinnyParams& p, float (&v)[16], int t0, int n, bool n_ok, int half,
-                                               float bias_n, float* xchg, uint32_t& turn) {
-  float* buf = xchg + (turn & 1u) * (16 * 64) + (n & 63);
-  turn ^= 1u;
+// What a thread of a gated tile has of its feature n: the biases, and with GN = 64
+// its half (0: the gate) and the exchange's place.
+struct GatedLane {
+  int n;
+  bool n_ok;
+  float bias_g, bias_u;
+  int half;
+  float* xchg;    // [2][16][64]
+  uint32_t turn;  // which of the two is next: with two, one barrier a call is enough (a
+                  // buffer is written again only after the call between, whose
+                  // barrier its readers have passed)
+};
+
+// 16 rows t0 .. t0 + 15 of this thread's pre-activations, the biases not yet added:
+// GN = 128: gate (g) and up projection (u) of feature n. GN = 64: g holds those of
+// this thread's half; 8 rows go to the thread of the other half, the other 8 are
+// finished here. Called by the 128 epilogue threads alike.
+template <int GN, bool BF16>
+__device__ __forceinline__ void skinny_gated16(const SkinnyParams& p, float (&g)[16], float (&u)[16], int t0, GatedLane& w) {
+  float none[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    v[j] += bias_n;
+    g[j] += GN == 64 && w.half ? w.bias_u : w.bias_g;
+    if constexpr (GN == 128) u[j] += w.bias_u;
     const int t = t0 + j;
-    if (p.aux_out && n_ok && t < p.T)
-      store_16<BF16>(p.aux_out, (static_cast<int64_t>(t) * 2 + half) * p.N + n, v[j]);
+    if (p.aux_out && w.n_ok && t < p.T) {
+      const int64_t at = static_cast<int64_t>(t) * 2 * p.N + w.n;
+      store_16<BF16>(p.aux_out, at + (GN == 64 && w.half ? p.N : 0), g[j]);
+      if constexpr (GN == 128) store_16<BF16>(p.aux_out, at + p.N, u[j]);
+    }
   }
-  // (static indices: v stays in registers)
+  constexpr int ROWS = GN == 128 ? 16 : 8;
+  float a[ROWS], b[ROWS];
+  if constexpr (GN == 128) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) buf[(half ? j : 8 + j) * 64] = half ? v[j] : v[8 + j];
-  named_bar_sync(2, 128);
-  float g[8], u[8], none[8];
+    for (int j = 0; j < 16; ++j) {
+      a[j] = g[j];
+      b[j] = u[j];
+    }
+  } else {
+    float* buf = w.xchg + (w.turn & 1u) * (16 * 64) + (w.n & 63);
+    w.turn ^= 1u;
+    // (static indices: g stays in registers)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float mine = half ? v[8 + j] : v[j], other = buf[(half ? 8 + j : j) * 64];
-    g[j] = half ? other : mine;
-    u[j] = half ? mine : other;
+    for (int j = 0; j < 8; ++j) buf[(w.half ? j : 8 + j) * 64] = w.half ? g[j] : g[8 + j];
+    named_bar_sync(2, 128);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float mine = w.half ? g[8 + j] : g[j], other = buf[(w.half ? 8 + j : j) * 64];
+      a[j] = w.half ? other : mine;
+      b[j] = w.half ? mine : other;
+    }
+    t0 += 8 * w.half;
   }
-  act_values<8, false>(p.act, g, g, none);
+  float d[ROWS];
+  act_values<ROWS, false>(p.act, a, a, d);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int t = t0 + 8 * half + j;
-    if (n_ok && t < p.T) store_out<BF16, 2>(p, static_cast<int64_t>(t) * p.N + n, g[j] * u[j]);
+  for (int j = 0; j < ROWS; ++j)
+    if (w.n_ok && t0 + j < p.T) store_out<BF16, 2>(p, static_cast<int64_t>(t0 + j) * p.N + w.n, a[j] * b[j]);
+}
+
+// The segments' partials of one gated tile (GN = 128: [gate, up][TP][128]; 64:
+// [TP][128]), 16 rows at a time, summed in segment order, four segments' loads in
+// flight.
+template <int GN, int TP, bool BF16>
+__device__ __forceinline__ void skinny_gated_fixup(const SkinnyParams& p, const float* base, int nsegs, GatedLane& w) {
+  constexpr int SEG = (GN / 64) * TP * 128;
+#pragma unroll 1
+  for (int t0 = 0; t0 < TP; t0 += 16) {
+    if (t0 >= p.T) break;
+    float g[16], u[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) g[j] = u[j] = 0.f;
+    for (int s0 = 0; s0 < nsegs; s0 += 4) {
+      float x[4][16], y[4][16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float* at = base + static_cast<int64_t>(s0 + i) * SEG + (t0 + j) * 128;
+          const bool in = s0 + i < nsegs && t0 + j < p.T;
+          x[i][j] = in ? __ldcg(at) : 0.f;
+          if constexpr (GN == 128) y[i][j] = in ? __ldcg(at + TP * 128) : 0.f;
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          g[j] += x[i][j];
+          if constexpr (GN == 128) u[j] += y[i][j];
+        }
+    }
+    skinny_gated16<GN, BF16>(p, g, u, t0, w);
   }
 }
 
@@ -273,8 +338,7 @@ __device__ __forceinline__ void skinny_gated16(const SkinnyParams& p, float (&v)
 // L2 round trips; issued one by one they would dominate the kernel).
 template <int S, int TP, int EPI, bool BF16>
 __device__ __forceinline__ void skinny_fixup(const SkinnyParams& p, const float* base, int nsegs, int n, bool n_ok,
-                                             int word, float bias_n, float& dbias_acc, int half, float* xchg,
-                                             uint32_t& turn) {
+                                             int word, float bias_n, float& dbias_acc) {
   constexpr int SEG = TP * 128;
   constexpr int RB = TP < 32 ? TP : 32;  // rows per batch
 #pragma unroll 1
@@ -312,27 +376,26 @@ __device__ __forceinline__ void skinny_fixup(const SkinnyParams& p, const float*
       float w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = v[h * 16 + j];
-      if constexpr (EPI == EPI_GATED)
-        skinny_gated16<BF16>(p, w, t0 + h * 16, n, n_ok, half, bias_n, xchg, turn);
-      else
-        skinny_finish16_rows<EPI, BF16, 2, false>(p, w, t0 + h * 16, n, n_ok, word, bias_n, dbias_acc, mk[h]);
+      skinny_finish16_rows<EPI, BF16, 2, false>(p, w, t0 + h * 16, n, n_ok, word, bias_n, dbias_acc, mk[h]);
     }
   }
 }
 
-// BK (gated layers only): the weight is given N x K, its chunks of 64 features
-// are staged K-major, one box of 64 k each.
-template <int TP, int KPS, int EPI, bool BF16, bool BK = false>
+// BK (gated layers only): the weight is given N x K, staged K-major in boxes of 64
+// k x GN features. GN: see SkinnySmem.
+template <int TP, int KPS, int EPI, bool BF16, bool BK = false, int GN = 0>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const SkinnyParams p) {
   constexpr bool GATED = EPI == EPI_GATED;
-  using L = SkinnySmem<TP, KPS, GATED>;
+  static_assert(GATED ? GN == 64 || GN == 128 : GN == 0, "features of H in a gated tile");
+  using L = SkinnySmem<TP, KPS, GN>;
+  constexpr int TN = GN == 64 ? 64 : 128;  // output features of a tile
   constexpr int STAGES = L::STAGES;
-  constexpr int TN = GATED ? 64 : 128;  // output features of a tile
   static_assert(GATED || !BK, "N x K weights: gated layers only");
   static_assert(TP == 16 || TP == 32 || TP == 64 || TP == 128 || TP == 256, "TP must be a power of two in [16, 256]");
-  constexpr uint32_t TMEM_COLS = 2 * TP < 32 ? 32 : 2 * TP;
+  constexpr uint32_t DC = GN == 128 ? 2 * TP : TP;  // columns of an accumulator (the gate's, then the up projection's)
+  constexpr uint32_t TMEM_COLS = 2 * DC < 32 ? 32 : 2 * DC;
   constexpr uint32_t IDESC = idesc_f16(BF16, /*A MN-major*/ !BK, /*B MN-major*/ false, 128, TP);
 
   extern __shared__ uint8_t smem_raw[];
@@ -408,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
       while (ok && skinny_segment(p, hi, g, s)) {
         const int n0 = s.tile * TN;
-        const int n1 = GATED ? p.N + n0 : n0 + 64;  // the second chunk of 64 features
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++it, ++gk) {
           if (p.prefetch > 0) prefetch_upto(gk + static_cast<uint32_t>(p.prefetch));
           const uint32_t st = it % STAGES;
@@ -418,23 +480,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[st], L::STAGE);
-          if constexpr (BK) {  // per 64 k: 64 features of the gate, then 64 of the up projection, 8 KB each
+          if constexpr (GATED) {
 #pragma unroll
-            for (int j = 0; j < KPS; ++j) {
-              uint8_t* a = sA + st * L::A_BYTES + j * 2 * L::A_SUB;
-              tma_load_2d_hint(a, &tmW, &full[st], kb * L::BK + j * kBK, n0, pol_w);
-              tma_load_2d_hint(a + L::A_SUB, &tmW, &full[st], kb * L::BK + j * kBK, n1, pol_w);
-              tma_load_2d_hint(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0, pol_x);
+            for (int m = 0; m < 2; ++m) {  // the gate's features, the up projection's
+              const int nm = m * p.N + n0;
+              uint8_t* a = sA + st * L::A_BYTES;
+              if constexpr (BK) {  // per 64 k: all of an operand's features
+#pragma unroll
+                for (int j = 0; j < KPS; ++j)
+                  tma_load_2d_hint(GN == 128 ? a + m * L::A_OP + j * 2 * L::A_SUB : a + (2 * j + m) * L::A_SUB, &tmW,
+                                   &full[st], kb * L::BK + j * kBK, nm, pol_w);
+              } else {  // per 64 features: all k of a stage
+#pragma unroll
+                for (int c = 0; c < GN / 64; ++c)
+                  tma_load_2d_hint(a + (m * (GN / 64) + c) * L::A_CHUNK, &tmW, &full[st], nm + c * 64, kb * L::BK, pol_w);
+              }
             }
+#pragma unroll
+            for (int j = 0; j < KPS; ++j)
+              tma_load_2d_hint(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0, pol_x);
           } else if (p.cache_hints) {
             tma_load_2d_hint(sA + st * L::A_BYTES, &tmW, &full[st], n0, kb * L::BK, pol_w);
-            tma_load_2d_hint(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n1, kb * L::BK, pol_w);
+            tma_load_2d_hint(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n0 + 64, kb * L::BK, pol_w);
 #pragma unroll
             for (int j = 0; j < KPS; ++j)
               tma_load_2d_hint(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0, pol_x);
           } else {
             tma_load_2d(sA + st * L::A_BYTES, &tmW, &full[st], n0, kb * L::BK);
-            tma_load_2d(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n1, kb * L::BK);
+            tma_load_2d(sA + st * L::A_BYTES + L::A_CHUNK, &tmW, &full[st], n0 + 64, kb * L::BK);
 #pragma unroll
             for (int j = 0; j < KPS; ++j)
               tma_load_2d(sB + st * L::B_BYTES + j * L::B_SUB, &tmX, &full[st], kb * L::BK + j * kBK, 0);
@@ -459,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++scount;
         if (!wait_bounded(&tempty[buf], tph ^ 1u, wp, abort_flag, 3)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * TP;
+        const uint32_t d_tmem = tmem_base + buf * DC;
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
           const uint32_t st = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
@@ -474,13 +547,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < KPS; ++j) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
-              // A = W^T: feature-major, 64-feature chunks A_CHUNK apart (LBO), 8 k-rows 1 KB apart (SBO)
-              // (BK: K-major 128-byte rows, 8-feature groups 1 KB apart, 128 features per 64 k)
-              const uint64_t adesc = BK ? smem_desc_sw128(a0 + j * 2 * L::A_SUB + kk * 32, 16, 1024)
-                                        : smem_desc_sw128(a0 + j * L::A_SUB + kk * 2048, L::A_CHUNK, 1024);
               // B = X: K-major 128-byte rows, 8-row groups 1 KB apart, one TP-row block per 64 k
               const uint64_t bdesc = smem_desc_sw128(b0 + j * L::B_SUB + kk * 32, 16, 1024);
-              umma_f16(d_tmem, adesc, bdesc, IDESC, (kb > s.kb0 || j > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+              for (int m = 0; m < (GN == 128 ? 2 : 1); ++m) {
+                // A = W^T: feature-major, 64-feature chunks A_CHUNK apart (LBO), 8 k-rows 1 KB apart (SBO);
+                // BK: K-major 128-byte rows, 8-feature groups 1 KB apart, 128 features per 64 k
+                const uint32_t am = a0 + m * L::A_OP;
+                const uint64_t adesc = BK ? smem_desc_sw128(am + j * 2 * L::A_SUB + kk * 32, 16, 1024)
+                                          : smem_desc_sw128(am + j * L::A_SUB + kk * 2048, L::A_CHUNK, 1024);
+                umma_f16(d_tmem + m * TP, adesc, bdesc, IDESC, (kb > s.kb0 || j > 0 || kk > 0) ? 1u : 0u);
+              }
             }
           }
           umma_commit(&empty[st]);
@@ -497,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const uint32_t ew = warp & 3u;
     const uint32_t et = threadIdx.x - 64;
-    float* xchg = reinterpret_cast<float*>(smem + L::OFF_XCHG);  // GATED
-    uint32_t turn = 0;
+    GatedLane gl{};
+    if constexpr (GN == 64) gl.xchg = reinterpret_cast<float*>(smem + L::OFF_XCHG);
     uint32_t scount = 0;
     bool ok = true;
     uint32_t g = lo;
@@ -508,16 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tph = (scount >> 1) & 1u;
       ++scount;
       const int n_local = static_cast<int>(ew * 32 + lane);
-      const int half = GATED ? n_local >> 6 : 0;  // 1: the up projection
-      const int n = s.tile * TN + (GATED ? n_local & 63 : n_local);
+      const int n = s.tile * TN + (GN == 64 ? n_local & 63 : n_local);
       const bool n_ok = n < p.N;
       const bool warp_ok = __all_sync(0xffffffffu, n_ok);  // all 32 features of this warp in range
       const int word = (s.tile * 128 + static_cast<int>(ew) * 32) >> 5;
       float bias_n = 0.f;
       if constexpr (AddsBias<EPI>::value)
         bias_n = n_ok ? load_bias<BF16>(p.bias, p.bias_f32, n) : 0.f;
-      if constexpr (GATED)
-        if (p.bias && n_ok) bias_n = load_bias<BF16>(p.bias, p.bias_f32, static_cast<int64_t>(half) * p.N + n);
+      if constexpr (GATED) {
+        gl.n = n;
+        gl.n_ok = n_ok;
+        gl.half = GN == 64 ? n_local >> 6 : 0;
+        const bool on = p.bias && n_ok;
+        gl.bias_g = on ? load_bias<BF16>(p.bias, p.bias_f32, n) : 0.f;
+        gl.bias_u = on ? load_bias<BF16>(p.bias, p.bias_f32, p.N + n) : 0.f;
+      }
       float dbias_acc = 0.f;
       const bool whole = s.kb0 == 0 && s.kb1 == p.kbt;
       // DRELU_BGRAD, whole tile: every mask word the tile needs, loaded before
@@ -536,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       if (ok) ok = wait_bounded(&tfull[buf], tph, wp, abort_flag, 6);
       ok = __all_sync(0xffffffffu, ok);
-      if constexpr (GATED) ok = named_bar_and(2, 128, ok);  // the rows' exchange needs all four warps
-      const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * TP;
-      float* slot = p.partials + (static_cast<int64_t>(s.tile) * p.max_segs + s.seg) * (TP * 128);
+      if constexpr (GN == 64) ok = named_bar_and(2, 128, ok);  // the rows' exchange needs all four warps
+      const uint32_t tbase = tmem_base + ((ew * 32u) << 16) + buf * DC;
+      float* slot = p.partials + (static_cast<int64_t>(s.tile) * p.max_segs + s.seg) * (DC * 128);
       if (ok) {
         tc_fence_after();
 #pragma unroll 1
@@ -559,8 +641,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-          if (GATED && whole) {
-            skinny_gated16<BF16>(p, v, c * 16, n, n_ok, half, bias_n, xchg, turn);
+          if constexpr (GATED) {
+            float u[16];
+            if constexpr (GN == 128) {
+              uint32_t ru[16];
+              tmem_ld_32x32b_x16(tbase + TP + c * 16, ru);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] = __uint_as_float(ru[j]);
+            }
+            if (whole) {
+              skinny_gated16<GN, BF16>(p, v, u, c * 16, gl);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c * 16 + j < p.T) {
+                  slot[(c * 16 + j) * 128 + n_local] = v[j];
+                  if constexpr (GN == 128) slot[(TP + c * 16 + j) * 128 + n_local] = u[j];
+                }
+            }
           } else if (whole) {
             skinny_finish16<EPI, BF16, (TP > 16)>(p, v, c * 16, n, n_ok, warp_ok, word, bias_n, dbias_acc, mk);
           } else if (TP > 16 && c * 16 + 16 <= p.T) {
@@ -596,12 +695,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = *last_flag != 0;
         if (ok && last) {
           __threadfence();
-          const float* base = p.partials + static_cast<int64_t>(s.tile) * p.max_segs * (TP * 128) + n_local;
-          switch (s.nsegs) {
-            case 2: skinny_fixup<2, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
-            case 3: skinny_fixup<3, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
-            case 4: skinny_fixup<4, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
-            default: skinny_fixup<0, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc, half, xchg, turn); break;
+          const float* base = p.partials + static_cast<int64_t>(s.tile) * p.max_segs * (DC * 128) + n_local;
+          if constexpr (GATED)
+            skinny_gated_fixup<GN, TP, BF16>(p, base, s.nsegs, gl);
+          else switch (s.nsegs) {
+            case 2: skinny_fixup<2, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
+            case 3: skinny_fixup<3, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
+            case 4: skinny_fixup<4, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
+            default: skinny_fixup<0, TP, EPI, BF16>(p, base, s.nsegs, n, n_ok, word, bias_n, dbias_acc); break;
           }
           if constexpr (EPI == EPI_DRELU_BGRAD)
             if (n_ok) p.dbias[n] = dbias_acc;

@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
   constexpr uint32_t IDESC = idesc_f16(BF16, /*A MN-major*/ A_MN, /*B MN-major*/ true, 2 * kBM, BN);
   constexpr uint32_t IDESC_HALF = idesc_f16(BF16, A_MN, true, 2 * kBM, BN / 2);
   constexpr uint32_t IDESC_BK = idesc_f16(BF16, A_MN, /*B MN-major*/ false, 2 * kBM, BN);
+  constexpr uint32_t IDESC_BK_HALF = idesc_f16(BF16, A_MN, /*B MN-major*/ false, 2 * kBM, BN / 2);
   constexpr uint32_t PAIR_TX = 2 * (L::A_BYTES + L::B_BYTES);
   constexpr uint32_t PAIR_TX_HALF = 2 * (L::A_BYTES + L::B_CHUNK);
   constexpr uint16_t BOTH = 0x3;
@@ -306,9 +307,11 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
   const uint32_t tmem_base = *tmem_slot;
   if constexpr (IsGated<EPI>::value) wait_for_inputs();
   const int m2_tiles = (p.m_tiles + 1) / 2;  // 256-row tiles
-  // half units would need a 64-row box of a K-major W: with BK every unit is a whole tile
+  // half units need 64-row boxes of a K-major W, which only gated layers' maps have:
+  // with BK every other unit is a whole tile
+  constexpr bool HALF_BK = BK && IsGated<EPI>::value;
   TileParams pw = p;
-  if constexpr (BK) pw.tail_split = 0;
+  if constexpr (BK && !HALF_BK) pw.tail_split = 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -344,7 +347,10 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
             } else {
               tma_load_2d_pair(sA + s * L::A_BYTES, &tmA, fbar, kb * kBK, m0);
             }
-            if constexpr (BK) {  // this CTA's 128 rows of the N x K weight in one box
+            if constexpr (HALF_BK) {
+              for (int j = 0; j < nchunks; ++j)
+                tma_load_2d_pair(sB + s * L::B_BYTES + j * L::B_CHUNK, &tmB, fbar, kb * kBK, nh0 + j * 64);
+            } else if constexpr (BK) {  // this CTA's 128 rows of the N x K weight in one box
               tma_load_2d_pair(sB + s * L::B_BYTES, &tmB, fbar, kb * kBK, nh0);
             } else {
               for (int j = 0; j < nchunks; ++j)
@@ -369,7 +375,8 @@ __global__ void __launch_bounds__(64 + 32 * PairEpiWarps<EPI, SPLIT>::value, 1)
         PairWork<SPLIT> work(pw, pair, npairs, m2_tiles);
         PairUnit w;
         for (; ok && work.next(w); ++tcount) {
-          const uint32_t idesc = BK ? IDESC_BK : w.half < 0 ? IDESC : IDESC_HALF;
+          const uint32_t idesc = BK ? (HALF_BK && w.half >= 0 ? IDESC_BK_HALF : IDESC_BK)
+                                    : w.half < 0 ? IDESC : IDESC_HALF;
           const uint32_t buf = tcount & 1u;
           const uint32_t tph = (tcount >> 1) & 1u;
           bool room = wait_bounded(&tempty[buf], tph ^ 1u, p, abort_flag, 3);

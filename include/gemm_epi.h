@@ -490,7 +490,7 @@ typedef enum {
  * gemm_epi_plan_ex. N is the number of columns of H, also for DGATED, where K is
  * the contraction length of dY.W2. Flags GEMM_EPI_FLAG_W_NK (W or W2) and
  * GEMM_EPI_FLAG_OUT_F32 (H or dZ; aux stays 16-bit). gemm_epi_query reports
- * kernels 0 to 2. Both weight layouts have a few-row kernel (forward, T <= 128).
+ * kernels 0 to 2. Both weight layouts have a few-row kernel (forward, T <= 32).
  */
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_gated_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
                                                  gemm_epi_gated_epilog epilog, gemm_epi_act act, uint32_t flags);
