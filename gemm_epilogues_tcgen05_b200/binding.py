@@ -34,7 +34,9 @@ EXPORTED = ["gemm_epi_plan", "gemm_epi_execute", "drelu_bgrad_execute", "gemm_ep
             "gemm_epi_grouped_plan", "gemm_epi_grouped_execute", "gemm_epi_grouped_drelu_bgrad_execute",
             "gemm_epi_grouped_wgrad_execute", "gemm_epi_mx_scales_bytes", "gemm_epi_mx_quantize",
             "gemm_epi_mx_dequantize", "gemm_epi_mx_plan", "gemm_epi_mx_execute", "gemm_epi_gated_plan",
-            "gemm_epi_gated_execute", "gemm_epi_dgated_execute"]
+            "gemm_epi_gated_execute", "gemm_epi_dgated_execute", "gemm_epi_w4_bytes", "gemm_epi_w4_scales",
+            "gemm_epi_w4_quantize", "gemm_epi_w4_pack", "gemm_epi_w4_dequantize", "gemm_epi_w4_plan",
+            "gemm_epi_w4_execute"]
 GATED_EPILOGS = {"GATED": 8, "DGATED": 9, "GATED_AUX": 10}  # gemm_epi_gated_epilog
 ACTS = {"SILU": 0, "GELU": 1, "RELU": 2}  # gemm_epi_act
 MX_TRANSPOSED = 1  # GEMM_EPI_MX_TRANSPOSED
@@ -122,6 +124,19 @@ def lib() -> ctypes.CDLL:
         L.gemm_epi_gated_execute.argtypes = [vp] * 7
         L.gemm_epi_dgated_execute.restype = ci
         L.gemm_epi_dgated_execute.argtypes = [vp] * 7
+        for size in (L.gemm_epi_w4_bytes, L.gemm_epi_w4_scales):
+            size.restype = i64
+            size.argtypes = [i64] * 4
+        L.gemm_epi_w4_quantize.restype = ci
+        L.gemm_epi_w4_quantize.argtypes = [i64] * 4 + [ci] + [vp] * 5
+        L.gemm_epi_w4_pack.restype = ci
+        L.gemm_epi_w4_pack.argtypes = [i64] * 4 + [vp] * 7
+        L.gemm_epi_w4_dequantize.restype = ci
+        L.gemm_epi_w4_dequantize.argtypes = [i64] * 4 + [ci, ctypes.c_uint32] + [vp] * 5
+        L.gemm_epi_w4_plan.restype = vp
+        L.gemm_epi_w4_plan.argtypes = [i64] * 4 + [ci, ci, ci, ctypes.c_uint32]
+        L.gemm_epi_w4_execute.restype = ci
+        L.gemm_epi_w4_execute.argtypes = [vp] * 8
         _lib = L
     return _lib
 
@@ -646,3 +661,121 @@ class GatedPlan(_DevicePlan):
         dbias = _empty((2 * self.N,), torch.float32, dY.device, stream) if with_dbias else None
         self.gemm_epi_dgated_execute(dY, W2, aux, dZ, dbias, stream)
         return (dZ, dbias) if with_dbias else dZ
+
+
+def w4_empty(N: int, K: int, dtype: torch.dtype, group: int = 128, zeros: bool = False, batch: int = 1, device=None,
+             stream=None):
+    """Uninitialised (q, scales, zeros or None) of ``batch`` weights of N x K held in 4 bits
+    with a scale (and zero point) for each ``group`` columns. All three are flat."""
+    nq, ns = lib().gemm_epi_w4_bytes(batch, N, K, group), lib().gemm_epi_w4_scales(batch, N, K, group)
+    if nq < 0 or ns < 0:
+        raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
+    device = torch.device("cuda") if device is None else device
+    return (_empty((nq,), torch.uint8, device, stream), _empty((ns,), dtype, device, stream),
+            _empty((ns,), torch.uint8, device, stream) if zeros else None)
+
+
+def _w4_args(values, name, q, scales, zeros, group, dtype, cols):
+    """Check one call's tensors: ``values`` is (batch x) N x ``cols(shape)`` on the device of all;
+    device, batch, N, K and the pointers of values, q, scales, zeros."""
+    if not isinstance(values, torch.Tensor) or values.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a tensor of 2 or 3 dimensions")
+    if not values.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    index, batch, N, K = values.get_device(), 1 if values.dim() == 2 else values.shape[0], values.shape[-2], cols(values.shape)
+    nq, ns = lib().gemm_epi_w4_bytes(batch, N, K, group), lib().gemm_epi_w4_scales(batch, N, K, group)
+    if nq < 0 or ns < 0:
+        raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
+    return (index, batch, N, K, _ptr_on(index, values, values.shape, values.dtype, name),
+            _ptr_on(index, q, (nq,), torch.uint8, "q"), _ptr_on(index, scales, (ns,), dtype, "scales"),
+            None if zeros is None else _ptr_on(index, zeros, (ns,), torch.uint8, "zeros"))
+
+
+def gemm_epi_w4_quantize(W, q, scales, zeros=None, group=128, stream=None):
+    """Quantise W (N x K or batch x N x K, 16-bit) to 4 bits: q, scales (W's type) and, if given, zeros."""
+    dtype = DTYPES.get(getattr(W, "dtype", None))
+    if dtype is None:
+        raise ValueError("W must be a float16 or bfloat16 tensor")
+    index, batch, N, K, pw, pq, ps, pz = _w4_args(W, "W", q, scales, zeros, group, W.dtype, lambda s: s[-1])
+    _on_device(index, lib().gemm_epi_w4_quantize, batch, N, K, group, dtype, pw, pq, ps, pz, _raw_stream(index, stream))
+
+
+def gemm_epi_w4_dequantize(q, scales, zeros, out, group=128, stream=None):
+    """The values that q, scales and zeros (or None) stand for, into out (the scales' type, or float32)."""
+    dtype = DTYPES.get(getattr(scales, "dtype", None))
+    if dtype is None or getattr(out, "dtype", None) not in (scales.dtype, torch.float32):
+        raise ValueError("scales must be float16 or bfloat16, and out of that type or float32")
+    index, batch, N, K, po, pq, ps, pz = _w4_args(out, "out", q, scales, zeros, group, scales.dtype, lambda s: s[-1])
+    _on_device(index, lib().gemm_epi_w4_dequantize, batch, N, K, group, dtype,
+               FLAG_OUT_F32 if out.dtype is torch.float32 else 0, pq, ps, pz, po, _raw_stream(index, stream))
+
+
+def gemm_epi_w4_pack(codes, src_scales, src_zeros, q, scales, zeros=None, stream=None):
+    """Codes ((batch x) N x K / 2 bytes, the lower column in the low 4 bits), scales ((batch x)
+    N x K / group) and zeros (the same, uint8, or None) as a checkpoint has them, to the product's layout."""
+    if getattr(src_scales, "dtype", None) not in DTYPES or getattr(codes, "dtype", None) is not torch.uint8:
+        raise ValueError("codes must be uint8, scales float16 or bfloat16")
+    K, groups = 2 * codes.shape[-1], src_scales.shape[-1]
+    group = K // groups if groups else 0
+    if (src_zeros is None) != (zeros is None):
+        raise ValueError("zeros on one side alone")
+    index, batch, N, K, pc, pq, ps, pz = _w4_args(codes, "codes", q, scales, zeros, group, src_scales.dtype,
+                                                  lambda s: 2 * s[-1])
+    shape = (*codes.shape[:-1], K // group)
+    sc = _ptr_on(index, src_scales, shape, src_scales.dtype, "scales")
+    sz = None if src_zeros is None else _ptr_on(index, src_zeros, shape, torch.uint8, "zeros")
+    _on_device(index, lib().gemm_epi_w4_pack, batch, N, K, group, pc, sc, sz, pq, ps, pz, _raw_stream(index, stream))
+
+
+def w4_quantize(W, group=128, zeros=False, stream=None):
+    """gemm_epi_w4_quantize with allocated outputs: (q, scales, zeros or None)."""
+    out = w4_empty(W.shape[-2], W.shape[-1], W.dtype, group, zeros, W.shape[0] if W.dim() == 3 else 1, W.device, stream)
+    gemm_epi_w4_quantize(W, *out, group=group, stream=stream)
+    return out
+
+
+def w4_pack(codes, scales, zeros=None, stream=None):
+    """gemm_epi_w4_pack with allocated outputs: (q, scales, zeros or None)."""
+    K, groups = 2 * codes.shape[-1], scales.shape[-1]
+    out = w4_empty(codes.shape[-2], K, scales.dtype, K // groups if groups else 0, zeros is not None,
+                   codes.shape[0] if codes.dim() == 3 else 1, codes.device, stream)
+    gemm_epi_w4_pack(codes, scales, zeros, *out, stream=stream)
+    return out
+
+
+class W4Plan(_DevicePlan):
+    """A plan for Y = epilog(X . W^T) of few 16-bit rows (T <= 256) and a weight held in 4
+    bits with a scale for each ``group`` columns (w4_quantize, w4_pack): epilog BIAS,
+    RELU_BIAS, GELU_BIAS or NONE, or "GATED": two weights of N rows (a batch of two, the
+    gate's first), H = act(X . W0^T) * (X . W1^T) with act "SILU", "GELU" or "RELU"."""
+
+    def __init__(self, T: int, N: int, K: int, dtype: torch.dtype, epilog: str | int, group: int = 128, act: str = "SILU",
+                 out_f32: bool = False):
+        self.T, self.N, self.K, self.group = T, N, K, group
+        self.out_dtype = torch.float32 if out_f32 else dtype
+        self.dtype = self.bias_dtype = dtype
+        self.epilog = {**EPILOGS, **GATED_EPILOGS}[epilog] if isinstance(epilog, str) else epilog
+        gated = self.epilog == GATED_EPILOGS["GATED"]
+        self._own(lib().gemm_epi_w4_plan(T, N, K, group, DTYPES[dtype], self.epilog,
+                                         ACTS[act] if isinstance(act, str) else act, FLAG_OUT_F32 if out_f32 else 0))
+        batch = 2 if gated else 1
+        self._shapes = ((T, K), (lib().gemm_epi_w4_bytes(batch, N, K, group),),
+                        (lib().gemm_epi_w4_scales(batch, N, K, group),), (batch * N,), (T, N))
+
+    def aux_spec(self):
+        return None
+
+    def gemm_epi_w4_execute(self, X, q, scales, zeros, bias, Y, stream=None):
+        """q, scales and zeros (None: 8 everywhere) as w4_quantize and w4_pack make them; bias
+        N (gated: 2N) values, or None for NONE and GATED."""
+        i, dt, (xs, qs, ss, bs, ys) = self.index, self.dtype, self._shapes
+        _check(lib().gemm_epi_w4_execute(
+            self.handle, _ptr_on(i, X, xs, dt, "X"), _ptr_on(i, q, qs, torch.uint8, "q"),
+            _ptr_on(i, scales, ss, dt, "scales"), None if zeros is None else _ptr_on(i, zeros, ss, torch.uint8, "zeros"),
+            None if bias is None else _ptr_on(i, bias, bs, self.bias_dtype, "bias"),
+            _ptr_on(i, Y, ys, self.out_dtype, "Y"), self._s(stream)))
+
+    def forward(self, X, q, scales, zeros=None, bias=None, stream=None):
+        Y = _empty((self.T, self.N), self.out_dtype, X.device, stream)
+        self.gemm_epi_w4_execute(X, q, scales, zeros, bias, Y, stream)
+        return Y

@@ -184,12 +184,6 @@ struct DGatedStream {
   }
 };
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr) : "memory");
-  return v;
-}
-
 template <bool BF16>
 __device__ __forceinline__ void unpack_2x(uint32_t w, float& lo, float& hi) {
   if constexpr (BF16) {

@@ -124,6 +124,15 @@ struct GroupedCfg {
   int slices = 1;  // WGRAD: row slices of the optional bias gradient
 };
 
+// A plan of few rows times 4-bit weights.
+struct W4Cfg {
+  ge_inst::W4KernelFn fn = nullptr;
+  int group = 0, nt = 0, threads = 0;
+  uint32_t smem = 0;
+  int items = 0, groups_of_items = 0;  // feature tiles, and the CTAs that share them
+  int slices = 1, slice_kt = 0, row_blocks = 1;
+};
+
 // Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`
 // rows of `d0` contiguous elements each; boxes of b0 x b1.
 inline int encode_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -250,7 +259,7 @@ class DeviceScope {
 }  // namespace ge_host
 
 struct gemm_epi_plan_s {
-  int kind = 0;      // 0: one product; 1: products grouped by expert (grouped.cu); 2: microscaled (mx.cu); 3: gated (gated.cu)
+  int kind = 0;      // 0: one product; 1: products grouped by expert (grouped.cu); 2: microscaled (mx.cu); 3: gated (gated.cu); 4: 4-bit weights (w4.cu)
   int64_t T, N, K;   // the kernels' rows, columns and contraction length
   int64_t uT, uK;    // the caller's T and K (WGRAD: rows = uK, contraction = uT)
   int dtype, epilog;
@@ -279,7 +288,8 @@ struct gemm_epi_plan_s {
   int bias_f32 = 0;      // gemm_epi_set_bias_f32: the forward bias is fp32
   int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
   int out_f32 = 0;       // GEMM_EPI_FLAG_OUT_F32: Y / dZ / dW written as fp32
-  int act = 0;           // kind 3: gemm_epi_act
+  int act = 0;           // kind 3, 4: gemm_epi_act
+  ge_host::W4Cfg w4;     // kind 4
   int cache_hints = 0;   // few-row kernel: L2 eviction policies on the operand loads (GEMM_EPI_CACHE_HINTS)
   // tensor-map cache
   const void* a_ptr = nullptr;
@@ -329,7 +339,7 @@ inline gemm_epi_plan_s* lookup_kind(gemm_epi_plan_t plan, int kind, const char* 
   if (!p) {
     *code = fail(GEMM_EPI_ERR_INVALID_ARG, "%s: unknown plan", call);
   } else if (p->kind != kind) {
-    const char* what[] = {"of one product", "of products grouped by expert", "of a microscaled product", "of a gated layer"};
+    const char* what[] = {"of one product", "of products grouped by expert", "of a microscaled product", "of a gated layer", "of 4-bit weights"};
     *code = fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "%s called on a plan %s", call, what[p->kind]);
     p = nullptr;
   }

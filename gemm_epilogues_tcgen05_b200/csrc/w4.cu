@@ -1,0 +1,267 @@
+// w4.cu -- C ABI of 4-bit weights with group scales: quantisation, packing, the
+// inverse, and the plan and call of the product with few rows.
+#include "host_common.h"
+#include "w4_kernel.cuh"
+#include "w4_quant.cuh"
+
+using namespace ge_host;
+
+namespace {
+
+constexpr int64_t kMaxCols = (int64_t)1 << 22;
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int kMaxT = 256;
+
+int64_t row_tiles(int64_t rows) { return (rows + 15) / 16; }
+int64_t col_tiles(int64_t cols) { return (cols + 127) / 128; }
+
+int check_shape(const char* call, int64_t batch, int64_t rows, int64_t cols, int64_t group) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "%s: bad group %lld (32, 64 or 128)", call, (long long)group);
+  if (batch < 1 || rows < 1 || cols < group || cols % group != 0 || rows > kMaxRows || cols > kMaxCols ||
+      batch > (int64_t)1 << 20 || batch * row_tiles(rows) * col_tiles(cols) > (int64_t)1 << 40)
+    return fail(GEMM_EPI_ERR_INVALID_ARG,
+                "%s: bad shape batch=%lld rows=%lld cols=%lld (need all >= 1, cols a multiple of the group and at most %lld)",
+                call, (long long)batch, (long long)rows, (long long)cols, (long long)kMaxCols);
+  return GEMM_EPI_OK;
+}
+
+int check_dtype(gemm_epi_dtype dtype) {
+  if (dtype != GEMM_EPI_F16 && dtype != GEMM_EPI_BF16) return fail(GEMM_EPI_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  return GEMM_EPI_OK;
+}
+
+ge::W4Params base_params(int64_t batch, int64_t rows, int64_t cols, int64_t group) {
+  ge::W4Params k{};
+  k.rows = (int32_t)rows;
+  k.cols = (int32_t)cols;
+  k.rt = (int32_t)row_tiles(rows);
+  k.kt = (int32_t)col_tiles(cols);
+  k.tiles = batch * k.rt * k.kt;
+  k.group = (int32_t)group;
+  return k;
+}
+
+int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int sms, cudaStream_t stream) {
+  const int64_t want = (k.tiles + 7) / 8, most = (int64_t)sms * 32;
+  Launch l((int)(want < most ? want : most), 256, 0, false, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, k);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "4-bit weight launch");
+}
+
+gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,
+                          gemm_epi_act act, uint32_t flags) {
+  if ((flags & ~(uint32_t)GEMM_EPI_FLAG_OUT_F32) != 0) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags);
+    return nullptr;
+  }
+  if (T < 1 || T > kMaxT || N < 8 || N % 8 != 0) {
+    fail(GEMM_EPI_ERR_INVALID_ARG,
+         "bad shape T=%lld N=%lld (need 1 <= T <= %d -- for more rows gemm_epi_w4_dequantize and a plan with "
+         "GEMM_EPI_FLAG_W_NK -- and N a multiple of 8)",
+         (long long)T, (long long)N, kMaxT);
+    return nullptr;
+  }
+  const bool gated = epilog == GEMM_EPI_GATED;
+  if (check_shape("gemm_epi_w4_plan", gated ? 2 : 1, N, K, group) || check_dtype(dtype)) return nullptr;
+  if (!gated && epilog != GEMM_EPI_BIAS && epilog != GEMM_EPI_RELU_BIAS && epilog != GEMM_EPI_GELU_BIAS &&
+      epilog != GEMM_EPI_NONE) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "epilog %d has no product with 4-bit weights (BIAS, RELU_BIAS, GELU_BIAS, NONE, GATED have)",
+         epilog);
+    return nullptr;
+  }
+  if (act != GEMM_EPI_SILU && act != GEMM_EPI_GELU && act != GEMM_EPI_RELU) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+    return nullptr;
+  }
+  int dev = 0, sms = 0;
+  if (require_b200(&dev, &sms)) return nullptr;
+  auto* p = new gemm_epi_plan_s();
+  p->kind = 4;
+  p->kernel = 8;
+  p->uT = p->T = T;
+  p->uK = p->K = K;
+  p->N = N;
+  p->dtype = dtype;
+  p->epilog = epilog;
+  p->act = act;
+  p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
+  p->device = dev;
+  p->num_sms = sms;
+  W4Cfg& c = p->w4;
+  c.group = (int)group;
+  c.nt = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
+  c.row_blocks = ceil_div(T, 8 * c.nt);
+  const int ng = (int)(128 / group);
+  const ge_inst::W4Instance inst =
+      dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16(c.nt, gated, ng) : ge_inst::w4_f16(c.nt, gated, ng);
+  c.fn = inst.fn;
+  c.threads = 32 * inst.warps;
+  c.items = (int)(gated || c.nt < 4 ? row_tiles(N) : (row_tiles(N) + 1) / 2);
+  // as many columns of X as shared memory holds beside the join's sums
+  const int rows = T < 8 * c.nt ? (int)T : 8 * c.nt, kt = (int)col_tiles(K);
+  const int room = ((232448 - inst.join_bytes) / rows - 64) / 256;
+  c.slices = (kt + room - 1) / room;
+  c.slice_kt = (kt + c.slices - 1) / c.slices;
+  c.slices = (kt + c.slice_kt - 1) / c.slice_kt;
+  c.smem = (uint32_t)(inst.join_bytes + rows * ge::w4_row_bytes(c.slice_kt));
+  const int share = sms / (c.slices * c.row_blocks);
+  c.groups_of_items = share < 1 ? 1 : share < c.items ? share : c.items;
+  p->grid = c.groups_of_items * c.slices * c.row_blocks;
+  cudaError_t e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
+  if (e == cudaSuccess && c.slices > 1) {
+    p->partial_bytes = (size_t)c.slices * (gated ? 2 : 1) * (size_t)T * 16 * (size_t)row_tiles(N) * sizeof(float);
+    e = cudaMalloc((void**)&p->partials, p->partial_bytes);
+  }
+  if (e == cudaSuccess) e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "plan of 4-bit weights");
+    if (p->partials) cudaFree(p->partials);
+    delete p;
+    return nullptr;
+  }
+  *p->status_host = 0;  // (these kernels wait for nothing; gemm_epi_status reads it)
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    live_plans().insert(p);
+  }
+  g_last_error.clear();
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_epi_w4_bytes(int64_t batch, int64_t rows, int64_t cols, int64_t group) {
+  if (check_shape("gemm_epi_w4_bytes", batch, rows, cols, group)) return -1;
+  return batch * row_tiles(rows) * col_tiles(cols) * 1024;
+}
+
+int64_t gemm_epi_w4_scales(int64_t batch, int64_t rows, int64_t cols, int64_t group) {
+  if (check_shape("gemm_epi_w4_scales", batch, rows, cols, group)) return -1;
+  return batch * row_tiles(rows) * col_tiles(cols) * 16 * (128 / group);
+}
+
+int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype, const void* W,
+                         uint8_t* q, void* scales, uint8_t* zeros, cudaStream_t stream) {
+  int rc = check_shape("gemm_epi_w4_quantize", batch, rows, cols, group);
+  if (!rc) rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (!W || !q || !scales) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_quantize: NULL W, q or scales");
+  if (!aligned(W, 16) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16))
+    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_quantize: q needs 32-byte, W, scales and zeros 16-byte alignment");
+  int dev = 0, sms = 0;
+  rc = require_b200(&dev, &sms);
+  if (rc) return rc;
+  ge::W4Params k = base_params(batch, rows, cols, group);
+  k.src = W;
+  k.q = q;
+  k.scales = scales;
+  k.zeros = zeros;
+  if (dtype == GEMM_EPI_BF16)
+    return run(zeros ? ge::w4_quantize_kernel<true, true> : ge::w4_quantize_kernel<true, false>, k, sms, stream);
+  return run(zeros ? ge::w4_quantize_kernel<false, true> : ge::w4_quantize_kernel<false, false>, k, sms, stream);
+}
+
+int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, const uint8_t* codes,
+                     const void* src_scales, const uint8_t* src_zeros, uint8_t* q, void* scales, uint8_t* zeros,
+                     cudaStream_t stream) {
+  int rc = check_shape("gemm_epi_w4_pack", batch, rows, cols, group);
+  if (rc) return rc;
+  if (!codes || !src_scales || !q || !scales || (src_zeros == nullptr) != (zeros == nullptr))
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_pack: NULL codes, scales or q, or zeros on one side alone");
+  if (!aligned(codes, 16) || !aligned(src_scales, 2) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16))
+    return fail(GEMM_EPI_ERR_MISALIGNED,
+                "gemm_epi_w4_pack: q needs 32-byte, codes, scales and zeros 16-byte, the given scales 2-byte alignment");
+  int dev = 0, sms = 0;
+  rc = require_b200(&dev, &sms);
+  if (rc) return rc;
+  ge::W4Params k = base_params(batch, rows, cols, group);
+  k.src = codes;
+  k.src_scales = src_scales;
+  k.src_zeros = src_zeros;
+  k.q = q;
+  k.scales = scales;
+  k.zeros = zeros;
+  return run(ge::w4_pack_kernel, k, sms, stream);
+}
+
+int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype, uint32_t flags,
+                           const uint8_t* q, const void* scales, const uint8_t* zeros, void* out, cudaStream_t stream) {
+  if (flags & ~(uint32_t)GEMM_EPI_FLAG_OUT_F32)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_dequantize: unknown flags 0x%x", flags);
+  int rc = check_shape("gemm_epi_w4_dequantize", batch, rows, cols, group);
+  if (!rc) rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (!q || !scales || !out) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_dequantize: NULL q, scales or out");
+  if (!aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(out, 16))
+    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_dequantize: q needs 32-byte, scales, zeros and out 16-byte alignment");
+  int dev = 0, sms = 0;
+  rc = require_b200(&dev, &sms);
+  if (rc) return rc;
+  ge::W4Params k = base_params(batch, rows, cols, group);
+  k.q = const_cast<uint8_t*>(q);
+  k.scales = const_cast<void*>(scales);
+  k.zeros = const_cast<uint8_t*>(zeros);
+  k.out = out;
+  const bool f32 = (flags & GEMM_EPI_FLAG_OUT_F32) != 0;
+  if (dtype == GEMM_EPI_BF16)
+    return run(f32 ? ge::w4_dequantize_kernel<true, true> : ge::w4_dequantize_kernel<true, false>, k, sms, stream);
+  return run(f32 ? ge::w4_dequantize_kernel<false, true> : ge::w4_dequantize_kernel<false, false>, k, sms, stream);
+}
+
+gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,
+                                 gemm_epi_act act, uint32_t flags) {
+  try {
+    return make_plan(T, N, K, group, dtype, epilog, act, flags);
+  } catch (...) {  // host memory ran out
+    return nullptr;
+  }
+}
+
+int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, const void* scales, const uint8_t* zeros,
+                        const void* bias, void* Y, cudaStream_t stream) {
+  int rc = 0;
+  gemm_epi_plan_s* p = lookup_kind(plan, 4, "gemm_epi_w4_execute", &rc);
+  if (!p) return rc;
+  const bool optional_bias = p->epilog == GEMM_EPI_NONE || p->epilog == GEMM_EPI_GATED;
+  if (!X || !q || !scales || !Y || (!bias && !optional_bias))
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_execute: NULL X, q, scales, bias or Y");
+  if (!aligned(X, 16) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(Y, 16) ||
+      !aligned(bias, p->bias_f32 ? 4 : 2))
+    return fail(GEMM_EPI_ERR_MISALIGNED,
+                "gemm_epi_w4_execute: q needs 32-byte, X, scales, zeros and Y 16-byte, bias 2-byte (fp32: 4-byte) alignment");
+  DeviceScope scope(p->device);
+  const W4Cfg& c = p->w4;
+  ge::W4MulParams k{};
+  k.T = (int32_t)p->T;
+  k.N = (int32_t)p->N;
+  k.K = (int32_t)p->K;
+  k.rt = (int32_t)row_tiles(p->N);
+  k.kt = (int32_t)col_tiles(p->K);
+  k.items = c.items;
+  k.slices = c.slices;
+  k.slice_kt = c.slice_kt;
+  k.epi = p->epilog;
+  k.act = p->act;
+  k.bias_f32 = p->bias_f32;
+  k.out_f32 = p->out_f32;
+  k.X = X;
+  k.q = q;
+  k.scales = scales;
+  k.zeros = zeros;
+  k.bias = p->epilog == GEMM_EPI_NONE ? nullptr : bias;
+  k.out = Y;
+  k.sums = p->partials;
+  Launch l(dim3((unsigned)c.groups_of_items, (unsigned)c.slices, (unsigned)c.row_blocks), c.threads, c.smem, false, stream);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, k);
+  if (e != cudaSuccess) return cuda_fail(e, "launch of the product with 4-bit weights");
+  if (c.slices == 1) return GEMM_EPI_OK;
+  const int64_t blocks = (p->T * p->N + 255) / 256, most = (int64_t)p->num_sms * 8;
+  Launch f((int)(blocks < most ? blocks : most), 256, 0, false, stream);
+  e = cudaLaunchKernelEx(&f.cfg, p->dtype == GEMM_EPI_BF16 ? ge::w4_finish_kernel<true> : ge::w4_finish_kernel<false>, k);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the slices' sum");
+}
+
+}  // extern "C"

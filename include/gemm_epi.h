@@ -125,8 +125,8 @@ typedef struct {
   int kernel;          /* 0 = tile kernel (one CTA per tile), 1 = few-row kernel (swap-AB,
                           stream-K), 2 = tile kernel on CTA pairs (256-row tiles); grouped
                           plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
-                          (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs).
-                          For 3 to 7 tile_m counts features and tile_n rows */
+                          (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs);
+                          4-bit weights: 8. For 3 to 8 tile_m counts features and tile_n rows */
   int tile_m, tile_n, tile_k, stages;  /* a gated layer's tiles count gate and up features alike */
   int split_k;         /* K slices per output tile (1 = none). Grouped plans: for experts of the mean
                           number of rows; a call that finds others may share a tile among fewer or
@@ -503,6 +503,78 @@ GEMM_EPI_API int gemm_epi_gated_execute(gemm_epi_plan_t plan, const void* X, con
 /* DGATED. dY, W2, aux and dZ 16-byte, dbias 4-byte aligned. Returns as gemm_epi_execute. */
 GEMM_EPI_API int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, const void* W2, const void* aux, void* dZ,
                                          float* dbias, cudaStream_t stream);
+
+/*
+ * Weights held in 4 bits with a 16-bit scale for each group of G = 32, 64 or 128
+ * consecutive columns, for products with few 16-bit rows (decoding: the weight is
+ * what is read, at a quarter of its 16-bit size).
+ *   W[n][k] = scale[n][k / G] (code[n][k] - zero[n][k / G]), code 0 .. 15; zero is 8
+ *   everywhere where no zeros are given (NULL), else 0 .. 127 (one byte)
+ * gemm_epi_w4_quantize, of a group w: without zeros scale = max|w| / 7 rounded to the
+ * 16-bit type and code = w / scale rounded (ties to even), held to -8 .. 7, plus 8; with
+ * zeros, lo = min(w, 0), hi = max(w, 0), scale = (hi - lo) / 15 rounded to the type,
+ * zero = -lo / scale rounded, held to 0 .. 15, code = w / scale rounded, plus zero, held to
+ * 0 .. 15. A scale that rounds to 0 gives codes that stand for 0; a group with an infinity or
+ * NaN (or, with zeros, a range beyond fp32) has a NaN scale and stands for NaN.
+ * Storage: q in tiles of 16 rows x 128 columns, 1024 bytes each, a row of ceil(cols /
+ * 128) tiles after the other; rows and columns past the matrix are held as zeros.
+ * With g = 0 .. 7, r = 0, 1, b = 0 .. 3, c = 0 .. 3: row g + 8 r, columns 32 b + 8 c .. + 7 of a
+ * tile are the 32-bit word at byte 32 (4 g + c) + 8 b + 4 r, column 2 m of the eight in bits
+ * 4 m .. 4 m + 3 and column 2 m + 1 in bits 4 m + 16 .. 4 m + 19. The scales (16-bit) and zeros (bytes) of a
+ * tile's 128 / G groups k are at 16 (128 / G) tile + (g (128 / G) + k) 2 + r. Matrices of a batch
+ * follow one another in whole tiles. gemm_epi_w4_pack makes this of row-major codes.
+ */
+
+/* Bytes of q, and the number of scales (and of zeros), of `batch` matrices of rows x
+ * cols; cols a multiple of group, at most 2^22, rows at most 2^24. -1 with the error
+ * set for a bad shape. */
+GEMM_EPI_API int64_t gemm_epi_w4_bytes(int64_t batch, int64_t rows, int64_t cols, int64_t group);
+GEMM_EPI_API int64_t gemm_epi_w4_scales(int64_t batch, int64_t rows, int64_t cols, int64_t group);
+
+/* gemm_epi_w4_quantize: `batch` row-major matrices of rows x cols (dtype, which the
+ * scales have too). q 32-byte, W, scales and zeros 16-byte aligned; zeros NULL:
+ * without. Asynchronous on `stream`, one launch on the current device. */
+GEMM_EPI_API int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype,
+                                      const void* W, uint8_t* q, void* scales, uint8_t* zeros, cudaStream_t stream);
+
+/* gemm_epi_w4_pack: codes (rows x cols / 2 bytes, the lower column in the low 4
+ * bits), scales (rows x cols / group, 16-bit) and zeros (the same, bytes, of which 7
+ * bits count; NULL on both sides or neither) as a checkpoint has them, to the
+ * layout above. codes 16-byte, src_scales 2-byte aligned, the rest as above. */
+GEMM_EPI_API int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, const uint8_t* codes,
+                                  const void* src_scales, const uint8_t* src_zeros, uint8_t* q, void* scales,
+                                  uint8_t* zeros, cudaStream_t stream);
+
+/* gemm_epi_w4_dequantize: the values, row-major, rounded to dtype, or as fp32 with
+ * GEMM_EPI_FLAG_OUT_F32 (exact). For prompts: the 16-bit values are a plan's weight
+ * with GEMM_EPI_FLAG_W_NK. */
+GEMM_EPI_API int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype,
+                                        uint32_t flags, const uint8_t* q, const void* scales, const uint8_t* zeros,
+                                        void* out, cudaStream_t stream);
+
+/*
+ * gemm_epi_w4_plan: Y = epilog(X . W^T), X T x K (1 <= T <= 256), W N x K, N a multiple of 8, K of
+ * group. epilog BIAS, RELU_BIAS, GELU_BIAS or NONE, or GEMM_EPI_GATED: a batch of two
+ * matrices of N rows, the gate's first, and H = act(X . W0^T + bias) * (X . W1^T +
+ * bias[N..]) with `act` (otherwise ignored but checked). dtype is X's, the scales', the bias's and
+ * Y's; flags GEMM_EPI_FLAG_OUT_F32 or 0. Products are exact in fp32 before they are
+ * summed: code - zero is a small integer, its group's sum is scaled in fp32. A plan keeps no
+ * weight: one serves all layers of its shape. It owns a workspace where T x K is large
+ * (query: split_k > 1; then a call is two launches).
+ */
+GEMM_EPI_API gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype,
+                                              int epilog, gemm_epi_act act, uint32_t flags);
+
+/*
+ * gemm_epi_w4_execute: q, scales and zeros (NULL: 8) as gemm_epi_w4_quantize or
+ * _pack make them. q 32-byte, X, scales, zeros and Y 16-byte, bias as
+ * gemm_epi_execute (NULL allowed for NONE, where it is ignored, and GATED, 2N
+ * values). A call runs on the plan's device whichever is current. Returns as
+ * gemm_epi_execute (never GEMM_EPI_ERR_TIMEOUT). gemm_epi_free, _query, _status and
+ * _set_bias_f32 take the plan too.
+ */
+GEMM_EPI_API int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, const void* scales,
+                                     const uint8_t* zeros, const void* bias, void* Y, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
