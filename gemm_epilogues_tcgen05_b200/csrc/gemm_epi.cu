@@ -643,14 +643,14 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->launches = 1;
     info->workspace_bytes = p->partial_bytes + p->split_bytes + sizeof(int) * (size_t)p->n_tickets;
   } else if (p->kind == 4) {
-    info->tile_m = 16;
-    info->tile_n = 8 * p->w4.nt;
+    info->tile_m = 128;
+    info->tile_n = p->w4.tp;
     info->tile_k = 128;
-    info->stages = 0;
-    info->split_k = p->w4.slices;
+    info->stages = 4;
+    info->split_k = p->w4.max_segs;
     info->grid = p->grid;
-    info->launches = p->w4.slices > 1 ? 2 : 1;
-    info->workspace_bytes = p->partial_bytes;
+    info->launches = 1;
+    info->workspace_bytes = p->sk_bytes;
   } else if (p->kernel == 1) {
     info->tile_m = 128;  // features per tile (the MMA's M)
     info->tile_n = p->sk.TP;  // padded rows (the MMA's N)

@@ -127,10 +127,8 @@ struct GroupedCfg {
 // A plan of few rows times 4-bit weights.
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
-  int group = 0, nt = 0, threads = 0;
   uint32_t smem = 0;
-  int items = 0, groups_of_items = 0;  // feature tiles, and the CTAs that share them
-  int slices = 1, slice_kt = 0, row_blocks = 1;
+  int tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1;
 };
 
 // Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`

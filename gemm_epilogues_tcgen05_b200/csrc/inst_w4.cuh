@@ -7,26 +7,19 @@
 
 namespace ge_inst {
 
-template <int NT, bool GATED, int NG, bool BF>
-W4Instance w4_one() {
-  constexpr int MATS = GATED || NT >= 4 ? 2 : 1;
-  using S = ge::W4Shape<NT>;
-  return {ge::w4_kernel<NT, MATS, GATED, NG, BF>, S::WARPS, S::BUFS * S::WARPS * MATS * S::PART * 4};
-}
-
-template <int NT, bool BF>
-W4Instance w4_nt(bool gated, int ng) {
-  if (ng == 1) return gated ? w4_one<NT, true, 1, BF>() : w4_one<NT, false, 1, BF>();
-  if (ng == 2) return gated ? w4_one<NT, true, 2, BF>() : w4_one<NT, false, 2, BF>();
-  return gated ? w4_one<NT, true, 4, BF>() : w4_one<NT, false, 4, BF>();
+template <int TP, bool GATED, bool BF>
+W4Instance w4_ng(int ng) {
+  if (ng == 1) return {ge::w4_kernel<TP, GATED, 1, BF>, ge::W4Smem<TP, 1>::BYTES};
+  if (ng == 2) return {ge::w4_kernel<TP, GATED, 2, BF>, ge::W4Smem<TP, 2>::BYTES};
+  return {ge::w4_kernel<TP, GATED, 4, BF>, ge::W4Smem<TP, 4>::BYTES};
 }
 
 template <bool BF>
-W4Instance w4_any(int nt, bool gated, int ng) {
-  return nt == 1   ? w4_nt<1, BF>(gated, ng)
-         : nt == 2 ? w4_nt<2, BF>(gated, ng)
-         : nt == 4 ? w4_nt<4, BF>(gated, ng)
-                   : w4_nt<8, BF>(gated, ng);
+W4Instance w4_any(int tp, bool gated, int ng) {
+  if (tp == 16) return gated ? w4_ng<16, true, BF>(ng) : w4_ng<16, false, BF>(ng);
+  if (tp == 32) return gated ? w4_ng<32, true, BF>(ng) : w4_ng<32, false, BF>(ng);
+  if (tp == 64) return gated ? w4_ng<64, true, BF>(ng) : w4_ng<64, false, BF>(ng);
+  return gated ? W4Instance{} : w4_ng<128, false, BF>(ng);
 }
 
 }  // namespace ge_inst

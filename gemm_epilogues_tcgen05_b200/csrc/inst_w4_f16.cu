@@ -2,5 +2,5 @@
 #include "inst_w4.cuh"
 
 namespace ge_inst {
-W4Instance w4_f16(int nt, bool gated, int ng) { return w4_any<false>(nt, gated, ng); }
+W4Instance w4_f16(int tp, bool gated, int ng) { return w4_any<false>(tp, gated, ng); }
 }  // namespace ge_inst

@@ -91,14 +91,14 @@ GatedSkinnyInstance gated_skinny_f16_nk(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_mn(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_nk(int tp, int gn);
 
-// Few rows times 4-bit weights: 8 nt rows (nt = 1, 2, 4, 8), groups of 128 / ng
-// columns; two streams of tiles for gated layers and for nt >= 4, else one.
-using W4KernelFn = void (*)(ge::W4MulParams);
+// Few rows times 4-bit weights: tp = 16, 32, 64 or (not gated) 128 padded rows,
+// groups of 128 / ng columns.
+using W4KernelFn = void (*)(CUtensorMap, ge::W4MulParams);
 struct W4Instance {
   W4KernelFn fn;
-  int warps, join_bytes;
+  uint32_t smem;
 };
-W4Instance w4_f16(int nt, bool gated, int ng);
-W4Instance w4_bf16(int nt, bool gated, int ng);
+W4Instance w4_f16(int tp, bool gated, int ng);
+W4Instance w4_bf16(int tp, bool gated, int ng);
 
 }  // namespace ge_inst

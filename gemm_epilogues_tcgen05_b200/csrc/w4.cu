@@ -1,6 +1,6 @@
 // w4.cu -- C ABI of 4-bit weights with group scales: quantisation, packing, the
 // inverse, and the plan and call of the product with few rows.
-#include "host_common.h"
+#include "host_tiles.h"
 #include "w4_kernel.cuh"
 #include "w4_quant.cuh"
 
@@ -12,7 +12,7 @@ constexpr int64_t kMaxCols = (int64_t)1 << 22;
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int kMaxT = 256;
 
-int64_t row_tiles(int64_t rows) { return (rows + 15) / 16; }
+int64_t row_tiles(int64_t rows) { return (rows + 31) / 32; }
 int64_t col_tiles(int64_t cols) { return (cols + 127) / 128; }
 
 int check_shape(const char* call, int64_t batch, int64_t rows, int64_t cols, int64_t group) {
@@ -76,6 +76,11 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   }
   int dev = 0, sms = 0;
   if (require_b200(&dev, &sms)) return nullptr;
+  const int64_t tiles = (N + 127) / 128, kt = col_tiles(K);
+  if ((tiles * kt + 1) * sms >= (int64_t)1 << 31) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "shape too large for 32-bit tile coordinates");
+    return nullptr;
+  }
   auto* p = new gemm_epi_plan_s();
   p->kind = 4;
   p->kernel = 8;
@@ -88,39 +93,54 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
   p->device = dev;
   p->num_sms = sms;
+  const WatchdogEnv wd = watchdog_env();
+  p->timeout_ns = wd.timeout_ns;
+  p->inject_stall = wd.inject_stall;
   W4Cfg& c = p->w4;
-  c.group = (int)group;
-  c.nt = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
-  c.row_blocks = ceil_div(T, 8 * c.nt);
-  const int ng = (int)(128 / group);
-  const ge_inst::W4Instance inst =
-      dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16(c.nt, gated, ng) : ge_inst::w4_f16(c.nt, gated, ng);
+  // a gated layer's accumulating warps hold two sums a row
+  c.tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 || gated ? 64 : 128;
+  c.row_blocks = ceil_div(T, c.tp);
+  const ge_inst::W4Instance inst = (dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16 : ge_inst::w4_f16)(c.tp, gated, (int)(128 / group));
   c.fn = inst.fn;
-  c.threads = 32 * inst.warps;
-  c.items = (int)(gated || c.nt < 4 ? row_tiles(N) : (row_tiles(N) + 1) / 2);
-  // as many columns of X as shared memory holds beside the join's sums
-  const int rows = T < 8 * c.nt ? (int)T : 8 * c.nt, kt = (int)col_tiles(K);
-  const int room = ((232448 - inst.join_bytes) / rows - 64) / 256;
-  c.slices = (kt + room - 1) / room;
-  c.slice_kt = (kt + c.slices - 1) / c.slices;
-  c.slices = (kt + c.slice_kt - 1) / c.slice_kt;
-  c.smem = (uint32_t)(inst.join_bytes + rows * ge::w4_row_bytes(c.slice_kt));
-  const int share = sms / (c.slices * c.row_blocks);
-  c.groups_of_items = share < 1 ? 1 : share < c.items ? share : c.items;
-  p->grid = c.groups_of_items * c.slices * c.row_blocks;
+  c.smem = inst.smem;
+  c.tiles = (int)tiles;
+  c.kt = (int)kt;
+  // equal shares of all blocks of 128 columns, at least two each
+  const int total = c.tiles * c.kt, share = sms / c.row_blocks;
+  c.grid = total / 2 < 1 ? 1 : total / 2 < share ? total / 2 : share;
+  if (const char* f = getenv("GEMM_EPI_SKINNY_GRID")) {  // tuning override
+    const int v = atoi(f);
+    if (v >= 1 && v <= total && v <= share) c.grid = v;
+  }
+  p->grid = c.grid * c.row_blocks;
+  for (int t = 0; t < c.tiles; ++t) {
+    const int64_t first = ge::skinny_owner((int64_t)t * c.kt, c.grid, total);
+    const int64_t last = ge::skinny_owner((int64_t)(t + 1) * c.kt - 1, c.grid, total);
+    if (last - first + 1 > c.max_segs) c.max_segs = (int)(last - first + 1);
+  }
   cudaError_t e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
-  if (e == cudaSuccess && c.slices > 1) {
-    p->partial_bytes = (size_t)c.slices * (gated ? 2 : 1) * (size_t)T * 16 * (size_t)row_tiles(N) * sizeof(float);
-    e = cudaMalloc((void**)&p->partials, p->partial_bytes);
+  if (e == cudaSuccess && c.max_segs > 1) {
+    const size_t items = (size_t)c.row_blocks * (size_t)c.tiles;
+    p->sk_bytes = items * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
+    e = cudaMalloc((void**)&p->sk_partials, p->sk_bytes);
+    if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * items);
+    if (e == cudaSuccess) e = zero_counts(p->sk_tickets, items);
+    p->split_items = (int)items;
+    p->sk_bytes += sizeof(int) * items;
   }
   if (e == cudaSuccess) e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
+  if (e == cudaSuccess) {
+    *p->status_host = 0;
+    e = cudaHostGetDevicePointer((void**)&p->status_dev, p->status_host, 0);
+  }
   if (e != cudaSuccess) {
     cuda_fail(e, "plan of 4-bit weights");
-    if (p->partials) cudaFree(p->partials);
+    if (p->sk_partials) cudaFree(p->sk_partials);
+    if (p->sk_tickets) cudaFree(p->sk_tickets);
+    if (p->status_host) cudaFreeHost(p->status_host);
     delete p;
     return nullptr;
   }
-  *p->status_host = 0;  // (these kernels wait for nothing; gemm_epi_status reads it)
   {
     std::lock_guard<std::mutex> lock(g_mu);
     live_plans().insert(p);
@@ -135,12 +155,12 @@ extern "C" {
 
 int64_t gemm_epi_w4_bytes(int64_t batch, int64_t rows, int64_t cols, int64_t group) {
   if (check_shape("gemm_epi_w4_bytes", batch, rows, cols, group)) return -1;
-  return batch * row_tiles(rows) * col_tiles(cols) * 1024;
+  return batch * row_tiles(rows) * col_tiles(cols) * 2048;
 }
 
 int64_t gemm_epi_w4_scales(int64_t batch, int64_t rows, int64_t cols, int64_t group) {
   if (check_shape("gemm_epi_w4_scales", batch, rows, cols, group)) return -1;
-  return batch * row_tiles(rows) * col_tiles(cols) * 16 * (128 / group);
+  return batch * row_tiles(rows) * col_tiles(cols) * 32 * (128 / group);
 }
 
 int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype, const void* W,
@@ -149,8 +169,8 @@ int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t grou
   if (!rc) rc = check_dtype(dtype);
   if (rc) return rc;
   if (!W || !q || !scales) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_quantize: NULL W, q or scales");
-  if (!aligned(W, 16) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16))
-    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_quantize: q needs 32-byte, W, scales and zeros 16-byte alignment");
+  if (!aligned(W, 16) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(zeros, 16))
+    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_quantize: W, q, scales and zeros need 16-byte alignment");
   int dev = 0, sms = 0;
   rc = require_b200(&dev, &sms);
   if (rc) return rc;
@@ -171,9 +191,9 @@ int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, c
   if (rc) return rc;
   if (!codes || !src_scales || !q || !scales || (src_zeros == nullptr) != (zeros == nullptr))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_pack: NULL codes, scales or q, or zeros on one side alone");
-  if (!aligned(codes, 16) || !aligned(src_scales, 2) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16))
+  if (!aligned(codes, 16) || !aligned(src_scales, 2) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(zeros, 16))
     return fail(GEMM_EPI_ERR_MISALIGNED,
-                "gemm_epi_w4_pack: q needs 32-byte, codes, scales and zeros 16-byte, the given scales 2-byte alignment");
+                "gemm_epi_w4_pack: codes, q, scales and zeros need 16-byte, the given scales 2-byte alignment");
   int dev = 0, sms = 0;
   rc = require_b200(&dev, &sms);
   if (rc) return rc;
@@ -195,8 +215,8 @@ int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t gr
   if (!rc) rc = check_dtype(dtype);
   if (rc) return rc;
   if (!q || !scales || !out) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_dequantize: NULL q, scales or out");
-  if (!aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(out, 16))
-    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_dequantize: q needs 32-byte, scales, zeros and out 16-byte alignment");
+  if (!aligned(q, 16) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(out, 16))
+    return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_w4_dequantize: q, scales, zeros and out need 16-byte alignment");
   int dev = 0, sms = 0;
   rc = require_b200(&dev, &sms);
   if (rc) return rc;
@@ -228,40 +248,42 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   const bool optional_bias = p->epilog == GEMM_EPI_NONE || p->epilog == GEMM_EPI_GATED;
   if (!X || !q || !scales || !Y || (!bias && !optional_bias))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_execute: NULL X, q, scales, bias or Y");
-  if (!aligned(X, 16) || !aligned(q, 32) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(Y, 16) ||
+  if (!aligned(X, 16) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(Y, 16) ||
       !aligned(bias, p->bias_f32 ? 4 : 2))
     return fail(GEMM_EPI_ERR_MISALIGNED,
-                "gemm_epi_w4_execute: q needs 32-byte, X, scales, zeros and Y 16-byte, bias 2-byte (fp32: 4-byte) alignment");
+                "gemm_epi_w4_execute: X, q, scales, zeros and Y need 16-byte, bias 2-byte (fp32: 4-byte) alignment");
   DeviceScope scope(p->device);
+  rc = begin_call(p, stream);
+  if (rc) return rc;
   const W4Cfg& c = p->w4;
+  CUtensorMap x;
+  rc = encode_2d(&x, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, (uint32_t)c.tp, "the row operand");
+  if (rc) return rc;
   ge::W4MulParams k{};
   k.T = (int32_t)p->T;
   k.N = (int32_t)p->N;
   k.K = (int32_t)p->K;
   k.rt = (int32_t)row_tiles(p->N);
-  k.kt = (int32_t)col_tiles(p->K);
-  k.items = c.items;
-  k.slices = c.slices;
-  k.slice_kt = c.slice_kt;
+  k.kt = c.kt;
+  k.total = c.tiles * c.kt;
+  k.max_segs = c.max_segs;
   k.epi = p->epilog;
   k.act = p->act;
   k.bias_f32 = p->bias_f32;
   k.out_f32 = p->out_f32;
-  k.X = X;
   k.q = q;
   k.scales = scales;
   k.zeros = zeros;
   k.bias = p->epilog == GEMM_EPI_NONE ? nullptr : bias;
   k.out = Y;
-  k.sums = p->partials;
-  Launch l(dim3((unsigned)c.groups_of_items, (unsigned)c.slices, (unsigned)c.row_blocks), c.threads, c.smem, false, stream);
-  cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, k);
-  if (e != cudaSuccess) return cuda_fail(e, "launch of the product with 4-bit weights");
-  if (c.slices == 1) return GEMM_EPI_OK;
-  const int64_t blocks = (p->T * p->N + 255) / 256, most = (int64_t)p->num_sms * 8;
-  Launch f((int)(blocks < most ? blocks : most), 256, 0, false, stream);
-  e = cudaLaunchKernelEx(&f.cfg, p->dtype == GEMM_EPI_BF16 ? ge::w4_finish_kernel<true> : ge::w4_finish_kernel<false>, k);
-  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the slices' sum");
+  k.partials = p->sk_partials;
+  k.tickets = p->sk_tickets;
+  k.status = p->status_dev;
+  k.timeout_ns = p->timeout_ns;
+  k.inject_stall = p->inject_stall;
+  Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), ge::kW4Threads, c.smem, false, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, x, k);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");
 }
 
 }  // extern "C"

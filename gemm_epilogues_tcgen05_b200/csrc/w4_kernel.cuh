@@ -2,92 +2,82 @@
 // w4_quant.cuh): Y[t][n] = epilog(sum_k X[t][k] s_g (q[n][k] - z_g)), and as a gated
 // layer (two matrices).
 //
-// The weight is streamed once, 32 bytes a lane and instruction, and is the bound:
-// N K / 2 bytes and the scales. q - z is a small integer, exact in the 16-bit type:
-// a shift, a mask, an or with 128's (1024's) bits and one subtraction make two of them, with no
-// rounding of weights anywhere. A warp multiplies 16 features (the M slot) x 32
-// columns with 8 NT rows of X (the N slot) by m16n8k16 tensor-core instructions,
-// adds up a group in fp32, then adds the group's sum times its scale to the
-// feature's sum. (The tensor memory path wants its operand in shared or tensor
-// memory and 128 features at a time, and could scale the sums only per tile
-// read; with few rows the instructions per weight, not the MMA rate, count.)
+// Swap-AB, as the few-row kernel: 128 features in the MMA's M slot, the rows of X,
+// padded to TP, in its N slot. The weight's operand comes from tensor memory: a
+// dequantising warp unpacks 32 columns of a lane's own feature to the integers q - z,
+// exact in the 16-bit type (a shift, a mask with 128's or 1024's exponent, a subtraction
+// for two), and stores them as 16 columns of its lane (tcgen05.st), so that
+// no unpacked weight passes through shared memory. One MMA chain per group
+// of G columns leaves the group's sums (fp32) in one of several accumulators, and
+// accumulating warps add them, times the scale of their lane's feature, to sums in registers:
+// no weight is rounded anywhere.
+// (The same on mma.sync fragments took 11.4 us for T = 1, K = 4096, N = 11008 and
+// 52 us for T = 64: its MMAs run at about a sixteenth of tcgen05's rate here, 27 cycles a
+// quarter SM for 16 x 8 x 16.)
 //
-// A CTA takes a run of feature tiles; its warps share each tile's columns, 128 at a
-// time in turn, across tile ends, DEPTH tiles of loads ahead, and join their
-// fp32 sums through shared memory in a fixed order. X (its columns of the
-// slice) stays in shared memory. Where X of all columns does not fit, the columns
-// are cut into slices for different CTAs, which leave fp32 sums in the workspace for
-// w4_finish_kernel.
+// Warp roles:
+//   0..7    dequantise: lane quarter warp % 4, columns 64 (warp / 4) .. + 63 of each block of 128
+//   8..15   accumulate and finish: lane quarter warp % 4, half of the TP rows each
+//   16      X by TMA, 128 columns a stage
+//   17      tensor memory, MMAs
+// Codes, zeros and scales come in by cp.async, each warp its own, `AHEAD` blocks
+// ahead of its work.
+//
+// Work split (stream-K) and joining of shared tiles: as the few-row kernel
+// (skinny_kernel.cuh), blocks of 128 columns instead of its k-blocks.
 #pragma once
 
 #include "activation.cuh"
-#include "tile_kernel.cuh"
+#include "skinny_kernel.cuh"
 #include "w4_quant.cuh"
 
 namespace ge {
 
 struct W4MulParams {
   int32_t T, N, K;
-  int32_t rt, kt;        // 16-feature tiles of a matrix; 128-column blocks
-  int32_t items;         // feature tiles (MATS = 2, not gated: pairs of them)
-  int32_t slices, slice_kt;  // column slices, blocks of each (the last may have fewer)
+  int32_t rt, kt;        // 32-feature tiles of a matrix, 128-column blocks
+  int32_t total;         // 128-feature tiles x kt
+  int32_t max_segs;
   int32_t epi, act;      // EpiKind; gated: an ActKind
   int32_t bias_f32, out_f32;
-  const void* X;
   const uint8_t* q;
   const void* scales;
   const uint8_t* zeros;
   const void* bias;
   void* out;
-  float* sums;           // slices > 1: [slices][matrices][T][16 rt]
+  float* partials;       // [row blocks][tiles][max_segs][matrices][TP][128]
+  int* tickets;          // [row blocks][tiles], zero between launches
+  int* status;
+  uint64_t timeout_ns;
+  int32_t inject_stall;
 };
 
-template <int NT>
-struct W4Shape {
-  static constexpr int WARPS = NT <= 2 ? 16 : 8;
-  static constexpr int BUFS = NT <= 2 ? 2 : 1;       // of the join
-  static constexpr int COL = 20;                      // floats of a row's 16 features in it (no bank conflicts)
-  static constexpr int PART = 8 * NT * COL;           // floats of a warp and matrix
+constexpr int kW4Threads = 32 * 18;
+constexpr int kW4Ahead = 6;    // blocks that a warp's copies run ahead
+constexpr int kW4Stages = 4;   // of 128 columns: unpacked weights (tensor memory), X (shared memory)
+
+template <int TP, int NG>
+struct W4Smem {
+  static constexpr uint32_t X_SUB = TP * kBK * 2;             // TP rows x 64 columns
+  static constexpr uint32_t X_BYTES = 2 * X_SUB;
+  static constexpr uint32_t CODES = 1024 + 32 * NG;           // of a dequantising warp and block: codes, zeros
+  static constexpr uint32_t SCALES = 64 * NG;                 // of an accumulating warp and block
+  static constexpr int D_BUFS = TP <= 32 ? 8 : TP == 64 ? 4 : 2;  // accumulators
+  static constexpr uint32_t OFF_X = 0;
+  static constexpr uint32_t OFF_CODES = OFF_X + kW4Stages * X_BYTES;
+  static constexpr uint32_t OFF_SCALES = OFF_CODES + 8 * kW4Ahead * CODES;
+  static constexpr uint32_t OFF_BAR = OFF_SCALES + 8 * kW4Ahead * SCALES;
+  static constexpr uint32_t N_BARS = 4 * kW4Stages + 2 * D_BUFS + 1;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;
+  static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t COL_A = 0, COL_D = kW4Stages * 64;
+  static_assert(COL_D + D_BUFS * TP <= TMEM_COLS, "tensor memory columns");
+  static_assert(BYTES <= 232448, "above the per-CTA limit");
 };
 
-// bytes of a row of X in shared memory: 64 past a multiple of 128, so that rows are on other banks
-__host__ __device__ constexpr int w4_row_bytes(int blocks) { return blocks * 256 + 64; }
-
-struct W4Tile {
-  uint32_t w[8];   // [4 blocks of 32 columns][r]
-  uint32_t s[4];   // [groups]: the scales of both rows
-  uint32_t z[2];   // [groups][r] bytes
-};
-
-template <int NG>
-__device__ __forceinline__ void w4_load_tile(W4Tile& t, const W4MulParams& p, int64_t tile) {
-  const uint32_t lane = lane_id();
-  asm volatile("ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(t.w[0]), "=r"(t.w[1]), "=r"(t.w[2]), "=r"(t.w[3]), "=r"(t.w[4]), "=r"(t.w[5]), "=r"(t.w[6]), "=r"(t.w[7])
-               : "l"(p.q + tile * 1024 + lane * 32));
-  const uint32_t* s = reinterpret_cast<const uint32_t*>(p.scales) + (tile * 8 + (lane >> 2)) * NG;
-  if constexpr (NG == 4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
-    t.s[0] = v.x, t.s[1] = v.y, t.s[2] = v.z, t.s[3] = v.w;
-  } else if constexpr (NG == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-    t.s[0] = v.x, t.s[1] = v.y;
-  } else {
-    t.s[0] = __ldg(s);
-  }
-  if (p.zeros) {
-    const uint8_t* z = p.zeros + (tile * 8 + (lane >> 2)) * (2 * NG);
-    if constexpr (NG == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
-      t.z[0] = v.x, t.z[1] = v.y;
-    } else if constexpr (NG == 2) {
-      t.z[0] = __ldg(reinterpret_cast<const uint32_t*>(z));
-    } else {
-      t.z[0] = __ldg(reinterpret_cast<const uint16_t*>(z));
-    }
-  } else {
-    t.z[0] = t.z[1] = 0x08080808u;
-  }
+__device__ __forceinline__ void w4_copy_16(uint32_t saddr, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "l"(policy) : "memory");
 }
 
 template <bool BF16>
@@ -101,49 +91,48 @@ __device__ __forceinline__ uint32_t w4_sub(uint32_t a, uint32_t b) {
   }
 }
 
-// zero point z (0 .. 127) as two halves of 128 + z (1024 + z), exact in the type
+// 128 + v (1024 + v) twice, exact in the type for v up to 127
 template <bool BF16>
-__device__ __forceinline__ uint32_t w4_zero2(uint32_t z) {
-  if constexpr (BF16) {
-    // 128 + z: the exponent of 128, z in the 7 bits below
-    return 0x43004300u + z * 0x00010001u;
-  } else {
-    return 0x64006400u + z * 0x00010001u;
-  }
+__device__ __forceinline__ uint32_t w4_biased(uint32_t pair) {
+  return pair | (BF16 ? 0x43004300u : 0x64006400u);
 }
 
-// q - z of two neighbouring columns, exactly
-template <bool BF16>
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int m, uint32_t zero2) {
-  constexpr uint32_t kOne = BF16 ? 0x43004300u : 0x64006400u;
-  return w4_sub<BF16>(((word >> (4 * m)) & 0x000f000fu) | kOne, zero2);
+// 16 registers to 16 columns of this warp's lane quarter
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
-template <bool BF16>
-__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D[tmem] (+)= A[tmem] * B[smem]: A's 16 k of a row are 8 columns of its lane
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // One output from its sums (gated: gate and up projection), feature n of row t.
-template <bool BF16>
-__device__ __forceinline__ void w4_output(const W4MulParams& p, float a, float b, int t, int n) {
-  const bool gated = p.epi == EPI_GATED;
-  if (p.bias && p.epi != EPI_STORE) {
-    a += load_bias<BF16>(p.bias, p.bias_f32, n);
-    if (gated) b += load_bias<BF16>(p.bias, p.bias_f32, p.N + n);
-  }
-  if (gated || p.epi == EPI_GELU_BIAS) {
+template <bool GATED, bool BF16>
+__device__ __forceinline__ void w4_output(const W4MulParams& p, float a, float b, int t, int n, float bias_a, float bias_b) {
+  a += bias_a;
+  if (GATED || p.epi == EPI_GELU_BIAS) {
     float z[2] = {a, a}, v[2], none[2];
-    act_values<2, false>(gated ? p.act : ACT_GELU, z, v, none);
-    a = gated ? v[0] * b : v[0];
+    act_values<2, false>(GATED ? p.act : ACT_GELU, z, v, none);
+    a = GATED ? v[0] * (b + bias_b) : v[0];
   } else if (p.epi == EPI_RELU_BIAS) {
     a = a > 0.f ? a : 0.f;
   }
@@ -154,203 +143,359 @@ __device__ __forceinline__ void w4_output(const W4MulParams& p, float a, float b
     reinterpret_cast<uint16_t*>(p.out)[o] = w4_round16<BF16>(a);
 }
 
-// MATS streams of tiles share the fragments of X: the gate's and the up
-// projection's tile (GATED), or two neighbouring tiles of one matrix.
-template <int NT, int MATS, bool GATED, int NG, bool BF16>
-__global__ void __launch_bounds__(32 * W4Shape<NT>::WARPS, 1) w4_kernel(const W4MulParams p) {
-  using S = W4Shape<NT>;
-  constexpr int W = S::WARPS, THREADS = 32 * W;
-  constexpr int DEPTH = MATS == 1 ? 4 : 2;  // tiles of each stream whose loads are under way
-  static_assert(MATS == 2 || !GATED, "a gated layer has two streams");
-  extern __shared__ __align__(16) uint8_t w4_smem[];
-  float* join = reinterpret_cast<float*>(w4_smem);  // [BUFS][W][MATS][PART]
-  uint8_t* xs = w4_smem + S::BUFS * W * MATS * S::PART * 4;
+template <int TP, bool GATED, int NG, bool BF16>
+__global__ void __launch_bounds__(kW4Threads, 1)
+    w4_kernel(const __grid_constant__ CUtensorMap tmX, const W4MulParams p) {
+  using L = W4Smem<TP, NG>;
+  constexpr int MATS = GATED ? 2 : 1, STAGES = kW4Stages, BUFS = L::D_BUFS, AHEAD = kW4Ahead;
+  constexpr int ROWS = TP / 2;  // of an accumulating warp
+  constexpr uint32_t IDESC = idesc_f16(BF16, false, false, 128, TP);
 
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
-  const int row0 = blockIdx.z * 8 * NT, rows = min(p.T - row0, 8 * NT);
-  const int kb0 = blockIdx.y * p.slice_kt, nkb = min(p.kt - kb0, p.slice_kt);
-  const int lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.items / gridDim.x);
-  const int hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.items / gridDim.x);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* afull = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* aempty = afull + STAGES;
+  uint64_t* xfull = aempty + STAGES;
+  uint64_t* xempty = xfull + STAGES;
+  uint64_t* dfull = xempty + STAGES;
+  uint64_t* dempty = dfull + BUFS;
+  uint64_t* drain = dempty + BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
+
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const int row0 = blockIdx.y * TP;
+  SkinnyParams sp{};  // what a segment is found by
+  sp.kbt = p.kt;
+  sp.total_kb = p.total;
+  const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(blockIdx.x) * p.total / gridDim.x);
+  const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(blockIdx.x + 1) * p.total / gridDim.x);
+  TileParams wp{};
+  wp.status = p.status;
+  wp.timeout_ns = p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&afull[s], 8);
+      mbar_init(&aempty[s], 1);
+      mbar_init(&xfull[s], 1);
+      mbar_init(&xempty[s], 1);
+    }
+    for (int b = 0; b < BUFS; ++b) {
+      mbar_init(&dfull[b], 1);
+      mbar_init(&dempty[b], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *last_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 16 && lane == 0) prefetch_tensormap(&tmX);
+  if (warp == 17) {
+    tmem_alloc(tmem_slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
   wait_for_inputs();
 
-  const auto tile_of = [&](int item, int m, int b) {
-    const int i = GATED ? m * p.rt + item : MATS == 2 ? min(2 * item + m, p.rt - 1) : item;
-    return static_cast<int64_t>(i) * p.kt + kb0 + b;
-  };
-  // this warp's sequence: blocks warp, warp + W, ... of the run of tiles, (item, b)
-  W4Tile ring[DEPTH][MATS];
-  int li = lo, lb = static_cast<int>(warp);  // the next to be loaded
-  while (lb >= nkb) {
-    lb -= nkb;
-    ++li;
-  }
-  const auto load = [&](W4Tile (&t)[MATS]) {
-    if (li < hi) {
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) w4_load_tile<NG>(t[m], p, tile_of(li, m, lb));
-      lb += W;
-      while (lb >= nkb) {
-        lb -= nkb;
-        ++li;
-      }
-    }
-  };
-  int item = lo, b = static_cast<int>(warp);
-  while (b >= nkb) {
-    b -= nkb;
-    ++item;
-  }
-#pragma unroll
-  for (int d = 0; d < DEPTH; ++d) load(ring[d]);
-
-  // X: this slice's columns of this CTA's rows, zeros past K
-  const int xb = w4_row_bytes(p.slice_kt);
-  const int units = nkb * 16;  // of 8 columns
-  for (int e = threadIdx.x; e < rows * units; e += THREADS) {
-    const int r = e / units, u = e - r * units, col = kb0 * 128 + u * 8;
-    const uint4 v = col < p.K ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) +
-                                                                     static_cast<int64_t>(row0 + r) * p.K + col))
-                              : make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(xs + r * xb + u * 16) = v;
-  }
-  __syncthreads();
-
-  float acc[MATS][NT][4];
-  const auto clear = [&]() {
-#pragma unroll
-    for (int m = 0; m < MATS; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.f;
-  };
-  clear();
-  const uint32_t x0 = smem_u32(xs) + g * xb + c * 16;
-
-  // the sums of item `at` are complete: join the warps' and finish
-  int turn = 0;
-  const auto finish = [&](int at) {
-    float* buf = join + (S::BUFS == 2 ? (turn & 1) * (W * MATS * S::PART) : 0);
-    float* mine = buf + warp * (MATS * S::PART);
-    if (S::BUFS == 1 && turn > 0) __syncthreads();  // the last one has been read
-    ++turn;
-#pragma unroll
-    for (int m = 0; m < MATS; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mine[m * S::PART + (t * 8 + 2 * c + (e & 1)) * S::COL + g + 8 * (e >> 1)] = acc[m][t][e];
-    clear();
-    __syncthreads();
-    const int n_out = rows * 16 * (GATED ? 1 : MATS);
-    for (int o = threadIdx.x; o < n_out; o += THREADS) {
-      const int f = o & 15, m = GATED ? 0 : (o >> 4) % MATS, t = GATED ? o >> 4 : (o >> 4) / MATS;
-      const float* from = buf + m * S::PART + t * S::COL + f;
-      float a = 0.f, u = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        a += from[w * (MATS * S::PART)];
-        if constexpr (GATED) u += from[w * (MATS * S::PART) + S::PART];
-      }
-      const int n = (GATED ? at : MATS * at + m) * 16 + f;
-      if (n >= p.N) continue;
-      if (p.slices == 1) {
-        w4_output<BF16>(p, a, u, row0 + t, n);
-      } else {
-        const int64_t ld = static_cast<int64_t>(p.rt) * 16;
-        float* to = p.sums + (static_cast<int64_t>(blockIdx.y) * (GATED ? 2 : 1) * p.T + row0 + t) * ld + n;
-        to[0] = a;
-        if constexpr (GATED) to[p.T * ld] = u;
-      }
-    }
-  };
-
-  const auto work = [&](const W4Tile (&tile)[MATS], int block) {
-    const uint32_t xk = x0 + block * 256;
-    float part[MATS][NT][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // 32 columns
-      constexpr int PER = 4 / NG;  // of them in a group
-      if (k % PER == 0) {
-#pragma unroll
-        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[m][t][e] = 0.f;
-      }
-      uint4 x[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        x[t] = t * 8 + static_cast<int>(g) < rows ? ld_shared_v4(xk + t * 8 * xb + k * 64) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        const uint32_t zz = tile[m].z[(k / PER) >> 1] >> (16 * ((k / PER) & 1));
-        const uint32_t z0 = w4_zero2<BF16>(zz & 127u), z1 = w4_zero2<BF16>((zz >> 8) & 127u);
-        const uint32_t w0 = tile[m].w[2 * k], w1 = tile[m].w[2 * k + 1];
-        uint32_t a[4], bq[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = w4_pair<BF16>(w0, e, z0);
-          bq[e] = w4_pair<BF16>(w1, e, z1);
+  // blocks lo .. hi - 1 of (tile, kb), the matrices of each one after the other
+  if (warp < 8) {
+    // --------------------------------------------------------- dequantise
+    const uint32_t quarter = warp & 3u, half = warp >> 2;
+    const uint32_t ring = smem_u32(smem + L::OFF_CODES) + warp * (AHEAD * L::CODES);
+    const uint64_t policy = l2_policy_evict_first();
+    struct Cursor {
+      uint32_t tile, kb;
+      int m;
+    };
+    const uint32_t kt = static_cast<uint32_t>(p.kt);
+    const uint32_t steps = (hi - lo) * MATS;
+    Cursor in{lo / kt, lo % kt, 0};
+    uint32_t fetched = 0, place_in = ring;
+    const auto fetch = [&]() {
+      if (fetched < steps) {
+        const uint32_t i = 4 * in.tile + quarter;
+        if (i < static_cast<uint32_t>(p.rt)) {
+          const int64_t tile = (static_cast<int64_t>(in.m) * p.rt + i) * p.kt + in.kb;
+          const uint8_t* q = p.q + tile * kW4TileBytes + half * 1024 + lane * 16;
+          w4_copy_16(place_in + lane * 16, q, policy);
+          w4_copy_16(place_in + 512 + lane * 16, q + 512, policy);
+          if (p.zeros && lane < 2 * NG) w4_copy_16(place_in + 1024 + lane * 16, p.zeros + tile * (32 * NG) + lane * 16, policy);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          w4_mma<BF16>(part[m][t], a[0], bq[0], a[1], bq[1], x[t].x, x[t].y);
-          w4_mma<BF16>(part[m][t], a[2], bq[2], a[3], bq[3], x[t].z, x[t].w);
+        if (MATS == 2 && in.m == 0) {
+          in.m = 1;
+        } else {
+          in.m = 0;
+          if (++in.kb == kt) {
+            in.kb = 0;
+            ++in.tile;
+          }
         }
-        if (k % PER == PER - 1) {
-          const uint32_t s2 = tile[m].s[k / PER];
-          const float s0 = w4_float<BF16>(static_cast<uint16_t>(s2 & 0xffffu));
-          const float s1 = w4_float<BF16>(static_cast<uint16_t>(s2 >> 16));
+        place_in = place_in + L::CODES == ring + AHEAD * L::CODES ? ring : place_in + L::CODES;
+        ++fetched;
+      }
+      cp_async_commit();
+    };
+    for (int d = 0; d < AHEAD; ++d) fetch();
+    uint32_t place = ring;
+    bool ok = true;
+    for (uint32_t it = 0; it < steps; ++it) {
+      const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+      cp_async_wait<AHEAD - 1>();
+      __syncwarp();
+      uint4 c[2];
+      c[0] = ld_shared_v4(place + lane * 16);
+      c[1] = ld_shared_v4(place + 512 + lane * 16);
+      uint32_t z[2] = {8u, 8u};  // of either 32 columns
+      if (p.zeros) {
+        z[0] = ld_shared_u8(place + 1024 + (2 * half * NG / 4) * 32 + lane);
+        z[1] = ld_shared_u8(place + 1024 + ((2 * half + 1) * NG / 4) * 32 + lane);
+      }
+      __syncwarp();
+      fetch();
+      place = place + L::CODES == ring + AHEAD * L::CODES ? ring : place + L::CODES;
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&aempty[s], ph ^ 1u, wp, abort_flag, 1));
+      if (!ok) continue;  // (the copies under way are waited for below)
+      tc_fence_after();
+      const uint32_t a = tmem_base + ((quarter * 32u) << 16) + L::COL_A + s * 64 + half * 32;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            acc[m][t][0] = fmaf(s0, part[m][t][0], acc[m][t][0]);
-            acc[m][t][1] = fmaf(s0, part[m][t][1], acc[m][t][1]);
-            acc[m][t][2] = fmaf(s1, part[m][t][2], acc[m][t][2]);
-            acc[m][t][3] = fmaf(s1, part[m][t][3], acc[m][t][3]);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+        const uint32_t zero = w4_biased<BF16>((z[h] & 127u) * 0x00010001u);
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          r[i] = w4_sub<BF16>(w4_biased<BF16>((w[i / 4] >> (4 * (i % 4))) & 0x000f000fu), zero);
+        tmem_st_32x32b_x16(a + 16 * h, r);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&afull[s]);
+    }
+    cp_async_wait<0>();
+  } else if (warp < 16) {
+    // ------------------------------------------- accumulate, join, finish
+    const uint32_t quarter = warp & 3u, part = (warp - 8u) >> 2;  // part: rows ROWS part .. of TP
+    const uint32_t ring = smem_u32(smem + L::OFF_SCALES) + (warp - 8u) * (AHEAD * L::SCALES);
+    const uint64_t policy = l2_policy_evict_first();
+    const uint32_t et = threadIdx.x - 256;
+    const uint32_t kt = static_cast<uint32_t>(p.kt), steps = (hi - lo) * MATS;
+    uint32_t tile_in = lo / kt, kb_in = lo % kt, fetched = 0, place_in = ring;
+    int m_in = 0;
+    const auto fetch = [&]() {
+      if (fetched < steps) {
+        const uint32_t i = 4 * tile_in + quarter;
+        if (i < static_cast<uint32_t>(p.rt) && lane < 4 * NG) {
+          const int64_t tile = (static_cast<int64_t>(m_in) * p.rt + i) * p.kt + kb_in;
+          w4_copy_16(place_in + lane * 16, reinterpret_cast<const uint8_t*>(p.scales) + tile * (64 * NG) + lane * 16, policy);
+        }
+        if (MATS == 2 && m_in == 0) {
+          m_in = 1;
+        } else {
+          m_in = 0;
+          if (++kb_in == kt) {
+            kb_in = 0;
+            ++tile_in;
+          }
+        }
+        place_in = place_in + L::SCALES == ring + AHEAD * L::SCALES ? ring : place_in + L::SCALES;
+        ++fetched;
+      }
+      cp_async_commit();
+    };
+    for (int d = 0; d < AHEAD; ++d) fetch();
+    uint32_t place = ring, buf = 0, dph = 0;
+    bool ok = true;
+    uint32_t gpos = lo;
+    Segment seg;
+    while (skinny_segment(sp, hi, gpos, seg)) {
+      const int n_local = static_cast<int>(quarter * 32 + lane), n = seg.tile * 128 + n_local;
+      const bool n_ok = n < p.N;
+      float acc[MATS][ROWS];
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int t = 0; t < ROWS; ++t) acc[m][t] = 0.f;
+      for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          cp_async_wait<AHEAD - 1>();
+          __syncwarp();
+          float sc[NG];
+#pragma unroll
+          for (int k = 0; k < NG; ++k)
+            sc[k] = w4_float<BF16>(static_cast<uint16_t>(ld_shared_u16(place + k * 64 + lane * 2)));
+          __syncwarp();
+          fetch();
+          place = place + L::SCALES == ring + AHEAD * L::SCALES ? ring : place + L::SCALES;
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dfull[buf], dph, wp, abort_flag, 6));
+            if (ok) {
+              tc_fence_after();
+              const uint32_t d = tmem_base + ((quarter * 32u) << 16) + L::COL_D + buf * TP + part * ROWS;
+              constexpr int STEP = ROWS < 32 ? ROWS : 32;
+#pragma unroll
+              for (int t0 = 0; t0 < ROWS; t0 += STEP) {
+                uint32_t r[STEP];
+                if constexpr (STEP == 8)
+                  tmem_ld_32x32b_x8(d + t0, r);
+                else if constexpr (STEP == 16)
+                  tmem_ld_32x32b_x16(d + t0, r);
+                else
+                  tmem_ld_32x32b_x32(d + t0, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int t = 0; t < STEP; ++t) acc[m][t0 + t] = fmaf(sc[k], __uint_as_float(r[t]), acc[m][t0 + t]);
+              }
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&dempty[buf]);
+            }
+            if (++buf == BUFS) {
+              buf = 0;
+              dph ^= 1u;
+            }
           }
         }
       }
-    }
-  };
-
-  int at = lo;  // the item that acc holds
-  while (at < hi) {
+      const bool whole = seg.kb0 == 0 && seg.kb1 == p.kt;
+      float bias_a = 0.f, bias_b = 0.f;
+      if (p.bias && n_ok) {
+        bias_a = load_bias<BF16>(p.bias, p.bias_f32, n);
+        if constexpr (GATED) bias_b = load_bias<BF16>(p.bias, p.bias_f32, p.N + n);
+      }
+      const int t0 = static_cast<int>(part) * ROWS;
+      if (whole) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      // (every warp finishes every item once, also one that had none of its blocks)
-      while (at < item && at < hi) finish(at++);
-      if (at < hi) {
-        work(ring[d], b);
-        load(ring[d]);
-        b += W;
-        while (b >= nkb) {
-          b -= nkb;
-          ++item;
+        for (int t = 0; t < ROWS; ++t)
+          if (ok && n_ok && row0 + t0 + t < p.T)
+            w4_output<GATED, BF16>(p, acc[0][t], acc[MATS - 1][t], row0 + t0 + t, n, bias_a, bias_b);
+        continue;
+      }
+      // this segment's sums, a ticket; the last segment of the tile finishes it
+      const int64_t tiles = p.total / p.kt;
+      const int64_t at = (blockIdx.y * tiles + seg.tile) * p.max_segs;
+      float* slot = p.partials + (at + seg.seg) * (MATS * TP * 128) + n_local;
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int t = 0; t < ROWS; ++t)
+          if (row0 + t0 + t < p.T) slot[(m * TP + t0 + t) * 128] = acc[m][t];
+      __threadfence();
+      named_bar_sync(1, 256);
+      if (et == 0) {
+        int last = 0;
+        if (ok) {
+          int* ticket = p.tickets + blockIdx.y * tiles + seg.tile;
+          last = atomicAdd(ticket, 1) == seg.nsegs - 1;
+          if (last) *ticket = 0;  // ready for the next launch
+        }
+        *last_flag = last;
+      }
+      named_bar_sync(1, 256);
+      if (ok && *last_flag) {
+        __threadfence();
+        const float* from = p.partials + at * (MATS * TP * 128) + n_local;
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+          for (int t = 0; t < ROWS; ++t) acc[m][t] = 0.f;
+        for (int sg = 0; sg < seg.nsegs; ++sg) {
+          const float* f = from + static_cast<int64_t>(sg) * (MATS * TP * 128);
+#pragma unroll
+          for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int t = 0; t < ROWS; ++t)
+              if (row0 + t0 + t < p.T) acc[m][t] += __ldcg(f + (m * TP + t0 + t) * 128);
+        }
+#pragma unroll
+        for (int t = 0; t < ROWS; ++t)
+          if (n_ok && row0 + t0 + t < p.T)
+            w4_output<GATED, BF16>(p, acc[0][t], acc[MATS - 1][t], row0 + t0 + t, n, bias_a, bias_b);
+      }
+      named_bar_sync(1, 256);  // last_flag is reused by the next segment
+    }
+    cp_async_wait<0>();
+  } else if (warp == 16) {
+    // ------------------------------------------------------------------- X
+    if (lane == 0) {
+      const uint64_t policy = l2_policy_evict_last();
+      uint32_t it = 0, kb = lo % static_cast<uint32_t>(p.kt);
+      for (uint32_t b = lo; b < hi; ++b, ++it) {
+        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+        if (!wait_bounded(&xempty[s], ph ^ 1u, wp, abort_flag, 2)) break;
+        mbar_arrive_expect_tx(&xfull[s], L::X_BYTES);
+        uint8_t* x = smem + L::OFF_X + s * L::X_BYTES;
+        const int k = static_cast<int>(kb) * 128;
+        tma_load_2d_hint(x, &tmX, &xfull[s], k, row0, policy);
+        tma_load_2d_hint(x + L::X_SUB, &tmX, &xfull[s], k + 64, row0, policy);
+        if (++kb == static_cast<uint32_t>(p.kt)) kb = 0;
+      }
+      // what was issued lands before the CTA leaves
+      const uint32_t inflight = it < STAGES ? it : STAGES;
+      for (uint32_t i = it - inflight; i < it; ++i)
+        wait_bounded(&xfull[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 3, /*honour_abort=*/false);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------------- MMA
+    const bool issuer = elect_one();
+    uint32_t it = 0, buf = 0, dph = 0;
+    bool ok = true;
+    for (uint32_t b = lo; ok && b < hi; ++b) {
+      const uint32_t xi = b - lo, xst = xi % STAGES, xph = (xi / STAGES) & 1u;
+      ok = __all_sync(0xffffffffu, wait_bounded(&xfull[xst], xph, wp, abort_flag, 4));
+      if (!ok) break;
+      const uint32_t x = smem_u32(smem + L::OFF_X + xst * L::X_BYTES);
+      for (int m = 0; ok && m < MATS; ++m, ++it) {
+        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+        ok = __all_sync(0xffffffffu, wait_bounded(&afull[s], ph, wp, abort_flag, 5));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = tmem_base + L::COL_A + s * 64;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dempty[buf], dph ^ 1u, wp, abort_flag, 7));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem_base + L::COL_D + buf * TP;
+          if (issuer) {
+#pragma unroll
+            for (int j = 0; j < 8 / NG; ++j) {
+              const int kk = g * (8 / NG) + j;  // 16 columns each
+              const uint64_t bdesc = smem_desc_sw128(x + (kk >> 2) * L::X_SUB + (kk & 3) * 32, 16, 1024);
+              umma_f16_ts(d, a + kk * 8, bdesc, IDESC, j > 0 ? 1u : 0u);
+            }
+            // (fault injection: the accumulating warps then wait for a sum that is never announced)
+            if (!(p.inject_stall && it == 0 && g == 0)) umma_commit(&dfull[buf]);
+          }
+          if (++buf == BUFS) {
+            buf = 0;
+            dph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (issuer) {
+          umma_commit(&aempty[s]);
+          if (m == MATS - 1) umma_commit(&xempty[xst]);
         }
       }
     }
+    if (issuer) umma_commit(drain);
+    wait_bounded(drain, 0, wp, abort_flag, 8, /*honour_abort=*/false);
+    __syncwarp();
   }
-}
 
-// Column slices' sums added in order, then the epilog.
-template <bool BF16>
-__global__ void __launch_bounds__(256) w4_finish_kernel(const W4MulParams p) {
-  wait_for_inputs();
-  const int64_t ld = static_cast<int64_t>(p.rt) * 16, mat = static_cast<int64_t>(p.T) * ld;
-  const int mats = p.epi == EPI_GATED ? 2 : 1;
-  for (int64_t o = blockIdx.x * 256ll + threadIdx.x; o < static_cast<int64_t>(p.T) * p.N; o += gridDim.x * 256ll) {
-    const int t = static_cast<int>(o / p.N), n = static_cast<int>(o - static_cast<int64_t>(t) * p.N);
-    const float* from = p.sums + t * ld + n;
-    float a = 0.f, u = 0.f;
-    for (int s = 0; s < p.slices; ++s) {
-      a += __ldcg(from + s * mats * mat);
-      if (mats == 2) u += __ldcg(from + (s * mats + 1) * mat);
-    }
-    w4_output<BF16>(p, a, u, t, n);
-  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 17) tmem_dealloc(tmem_base, L::TMEM_COLS);
 }
 
 }  // namespace ge

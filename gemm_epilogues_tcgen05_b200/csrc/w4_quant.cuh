@@ -8,14 +8,13 @@
 //                  zero = clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15)
 // (rint: ties to even; a scale that rounds to 0 gives codes that are the zero.)
 //
-// Layout: tiles of 16 features x 128 columns, tile (i, j) of a matrix at 1024 (i kt +
-// j) bytes, as the product's warps read them -- one instruction a tile, 32 bytes a
-// lane. Lane l = 4 g + c has features g (r = 0) and g + 8 (r = 1) of the tile, and of the
-// 32-column block b = 0..3 the columns 8c .. 8c + 7 as a word of eight codes at byte 32 l + 8 b + 4 r:
-// column 2 m in bits 4m .. 4m+3, column 2 m + 1 in bits 4m+16 .. 4m+19, so that a shift and
-// a mask leave two neighbouring columns in a register's halves, as the tensor
-// cores want them. Scales (and zeros) of a tile: [g][128 / G groups][r]. Rows and columns
-// past the matrix are code 0 with scale 0.
+// Layout: tiles of 32 features x 128 columns, tile (i, j) of a matrix at 2048 (i kt +
+// j) bytes. Feature f, 32-column block b, 8-column word w of a tile are the 4 bytes at 512 b + 16 f + 4 w:
+// a warp of the product reads 512 contiguous bytes, 16 a lane, 32 columns of the
+// lane's own feature. In a word, column 2 m is in bits 4m .. 4m+3 and column 2 m + 1 in
+// bits 4m+16 .. 4m+19, so that a shift and a mask leave two neighbouring columns in
+// a register's halves. Scales (and zeros) of a tile: [128 / G groups][f]. Rows
+// and columns past the matrix are code 0 with scale 0.
 //
 // A warp takes a tile. Bound by memory: a weight of 11008 x 4096 is 90 MB to read and
 // 23.2 to write.
@@ -31,7 +30,7 @@ namespace ge {
 struct W4Params {
   int64_t tiles;         // of all matrices
   int32_t rows, cols;    // of one matrix
-  int32_t rt, kt;        // tiles along the rows and the columns of one matrix
+  int32_t rt, kt;        // tiles along the rows (32) and the columns (128) of one matrix
   int32_t group;
   const void* src;       // quantise: the 16-bit matrix; pack: the codes, two a byte, the lower column in the low 4 bits
   const void* src_scales;
@@ -42,14 +41,10 @@ struct W4Params {
   void* out;             // dequantise
 };
 
-// byte of the word of feature f (0..15) and 8-column unit u (0..15) in a tile
-__device__ __forceinline__ uint32_t w4_word(uint32_t f, uint32_t u) {
-  return 32 * (4 * (f & 7u) + (u & 3u)) + 8 * (u >> 2) + 4 * (f >> 3);
-}
-// index of the scale of feature f, group k of a tile of ng groups
-__device__ __forceinline__ uint32_t w4_scale(uint32_t f, uint32_t k, uint32_t ng) {
-  return ((f & 7u) * ng + k) * 2 + (f >> 3);
-}
+constexpr int kW4Rows = 32, kW4TileBytes = 2048;
+
+// byte of the word of feature f (0..31) and 8-column unit u (0..15) in a tile
+__device__ __forceinline__ uint32_t w4_word(uint32_t f, uint32_t u) { return 512 * (u >> 2) + 16 * f + 4 * (u & 3u); }
 
 template <bool BF16>
 __device__ __forceinline__ float w4_float(uint16_t h) {
@@ -71,14 +66,13 @@ __device__ __forceinline__ uint4 w4_load_once(const void* p) {
   return v;
 }
 
-// The tile's word as staged by its warp, out to the packed weight: 32 bytes a lane.
+// The tile's words as staged by its warp, out to the packed weight.
 __device__ __forceinline__ void w4_store_tile(uint8_t* q, const uint32_t* stage) {
   const uint32_t lane = lane_id();
   __syncwarp();
-  const uint4* from = reinterpret_cast<const uint4*>(stage);
-  uint4* to = reinterpret_cast<uint4*>(q);
-  to[lane] = from[lane];
-  to[32 + lane] = from[32 + lane];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<uint4*>(q)[32 * i + lane] = reinterpret_cast<const uint4*>(stage)[32 * i + lane];
   __syncwarp();
 }
 
@@ -91,11 +85,11 @@ __device__ __forceinline__ float w4_divide(float w, float s, float r) {
   return fmaf(fmaf(-q0, s, w), r, q0);
 }
 
-// Half a warp holds a row of the tile, a lane 8 columns of it, eight such pairs of
-// rows one after the other.
+// Half a warp holds a row of the tile, a lane 8 columns of it, 16 such pairs of
+// rows one after the other, eight loads ahead.
 template <bool BF16, bool ZEROS>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4Params p) {
-  __shared__ uint32_t stage[8][256];
+  __shared__ __align__(16) uint32_t stage[8][kW4TileBytes / 4];
   wait_for_inputs();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, u = lane & 15u, ng = 128u / p.group;
   const int lanes = p.group / 8;  // that share a group: 4, 8 or 16
@@ -105,66 +99,69 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4Params p) {
     const int i = static_cast<int>(row_tile % p.rt);
     const int64_t m = row_tile / p.rt;
     const int col = j * 128 + 8 * static_cast<int>(u);
-    uint4 in[8];
+#pragma unroll 1
+    for (int k0 = 0; k0 < 16; k0 += 8) {
+      uint4 in[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int row = i * 16 + 2 * k + static_cast<int>(lane >> 4);
-      in[k] = row < p.rows && col < p.cols
-                  ? w4_load_once(reinterpret_cast<const uint16_t*>(p.src) + (m * p.rows + row) * p.cols + col)
-                  : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 8; ++k) {
+        const int row = i * kW4Rows + 2 * (k0 + k) + static_cast<int>(lane >> 4);
+        in[k] = row < p.rows && col < p.cols
+                    ? w4_load_once(reinterpret_cast<const uint16_t*>(p.src) + (m * p.rows + row) * p.cols + col)
+                    : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t f = 2 * (k0 + k) + (lane >> 4);
+        const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = w4_float<BF16>(static_cast<uint16_t>(w[e] & 0xffffu));
+          v[2 * e + 1] = w4_float<BF16>(static_cast<uint16_t>(w[e] >> 16));
+        }
+        float lo = 0.f, hi = 0.f;  // (NaN stays: max.NaN, min.NaN)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(ZEROS ? v[e] : fabsf(v[e])));
+          if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(v[e]));
+        }
+        for (int off = 1; off < lanes; off <<= 1) {
+          asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(__shfl_xor_sync(0xffffffffu, hi, off)));
+          if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(__shfl_xor_sync(0xffffffffu, lo, off)));
+        }
+        float top = ZEROS ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f);
+        if (!(top <= 3.4e38f)) top = __uint_as_float(0x7fc00000u);  // an infinity or NaN: the group stands for NaN
+        const uint16_t s16 = w4_round16<BF16>(top);
+        const float s = w4_float<BF16>(s16);
+        float zero = 8.f;
+        if constexpr (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;
+        uint32_t word = 0;
+        const bool tiny = s < 1e-30f;  // the reciprocal would leave fp32
+        const float r = tiny ? 0.f : __frcp_rn(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float c = zero;
+          if (s > 0.f) c = rintf(tiny ? __fdiv_rn(v[e], s) : w4_divide(v[e], s, r)) + zero;
+          const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
+          word |= code << (4 * (e >> 1) + 16 * (e & 1));
+        }
+        const bool in_matrix = i * kW4Rows + static_cast<int>(f) < p.rows && col < p.cols;
+        stage[warp][w4_word(f, u) / 4] = in_matrix ? word : 0u;
+        if ((u & static_cast<uint32_t>(lanes - 1)) == 0) {
+          const int64_t at = (tile * ng + u / lanes) * kW4Rows + f;
+          reinterpret_cast<uint16_t*>(p.scales)[at] = in_matrix ? s16 : 0;
+          if constexpr (ZEROS) p.zeros[at] = in_matrix ? static_cast<uint8_t>(zero) : 0;
+        }
+      }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t f = 2 * k + (lane >> 4);
-      const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = w4_float<BF16>(static_cast<uint16_t>(w[e] & 0xffffu));
-        v[2 * e + 1] = w4_float<BF16>(static_cast<uint16_t>(w[e] >> 16));
-      }
-      float lo = 0.f, hi = 0.f;  // (NaN stays: max.NaN, min.NaN)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(ZEROS ? v[e] : fabsf(v[e])));
-        if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(v[e]));
-      }
-      for (int off = 1; off < lanes; off <<= 1) {
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(__shfl_xor_sync(0xffffffffu, hi, off)));
-        if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(__shfl_xor_sync(0xffffffffu, lo, off)));
-      }
-      float top = ZEROS ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f);
-      if (!(top <= 3.4e38f)) top = __uint_as_float(0x7fc00000u);  // an infinity or NaN: the group stands for NaN
-      const uint16_t s16 = w4_round16<BF16>(top);
-      const float s = w4_float<BF16>(s16);
-      float zero = 8.f;
-      if constexpr (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;
-      uint32_t word = 0;
-      const bool tiny = s < 1e-30f;  // the reciprocal would leave fp32
-      const float r = tiny ? 0.f : __frcp_rn(s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float c = zero;
-        if (s > 0.f) c = rintf(tiny ? __fdiv_rn(v[e], s) : w4_divide(v[e], s, r)) + zero;
-        const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
-        word |= code << (4 * (e >> 1) + 16 * (e & 1));
-      }
-      const bool in_matrix = i * 16 + static_cast<int>(f) < p.rows && col < p.cols;
-      stage[warp][w4_word(f, u) / 4] = in_matrix ? word : 0u;
-      if ((u & static_cast<uint32_t>(lanes - 1)) == 0) {
-        const int64_t at = tile * 16 * ng + w4_scale(f, u / lanes, ng);
-        reinterpret_cast<uint16_t*>(p.scales)[at] = in_matrix ? s16 : 0;
-        if constexpr (ZEROS) p.zeros[at] = in_matrix ? static_cast<uint8_t>(zero) : 0;
-      }
-    }
-    w4_store_tile(p.q + tile * 1024, stage[warp]);
+    w4_store_tile(p.q + tile * kW4TileBytes, stage[warp]);
   }
 }
 
 // Codes as a checkpoint has them (rows x cols / 2 bytes), scales and zeros rows x
 // cols / G, to the layout. Copies only.
 static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
-  __shared__ uint32_t stage[8][256];
+  __shared__ __align__(16) uint32_t stage[8][kW4TileBytes / 4];
   wait_for_inputs();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, u = lane & 15u, ng = 128u / p.group;
   const int groups = p.cols / p.group;
@@ -175,9 +172,9 @@ static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
     const int64_t m = row_tile / p.rt;
     const int col = j * 128 + 8 * static_cast<int>(u);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 16; ++k) {
       const uint32_t f = 2 * k + (lane >> 4);
-      const int row = i * 16 + static_cast<int>(f);
+      const int row = i * kW4Rows + static_cast<int>(f);
       uint32_t src = 0;
       if (row < p.rows && col < p.cols)
         src = __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.src) +
@@ -189,15 +186,14 @@ static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
       };
       stage[warp][w4_word(f, u) / 4] = gather(src) | (gather(src >> 4) << 16);
     }
-    for (uint32_t e = lane; e < 16 * ng; e += 32) {
-      const uint32_t f = e / ng, k = e % ng;
-      const int row = i * 16 + static_cast<int>(f), g = j * static_cast<int>(ng) + static_cast<int>(k);
+    for (uint32_t k = 0; k < ng; ++k) {  // a lane its feature
+      const int row = i * kW4Rows + static_cast<int>(lane), g = j * static_cast<int>(ng) + static_cast<int>(k);
       const bool in = row < p.rows && g < groups;
-      const int64_t from = in ? (m * p.rows + row) * groups + g : 0, at = tile * 16 * ng + w4_scale(f, k, ng);
+      const int64_t from = in ? (m * p.rows + row) * groups + g : 0, at = (tile * ng + k) * kW4Rows + lane;
       reinterpret_cast<uint16_t*>(p.scales)[at] = in ? reinterpret_cast<const uint16_t*>(p.src_scales)[from] : 0;
       if (p.zeros) p.zeros[at] = in ? (p.src_zeros[from] & 127u) : 0;
     }
-    w4_store_tile(p.q + tile * 1024, stage[warp]);
+    w4_store_tile(p.q + tile * kW4TileBytes, stage[warp]);
   }
 }
 
@@ -205,7 +201,7 @@ static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
 // 8), or two rows, eight columns a lane (16-bit, rounded once).
 template <bool BF16, bool F32>
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Params p) {
-  __shared__ uint32_t stage[8][256];
+  __shared__ __align__(16) uint32_t stage[8][kW4TileBytes / 4];
   wait_for_inputs();
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, ng = 128u / p.group;
   for (int64_t tile = static_cast<int64_t>(blockIdx.x) * 8 + warp; tile < p.tiles; tile += static_cast<int64_t>(gridDim.x) * 8) {
@@ -213,18 +209,18 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Params p) {
     const int64_t row_tile = tile / p.kt;
     const int i = static_cast<int>(row_tile % p.rt);
     const int64_t m = row_tile / p.rt;
-    const uint4* q = reinterpret_cast<const uint4*>(p.q + tile * 1024);
-    reinterpret_cast<uint4*>(stage[warp])[lane] = w4_load_once(q + lane);
-    reinterpret_cast<uint4*>(stage[warp])[32 + lane] = w4_load_once(q + 32 + lane);
-    __syncwarp();
-    constexpr int V = F32 ? 4 : 8;  // columns a lane: 16 or 8 turns for the 16 rows
+    const uint4* q = reinterpret_cast<const uint4*>(p.q + tile * kW4TileBytes);
 #pragma unroll
-    for (int k = 0; k < 64 / V; ++k) {
+    for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(stage[warp])[32 * k + lane] = w4_load_once(q + 32 * k + lane);
+    __syncwarp();
+    constexpr int V = F32 ? 4 : 8;  // columns a lane: 32 or 16 turns for the 32 rows
+#pragma unroll 8
+    for (int k = 0; k < 128 / V; ++k) {
       const uint32_t f = F32 ? k : 2 * k + (lane >> 4);
       const uint32_t c0 = F32 ? lane * 4 : (lane & 15u) * 8;
-      const int row = i * 16 + static_cast<int>(f), col = j * 128 + static_cast<int>(c0);
+      const int row = i * kW4Rows + static_cast<int>(f), col = j * 128 + static_cast<int>(c0);
       if (row >= p.rows || col >= p.cols) continue;
-      const int64_t at = tile * 16 * ng + w4_scale(f, c0 / p.group, ng);
+      const int64_t at = (tile * ng + c0 / p.group) * kW4Rows + f;
       const float s = w4_float<BF16>(__ldg(reinterpret_cast<const uint16_t*>(p.scales) + at));
       const float z = p.zeros ? static_cast<float>(__ldg(p.zeros + at)) : 8.f;
       const uint32_t word = stage[warp][w4_word(f, c0 / 8) / 4];

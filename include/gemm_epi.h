@@ -516,13 +516,13 @@ GEMM_EPI_API int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, c
  * zero = -lo / scale rounded, held to 0 .. 15, code = w / scale rounded, plus zero, held to
  * 0 .. 15. A scale that rounds to 0 gives codes that stand for 0; a group with an infinity or
  * NaN (or, with zeros, a range beyond fp32) has a NaN scale and stands for NaN.
- * Storage: q in tiles of 16 rows x 128 columns, 1024 bytes each, a row of ceil(cols /
- * 128) tiles after the other; rows and columns past the matrix are held as zeros.
- * With g = 0 .. 7, r = 0, 1, b = 0 .. 3, c = 0 .. 3: row g + 8 r, columns 32 b + 8 c .. + 7 of a
- * tile are the 32-bit word at byte 32 (4 g + c) + 8 b + 4 r, column 2 m of the eight in bits
- * 4 m .. 4 m + 3 and column 2 m + 1 in bits 4 m + 16 .. 4 m + 19. The scales (16-bit) and zeros (bytes) of a
- * tile's 128 / G groups k are at 16 (128 / G) tile + (g (128 / G) + k) 2 + r. Matrices of a batch
- * follow one another in whole tiles. gemm_epi_w4_pack makes this of row-major codes.
+ * Storage: q in tiles of 32 rows x 128 columns, 2048 bytes each, a row of ceil(cols /
+ * 128) tiles after the other; rows and columns past the matrix are held as zeros. Row
+ * f, columns 32 b + 8 w .. + 7 of a tile are the 32-bit word at byte 512 b + 16 f + 4 w, column
+ * 2 m of the eight in bits 4 m .. 4 m + 3 and column 2 m + 1 in bits 4 m + 16 .. 4 m + 19. The
+ * scale (16-bit) and zero (a byte) of row f, group k of a tile's 128 / G are at index 32 ((128 /
+ * G) tile + k) + f. Matrices of a batch follow one another in whole tiles.
+ * gemm_epi_w4_pack makes this of row-major codes.
  */
 
 /* Bytes of q, and the number of scales (and of zeros), of `batch` matrices of rows x
@@ -532,8 +532,7 @@ GEMM_EPI_API int64_t gemm_epi_w4_bytes(int64_t batch, int64_t rows, int64_t cols
 GEMM_EPI_API int64_t gemm_epi_w4_scales(int64_t batch, int64_t rows, int64_t cols, int64_t group);
 
 /* gemm_epi_w4_quantize: `batch` row-major matrices of rows x cols (dtype, which the
- * scales have too). q 32-byte, W, scales and zeros 16-byte aligned; zeros NULL:
- * without. Asynchronous on `stream`, one launch on the current device. */
+ * scales have too). W, q, scales and zeros 16-byte aligned; zeros NULL: without. Asynchronous on `stream`, one launch on the current device. */
 GEMM_EPI_API int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype,
                                       const void* W, uint8_t* q, void* scales, uint8_t* zeros, cudaStream_t stream);
 
@@ -558,20 +557,19 @@ GEMM_EPI_API int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t col
  * matrices of N rows, the gate's first, and H = act(X . W0^T + bias) * (X . W1^T +
  * bias[N..]) with `act` (otherwise ignored but checked). dtype is X's, the scales', the bias's and
  * Y's; flags GEMM_EPI_FLAG_OUT_F32 or 0. Products are exact in fp32 before they are
- * summed: code - zero is a small integer, its group's sum is scaled in fp32. A plan keeps no
- * weight: one serves all layers of its shape. It owns a workspace where T x K is large
- * (query: split_k > 1; then a call is two launches).
+ * summed: code - zero is a small integer, a group's sum is scaled in fp32. A plan keeps no
+ * weight: one serves all layers of its shape.
  */
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype,
                                               int epilog, gemm_epi_act act, uint32_t flags);
 
 /*
  * gemm_epi_w4_execute: q, scales and zeros (NULL: 8) as gemm_epi_w4_quantize or
- * _pack make them. q 32-byte, X, scales, zeros and Y 16-byte, bias as
+ * _pack make them. X, q, scales, zeros and Y 16-byte aligned, bias as
  * gemm_epi_execute (NULL allowed for NONE, where it is ignored, and GATED, 2N
  * values). A call runs on the plan's device whichever is current. Returns as
- * gemm_epi_execute (never GEMM_EPI_ERR_TIMEOUT). gemm_epi_free, _query, _status and
- * _set_bias_f32 take the plan too.
+ * gemm_epi_execute. gemm_epi_free, _query, _status and _set_bias_f32 take the plan
+ * too.
  */
 GEMM_EPI_API int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, const void* scales,
                                      const uint8_t* zeros, const void* bias, void* Y, cudaStream_t stream);

@@ -2,14 +2,14 @@
 their definition in 64 bits.
 
 Exact products: X holds integers in [-3, 3] and the scales are powers of two in a
-narrow range, so that every product, group sum and feature sum is exact in fp32 (a
-multiple of 2^-6 below 2^18) and Y has one right value, rounded once.
+narrow range, so that every product, group sum and feature sum is exact in fp32 (multiples
+of 2^-6 below 2^18) and Y has one right value, rounded once.
 
 Products of other scales: a group's sum of up to 128 exact products errs by at most
 128 x 2 e of its magnitudes (e = 2^-24; 2 for a truncating adder), the groups' sums,
-scaled and added, by (groups + warps + slices + 4) e: with K / G groups and 16 warps at
-most (2 x 128 + K / G + 40) e S, S the sum of |x w|; then the epilog's own errors (its
-bounds as derived for gated layers) and one rounding of u |Y|.
+scaled and added, by (K / G + 8) e more: (2 x 128 + K / G + 8) e S, S the sum of |x w|;
+then the epilog's own errors (its bounds as derived for gated layers) and one rounding
+of u |Y|.
 """
 import math
 
@@ -40,15 +40,15 @@ def reference_codes(W, G, zeros):
 
 def unpack(q, s, z, N, K, G):
     """The layout, as the header states it -> row-major codes, scales, zeros."""
-    rt, kt, ng = (N + 15) // 16, (K + 127) // 128, 128 // G
+    kt, ng = (K + 127) // 128, 128 // G
     n = torch.arange(N, device="cuda")[:, None]
     k = torch.arange(K, device="cuda")[None, :]
-    tile, f, c = (n // 16) * kt + k // 128, n % 16, k % 128
-    word = tile * 1024 + 32 * (4 * (f % 8) + c % 32 // 8) + 8 * (c // 32) + 4 * (f // 8)
+    tile, f, c = (n // 32) * kt + k // 128, n % 32, k % 128
+    word = 2048 * tile + 512 * (c // 32) + 16 * f + 4 * (c % 32 // 8)
     bit = 4 * (c % 8 // 2) + 16 * (c % 2)
     codes = (q.long()[word + bit // 8] >> (bit % 8)) & 15
     k = torch.arange(K // G, device="cuda")[None, :]
-    at = 16 * ng * ((n // 16) * kt + k // ng) + (f % 8 * ng + k % ng) * 2 + f // 8
+    at = 32 * (ng * ((n // 32) * kt + k // ng) + k % ng) + f
     return codes.to(torch.uint8), s[at], None if z is None else z[at]
 
 
@@ -163,7 +163,7 @@ def test_products_exact(T, N, K, G, zeros):
         with W4Plan(T, N, K, dt, epi, group=G, out_f32=f32) as p:
             if bias == "32":
                 p.set_bias_f32()
-            assert p.info()["kernel"] == 8 and p.info()["launches"] == (2 if p.info()["split_k"] > 1 else 1)
+            assert p.info()["kernel"] == 8 and p.info()["launches"] == 1
             p.gemm_epi_w4_execute(X, *w4, b, Y)
             first = Y.clone()
             p.gemm_epi_w4_execute(X, *w4, b, Y)
@@ -196,7 +196,7 @@ def test_products_of_any_scales(T, N, K, G, zeros):
         if b is not None:
             y = y + b.double()
             size = size + b.double().abs()
-        err = (2 * 128 + K / G + 40) * E * size
+        err = (2 * 128 + K / G + 8) * E * size
         u = U[Y.dtype]
         if not gated:
             if epi == "GELU_BIAS":
@@ -224,7 +224,7 @@ def test_wide_weight_and_many_tiles():
 
 
 def test_long_contraction():
-    """K of 65 536 (several slices at 8 rows too)."""
+    """K of 65 536, shared by many CTAs."""
     T, N, K, G = 8, 40, 65536, 64
     codes, s, z = weights(N, K, G, torch.float16, 1, False, True)
     X = ints((T, K), 2, gen(1), torch.float16)
@@ -306,6 +306,49 @@ def test_streams_graphs_and_shared_plans(T, K):
         within(Y, r, (U[dt] + 2 * E) * r.abs() + TINY[dt], "gated")
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_shared_tiles(gated, monkeypatch):
+    """Tiles cut at any block among 1 to 37 CTAs."""
+    T, N, K, G, dt = 20, 400, 1408, 64, torch.bfloat16
+    codes, s, z = weights(N, K, G, dt, 4, True, True, 2 if gated else None)
+    w4 = w4_pack(rowmajor(codes), s, z)
+    X = ints((T, K), 3, gen(4), dt)
+    y = X.double() @ values(codes, s, z, G).reshape(-1, K).t()
+    for grid in (1, 2, 3, 7, 12, 37):
+        monkeypatch.setenv("GEMM_EPI_SKINNY_GRID", str(grid))
+        with W4Plan(T, N, K, dt, "GATED" if gated else "NONE", group=G, act="RELU", out_f32=True) as p:
+            assert p.info()["grid"] == grid
+            Y = p.forward(X, *w4)
+            for _ in range(3):
+                assert torch.equal(Y, p.forward(X, *w4))
+            assert p.status() == 0
+        if gated:
+            r = y[:, :N].clamp(min=0) * y[:, N:]
+            within(Y, r, 2 * E * r.abs(), "gated")  # one fp32 product of exact sums
+        else:
+            assert torch.equal(Y.double(), y)
+
+
+def test_watchdog_reports_and_the_plan_recovers(monkeypatch):
+    T, N, K, G, dt = 20, 400, 1408, 64, torch.bfloat16
+    codes, s, z = weights(N, K, G, dt, 4, True, True)
+    w4 = w4_pack(rowmajor(codes), s, z)
+    X = ints((T, K), 3, gen(4), dt)
+    monkeypatch.setenv("GEMM_EPI_WAIT_TIMEOUT_MS", "50")
+    monkeypatch.setenv("GEMM_EPI_TEST_HOOKS", "1")
+    monkeypatch.setenv("GEMM_EPI_INJECT_STALL", "1")
+    with W4Plan(T, N, K, dt, "NONE", group=G) as p:
+        p.forward(X, *w4)
+        torch.cuda.synchronize()
+        assert p.status() == binding.ERR_TIMEOUT and p.status() == 0
+    monkeypatch.delenv("GEMM_EPI_INJECT_STALL")
+    with W4Plan(T, N, K, dt, "NONE", group=G, out_f32=True) as p:
+        Y = p.forward(X, *w4)
+        torch.cuda.synchronize()
+        assert p.status() == 0
+    assert torch.equal(Y.double(), X.double() @ values(codes, s, z, G).t())
+
+
 def test_refusals():
     N, K, G, dt = 64, 256, 64, torch.bfloat16
     W = torch.zeros((N, K), dtype=dt, device="cuda")
@@ -318,7 +361,7 @@ def test_refusals():
         assert L.gemm_epi_w4_execute(d.handle, 32, 32, 32, None, None, 32, None) == binding.ERR_EPILOG_MISMATCH
         assert L.gemm_epi_execute(p.handle, 32, 32, 32, 32, None, None) == binding.ERR_EPILOG_MISMATCH
         bias = torch.zeros(N, dtype=dt, device="cuda")
-        assert L.gemm_epi_w4_execute(p.handle, X.data_ptr(), q.data_ptr() + 16, s.data_ptr(), None, bias.data_ptr(), Y.data_ptr(),
+        assert L.gemm_epi_w4_execute(p.handle, X.data_ptr(), q.data_ptr() + 8, s.data_ptr(), None, bias.data_ptr(), Y.data_ptr(),
                                      None) == binding.ERR_MISALIGNED
         for bad in ((X.float(), q, s, z, bias, Y), (X, q[1:], s, z, bias, Y), (X, q, s.float(), z, bias, Y), (X, q, s, z[1:], bias, Y),
                     (X, q, s, z, bias[1:], Y), (X.cpu(), q, s, z, bias, Y)):

@@ -14,9 +14,9 @@ def L():
 
 
 def test_sizes(L):
-    assert L.gemm_epi_w4_bytes(1, 16, 128, 128) == 1024 and L.gemm_epi_w4_scales(1, 16, 128, 128) == 16
-    assert L.gemm_epi_w4_bytes(1, 17, 160, 32) == 4 * 1024 and L.gemm_epi_w4_scales(1, 17, 160, 32) == 4 * 64
-    assert L.gemm_epi_w4_bytes(3, 1, 64, 64) == 3 * 1024 and L.gemm_epi_w4_scales(3, 1, 64, 64) == 3 * 32
+    assert L.gemm_epi_w4_bytes(1, 32, 128, 128) == 2048 and L.gemm_epi_w4_scales(1, 32, 128, 128) == 32
+    assert L.gemm_epi_w4_bytes(1, 33, 160, 32) == 4 * 2048 and L.gemm_epi_w4_scales(1, 33, 160, 32) == 4 * 128
+    assert L.gemm_epi_w4_bytes(3, 1, 64, 64) == 3 * 2048 and L.gemm_epi_w4_scales(3, 1, 64, 64) == 3 * 64
 
 
 @pytest.mark.parametrize("batch,rows,cols,group", [(1, 16, 128, 16), (1, 16, 128, 0), (1, 16, 96, 64), (1, 0, 128, 64), (0, 16, 128, 64),
@@ -35,14 +35,14 @@ def test_refusals(L):
     ok = (1, 64, 256, 64)
     assert L.gemm_epi_w4_quantize(*ok, 5, 32, 32, 32, None, None) == binding.ERR_INVALID_ARG   # dtype
     assert L.gemm_epi_w4_quantize(*ok, 0, None, 32, 32, None, None) == binding.ERR_INVALID_ARG
-    assert L.gemm_epi_w4_quantize(*ok, 0, 32, 16, 32, None, None) == binding.ERR_MISALIGNED    # q: 32 bytes
+    assert L.gemm_epi_w4_quantize(*ok, 0, 32, 40, 32, None, None) == binding.ERR_MISALIGNED
     assert L.gemm_epi_w4_quantize(*ok, 0, 32, 32, 32, 8, None) == binding.ERR_MISALIGNED
     assert L.gemm_epi_w4_pack(*ok, 32, 32, 32, 32, 32, None, None) == binding.ERR_INVALID_ARG  # zeros on one side
     assert L.gemm_epi_w4_pack(*ok, 32, 32, None, 32, 32, 32, None) == binding.ERR_INVALID_ARG
     assert L.gemm_epi_w4_pack(*ok, 32, 33, None, 32, 32, None, None) == binding.ERR_MISALIGNED
     assert L.gemm_epi_w4_dequantize(*ok, 0, 1, 32, 32, None, 32, None) == binding.ERR_INVALID_ARG  # flags
     assert L.gemm_epi_w4_dequantize(*ok, 0, 0, 32, None, None, 32, None) == binding.ERR_INVALID_ARG
-    assert L.gemm_epi_w4_dequantize(*ok, 0, 0, 16, 32, None, 32, None) == binding.ERR_MISALIGNED
+    assert L.gemm_epi_w4_dequantize(*ok, 0, 0, 24, 32, None, 32, None) == binding.ERR_MISALIGNED
 
 
 @pytest.mark.parametrize("T,N,K,group,dtype,epi,act,flags,word",
