@@ -128,7 +128,7 @@ struct GroupedCfg {
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
   uint32_t smem = 0;
-  int tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1;
+  int threads = 0, tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1;
 };
 
 // Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`

@@ -7,19 +7,27 @@
 
 namespace ge_inst {
 
-template <int TP, bool GATED, bool BF>
-W4Instance w4_ng(int ng) {
-  if (ng == 1) return {ge::w4_kernel<TP, GATED, 1, BF>, ge::W4Smem<TP, 1>::BYTES};
-  if (ng == 2) return {ge::w4_kernel<TP, GATED, 2, BF>, ge::W4Smem<TP, 2>::BYTES};
-  return {ge::w4_kernel<TP, GATED, 4, BF>, ge::W4Smem<TP, 4>::BYTES};
+template <int TP, bool GATED, int NG, bool BF>
+W4Instance w4_one() {
+  using L = ge::W4Smem<TP, NG>;
+  return {ge::w4_kernel<TP, GATED, NG, BF>, L::BYTES, L::THREADS};
+}
+
+// tp at most 128 / ng (tensor memory), gated 64 (registers)
+template <bool GATED, bool BF>
+W4Instance w4_tp(int tp, int ng) {
+  if (ng == 4) return tp == 16 ? w4_one<16, GATED, 4, BF>() : w4_one<32, GATED, 4, BF>();
+  if (ng == 2)
+    return tp == 16 ? w4_one<16, GATED, 2, BF>() : tp == 32 ? w4_one<32, GATED, 2, BF>() : w4_one<64, GATED, 2, BF>();
+  if (tp == 16) return w4_one<16, GATED, 1, BF>();
+  if (tp == 32) return w4_one<32, GATED, 1, BF>();
+  if (tp == 64 || GATED) return w4_one<64, GATED, 1, BF>();
+  if constexpr (!GATED) return w4_one<128, GATED, 1, BF>();
 }
 
 template <bool BF>
 W4Instance w4_any(int tp, bool gated, int ng) {
-  if (tp == 16) return gated ? w4_ng<16, true, BF>(ng) : w4_ng<16, false, BF>(ng);
-  if (tp == 32) return gated ? w4_ng<32, true, BF>(ng) : w4_ng<32, false, BF>(ng);
-  if (tp == 64) return gated ? w4_ng<64, true, BF>(ng) : w4_ng<64, false, BF>(ng);
-  return gated ? W4Instance{} : w4_ng<128, false, BF>(ng);
+  return gated ? w4_tp<true, BF>(tp, ng) : w4_tp<false, BF>(tp, ng);
 }
 
 }  // namespace ge_inst

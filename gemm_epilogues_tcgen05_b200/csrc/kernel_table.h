@@ -91,12 +91,13 @@ GatedSkinnyInstance gated_skinny_f16_nk(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_mn(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_nk(int tp, int gn);
 
-// Few rows times 4-bit weights: tp = 16, 32, 64 or (not gated) 128 padded rows,
-// groups of 128 / ng columns.
+// Few rows times 4-bit weights: groups of 128 / ng columns, tp = 16, 32, 64 or 128
+// padded rows, at most 128 / ng and, gated, 64.
 using W4KernelFn = void (*)(CUtensorMap, ge::W4MulParams);
 struct W4Instance {
   W4KernelFn fn;
   uint32_t smem;
+  int threads;
 };
 W4Instance w4_f16(int tp, bool gated, int ng);
 W4Instance w4_bf16(int tp, bool gated, int ng);

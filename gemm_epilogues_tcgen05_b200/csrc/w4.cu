@@ -97,12 +97,14 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   p->timeout_ns = wd.timeout_ns;
   p->inject_stall = wd.inject_stall;
   W4Cfg& c = p->w4;
-  // a gated layer's accumulating warps hold two sums a row
-  c.tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 || gated ? 64 : 128;
+  const int most = gated && group == 128 ? 64 : (int)group;  // rows of an instance
+  c.tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  if (c.tp > most) c.tp = most;
   c.row_blocks = ceil_div(T, c.tp);
   const ge_inst::W4Instance inst = (dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16 : ge_inst::w4_f16)(c.tp, gated, (int)(128 / group));
   c.fn = inst.fn;
   c.smem = inst.smem;
+  c.threads = inst.threads;
   c.tiles = (int)tiles;
   c.kt = (int)kt;
   // equal shares of all blocks of 128 columns, at least two each
@@ -281,7 +283,7 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   k.status = p->status_dev;
   k.timeout_ns = p->timeout_ns;
   k.inject_stall = p->inject_stall;
-  Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), ge::kW4Threads, c.smem, false, stream);
+  Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.threads, c.smem, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, x, k);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");
 }

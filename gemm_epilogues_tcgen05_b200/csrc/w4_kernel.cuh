@@ -16,11 +16,13 @@
 // quarter SM for 16 x 8 x 16.)
 //
 // Warp roles:
-//   0..7    dequantise: lane quarter warp % 4, columns 64 (warp / 4) .. + 63 of each block of 128
-//   8..15   accumulate and finish: lane quarter warp % 4, half of the TP rows each
-//   16      X by TMA, 128 columns a stage
-//   17      tensor memory, MMAs
-// Codes, zeros and scales come in by cp.async, each warp its own, `AHEAD` blocks
+//   0..7    dequantise: lane quarter warp % 4, every second block of 128 columns (gated: of
+//           the gate's weight, or of the up projection's)
+//   then 4 (TP <= 32) or 8: accumulate and finish: lane quarter warp % 4, with 8 half
+//           of the TP rows each
+//   then 1  X by TMA, 128 columns a stage
+//   last    tensor memory, MMAs
+// Codes, zeros and scales come in by cp.async, each warp its own, kW4Ahead blocks
 // ahead of its work.
 //
 // Work split (stream-K) and joining of shared tiles: as the few-row kernel
@@ -52,32 +54,50 @@ struct W4MulParams {
   int32_t inject_stall;
 };
 
-constexpr int kW4Threads = 32 * 18;
-constexpr int kW4Ahead = 6;    // blocks that a warp's copies run ahead
-constexpr int kW4Stages = 4;   // of 128 columns: unpacked weights (tensor memory), X (shared memory)
+constexpr int kW4Ahead = 4;    // blocks that a warp's copies run ahead
 
 template <int TP, int NG>
 struct W4Smem {
+  // A stage is 128 columns: the unpacked weights (64 columns of tensor memory), X, and an
+  // accumulator for each group. Where four stages' do not fit, two.
+  static constexpr int STAGES = 4 * (64 + NG * TP) <= 512 ? 4 : 2;
   static constexpr uint32_t X_SUB = TP * kBK * 2;             // TP rows x 64 columns
   static constexpr uint32_t X_BYTES = 2 * X_SUB;
-  static constexpr uint32_t CODES = 1024 + 32 * NG;           // of a dequantising warp and block: codes, zeros
+  static constexpr int ACC = TP <= 32 ? 4 : 8;                // accumulating warps
+  static constexpr int THREADS = 32 * (8 + ACC + 2);
+  static constexpr uint32_t CODES = 2048 + 32 * NG;           // of a dequantising warp and block: codes, zeros
   static constexpr uint32_t SCALES = 64 * NG;                 // of an accumulating warp and block
-  static constexpr int D_BUFS = TP <= 32 ? 8 : TP == 64 ? 4 : 2;  // accumulators
   static constexpr uint32_t OFF_X = 0;
-  static constexpr uint32_t OFF_CODES = OFF_X + kW4Stages * X_BYTES;
+  static constexpr uint32_t OFF_CODES = OFF_X + STAGES * X_BYTES;
   static constexpr uint32_t OFF_SCALES = OFF_CODES + 8 * kW4Ahead * CODES;
-  static constexpr uint32_t OFF_BAR = OFF_SCALES + 8 * kW4Ahead * SCALES;
-  static constexpr uint32_t N_BARS = 4 * kW4Stages + 2 * D_BUFS + 1;
+  static constexpr uint32_t OFF_BAR = OFF_SCALES + ACC * kW4Ahead * SCALES;
+  static constexpr uint32_t N_BARS = (3 + NG) * STAGES + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t COL_A = 0, COL_D = kW4Stages * 64;
-  static_assert(COL_D + D_BUFS * TP <= TMEM_COLS, "tensor memory columns");
+  static constexpr uint32_t COL_A = 0, COL_D = STAGES * 64;
+  static_assert(COL_D + STAGES * NG * TP <= TMEM_COLS, "tensor memory columns");
   static_assert(BYTES <= 232448, "above the per-CTA limit");
 };
 
 __device__ __forceinline__ void w4_copy_16(uint32_t saddr, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "l"(policy) : "memory");
+}
+
+// one test of two phases, the second's while the first's is under way (either takes
+// about 200 cycles, and a stage's products little more)
+__device__ __forceinline__ bool mbar_try_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, 20000;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+      : "memory");
+  return done != 0;
 }
 
 template <bool BF16>
@@ -91,28 +111,51 @@ __device__ __forceinline__ uint32_t w4_sub(uint32_t a, uint32_t b) {
   }
 }
 
-// 128 + v (1024 + v) twice, exact in the type for v up to 127
+// The eight codes of a word less their zero point z (0 .. 127), as four operand
+// registers. bf16: 128 + q - (128 + z), the codes below 128's exponent. fp16 has room
+// for a nibble and the next: 1024 + q - (1024 + z), and (1024 + 16 q) / 16 - (64 + z) of the
+// one above, which saves two of three shifts (they, and the logical operations, run at
+// half rate: unpacking is what bounds a block).
 template <bool BF16>
-__device__ __forceinline__ uint32_t w4_biased(uint32_t pair) {
-  return pair | (BF16 ? 0x43004300u : 0x64006400u);
-}
+struct W4Unpack {
+  uint32_t zero, zero16;
+  __device__ __forceinline__ explicit W4Unpack(uint32_t z) {
+    z = (z & 127u) * 0x00010001u;
+    zero = z | (BF16 ? 0x43004300u : 0x64006400u);
+    const __half2 n = __hneg2(__hsub2(*reinterpret_cast<const __half2*>(&zero), __float2half2_rn(960.f)));  // -(64 + z)
+    zero16 = BF16 ? 0u : *reinterpret_cast<const uint32_t*>(&n);
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&r)[32], int at) const {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) r[at + m] = w4_sub<true>(((w >> (4 * m)) & 0x000f000fu) | 0x43004300u, zero);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 4; m += 2) {
+        const uint32_t v = w >> (4 * m);
+        r[at + m] = w4_sub<false>((v & 0x000f000fu) | 0x64006400u, zero);
+        const uint32_t hi = (v & 0x00f000f0u) | 0x64006400u;
+        const __half2 f = __hfma2(*reinterpret_cast<const __half2*>(&hi), __float2half2_rn(0.0625f),
+                                  *reinterpret_cast<const __half2*>(&zero16));
+        r[at + m + 1] = *reinterpret_cast<const uint32_t*>(&f);
+      }
+    }
+  }
+};
 
-// 16 registers to 16 columns of this warp's lane quarter
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 32 registers to 32 columns of this warp's lane quarter
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
 
 // D[tmem] (+)= A[tmem] * B[smem]: A's 16 k of a row are 8 columns of its lane
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -144,22 +187,26 @@ __device__ __forceinline__ void w4_output(const W4MulParams& p, float a, float b
 }
 
 template <int TP, bool GATED, int NG, bool BF16>
-__global__ void __launch_bounds__(kW4Threads, 1)
+__global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
     w4_kernel(const __grid_constant__ CUtensorMap tmX, const W4MulParams p) {
   using L = W4Smem<TP, NG>;
-  constexpr int MATS = GATED ? 2 : 1, STAGES = kW4Stages, BUFS = L::D_BUFS, AHEAD = kW4Ahead;
-  constexpr int ROWS = TP / 2;  // of an accumulating warp
+  constexpr int MATS = GATED ? 2 : 1, STAGES = L::STAGES, AHEAD = kW4Ahead;
+  constexpr int XS = STAGES / MATS;  // stages of X: both matrices' share one
+  constexpr int ACC = L::ACC, ROWS = TP / (ACC / 4);  // of an accumulating warp
   constexpr uint32_t IDESC = idesc_f16(BF16, false, false, 128, TP);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // afull   the dequantising warps of a stage have stored (4 arrivals)
+  // xfull   X has come (transaction bytes)
+  // dfull   a group's products are complete (commit), one a stage and group
+  // sfree   the accumulating warps have read a stage's sums: everything of the stage,
+  //         the unpacked weights and X that its products read, may be replaced
   uint64_t* afull = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* aempty = afull + STAGES;
-  uint64_t* xfull = aempty + STAGES;
-  uint64_t* xempty = xfull + STAGES;
-  uint64_t* dfull = xempty + STAGES;
-  uint64_t* dempty = dfull + BUFS;
-  uint64_t* drain = dempty + BUFS;
+  uint64_t* xfull = afull + STAGES;
+  uint64_t* sfree = xfull + STAGES;
+  uint64_t* dfull = sfree + STAGES;
+  uint64_t* drain = dfull + STAGES * NG;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
@@ -177,22 +224,18 @@ __global__ void __launch_bounds__(kW4Threads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&afull[s], 8);
-      mbar_init(&aempty[s], 1);
+      mbar_init(&afull[s], 4);
       mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
-    }
-    for (int b = 0; b < BUFS; ++b) {
-      mbar_init(&dfull[b], 1);
-      mbar_init(&dempty[b], 8);
+      mbar_init(&sfree[s], ACC);
+      for (int k = 0; k < NG; ++k) mbar_init(&dfull[s * NG + k], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     *last_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 16 && lane == 0) prefetch_tensormap(&tmX);
-  if (warp == 17) {
+  if (warp == 8 + ACC && lane == 0) prefetch_tensormap(&tmX);
+  if (warp == 9 + ACC) {
     tmem_alloc(tmem_slot, L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -205,72 +248,70 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   // blocks lo .. hi - 1 of (tile, kb), the matrices of each one after the other
   if (warp < 8) {
     // --------------------------------------------------------- dequantise
-    const uint32_t quarter = warp & 3u, half = warp >> 2;
-    const uint32_t ring = smem_u32(smem + L::OFF_CODES) + warp * (AHEAD * L::CODES);
+    // steps first, first + 2, ... of (hi - lo) MATS
+    const uint32_t quarter = warp & 3u, first = warp >> 2;
+    const uint32_t ring = smem_u32(smem + L::OFF_CODES) + warp * (AHEAD * L::CODES), end = ring + AHEAD * L::CODES;
     const uint64_t policy = l2_policy_evict_first();
-    struct Cursor {
-      uint32_t tile, kb;
-      int m;
-    };
-    const uint32_t kt = static_cast<uint32_t>(p.kt);
-    const uint32_t steps = (hi - lo) * MATS;
-    Cursor in{lo / kt, lo % kt, 0};
-    uint32_t fetched = 0, place_in = ring;
+    const uint32_t kt = static_cast<uint32_t>(p.kt), steps = (hi - lo) * MATS;
+    const bool zeros = p.zeros != nullptr;
+    uint32_t tile_in = lo / kt, kb_in = lo % kt + (MATS == 1 ? first : 0), step_in = first, place_in = ring;
+    while (kb_in >= kt) {
+      kb_in -= kt;
+      ++tile_in;
+    }
     const auto fetch = [&]() {
-      if (fetched < steps) {
-        const uint32_t i = 4 * in.tile + quarter;
+      if (step_in < steps) {
+        const uint32_t i = 4 * tile_in + quarter;
         if (i < static_cast<uint32_t>(p.rt)) {
-          const int64_t tile = (static_cast<int64_t>(in.m) * p.rt + i) * p.kt + in.kb;
-          const uint8_t* q = p.q + tile * kW4TileBytes + half * 1024 + lane * 16;
-          w4_copy_16(place_in + lane * 16, q, policy);
-          w4_copy_16(place_in + 512 + lane * 16, q + 512, policy);
-          if (p.zeros && lane < 2 * NG) w4_copy_16(place_in + 1024 + lane * 16, p.zeros + tile * (32 * NG) + lane * 16, policy);
+          const int64_t tile = (static_cast<int64_t>(MATS == 2 ? first : 0) * p.rt + i) * p.kt + kb_in;
+          const uint8_t* q = p.q + tile * kW4TileBytes + lane * 16;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) w4_copy_16(place_in + 512 * b + lane * 16, q + 512 * b, policy);
+          if (zeros && lane < 2 * NG) w4_copy_16(place_in + 2048 + lane * 16, p.zeros + tile * (32 * NG) + lane * 16, policy);
         }
-        if (MATS == 2 && in.m == 0) {
-          in.m = 1;
-        } else {
-          in.m = 0;
-          if (++in.kb == kt) {
-            in.kb = 0;
-            ++in.tile;
-          }
+        kb_in += MATS == 2 ? 1 : 2;
+        while (kb_in >= kt) {
+          kb_in -= kt;
+          ++tile_in;
         }
-        place_in = place_in + L::CODES == ring + AHEAD * L::CODES ? ring : place_in + L::CODES;
-        ++fetched;
+        place_in = place_in + L::CODES == end ? ring : place_in + L::CODES;
+        step_in += 2;
       }
       cp_async_commit();
     };
     for (int d = 0; d < AHEAD; ++d) fetch();
     uint32_t place = ring;
     bool ok = true;
-    for (uint32_t it = 0; it < steps; ++it) {
+    for (uint32_t it = first; it < steps; it += 2) {
       const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
       cp_async_wait<AHEAD - 1>();
       __syncwarp();
-      uint4 c[2];
-      c[0] = ld_shared_v4(place + lane * 16);
-      c[1] = ld_shared_v4(place + 512 + lane * 16);
-      uint32_t z[2] = {8u, 8u};  // of either 32 columns
-      if (p.zeros) {
-        z[0] = ld_shared_u8(place + 1024 + (2 * half * NG / 4) * 32 + lane);
-        z[1] = ld_shared_u8(place + 1024 + ((2 * half + 1) * NG / 4) * 32 + lane);
-      }
-      __syncwarp();
+      uint4 c[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) c[b] = ld_shared_v4(place + 512 * b + lane * 16);
+      uint32_t z[NG];
+#pragma unroll
+      for (int k = 0; k < NG; ++k) z[k] = zeros ? ld_shared_u8(place + 2048 + k * 32 + lane) : 8u;
+      if (zeros) __syncwarp();  // (codes are copied and read by one lane)
       fetch();
-      place = place + L::CODES == ring + AHEAD * L::CODES ? ring : place + L::CODES;
-      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&aempty[s], ph ^ 1u, wp, abort_flag, 1));
+      place = place + L::CODES == end ? ring : place + L::CODES;
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&sfree[s], ph ^ 1u, wp, abort_flag, 1));
       if (!ok) continue;  // (the copies under way are waited for below)
       tc_fence_after();
-      const uint32_t a = tmem_base + ((quarter * 32u) << 16) + L::COL_A + s * 64 + half * 32;
+      const uint32_t a = tmem_base + ((quarter * 32u) << 16) + L::COL_A + s * 64;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-        const uint32_t zero = w4_biased<BF16>((z[h] & 127u) * 0x00010001u);
-        uint32_t r[16];
+        uint32_t r[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          r[i] = w4_sub<BF16>(w4_biased<BF16>((w[i / 4] >> (4 * (i % 4))) & 0x000f000fu), zero);
-        tmem_st_32x32b_x16(a + 16 * h, r);
+        for (int b = 2 * h; b < 2 * h + 2; ++b) {
+          const W4Unpack<BF16> unpack(z[b * NG / 4]);
+          const int at = 16 * (b & 1);
+          unpack(c[b].x, r, at);
+          unpack(c[b].y, r, at + 4);
+          unpack(c[b].z, r, at + 8);
+          unpack(c[b].w, r, at + 12);
+        }
+        tmem_st_32x32b_x32(a + 32 * h, r);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -278,7 +319,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       if (lane == 0) mbar_arrive(&afull[s]);
     }
     cp_async_wait<0>();
-  } else if (warp < 16) {
+  } else if (warp < 8 + ACC) {
     // ------------------------------------------- accumulate, join, finish
     const uint32_t quarter = warp & 3u, part = (warp - 8u) >> 2;  // part: rows ROWS part .. of TP
     const uint32_t ring = smem_u32(smem + L::OFF_SCALES) + (warp - 8u) * (AHEAD * L::SCALES);
@@ -309,7 +350,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       cp_async_commit();
     };
     for (int d = 0; d < AHEAD; ++d) fetch();
-    uint32_t place = ring, buf = 0, dph = 0;
+    uint32_t place = ring, it = 0;
     bool ok = true;
     uint32_t gpos = lo;
     Segment seg;
@@ -323,7 +364,8 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         for (int t = 0; t < ROWS; ++t) acc[m][t] = 0.f;
       for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
 #pragma unroll
-        for (int m = 0; m < MATS; ++m) {
+        for (int m = 0; m < MATS; ++m, ++it) {
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
           cp_async_wait<AHEAD - 1>();
           __syncwarp();
           float sc[NG];
@@ -335,17 +377,15 @@ __global__ void __launch_bounds__(kW4Threads, 1)
           place = place + L::SCALES == ring + AHEAD * L::SCALES ? ring : place + L::SCALES;
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dfull[buf], dph, wp, abort_flag, 6));
+            if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dfull[s * NG + k], ph, wp, abort_flag, 6));
             if (ok) {
               tc_fence_after();
-              const uint32_t d = tmem_base + ((quarter * 32u) << 16) + L::COL_D + buf * TP + part * ROWS;
+              const uint32_t d = tmem_base + ((quarter * 32u) << 16) + L::COL_D + (s * NG + k) * TP + part * ROWS;
               constexpr int STEP = ROWS < 32 ? ROWS : 32;
 #pragma unroll
               for (int t0 = 0; t0 < ROWS; t0 += STEP) {
                 uint32_t r[STEP];
-                if constexpr (STEP == 8)
-                  tmem_ld_32x32b_x8(d + t0, r);
-                else if constexpr (STEP == 16)
+                if constexpr (STEP == 16)
                   tmem_ld_32x32b_x16(d + t0, r);
                 else
                   tmem_ld_32x32b_x32(d + t0, r);
@@ -353,15 +393,11 @@ __global__ void __launch_bounds__(kW4Threads, 1)
 #pragma unroll
                 for (int t = 0; t < STEP; ++t) acc[m][t0 + t] = fmaf(sc[k], __uint_as_float(r[t]), acc[m][t0 + t]);
               }
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&dempty[buf]);
-            }
-            if (++buf == BUFS) {
-              buf = 0;
-              dph ^= 1u;
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&sfree[s]);
         }
       }
       const bool whole = seg.kb0 == 0 && seg.kb1 == p.kt;
@@ -388,7 +424,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         for (int t = 0; t < ROWS; ++t)
           if (row0 + t0 + t < p.T) slot[(m * TP + t0 + t) * 128] = acc[m][t];
       __threadfence();
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 32 * ACC);
       if (et == 0) {
         int last = 0;
         if (ok) {
@@ -398,7 +434,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         }
         *last_flag = last;
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 32 * ACC);
       if (ok && *last_flag) {
         __threadfence();
         const float* from = p.partials + at * (MATS * TP * 128) + n_local;
@@ -419,17 +455,18 @@ __global__ void __launch_bounds__(kW4Threads, 1)
           if (n_ok && row0 + t0 + t < p.T)
             w4_output<GATED, BF16>(p, acc[0][t], acc[MATS - 1][t], row0 + t0 + t, n, bias_a, bias_b);
       }
-      named_bar_sync(1, 256);  // last_flag is reused by the next segment
+      named_bar_sync(1, 32 * ACC);  // last_flag is reused by the next segment
     }
     cp_async_wait<0>();
-  } else if (warp == 16) {
+  } else if (warp == 8 + ACC) {
     // ------------------------------------------------------------------- X
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_last();
       uint32_t it = 0, kb = lo % static_cast<uint32_t>(p.kt);
       for (uint32_t b = lo; b < hi; ++b, ++it) {
-        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-        if (!wait_bounded(&xempty[s], ph ^ 1u, wp, abort_flag, 2)) break;
+        // (a place is free when the last of the stages that read it is)
+        const uint32_t s = it % XS, last = it * MATS + MATS - 1;
+        if (!wait_bounded(&sfree[last % STAGES], ((last / STAGES) & 1u) ^ 1u, wp, abort_flag, 2)) break;
         mbar_arrive_expect_tx(&xfull[s], L::X_BYTES);
         uint8_t* x = smem + L::OFF_X + s * L::X_BYTES;
         const int k = static_cast<int>(kb) * 128;
@@ -438,52 +475,31 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         if (++kb == static_cast<uint32_t>(p.kt)) kb = 0;
       }
       // what was issued lands before the CTA leaves
-      const uint32_t inflight = it < STAGES ? it : STAGES;
+      const uint32_t inflight = it < XS ? it : XS;
       for (uint32_t i = it - inflight; i < it; ++i)
-        wait_bounded(&xfull[i % STAGES], (i / STAGES) & 1u, wp, abort_flag, 3, /*honour_abort=*/false);
+        wait_bounded(&xfull[i % XS], (i / XS) & 1u, wp, abort_flag, 3, /*honour_abort=*/false);
     }
     __syncwarp();
   } else {
     // ----------------------------------------------------------------- MMA
     const bool issuer = elect_one();
-    uint32_t it = 0, buf = 0, dph = 0;
-    bool ok = true;
-    for (uint32_t b = lo; ok && b < hi; ++b) {
-      const uint32_t xi = b - lo, xst = xi % STAGES, xph = (xi / STAGES) & 1u;
-      ok = __all_sync(0xffffffffu, wait_bounded(&xfull[xst], xph, wp, abort_flag, 4));
-      if (!ok) break;
-      const uint32_t x = smem_u32(smem + L::OFF_X + xst * L::X_BYTES);
-      for (int m = 0; ok && m < MATS; ++m, ++it) {
-        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-        ok = __all_sync(0xffffffffu, wait_bounded(&afull[s], ph, wp, abort_flag, 5));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a = tmem_base + L::COL_A + s * 64;
+    const uint32_t steps = (hi - lo) * MATS;
+    for (uint32_t it = 0; it < steps; ++it) {
+      const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u, xi = it / MATS, xs = xi % XS, xph = (xi / XS) & 1u;
+      bool ok = mbar_try_wait2(&afull[s], ph, &xfull[xs], xph);
+      if (!ok) ok = wait_bounded(&xfull[xs], xph, wp, abort_flag, 4) && wait_bounded(&afull[s], ph, wp, abort_flag, 5);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (issuer) {
+        const uint32_t x = smem_u32(smem + L::OFF_X + xs * L::X_BYTES);
+        const uint32_t a = tmem_base + L::COL_A + s * 64, d = tmem_base + L::COL_D + s * (NG * TP);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dempty[buf], dph ^ 1u, wp, abort_flag, 7));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem_base + L::COL_D + buf * TP;
-          if (issuer) {
-#pragma unroll
-            for (int j = 0; j < 8 / NG; ++j) {
-              const int kk = g * (8 / NG) + j;  // 16 columns each
-              const uint64_t bdesc = smem_desc_sw128(x + (kk >> 2) * L::X_SUB + (kk & 3) * 32, 16, 1024);
-              umma_f16_ts(d, a + kk * 8, bdesc, IDESC, j > 0 ? 1u : 0u);
-            }
-            // (fault injection: the accumulating warps then wait for a sum that is never announced)
-            if (!(p.inject_stall && it == 0 && g == 0)) umma_commit(&dfull[buf]);
-          }
-          if (++buf == BUFS) {
-            buf = 0;
-            dph ^= 1u;
-          }
-        }
-        if (!ok) break;
-        if (issuer) {
-          umma_commit(&aempty[s]);
-          if (m == MATS - 1) umma_commit(&xempty[xst]);
+        for (int kk = 0; kk < 8; ++kk) {  // 16 columns each
+          constexpr int PER = 8 / NG;     // of them in a group
+          const uint64_t bdesc = smem_desc_sw128(x + (kk >> 2) * L::X_SUB + (kk & 3) * 32, 16, 1024);
+          umma_f16_ts(d + kk / PER * TP, a + kk * 8, bdesc, IDESC, kk % PER > 0 ? 1u : 0u);
+          // (fault injection: the accumulating warps then wait for a sum that is never announced)
+          if (kk % PER == PER - 1 && !(p.inject_stall && it == 0 && kk < PER)) umma_commit(&dfull[s * NG + kk / PER]);
         }
       }
     }
@@ -495,7 +511,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_dealloc(tmem_base, L::TMEM_COLS);
+  if (warp == 9 + ACC) tmem_dealloc(tmem_base, L::TMEM_COLS);
 }
 
 }  // namespace ge
