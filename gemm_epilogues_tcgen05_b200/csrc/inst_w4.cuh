@@ -10,7 +10,7 @@ namespace ge_inst {
 template <int TP, bool GATED, int NG, bool BF>
 W4Instance w4_one() {
   using L = ge::W4Smem<TP, NG>;
-  return {ge::w4_kernel<TP, GATED, NG, BF>, L::BYTES, L::THREADS};
+  return {ge::w4_kernel<TP, GATED, NG, BF>, L::BYTES, L::THREADS, L::ACC};
 }
 
 // tp at most 128 / ng (tensor memory), gated 64 (registers)
@@ -21,8 +21,9 @@ W4Instance w4_tp(int tp, int ng) {
     return tp == 16 ? w4_one<16, GATED, 2, BF>() : tp == 32 ? w4_one<32, GATED, 2, BF>() : w4_one<64, GATED, 2, BF>();
   if (tp == 16) return w4_one<16, GATED, 1, BF>();
   if (tp == 32) return w4_one<32, GATED, 1, BF>();
-  if (tp == 64 || GATED) return w4_one<64, GATED, 1, BF>();
-  if constexpr (!GATED) return w4_one<128, GATED, 1, BF>();
+  if constexpr (!GATED)
+    if (tp == 128) return w4_one<128, GATED, 1, BF>();
+  return w4_one<64, GATED, 1, BF>();
 }
 
 template <bool BF>

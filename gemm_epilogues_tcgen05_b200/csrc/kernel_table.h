@@ -97,7 +97,7 @@ using W4KernelFn = void (*)(CUtensorMap, ge::W4MulParams);
 struct W4Instance {
   W4KernelFn fn;
   uint32_t smem;
-  int threads;
+  int threads, tickets;  // counters a tile
 };
 W4Instance w4_f16(int tp, bool gated, int ng);
 W4Instance w4_bf16(int tp, bool gated, int ng);

@@ -122,8 +122,8 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   }
   cudaError_t e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
   if (e == cudaSuccess && c.max_segs > 1) {
-    const size_t items = (size_t)c.row_blocks * (size_t)c.tiles;
-    p->sk_bytes = items * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
+    const size_t blocks = (size_t)c.row_blocks * (size_t)c.tiles, items = blocks * (size_t)inst.tickets;
+    p->sk_bytes = blocks * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
     e = cudaMalloc((void**)&p->sk_partials, p->sk_bytes);
     if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * items);
     if (e == cudaSuccess) e = zero_counts(p->sk_tickets, items);

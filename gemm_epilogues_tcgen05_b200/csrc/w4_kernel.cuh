@@ -16,17 +16,22 @@
 // quarter SM for 16 x 8 x 16.)
 //
 // Warp roles:
-//   0..7    dequantise: lane quarter warp % 4, every second block of 128 columns (gated: of
-//           the gate's weight, or of the up projection's)
-//   then 4 (TP <= 32) or 8: accumulate and finish: lane quarter warp % 4, with 8 half
-//           of the TP rows each
-//   then 1  X by TMA, 128 columns a stage
+//   first 16 or 8: dequantise: lane quarter warp % 4, every fourth (second) stage of
+//           128 columns
+//   then 8 or 16: accumulate and finish: lane quarter warp % 4, up to 32 rows, every
+//           second stage (gated: the gate's, or the up projection's) but for TP = 128
+//   then 1  X by TMA
 //   last    tensor memory, MMAs
+// What a stage costs is mostly the handing on between them, about 200 cycles a wait:
+// with every role's work left out a stage took 500 ns when one set of accumulating
+// warps took each of its groups' sums with a wait of its own.
 // Codes, zeros and scales come in by cp.async, each warp its own, kW4Ahead blocks
 // ahead of its work.
 //
-// Work split (stream-K) and joining of shared tiles: as the few-row kernel
-// (skinny_kernel.cuh), blocks of 128 columns instead of its k-blocks.
+// Work split (stream-K): as the few-row kernel (skinny_kernel.cuh), blocks of 128
+// columns instead of its k-blocks. A shared tile's parts are joined warp by warp, each
+// with a ticket for its own lanes and rows: no accumulating warp waits for
+// another, and the stages under way cover the ticket's round trip.
 #pragma once
 
 #include "activation.cuh"
@@ -48,36 +53,43 @@ struct W4MulParams {
   const void* bias;
   void* out;
   float* partials;       // [row blocks][tiles][max_segs][matrices][TP][128]
-  int* tickets;          // [row blocks][tiles], zero between launches
+  int* tickets;          // [row blocks][tiles][accumulating warps], zero between launches
   int* status;
   uint64_t timeout_ns;
   int32_t inject_stall;
 };
 
-constexpr int kW4Ahead = 4;    // blocks that a warp's copies run ahead
+constexpr int kW4Ahead = 3;    // blocks that a warp's copies run ahead
 
 template <int TP, int NG>
 struct W4Smem {
   // A stage is 128 columns: the unpacked weights (64 columns of tensor memory), X, and an
-  // accumulator for each group. Where four stages' do not fit, two.
-  static constexpr int STAGES = 4 * (64 + NG * TP) <= 512 ? 4 : 2;
+  // accumulator for each group: as many stages as fit, an even number.
+  static constexpr int STAGES = 6 * (64 + NG * TP) <= 512 ? 6 : 4 * (64 + NG * TP) <= 512 ? 4 : 2;
   static constexpr uint32_t X_SUB = TP * kBK * 2;             // TP rows x 64 columns
   static constexpr uint32_t X_BYTES = 2 * X_SUB;
-  static constexpr int ACC = TP <= 32 ? 4 : 8;                // accumulating warps
-  static constexpr int THREADS = 32 * (8 + ACC + 2);
+  static constexpr int ROWS = TP < 32 ? TP : 32;              // of an accumulating warp
+  static constexpr int PARTS = TP / ROWS, SETS = TP <= 64 ? 2 : 1;
+  static constexpr int ACC = 4 * PARTS * SETS;                // accumulating warps
+  // dequantising warps: at most one set of four a stage, or a set would wait for a
+  // barrier two phases ahead and take it for this one
+  static constexpr int DQ = ACC == 8 && STAGES >= 4 ? 16 : 8;
+  static constexpr int THREADS = 32 * (DQ + ACC + 2);
   static constexpr uint32_t CODES = 2048 + 32 * NG;           // of a dequantising warp and block: codes, zeros
   static constexpr uint32_t SCALES = 64 * NG;                 // of an accumulating warp and block
   static constexpr uint32_t OFF_X = 0;
   static constexpr uint32_t OFF_CODES = OFF_X + STAGES * X_BYTES;
-  static constexpr uint32_t OFF_SCALES = OFF_CODES + 8 * kW4Ahead * CODES;
-  static constexpr uint32_t OFF_BAR = OFF_SCALES + ACC * kW4Ahead * SCALES;
-  static constexpr uint32_t N_BARS = (3 + NG) * STAGES + 1;
+  static constexpr uint32_t OFF_SCALES = OFF_CODES + DQ * kW4Ahead * CODES;
+  static constexpr uint32_t OFF_JOIN = OFF_SCALES + ACC * kW4Ahead * SCALES;  // the second set's sums: [TP][128]
+  static constexpr uint32_t OFF_BAR = OFF_JOIN + (SETS == 2 ? TP * 128 * 4 : 0);
+  static constexpr uint32_t N_BARS = 4 * STAGES + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_A = 0, COL_D = STAGES * 64;
   static_assert(COL_D + STAGES * NG * TP <= TMEM_COLS, "tensor memory columns");
   static_assert(BYTES <= 232448, "above the per-CTA limit");
+  static_assert(DQ / 4 <= STAGES, "a set of dequantising warps a stage at most");
 };
 
 __device__ __forceinline__ void w4_copy_16(uint32_t saddr, const void* src, uint64_t policy) {
@@ -125,7 +137,7 @@ struct W4Unpack {
     const __half2 n = __hneg2(__hsub2(*reinterpret_cast<const __half2*>(&zero), __float2half2_rn(960.f)));  // -(64 + z)
     zero16 = BF16 ? 0u : *reinterpret_cast<const uint32_t*>(&n);
   }
-  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&r)[32], int at) const {
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&r)[16], int at) const {
     if constexpr (BF16) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) r[at + m] = w4_sub<true>(((w >> (4 * m)) & 0x000f000fu) | 0x43004300u, zero);
@@ -143,16 +155,13 @@ struct W4Unpack {
   }
 };
 
-// 32 registers to 32 columns of this warp's lane quarter
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 registers to 16 columns of this warp's lane quarter
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -192,24 +201,24 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
   using L = W4Smem<TP, NG>;
   constexpr int MATS = GATED ? 2 : 1, STAGES = L::STAGES, AHEAD = kW4Ahead;
   constexpr int XS = STAGES / MATS;  // stages of X: both matrices' share one
-  constexpr int ACC = L::ACC, ROWS = TP / (ACC / 4);  // of an accumulating warp
+  constexpr int DQ = L::DQ, ACC = L::ACC, ROWS = L::ROWS;
+  static_assert(MATS == 1 || L::SETS == 2, "a gated layer's matrices have a set of accumulating warps each");
   constexpr uint32_t IDESC = idesc_f16(BF16, false, false, 128, TP);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // afull   the dequantising warps of a stage have stored (4 arrivals)
   // xfull   X has come (transaction bytes)
-  // dfull   a group's products are complete (commit), one a stage and group
+  // dfull   a stage's products are complete (commit)
   // sfree   the accumulating warps have read a stage's sums: everything of the stage,
   //         the unpacked weights and X that its products read, may be replaced
   uint64_t* afull = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* xfull = afull + STAGES;
   uint64_t* sfree = xfull + STAGES;
   uint64_t* dfull = sfree + STAGES;
-  uint64_t* drain = dfull + STAGES * NG;
+  uint64_t* drain = dfull + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
 
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const int row0 = blockIdx.y * TP;
@@ -226,16 +235,15 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&afull[s], 4);
       mbar_init(&xfull[s], 1);
-      mbar_init(&sfree[s], ACC);
-      for (int k = 0; k < NG; ++k) mbar_init(&dfull[s * NG + k], 1);
+      mbar_init(&sfree[s], 4 * L::PARTS);
+      mbar_init(&dfull[s], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *last_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 8 + ACC && lane == 0) prefetch_tensormap(&tmX);
-  if (warp == 9 + ACC) {
+  if (warp == DQ + ACC && lane == 0) prefetch_tensormap(&tmX);
+  if (warp == DQ + ACC + 1) {
     tmem_alloc(tmem_slot, L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -246,159 +254,172 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
   wait_for_inputs();
 
   // blocks lo .. hi - 1 of (tile, kb), the matrices of each one after the other
-  if (warp < 8) {
+  if (warp < DQ) {
     // --------------------------------------------------------- dequantise
-    // steps first, first + 2, ... of (hi - lo) MATS
-    const uint32_t quarter = warp & 3u, first = warp >> 2;
+    // steps set, set + SETS, ... of (hi - lo) MATS
+    constexpr uint32_t SETS = DQ / 4, KB_STEP = SETS / MATS;
+    const uint32_t quarter = warp & 3u, set = warp >> 2;
     const uint32_t ring = smem_u32(smem + L::OFF_CODES) + warp * (AHEAD * L::CODES), end = ring + AHEAD * L::CODES;
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t kt = static_cast<uint32_t>(p.kt), steps = (hi - lo) * MATS;
     const bool zeros = p.zeros != nullptr;
-    uint32_t tile_in = lo / kt, kb_in = lo % kt + (MATS == 1 ? first : 0), step_in = first, place_in = ring;
-    while (kb_in >= kt) {
-      kb_in -= kt;
-      ++tile_in;
-    }
+    uint32_t i_in = 4 * (lo / kt) + quarter, kb_in = lo % kt + set / MATS, step_in = set, place_in = ring;
+    int64_t tile = (static_cast<int64_t>(set % MATS) * p.rt + i_in) * p.kt + kb_in;
+    const auto settle = [&]() {
+      while (kb_in >= kt) {
+        kb_in -= kt;
+        i_in += 4;
+        tile += 3 * static_cast<int64_t>(kt);
+      }
+    };
+    settle();
     const auto fetch = [&]() {
       if (step_in < steps) {
-        const uint32_t i = 4 * tile_in + quarter;
-        if (i < static_cast<uint32_t>(p.rt)) {
-          const int64_t tile = (static_cast<int64_t>(MATS == 2 ? first : 0) * p.rt + i) * p.kt + kb_in;
+        if (i_in < static_cast<uint32_t>(p.rt)) {
           const uint8_t* q = p.q + tile * kW4TileBytes + lane * 16;
 #pragma unroll
           for (int b = 0; b < 4; ++b) w4_copy_16(place_in + 512 * b + lane * 16, q + 512 * b, policy);
           if (zeros && lane < 2 * NG) w4_copy_16(place_in + 2048 + lane * 16, p.zeros + tile * (32 * NG) + lane * 16, policy);
         }
-        kb_in += MATS == 2 ? 1 : 2;
-        while (kb_in >= kt) {
-          kb_in -= kt;
-          ++tile_in;
-        }
+        kb_in += KB_STEP;
+        tile += KB_STEP;
+        settle();
         place_in = place_in + L::CODES == end ? ring : place_in + L::CODES;
-        step_in += 2;
+        step_in += SETS;
       }
       cp_async_commit();
     };
     for (int d = 0; d < AHEAD; ++d) fetch();
     uint32_t place = ring;
     bool ok = true;
-    for (uint32_t it = first; it < steps; it += 2) {
+    for (uint32_t it = set; it < steps; it += SETS) {
       const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
       cp_async_wait<AHEAD - 1>();
-      __syncwarp();
-      uint4 c[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) c[b] = ld_shared_v4(place + 512 * b + lane * 16);
-      uint32_t z[NG];
-#pragma unroll
-      for (int k = 0; k < NG; ++k) z[k] = zeros ? ld_shared_u8(place + 2048 + k * 32 + lane) : 8u;
       if (zeros) __syncwarp();  // (codes are copied and read by one lane)
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&sfree[s], ph ^ 1u, wp, abort_flag, 1));
+      if (ok) {
+        tc_fence_after();
+        const uint32_t a = tmem_base + ((quarter * 32u) << 16) + L::COL_A + s * 64;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint4 c = ld_shared_v4(place + 512 * b + lane * 16);
+          const W4Unpack<BF16> unpack(zeros ? ld_shared_u8(place + 2048 + b * NG / 4 * 32 + lane) : 8u);
+          uint32_t r[16];
+          unpack(c.x, r, 0);
+          unpack(c.y, r, 4);
+          unpack(c.z, r, 8);
+          unpack(c.w, r, 12);
+          tmem_st_32x32b_x16(a + 16 * b, r);
+        }
+      }
+      if (zeros) __syncwarp();
       fetch();
       place = place + L::CODES == end ? ring : place + L::CODES;
-      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&sfree[s], ph ^ 1u, wp, abort_flag, 1));
       if (!ok) continue;  // (the copies under way are waited for below)
-      tc_fence_after();
-      const uint32_t a = tmem_base + ((quarter * 32u) << 16) + L::COL_A + s * 64;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t r[32];
-#pragma unroll
-        for (int b = 2 * h; b < 2 * h + 2; ++b) {
-          const W4Unpack<BF16> unpack(z[b * NG / 4]);
-          const int at = 16 * (b & 1);
-          unpack(c[b].x, r, at);
-          unpack(c[b].y, r, at + 4);
-          unpack(c[b].z, r, at + 8);
-          unpack(c[b].w, r, at + 12);
-        }
-        tmem_st_32x32b_x32(a + 32 * h, r);
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&afull[s]);
     }
     cp_async_wait<0>();
-  } else if (warp < 8 + ACC) {
+  } else if (warp < DQ + ACC) {
     // ------------------------------------------- accumulate, join, finish
-    const uint32_t quarter = warp & 3u, part = (warp - 8u) >> 2;  // part: rows ROWS part .. of TP
-    const uint32_t ring = smem_u32(smem + L::OFF_SCALES) + (warp - 8u) * (AHEAD * L::SCALES);
+    const uint32_t aw = warp - DQ, quarter = warp & 3u, part = (aw >> 2) % L::PARTS;  // part: rows ROWS part .. of TP
+    const uint32_t set = (aw >> 2) / L::PARTS;                                        // steps set, set + SETS, ...
+    constexpr uint32_t SETS = L::SETS, KB_STEP = SETS / MATS;
+    const uint32_t ring = smem_u32(smem + L::OFF_SCALES) + aw * (AHEAD * L::SCALES), end = ring + AHEAD * L::SCALES;
+    float* join = reinterpret_cast<float*>(smem + L::OFF_JOIN) + part * (ROWS * 128) + quarter * 32 + lane;
+    const uint32_t join_bar = 1 + part * 4 + quarter;
     const uint64_t policy = l2_policy_evict_first();
-    const uint32_t et = threadIdx.x - 256;
     const uint32_t kt = static_cast<uint32_t>(p.kt), steps = (hi - lo) * MATS;
-    uint32_t tile_in = lo / kt, kb_in = lo % kt, fetched = 0, place_in = ring;
-    int m_in = 0;
+    uint32_t i_in = 4 * (lo / kt) + quarter, kb_in = lo % kt + set / MATS, step_in = set, place_in = ring;
+    int64_t tile = (static_cast<int64_t>(set % MATS) * p.rt + i_in) * p.kt + kb_in;
+    const auto settle = [&]() {
+      while (kb_in >= kt) {
+        kb_in -= kt;
+        i_in += 4;
+        tile += 3 * static_cast<int64_t>(kt);
+      }
+    };
+    settle();
     const auto fetch = [&]() {
-      if (fetched < steps) {
-        const uint32_t i = 4 * tile_in + quarter;
-        if (i < static_cast<uint32_t>(p.rt) && lane < 4 * NG) {
-          const int64_t tile = (static_cast<int64_t>(m_in) * p.rt + i) * p.kt + kb_in;
+      if (step_in < steps) {
+        if (i_in < static_cast<uint32_t>(p.rt) && lane < 4 * NG)
           w4_copy_16(place_in + lane * 16, reinterpret_cast<const uint8_t*>(p.scales) + tile * (64 * NG) + lane * 16, policy);
-        }
-        if (MATS == 2 && m_in == 0) {
-          m_in = 1;
-        } else {
-          m_in = 0;
-          if (++kb_in == kt) {
-            kb_in = 0;
-            ++tile_in;
-          }
-        }
-        place_in = place_in + L::SCALES == ring + AHEAD * L::SCALES ? ring : place_in + L::SCALES;
-        ++fetched;
+        kb_in += KB_STEP;
+        tile += KB_STEP;
+        settle();
+        place_in = place_in + L::SCALES == end ? ring : place_in + L::SCALES;
+        step_in += SETS;
       }
       cp_async_commit();
     };
     for (int d = 0; d < AHEAD; ++d) fetch();
-    uint32_t place = ring, it = 0;
+    uint32_t place = ring, it = set, seg_end = 0;
     bool ok = true;
     uint32_t gpos = lo;
     Segment seg;
     while (skinny_segment(sp, hi, gpos, seg)) {
       const int n_local = static_cast<int>(quarter * 32 + lane), n = seg.tile * 128 + n_local;
       const bool n_ok = n < p.N;
-      float acc[MATS][ROWS];
+      seg_end += static_cast<uint32_t>(seg.kb1 - seg.kb0) * MATS;
+      float acc[ROWS];
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
+      for (int t = 0; t < ROWS; ++t) acc[t] = 0.f;
+      for (; it < seg_end; it += SETS) {
+        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+        cp_async_wait<AHEAD - 1>();
+        __syncwarp();
+        float sc[NG];
 #pragma unroll
-        for (int t = 0; t < ROWS; ++t) acc[m][t] = 0.f;
-      for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
+        for (int k = 0; k < NG; ++k)
+          sc[k] = w4_float<BF16>(static_cast<uint16_t>(ld_shared_u16(place + k * 64 + lane * 2)));
+        if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dfull[s], ph, wp, abort_flag, 6));
+        if (ok) {
+          tc_fence_after();
+          const uint32_t d = tmem_base + ((quarter * 32u) << 16) + L::COL_D + s * (NG * TP) + part * ROWS;
+          constexpr int G2 = ROWS == 16 && NG > 1 ? 2 : 1;  // groups whose loads are in flight
 #pragma unroll
-        for (int m = 0; m < MATS; ++m, ++it) {
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-          cp_async_wait<AHEAD - 1>();
-          __syncwarp();
-          float sc[NG];
+          for (int k = 0; k < NG; k += G2) {
 #pragma unroll
-          for (int k = 0; k < NG; ++k)
-            sc[k] = w4_float<BF16>(static_cast<uint16_t>(ld_shared_u16(place + k * 64 + lane * 2)));
-          __syncwarp();
-          fetch();
-          place = place + L::SCALES == ring + AHEAD * L::SCALES ? ring : place + L::SCALES;
+            for (int t0 = 0; t0 < ROWS; t0 += 16) {
+              uint32_t r[G2][16];
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&dfull[s * NG + k], ph, wp, abort_flag, 6));
-            if (ok) {
-              tc_fence_after();
-              const uint32_t d = tmem_base + ((quarter * 32u) << 16) + L::COL_D + (s * NG + k) * TP + part * ROWS;
-              constexpr int STEP = ROWS < 32 ? ROWS : 32;
+              for (int e = 0; e < G2; ++e) tmem_ld_32x32b_x16(d + (k + e) * TP + t0, r[e]);
+              tmem_wait_ld();
 #pragma unroll
-              for (int t0 = 0; t0 < ROWS; t0 += STEP) {
-                uint32_t r[STEP];
-                if constexpr (STEP == 16)
-                  tmem_ld_32x32b_x16(d + t0, r);
-                else
-                  tmem_ld_32x32b_x32(d + t0, r);
-                tmem_wait_ld();
+              for (int e = 0; e < G2; ++e)
 #pragma unroll
-                for (int t = 0; t < STEP; ++t) acc[m][t0 + t] = fmaf(sc[k], __uint_as_float(r[t]), acc[m][t0 + t]);
-              }
+                for (int t = 0; t < 16; ++t) acc[t0 + t] = fmaf(sc[k + e], __uint_as_float(r[e][t]), acc[t0 + t]);
             }
           }
           tc_fence_before();
           __syncwarp();
-          if (ok && lane == 0) mbar_arrive(&sfree[s]);
+          if (lane == 0) mbar_arrive(&sfree[s]);
         }
+        __syncwarp();
+        fetch();
+        place = place + L::SCALES == end ? ring : place + L::SCALES;
+      }
+      // the second set's sums to the first: the other half of the columns', or the up projection's
+      float up[MATS == 2 ? ROWS : 1];
+      if constexpr (SETS == 2) {
+        if (set == 1) {
+#pragma unroll
+          for (int t = 0; t < ROWS; ++t) join[t * 128] = acc[t];
+          named_bar_sync(join_bar, 64);
+          named_bar_sync(join_bar, 64);  // it has been read
+          continue;
+        }
+        named_bar_sync(join_bar, 64);
+#pragma unroll
+        for (int t = 0; t < ROWS; ++t) {
+          if constexpr (MATS == 2)
+            up[t] = join[t * 128];
+          else
+            acc[t] += join[t * 128];
+        }
+        named_bar_sync(join_bar, 64);
       }
       const bool whole = seg.kb0 == 0 && seg.kb1 == p.kt;
       float bias_a = 0.f, bias_b = 0.f;
@@ -411,54 +432,65 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
 #pragma unroll
         for (int t = 0; t < ROWS; ++t)
           if (ok && n_ok && row0 + t0 + t < p.T)
-            w4_output<GATED, BF16>(p, acc[0][t], acc[MATS - 1][t], row0 + t0 + t, n, bias_a, bias_b);
+            w4_output<GATED, BF16>(p, acc[t], MATS == 2 ? up[MATS == 2 ? t : 0] : 0.f, row0 + t0 + t, n, bias_a, bias_b);
         continue;
       }
-      // this segment's sums, a ticket; the last segment of the tile finishes it
-      const int64_t tiles = p.total / p.kt;
-      const int64_t at = (blockIdx.y * tiles + seg.tile) * p.max_segs;
-      float* slot = p.partials + (at + seg.seg) * (MATS * TP * 128) + n_local;
+      // this segment's sums, a ticket; the last segment's warp finishes its lanes and rows
+      const int64_t tiles = p.total / p.kt, at = blockIdx.y * tiles + seg.tile;
+      constexpr int64_t SEG = MATS * TP * 128;
+      float* slots = p.partials + at * p.max_segs * SEG + t0 * 128 + n_local;
+      float* own = slots + seg.seg * SEG;
 #pragma unroll
-      for (int m = 0; m < MATS; ++m)
-#pragma unroll
-        for (int t = 0; t < ROWS; ++t)
-          if (row0 + t0 + t < p.T) slot[(m * TP + t0 + t) * 128] = acc[m][t];
-      __threadfence();
-      named_bar_sync(1, 32 * ACC);
-      if (et == 0) {
-        int last = 0;
-        if (ok) {
-          int* ticket = p.tickets + blockIdx.y * tiles + seg.tile;
-          last = atomicAdd(ticket, 1) == seg.nsegs - 1;
-          if (last) *ticket = 0;  // ready for the next launch
+      for (int t = 0; t < ROWS; ++t)
+        if (row0 + t0 + t < p.T) {
+          own[t * 128] = acc[t];
+          if constexpr (MATS == 2) own[(TP + t) * 128] = up[t];
         }
-        *last_flag = last;
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0 && ok) {
+        int* ticket = p.tickets + at * ACC + aw;  // (of the first set's warps)
+        last = atomicAdd(ticket, 1) == seg.nsegs - 1;
+        if (last) *ticket = 0;  // ready for the next launch
       }
-      named_bar_sync(1, 32 * ACC);
-      if (ok && *last_flag) {
-        __threadfence();
-        const float* from = p.partials + at * (MATS * TP * 128) + n_local;
+      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+      __threadfence();
+      constexpr int B = MATS == 2 ? 4 : 8;  // rows whose loads of (four / MATS) segments are in flight
+#pragma unroll 1
+      for (int b = 0; b < ROWS; b += B) {
+        if (row0 + t0 + b >= p.T) break;
+        float sum[MATS][B];
 #pragma unroll
         for (int m = 0; m < MATS; ++m)
 #pragma unroll
-          for (int t = 0; t < ROWS; ++t) acc[m][t] = 0.f;
-        for (int sg = 0; sg < seg.nsegs; ++sg) {
-          const float* f = from + static_cast<int64_t>(sg) * (MATS * TP * 128);
+          for (int t = 0; t < B; ++t) sum[m][t] = 0.f;
+        for (int s0 = 0; s0 < seg.nsegs; s0 += 4 / MATS) {
+          float x[4 / MATS][MATS][B];
 #pragma unroll
-          for (int m = 0; m < MATS; ++m)
+          for (int k = 0; k < 4 / MATS; ++k)
 #pragma unroll
-            for (int t = 0; t < ROWS; ++t)
-              if (row0 + t0 + t < p.T) acc[m][t] += __ldcg(f + (m * TP + t0 + t) * 128);
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+              for (int t = 0; t < B; ++t)
+                x[k][m][t] = s0 + k < seg.nsegs && row0 + t0 + b + t < p.T
+                                 ? __ldcg(slots + (s0 + k) * SEG + (m * TP + b + t) * 128)
+                                 : 0.f;
+#pragma unroll
+          for (int k = 0; k < 4 / MATS; ++k)
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+              for (int t = 0; t < B; ++t) sum[m][t] += x[k][m][t];
         }
 #pragma unroll
-        for (int t = 0; t < ROWS; ++t)
-          if (n_ok && row0 + t0 + t < p.T)
-            w4_output<GATED, BF16>(p, acc[0][t], acc[MATS - 1][t], row0 + t0 + t, n, bias_a, bias_b);
+        for (int t = 0; t < B; ++t)
+          if (n_ok && row0 + t0 + b + t < p.T)
+            w4_output<GATED, BF16>(p, sum[0][t], sum[MATS - 1][t], row0 + t0 + b + t, n, bias_a, bias_b);
       }
-      named_bar_sync(1, 32 * ACC);  // last_flag is reused by the next segment
     }
     cp_async_wait<0>();
-  } else if (warp == 8 + ACC) {
+  } else if (warp == DQ + ACC) {
     // ------------------------------------------------------------------- X
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_last();
@@ -498,8 +530,8 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
           constexpr int PER = 8 / NG;     // of them in a group
           const uint64_t bdesc = smem_desc_sw128(x + (kk >> 2) * L::X_SUB + (kk & 3) * 32, 16, 1024);
           umma_f16_ts(d + kk / PER * TP, a + kk * 8, bdesc, IDESC, kk % PER > 0 ? 1u : 0u);
-          // (fault injection: the accumulating warps then wait for a sum that is never announced)
-          if (kk % PER == PER - 1 && !(p.inject_stall && it == 0 && kk < PER)) umma_commit(&dfull[s * NG + kk / PER]);
+          // (fault injection: the accumulating warps then wait for sums that are never announced)
+          if (kk == 7 && !(p.inject_stall && it == 0)) umma_commit(&dfull[s]);
         }
       }
     }
@@ -511,7 +543,7 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9 + ACC) tmem_dealloc(tmem_base, L::TMEM_COLS);
+  if (warp == DQ + ACC + 1) tmem_dealloc(tmem_base, L::TMEM_COLS);
 }
 
 }  // namespace ge
