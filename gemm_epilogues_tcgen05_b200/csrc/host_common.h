@@ -127,6 +127,8 @@ struct GroupedCfg {
 // A plan of few rows times 4-bit weights.
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
+  ge_inst::W4FewInstance few = {};       // at most 16 rows
+  int split = 1;                         // CTAs of its clusters
   uint32_t smem = 0;
   int threads = 0, tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1;
 };
@@ -223,16 +225,20 @@ struct Launch {
   Launch& operator=(const Launch&) = delete;
 };
 
-// CTA pairs of this kernel that the device holds at once; one per two SMs if
-// the query fails.
-inline int resident_pairs(const void* fn, int threads, uint32_t smem, int sms) {
-  Launch l(sms / 2 * 2, threads, smem, true, nullptr);
+// Clusters of `size` CTAs of this kernel that the device holds at once; one per `size`
+// SMs if the query fails.
+inline int resident_clusters(const void* fn, int size, int threads, uint32_t smem, int sms) {
+  Launch l(sms / size * size, threads, smem, true, nullptr);
+  l.attr[1].val.clusterDim.x = (unsigned)size;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
-    return sms / 2;
+    return sms / size;
   }
-  return n < sms / 2 ? n : sms / 2;
+  return n < sms / size ? n : sms / size;
+}
+inline int resident_pairs(const void* fn, int threads, uint32_t smem, int sms) {
+  return resident_clusters(fn, 2, threads, smem, sms);
 }
 
 // Makes `device` current for the calls of one entry point and puts the

@@ -1,0 +1,6 @@
+// inst_w4_few_f16.cu -- at most 16 fp16 rows times 4-bit weights.
+#include "inst_w4_few.cuh"
+
+namespace ge_inst {
+W4FewInstance w4_few_f16(int rows, bool gated, int ng) { return w4_few_any<false>(rows, gated, ng); }
+}  // namespace ge_inst

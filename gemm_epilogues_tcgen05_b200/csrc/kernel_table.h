@@ -99,6 +99,14 @@ struct W4Instance {
   uint32_t smem;
   int threads, tickets;  // counters a tile
 };
+using W4FewKernelFn = void (*)(ge::W4MulParams);
+struct W4FewInstance {  // [without, with zeros]
+  W4FewKernelFn fn[2];
+  uint32_t smem[2];
+  int threads;
+};
+W4FewInstance w4_few_f16(int rows, bool gated, int ng);  // rows <= 16
+W4FewInstance w4_few_bf16(int rows, bool gated, int ng);
 W4Instance w4_f16(int tp, bool gated, int ng);
 W4Instance w4_bf16(int tp, bool gated, int ng);
 

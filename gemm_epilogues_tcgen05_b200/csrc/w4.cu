@@ -1,7 +1,7 @@
 // w4.cu -- C ABI of 4-bit weights with group scales: quantisation, packing, the
 // inverse, and the plan and call of the product with few rows.
 #include "host_tiles.h"
-#include "w4_kernel.cuh"
+#include "w4_few.cuh"
 #include "w4_quant.cuh"
 
 using namespace ge_host;
@@ -47,6 +47,35 @@ int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int sms, cudaStream
   Launch l((int)(want < most ? want : most), 256, 0, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, k);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "4-bit weight launch");
+}
+
+// At most 16 rows: clusters along the features, the CTAs of one along the columns. A
+// warp's tiles are what a launch takes; the join over a cluster costs about what a tile does.
+cudaError_t plan_few(gemm_epi_plan_s* p, bool gated, int64_t group) {
+  W4Cfg& c = p->w4;
+  c.few = (p->dtype == GEMM_EPI_BF16 ? ge_inst::w4_few_bf16 : ge_inst::w4_few_f16)((int)p->T, gated, (int)(128 / group));
+  for (int z = 0; z < 2; ++z) {
+    const cudaError_t e = cudaFuncSetAttribute(c.few.fn[z], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.few.smem[z]);
+    if (e != cudaSuccess) return e;
+  }
+  const int rt = (int)row_tiles(p->N);
+  int64_t best = INT64_MAX;
+  for (int split = 1; split <= 8 && split <= c.kt; split *= 2) {
+    int clusters = split == 1 ? p->num_sms : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
+    if (clusters > rt) clusters = rt;
+    const int rows = (int)ceil_div(rt, clusters);
+    if (split > 1 && rows > ge::kW4FewWarps) break;  // (a warp keeps the sums of two rows of tiles)
+    const int64_t cost = ceil_div((int64_t)rows * ceil_div(c.kt, split), ge::kW4FewWarps) + (split > 1);
+    if (const char* f = getenv("W4SPLIT")) if (split < atoi(f)) continue;
+    if (cost >= best) continue;
+    best = cost;
+    c.split = split;
+    c.grid = clusters * split;
+    if (const char* f = getenv("W4SPLIT")) break;
+  }
+  p->grid = c.grid;
+  c.max_segs = c.split;
+  return cudaSuccess;
 }
 
 gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,
@@ -97,6 +126,12 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   p->timeout_ns = wd.timeout_ns;
   p->inject_stall = wd.inject_stall;
   W4Cfg& c = p->w4;
+  c.tiles = (int)tiles;
+  c.kt = (int)kt;
+  cudaError_t e = cudaSuccess;
+  if (T <= 16 && !getenv("W4OLD")) {
+    e = plan_few(p, gated, group);
+  } else {
   const int most = gated && group == 128 ? 64 : (int)group;  // rows of an instance
   c.tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   if (c.tp > most) c.tp = most;
@@ -105,8 +140,6 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   c.fn = inst.fn;
   c.smem = inst.smem;
   c.threads = inst.threads;
-  c.tiles = (int)tiles;
-  c.kt = (int)kt;
   // equal shares of all blocks of 128 columns, at least two each
   const int total = c.tiles * c.kt, share = sms / c.row_blocks;
   c.grid = total / 2 < 1 ? 1 : total / 2 < share ? total / 2 : share;
@@ -120,7 +153,7 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
     const int64_t last = ge::skinny_owner((int64_t)(t + 1) * c.kt - 1, c.grid, total);
     if (last - first + 1 > c.max_segs) c.max_segs = (int)(last - first + 1);
   }
-  cudaError_t e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
+  e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
   if (e == cudaSuccess && c.max_segs > 1) {
     const size_t blocks = (size_t)c.row_blocks * (size_t)c.tiles, items = blocks * (size_t)inst.tickets;
     p->sk_bytes = blocks * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
@@ -129,6 +162,7 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
     if (e == cudaSuccess) e = zero_counts(p->sk_tickets, items);
     p->split_items = (int)items;
     p->sk_bytes += sizeof(int) * items;
+  }
   }
   if (e == cudaSuccess) e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
   if (e == cudaSuccess) {
@@ -258,9 +292,6 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   rc = begin_call(p, stream);
   if (rc) return rc;
   const W4Cfg& c = p->w4;
-  CUtensorMap x;
-  rc = encode_2d(&x, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, (uint32_t)c.tp, "the row operand");
-  if (rc) return rc;
   ge::W4MulParams k{};
   k.T = (int32_t)p->T;
   k.N = (int32_t)p->N;
@@ -283,6 +314,17 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   k.status = p->status_dev;
   k.timeout_ns = p->timeout_ns;
   k.inject_stall = p->inject_stall;
+  if (c.few.threads) {
+    k.split = c.split;
+    k.X = X;
+    Launch l(c.grid, c.few.threads, c.few.smem[zeros != nullptr], c.split > 1, stream);
+    l.attr[1].val.clusterDim.x = (unsigned)c.split;
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.few.fn[zeros != nullptr], k);
+    return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");
+  }
+  CUtensorMap x;
+  rc = encode_2d(&x, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, (uint32_t)c.tp, "the row operand");
+  if (rc) return rc;
   Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.threads, c.smem, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, x, k);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");

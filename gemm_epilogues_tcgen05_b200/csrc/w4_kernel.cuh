@@ -47,6 +47,8 @@ struct W4MulParams {
   int32_t max_segs;
   int32_t epi, act;      // EpiKind; gated: an ActKind
   int32_t bias_f32, out_f32;
+  int32_t split;         // w4_few_kernel: CTAs of a cluster
+  const void* X;         // w4_few_kernel
   const uint8_t* q;
   const void* scales;
   const uint8_t* zeros;
@@ -123,6 +125,13 @@ __device__ __forceinline__ uint32_t w4_sub(uint32_t a, uint32_t b) {
   }
 }
 
+// (a & b) | c in one instruction (of the expression the compiler makes two)
+__device__ __forceinline__ uint32_t w4_and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // The eight codes of a word less their zero point z (0 .. 127), as four operand
 // registers. bf16: 128 + q - (128 + z), the codes below 128's exponent. fp16 has room
 // for a nibble and the next: 1024 + q - (1024 + z), and (1024 + 16 q) / 16 - (64 + z) of the
@@ -137,16 +146,17 @@ struct W4Unpack {
     const __half2 n = __hneg2(__hsub2(*reinterpret_cast<const __half2*>(&zero), __float2half2_rn(960.f)));  // -(64 + z)
     zero16 = BF16 ? 0u : *reinterpret_cast<const uint32_t*>(&n);
   }
-  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&r)[16], int at) const {
+  template <int R>
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&r)[R], int at) const {
     if constexpr (BF16) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) r[at + m] = w4_sub<true>(((w >> (4 * m)) & 0x000f000fu) | 0x43004300u, zero);
+      for (int m = 0; m < 4; ++m) r[at + m] = w4_sub<true>(w4_and_or(w >> (4 * m), 0x000f000fu, 0x43004300u), zero);
     } else {
 #pragma unroll
       for (int m = 0; m < 4; m += 2) {
         const uint32_t v = w >> (4 * m);
-        r[at + m] = w4_sub<false>((v & 0x000f000fu) | 0x64006400u, zero);
-        const uint32_t hi = (v & 0x00f000f0u) | 0x64006400u;
+        r[at + m] = w4_sub<false>(w4_and_or(v, 0x000f000fu, 0x64006400u), zero);
+        const uint32_t hi = w4_and_or(v, 0x00f000f0u, 0x64006400u);
         const __half2 f = __hfma2(*reinterpret_cast<const __half2*>(&hi), __float2half2_rn(0.0625f),
                                   *reinterpret_cast<const __half2*>(&zero16));
         r[at + m + 1] = *reinterpret_cast<const uint32_t*>(&f);
