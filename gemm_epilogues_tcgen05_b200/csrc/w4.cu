@@ -58,20 +58,18 @@ cudaError_t plan_few(gemm_epi_plan_s* p, bool gated, int64_t group) {
     const cudaError_t e = cudaFuncSetAttribute(c.few.fn[z], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.few.smem[z]);
     if (e != cudaSuccess) return e;
   }
-  const int rt = (int)row_tiles(p->N);
+  const int halves = (int)ceil_div(p->N, 16);  // of rows of tiles
   int64_t best = INT64_MAX;
   for (int split = 1; split <= 8 && split <= c.kt; split *= 2) {
     int clusters = split == 1 ? p->num_sms : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
-    if (clusters > rt) clusters = rt;
-    const int rows = (int)ceil_div(rt, clusters);
+    if (clusters > halves) clusters = halves;
+    const int rows = (int)ceil_div(halves, clusters);
     if (split > 1 && rows > ge::kW4FewWarps) break;  // (a warp keeps the sums of two rows of tiles)
-    const int64_t cost = ceil_div((int64_t)rows * ceil_div(c.kt, split), ge::kW4FewWarps) + (split > 1);
-    if (const char* f = getenv("W4SPLIT")) if (split < atoi(f)) continue;
+    const int64_t cost = ceil_div((int64_t)rows * ceil_div(c.kt, split), ge::kW4FewWarps) + 4 * (split > 1);
     if (cost >= best) continue;
     best = cost;
     c.split = split;
     c.grid = clusters * split;
-    if (const char* f = getenv("W4SPLIT")) break;
   }
   p->grid = c.grid;
   c.max_segs = c.split;
@@ -129,7 +127,7 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   c.tiles = (int)tiles;
   c.kt = (int)kt;
   cudaError_t e = cudaSuccess;
-  if (T <= 16 && !getenv("W4OLD")) {
+  if (T <= 16) {
     e = plan_few(p, gated, group);
   } else {
   const int most = gated && group == 128 ? 64 : (int)group;  // rows of an instance
@@ -315,7 +313,12 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   k.timeout_ns = p->timeout_ns;
   k.inject_stall = p->inject_stall;
   if (c.few.threads) {
-    k.split = c.split;
+    const uint32_t halves = (uint32_t)ceil_div(p->N, 16), clusters = (uint32_t)(c.grid / c.split);
+    while (1 << k.split < c.split) ++k.split;
+    k.half_quot = halves / clusters;
+    k.half_rest = halves % clusters;
+    k.kt_quot = (uint32_t)(c.kt / c.split);
+    k.kt_rest = (uint32_t)(c.kt % c.split);
     k.X = X;
     Launch l(c.grid, c.few.threads, c.few.smem[zeros != nullptr], c.split > 1, stream);
     l.attr[1].val.clusterDim.x = (unsigned)c.split;

@@ -33,10 +33,10 @@ struct W4Few {
   static constexpr uint32_t TILE = kW4TileBytes + (ZEROS ? 96 : 64) * NG, PLACE = MATS * TILE;
   static constexpr int LD = 36;                                 // floats between a sum's rows: no two lanes in a bank
   static constexpr uint32_t SUMS = MATS * NT * 8 * LD * 4;      // of a warp and a row of tiles
-  static constexpr int ROOM = (232448 / kW4FewWarps - SUMS) / PLACE;
+  static constexpr int ROOM = (232448 / kW4FewWarps - 8 - SUMS) / PLACE;
   static constexpr int DEPTH = ROOM < 6 ? ROOM : 6;             // places of a warp's ring
   static constexpr uint32_t WARP = DEPTH * PLACE + SUMS;        // its last row's sums take the ring's place
-  static constexpr uint32_t BYTES = kW4FewWarps * WARP;
+  static constexpr uint32_t BYTES = kW4FewWarps * (WARP + 8);
   static_assert(DEPTH >= 2 && SUMS <= DEPTH * PLACE && PLACE % 16 == 0 && SUMS % 16 == 0, "ring");
   static_assert(BYTES <= 232448, "above the per-CTA limit");
 };
@@ -55,14 +55,40 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], bool zero, uint32_t a0, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
 
-// first of `total` units of part `i` of `parts` (the plan keeps the products below 2^31)
-__device__ __forceinline__ uint32_t w4_share(uint32_t total, uint32_t i, uint32_t parts) { return total * i / parts; }
+// The tiles of a CTA's half rows [h0, h1) of tiles, nkb columns of tiles wide, row after row.
+// A tile that both halves are wanted of weighs 2, one of the first or last row
+// may weigh 1; the warps have equal shares of the weight, runs of tiles. (No divisions:
+// a handful of them ahead of the first load, and in the join, cost 3 us.)
+template <int H>
+struct W4Half {
+  static constexpr int value = H;
+};
+
+struct W4Runs {
+  uint32_t nkb, row0, rows, first, last_at, weight;  // rows of tiles; first: log2 of the weight of the first row's tiles
+  __device__ __forceinline__ W4Runs(uint32_t h0, uint32_t h1, uint32_t nkb_) : nkb(nkb_), row0(h0 >> 1) {
+    rows = ((h1 + 1) >> 1) - row0;
+    first = (h0 & 1u) || h1 - h0 == 1 ? 0 : 1;
+    weight = (h1 - h0) * nkb;
+    last_at = (h1 & 1u) && rows > 1 ? weight - nkb : weight;  // weight ahead of a last row that weighs 1
+  }
+  // the first tile of warp w: of the tiles that begin at its share or later
+  __device__ __forceinline__ uint32_t begin(uint32_t w) const {
+    const uint32_t x = weight * w / kW4FewWarps;
+    if (x <= nkb << first) return (x + first) >> first;
+    if (x <= last_at) return nkb + ((x - (nkb << first) + 1) >> 1);
+    return (rows - 1) * nkb + x - last_at;
+  }
+};
+
+// one of `parts` shares of `total` = quot parts + rest
+__device__ __forceinline__ uint32_t w4_share(uint32_t i, uint32_t quot, uint32_t rest) { return i * quot + min(i, rest); }
 
 template <int NT, bool GATED, int NG, bool ZEROS, bool BF16>
 __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4MulParams p) {
@@ -70,14 +96,18 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   using L = W4Few<NT, MATS, NG, ZEROS>;
   extern __shared__ __align__(16) uint8_t w4_smem[];
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
-  const uint32_t split = static_cast<uint32_t>(p.split), rank = blockIdx.x % split;  // CTAs of a cluster, along the columns
-  const uint32_t cluster = blockIdx.x / split, clusters = gridDim.x / split;
-  // this cluster's rows of tiles, this CTA's columns of them, this warp's tiles
-  const uint32_t row0 = w4_share(p.rt, cluster, clusters), rows = w4_share(p.rt, cluster + 1, clusters) - row0;
-  const uint32_t kb0 = w4_share(p.kt, rank, split), nkb = w4_share(p.kt, rank + 1, split) - kb0;
-  const uint32_t units = rows * nkb, parts = min(units, static_cast<uint32_t>(W));
-  const uint32_t u0 = warp < parts ? w4_share(units, warp, parts) : units, u1 = warp < parts ? w4_share(units, warp + 1, parts) : units;
+  const uint32_t rank = blockIdx.x & ((1u << p.split) - 1u), cluster = blockIdx.x >> p.split;  // rank: along the columns
+  const bool split = p.split > 0;
+  // this cluster's half rows of tiles, this CTA's columns of them, this warp's tiles
+  const uint32_t h0 = w4_share(cluster, p.half_quot, p.half_rest), h1 = w4_share(cluster + 1, p.half_quot, p.half_rest);
+  const uint32_t kb0 = w4_share(rank, p.kt_quot, p.kt_rest), nkb = w4_share(rank + 1, p.kt_quot, p.kt_rest) - kb0;
+  const W4Runs runs(h0, h1, nkb);
+  const uint32_t row0 = runs.row0, u0 = runs.begin(warp), u1 = runs.begin(warp + 1);
   uint8_t* ring = w4_smem + warp * L::WARP;
+  // the rows of tiles whose sums a warp keeps: the first, the last
+  int* kept = reinterpret_cast<int*>(w4_smem + kW4FewWarps * L::WARP);
+  if (lane < 2) kept[2 * warp + lane] = -1;
+  __syncwarp();
   wait_for_inputs();
 
   // ---- copies: unit u is tile (row0 + u / nkb, kb0 + u % nkb)
@@ -88,17 +118,20 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   // 16 bytes a lane of each kind: codes, then the first 4 NG lanes scales, the next 2 NG zeros
   const int64_t tile0 = static_cast<int64_t>(row0 + row) * p.kt + kb0 + kb, matrix = static_cast<int64_t>(p.rt) * p.kt;
   const uint8_t* q = p.q + tile0 * kW4TileBytes + lane * 16;
+  uint32_t in_row = row;
   const bool side_scales = lane < 4 * NG, side_in = lane < (ZEROS ? 6 : 4) * NG;
   const uint32_t side_bytes = side_scales ? 64 * NG : 32 * NG;
   const uint8_t* side = side_scales ? reinterpret_cast<const uint8_t*>(p.scales) + tile0 * (64 * NG) + lane * 16
                                     : p.zeros + tile0 * (32 * NG) + (lane - 4 * NG) * 16;
   const auto fetch = [&]() {
     if (in < u1) {
+      // (features 0 .. 15 are the lower lanes', and the half that another CTA takes is left out)
+      const bool wanted = 2 * (row0 + in_row) + (lane >> 4) - h0 < h1 - h0;
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          w4_copy_16(in_place + m * L::TILE + 512 * b, q + m * matrix * kW4TileBytes + 512 * b, policy);
+          if (wanted) w4_copy_16(in_place + m * L::TILE + 512 * b, q + m * matrix * kW4TileBytes + 512 * b, policy);
         if (side_in) w4_copy_16(in_place + m * L::TILE + kW4TileBytes, side + m * matrix * side_bytes, policy);
       }
       in_place = in_place + L::PLACE == ring_end ? ring_end - L::DEPTH * L::PLACE : in_place + L::PLACE;
@@ -107,6 +140,7 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
       ++in;
       if (++in_kb == nkb) {
         in_kb = 0;
+        ++in_row;
         q += static_cast<int64_t>(p.kt - nkb) * kW4TileBytes;
         side += static_cast<int64_t>(p.kt - nkb) * side_bytes;
       }
@@ -137,26 +171,12 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
 
   const uint4* X = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) + static_cast<int64_t>(g) * p.K + c * 8);
   const int64_t x_step = p.K;  // 8 rows, in units of 8 columns
-  const uint8_t* place = ring;
-  uint32_t seg_kb = kb;
-  for (uint32_t u = u0; u < u1; ++u) {
-    uint4 x[4][NT];
-    {
-      const uint4* xk = X + (kb0 + kb) * 16;
-      const int left = p.K - static_cast<int>(kb0 + kb) * 128;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int blocks = t * 8 + static_cast<int>(g) < p.T ? left : 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) x[b][t] = b * 32 < blocks ? __ldg(xk + t * x_step + b * 4) : make_uint4(0, 0, 0, 0);
-      }
-    }
-    cp_async_wait<L::DEPTH - 1>();
-    __syncwarp();
+  // a tile's products, of its halves from .. to - 1
+  const auto multiply = [&](const uint8_t* place, const uint4 (&x)[4][NT], auto from, auto to) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = decltype(from)::value; h < decltype(to)::value; ++h) {
         const uint8_t* tile = place + m * L::TILE;
         const uint32_t f = 16 * h + g;
         float part[NT][4];
@@ -185,19 +205,43 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
             for (int e = 0; e < 4; ++e) acc[m][t][h][e] = fmaf(e < 2 ? s0 : s1, part[t][e], acc[m][t][h][e]);
         }
       }
+  };
+  const uint8_t* place = ring;
+  uint32_t seg_kb = kb;
+  for (uint32_t u = u0; u < u1; ++u) {
+    uint4 x[4][NT];
+    {
+      const uint4* xk = X + (kb0 + kb) * 16;
+      const int left = p.K - static_cast<int>(kb0 + kb) * 128;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int blocks = t * 8 + static_cast<int>(g) < p.T ? left : 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) x[b][t] = b * 32 < blocks ? __ldg(xk + t * x_step + b * 4) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    cp_async_wait<L::DEPTH - 1>();
+    __syncwarp();
+    const uint32_t half = 2 * (row0 + row);
+    if (half >= h0 && half + 1 < h1)
+      multiply(place, x, W4Half<0>(), W4Half<2>());
+    else if (half >= h0)
+      multiply(place, x, W4Half<0>(), W4Half<1>());
+    else
+      multiply(place, x, W4Half<1>(), W4Half<2>());
     __syncwarp();  // the place has been read
     fetch();
     place = place + L::PLACE == ring + L::DEPTH * L::PLACE ? ring : place + L::PLACE;
     // the end of a row of tiles: a whole row that needs no other warp is finished, the
     // first row's and the last row's sums are kept
     if (++kb < nkb && u + 1 < u1) continue;
-    if (split == 1 && seg_kb == 0 && kb == nkb) {
+    if (!split && seg_kb == 0 && kb == nkb) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const int n = static_cast<int>((row0 + row) * 32 + 16 * h + g + 4 * e);
-          if (n >= p.N) continue;
+          if (n >= p.N || 2 * (row0 + row) + h - h0 >= h1 - h0) continue;
           const float bias_a = bias_of(n), bias_b = GATED ? bias_of(p.N + n) : 0.f;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -207,7 +251,9 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
                 w4_output<GATED, BF16>(p, acc[0][t][h][e + i], acc[MATS - 1][t][h][e + i], t * 8 + 2 * c + i, n, bias_a, bias_b);
         }
     } else {
-      stash(u + 1 == u1 ? ring : ring + L::DEPTH * L::PLACE);
+      const bool last = u + 1 == u1;
+      stash(last ? ring : ring + L::DEPTH * L::PLACE);
+      if (lane == 0) kept[2 * warp + last] = static_cast<int>(row);
     }
     clear();
     kb = seg_kb = 0;
@@ -215,39 +261,41 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   }
   cp_async_wait<0>();
   __syncwarp();
-  if (split > 1)
+  if (split)
     cluster_sync();
   else
     __syncthreads();
 
-  // ---- the rows that several warps share: outputs (row, t, feature), the CTAs of a
-  // cluster in turn
-  const uint32_t outs = rows * static_cast<uint32_t>(p.T) * 32;
-  for (uint32_t o = threadIdx.x + rank * (32 * W); o < outs; o += 32 * W * split) {
-    const uint32_t f = o & 31u, rt = o >> 5, r = rt / static_cast<uint32_t>(p.T), t = rt - r * static_cast<uint32_t>(p.T);
-    float a = 0.f, b = 0.f;
-    bool whole = false;
-    for (uint32_t s = 0; s < split; ++s) {
-      const uint32_t n = w4_share(p.kt, s + 1, split) - w4_share(p.kt, s, split), total = rows * n;
-      const uint32_t among = min(total, static_cast<uint32_t>(W));
-      const uint32_t base = split > 1 ? mapa_shared(smem_u32(w4_smem), s) : smem_u32(w4_smem);
-      uint32_t w = skinny_owner32(r * n, among, total);
-      const uint32_t last = skinny_owner32((r + 1) * n - 1, among, total);
-      whole = split == 1 && w == last;
-      if (whole) break;
-      for (; w <= last; ++w) {
-        const bool ends = w4_share(total, w + 1, among) <= (r + 1) * n;  // it is this warp's last row
-        const uint32_t at = base + w * L::WARP + (ends ? 0 : L::DEPTH * L::PLACE) + (t * L::LD + f) * 4;
-        a += ld_cluster_f32(at);
-        if constexpr (GATED) b += ld_cluster_f32(at + NT * 8 * L::LD * 4);
+  // ---- the rows that warps have kept: a warp takes a row of X of them (of a cluster's
+  // rows, the CTAs in turn), a lane a feature; lane e holds entry e of `kept`
+  const int own = kept[lane];
+  const uint32_t same = __match_any_sync(0xffffffffu, own);
+  uint32_t leaders = __ballot_sync(0xffffffffu, own >= 0 && (same & ((1u << lane) - 1u)) == 0);
+  uint32_t t = (rank << 4) + warp;  // (16 warps)
+  const uint32_t T = static_cast<uint32_t>(p.T);
+  for (; leaders; leaders &= leaders - 1) {
+    const int r = __shfl_sync(0xffffffffu, own, __ffs(leaders) - 1);
+    for (; t < T; t += (1u << p.split) * W) {
+      float a = 0.f, b = 0.f;
+      for (uint32_t s = 0; s < 1u << p.split; ++s) {
+        const uint32_t base = split ? mapa_shared(smem_u32(w4_smem), s) : smem_u32(w4_smem);
+        uint32_t from = __ballot_sync(0xffffffffu, static_cast<int>(ld_cluster_u32(base + W * L::WARP + 4 * lane)) == r);
+        for (; from; from &= from - 1) {
+          const uint32_t e = __ffs(from) - 1;
+          const uint32_t at = base + (e >> 1) * L::WARP + (e & 1u ? 0 : L::DEPTH * L::PLACE) + (t * L::LD + lane) * 4;
+          a += __uint_as_float(ld_cluster_u32(at));
+          if constexpr (GATED) b += __uint_as_float(ld_cluster_u32(at + NT * 8 * L::LD * 4));
+        }
       }
+      const uint32_t half = 2 * (row0 + r) + (lane >> 4);
+      const int n = static_cast<int>((row0 + r) * 32 + lane);
+      if (half >= h0 && half < h1 && n < p.N)
+        w4_output<GATED, BF16>(p, a, b, t, n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
     }
-    const int n = static_cast<int>((row0 + r) * 32 + f);
-    if (whole || n >= p.N) continue;
-    w4_output<GATED, BF16>(p, a, b, t, n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
+    t -= T;
   }
   __syncwarp();
-  if (split > 1) cluster_sync();  // (sums that another CTA reads)
+  if (split) cluster_sync();  // (sums that another CTA reads)
 }
 
 }  // namespace ge
