@@ -42,9 +42,14 @@ ge::W4Params base_params(int64_t batch, int64_t rows, int64_t cols, int64_t grou
   return k;
 }
 
-int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int sms, cudaStream_t stream) {
+// a warp takes a tile, at most 32 CTAs an SM
+int64_t tile_blocks(const ge::W4Params& k, int sms) {
   const int64_t want = (k.tiles + 7) / 8, most = (int64_t)sms * 32;
-  Launch l((int)(want < most ? want : most), 256, 0, false, stream);
+  return want < most ? want : most;
+}
+
+int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int64_t blocks, cudaStream_t stream) {
+  Launch l((int)blocks, 256, 0, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, k);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "4-bit weight launch");
 }
@@ -213,9 +218,12 @@ int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t grou
   k.q = q;
   k.scales = scales;
   k.zeros = zeros;
+  const int64_t blocks = batch * k.rt * ((k.kt + 1) / 2);  // two tiles a CTA
+  if (blocks >= (int64_t)1 << 31)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_quantize: too many tiles for one launch");
   if (dtype == GEMM_EPI_BF16)
-    return run(zeros ? ge::w4_quantize_kernel<true, true> : ge::w4_quantize_kernel<true, false>, k, sms, stream);
-  return run(zeros ? ge::w4_quantize_kernel<false, true> : ge::w4_quantize_kernel<false, false>, k, sms, stream);
+    return run(zeros ? ge::w4_quantize_kernel<true, true> : ge::w4_quantize_kernel<true, false>, k, blocks, stream);
+  return run(zeros ? ge::w4_quantize_kernel<false, true> : ge::w4_quantize_kernel<false, false>, k, blocks, stream);
 }
 
 int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, const uint8_t* codes,
@@ -238,7 +246,7 @@ int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, c
   k.q = q;
   k.scales = scales;
   k.zeros = zeros;
-  return run(ge::w4_pack_kernel, k, sms, stream);
+  return run(ge::w4_pack_kernel, k, tile_blocks(k, sms), stream);
 }
 
 int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype, uint32_t flags,
@@ -261,8 +269,8 @@ int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t gr
   k.out = out;
   const bool f32 = (flags & GEMM_EPI_FLAG_OUT_F32) != 0;
   if (dtype == GEMM_EPI_BF16)
-    return run(f32 ? ge::w4_dequantize_kernel<true, true> : ge::w4_dequantize_kernel<true, false>, k, sms, stream);
-  return run(f32 ? ge::w4_dequantize_kernel<false, true> : ge::w4_dequantize_kernel<false, false>, k, sms, stream);
+    return run(f32 ? ge::w4_dequantize_kernel<true, true> : ge::w4_dequantize_kernel<true, false>, k, tile_blocks(k, sms), stream);
+  return run(f32 ? ge::w4_dequantize_kernel<false, true> : ge::w4_dequantize_kernel<false, false>, k, tile_blocks(k, sms), stream);
 }
 
 gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,

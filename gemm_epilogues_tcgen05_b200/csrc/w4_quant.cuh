@@ -85,76 +85,108 @@ __device__ __forceinline__ float w4_divide(float w, float s, float r) {
   return fmaf(fmaf(-q0, s, w), r, q0);
 }
 
-// Half a warp holds a row of the tile, a lane 8 columns of it, 16 such pairs of
-// rows one after the other, eight loads ahead.
+// the larger (smaller) of two pairs; NaN stays
+template <bool BF16>
+__device__ __forceinline__ uint32_t w4_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t w4_min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A lane has 32 columns of one feature: a whole group or a half or a quarter of one, whose
+// extremes it finds two values at a time, and the 16 bytes of its codes. A warp takes 8
+// features of a tile, a CTA two tiles side by side.
 template <bool BF16, bool ZEROS>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4Params p) {
-  __shared__ __align__(16) uint32_t stage[8][kW4TileBytes / 4];
   wait_for_inputs();
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, u = lane & 15u, ng = 128u / p.group;
-  const int lanes = p.group / 8;  // that share a group: 4, 8 or 16
-  for (int64_t tile = static_cast<int64_t>(blockIdx.x) * 8 + warp; tile < p.tiles; tile += static_cast<int64_t>(gridDim.x) * 8) {
-    const int j = static_cast<int>(tile % p.kt);
-    const int64_t row_tile = tile / p.kt;
-    const int i = static_cast<int>(row_tile % p.rt);
-    const int64_t m = row_tile / p.rt;
-    const int col = j * 128 + 8 * static_cast<int>(u);
-#pragma unroll 1
-    for (int k0 = 0; k0 < 16; k0 += 8) {
-      uint4 in[8];
+  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, b = lane & 3u, f = 8 * (warp & 3u) + (lane >> 2);
+  const uint32_t pairs = (static_cast<uint32_t>(p.kt) + 1) / 2;
+  const uint32_t row_tile = blockIdx.x / pairs, j = 2 * (blockIdx.x - row_tile * pairs) + (warp >> 2);
+  if (j >= static_cast<uint32_t>(p.kt)) return;
+  const uint32_t m = row_tile / static_cast<uint32_t>(p.rt), row = (row_tile - m * p.rt) * kW4Rows + f, col = j * 128 + 32 * b;
+  const int64_t tile = static_cast<int64_t>(row_tile) * p.kt + j;
+  const bool in = row < static_cast<uint32_t>(p.rows) && col < static_cast<uint32_t>(p.cols);
+  uint32_t w[16];
+  {
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(p.src) + (static_cast<int64_t>(m) * p.rows + row) * p.cols + col;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = i * kW4Rows + 2 * (k0 + k) + static_cast<int>(lane >> 4);
-        in[k] = row < p.rows && col < p.cols
-                    ? w4_load_once(reinterpret_cast<const uint16_t*>(p.src) + (m * p.rows + row) * p.cols + col)
-                    : make_uint4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  uint32_t hi2 = 0, lo2 = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t f = 2 * (k0 + k) + (lane >> 4);
-        const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
-        float v[8];
+  for (int e = 0; e < 16; ++e) {
+    hi2 = w4_max2<BF16>(hi2, ZEROS ? w[e] : w[e] & 0x7fff7fffu);
+    if constexpr (ZEROS) lo2 = w4_min2<BF16>(lo2, w[e]);
+  }
+  hi2 = w4_max2<BF16>(hi2, __funnelshift_l(hi2, hi2, 16));
+  lo2 = w4_min2<BF16>(lo2, __funnelshift_l(lo2, lo2, 16));
+  for (int off = 1; off < p.group / 32; off <<= 1) {
+    hi2 = w4_max2<BF16>(hi2, __shfl_xor_sync(0xffffffffu, hi2, off));
+    if constexpr (ZEROS) lo2 = w4_min2<BF16>(lo2, __shfl_xor_sync(0xffffffffu, lo2, off));
+  }
+  const float hi = w4_float<BF16>(static_cast<uint16_t>(hi2)), lo = w4_float<BF16>(static_cast<uint16_t>(lo2));
+  float top = ZEROS ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f);
+  if (!(top <= 3.4e38f)) top = __uint_as_float(0x7fc00000u);  // an infinity or NaN: the group stands for NaN
+  const uint16_t s16 = w4_round16<BF16>(top);
+  const float s = w4_float<BF16>(s16);
+  float zero = 8.f;
+  if constexpr (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;
+  const uint32_t z = static_cast<uint32_t>(zero), z2 = z * 0x00010001u;
+  const auto value = [&](int e, int i) {
+    return w4_float<BF16>(static_cast<uint16_t>(i ? w[e] >> 16 : w[e] & 0xffffu));
+  };
+  uint32_t word[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = w4_float<BF16>(static_cast<uint16_t>(w[e] & 0xffffu));
-          v[2 * e + 1] = w4_float<BF16>(static_cast<uint16_t>(w[e] >> 16));
-        }
-        float lo = 0.f, hi = 0.f;  // (NaN stays: max.NaN, min.NaN)
+  for (int k = 0; k < 4; ++k) word[k] = z * 0x11111111u;
+  if (s >= 1e-30f) {
+    // |w / s| < 32 (an s that was rounded to few bits included), so that the integer is
+    // the low 16 bits of the quotient + 1.5 2^23, whose addition rounds it; two at a time from there
+    const float r = __frcp_rn(s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(ZEROS ? v[e] : fabsf(v[e])));
-          if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(v[e]));
-        }
-        for (int off = 1; off < lanes; off <<= 1) {
-          asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(__shfl_xor_sync(0xffffffffu, hi, off)));
-          if constexpr (ZEROS) asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(__shfl_xor_sync(0xffffffffu, lo, off)));
-        }
-        float top = ZEROS ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f);
-        if (!(top <= 3.4e38f)) top = __uint_as_float(0x7fc00000u);  // an infinity or NaN: the group stands for NaN
-        const uint16_t s16 = w4_round16<BF16>(top);
-        const float s = w4_float<BF16>(s16);
-        float zero = 8.f;
-        if constexpr (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;
-        uint32_t word = 0;
-        const bool tiny = s < 1e-30f;  // the reciprocal would leave fp32
-        const float r = tiny ? 0.f : __frcp_rn(s);
+    for (int k = 0; k < 4; ++k) {
+      word[k] = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float c = zero;
-          if (s > 0.f) c = rintf(tiny ? __fdiv_rn(v[e], s) : w4_divide(v[e], s, r)) + zero;
-          const uint32_t code = static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
-          word |= code << (4 * (e >> 1) + 16 * (e & 1));
-        }
-        const bool in_matrix = i * kW4Rows + static_cast<int>(f) < p.rows && col < p.cols;
-        stage[warp][w4_word(f, u) / 4] = in_matrix ? word : 0u;
-        if ((u & static_cast<uint32_t>(lanes - 1)) == 0) {
-          const int64_t at = (tile * ng + u / lanes) * kW4Rows + f;
-          reinterpret_cast<uint16_t*>(p.scales)[at] = in_matrix ? s16 : 0;
-          if constexpr (ZEROS) p.zeros[at] = in_matrix ? static_cast<uint8_t>(zero) : 0;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int e = 4 * k + i;
+        const uint32_t c0 = __float_as_uint(w4_divide(value(e, 0), s, r) + 12582912.f);
+        const uint32_t c1 = __float_as_uint(w4_divide(value(e, 1), s, r) + 12582912.f);
+        const uint32_t code = __viaddmin_s16x2_relu(__byte_perm(c0, c1, 0x5410), z2, 0x000f000fu);
+        word[k] += code << (4 * i);
       }
     }
-    w4_store_tile(p.q + tile * kW4TileBytes, stage[warp]);
+  } else if (s > 0.f) {  // the reciprocal would leave fp32
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      word[k] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float c = rintf(__fdiv_rn(value(4 * k + i / 2, i & 1), s)) + zero;
+        word[k] |= static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f)) << (4 * (i / 2) + 16 * (i & 1));
+      }
+    }
+  }
+  reinterpret_cast<uint4*>(p.q + tile * kW4TileBytes)[32 * b + f] =
+      in ? make_uint4(word[0], word[1], word[2], word[3]) : make_uint4(0, 0, 0, 0);
+  const uint32_t per = static_cast<uint32_t>(p.group) / 32;  // 1, 2 or 4 lanes
+  if ((b & (per - 1)) == 0) {
+    const int64_t at = (tile * (4 / per) + b / per) * kW4Rows + f;
+    reinterpret_cast<uint16_t*>(p.scales)[at] = in ? s16 : 0;
+    if constexpr (ZEROS) p.zeros[at] = in ? static_cast<uint8_t>(z) : 0;
   }
 }
 
