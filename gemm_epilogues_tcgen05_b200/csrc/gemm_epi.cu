@@ -643,10 +643,10 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->launches = 1;
     info->workspace_bytes = p->partial_bytes + p->split_bytes + sizeof(int) * (size_t)p->n_tickets;
   } else if (p->kind == 4) {
-    info->tile_m = 128;
+    info->tile_m = p->w4.few.threads ? 32 : 128;
     info->tile_n = p->w4.tp;
     info->tile_k = 128;
-    info->stages = 4;
+    info->stages = p->w4.stages;
     info->split_k = p->w4.max_segs;
     info->grid = p->grid;
     info->launches = 1;

@@ -127,10 +127,10 @@ struct GroupedCfg {
 // A plan of few rows times 4-bit weights.
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
-  ge_inst::W4FewInstance few = {};       // at most 16 rows
+  ge_inst::W4FewInstance few = {};       // the kernel of warps alone, if it has threads
   int split = 1;                         // CTAs of its clusters
   uint32_t smem = 0;
-  int threads = 0, tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1;
+  int threads = 0, tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1, stages = 0;
 };
 
 // Row-major matrices of bytes, 16-bit or 32-bit elements: `d2` of them, `d1`

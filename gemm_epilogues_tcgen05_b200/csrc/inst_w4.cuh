@@ -10,7 +10,7 @@ namespace ge_inst {
 template <int TP, bool GATED, int NG, bool BF>
 W4Instance w4_one() {
   using L = ge::W4Smem<TP, NG>;
-  return {ge::w4_kernel<TP, GATED, NG, BF>, L::BYTES, L::THREADS, L::ACC};
+  return {ge::w4_kernel<TP, GATED, NG, BF>, L::BYTES, L::THREADS, L::ACC, L::STAGES};
 }
 
 // tp at most 128 / ng (tensor memory), gated 64 (registers)

@@ -1,5 +1,5 @@
-// inst_w4_few.cuh -- kernel instances of the product of at most 16 rows with 4-bit
-// weights for one type (included by inst_w4_few_*.cu).
+// inst_w4_few.cuh -- kernel instances of the product with 4-bit weights whose warps do
+// all of it alone, for one type (included by inst_w4_few_*.cu).
 #pragma once
 
 #include "kernel_table.h"
@@ -11,7 +11,7 @@ template <int NT, bool GATED, int NG, bool BF>
 W4FewInstance w4_few_one() {
   return {{ge::w4_few_kernel<NT, GATED, NG, false, BF>, ge::w4_few_kernel<NT, GATED, NG, true, BF>},
           {ge::W4Few<NT, GATED ? 2 : 1, NG, false>::BYTES, ge::W4Few<NT, GATED ? 2 : 1, NG, true>::BYTES},
-          32 * ge::kW4FewWarps};
+          32 * ge::kW4FewWarps, ge::W4Few<NT, GATED ? 2 : 1, NG, true>::DEPTH};
 }
 
 template <int NT, bool GATED, bool BF>

@@ -1,4 +1,4 @@
-// inst_w4_few_bf16.cu -- at most 16 bf16 rows times 4-bit weights.
+// inst_w4_few_bf16.cu -- few bf16 rows times 4-bit weights, each warp alone.
 #include "inst_w4_few.cuh"
 
 namespace ge_inst {

@@ -1,4 +1,4 @@
-// inst_w4_few_f16.cu -- at most 16 fp16 rows times 4-bit weights.
+// inst_w4_few_f16.cu -- few fp16 rows times 4-bit weights, each warp alone.
 #include "inst_w4_few.cuh"
 
 namespace ge_inst {

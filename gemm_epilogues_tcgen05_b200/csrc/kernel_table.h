@@ -97,15 +97,15 @@ using W4KernelFn = void (*)(CUtensorMap, ge::W4MulParams);
 struct W4Instance {
   W4KernelFn fn;
   uint32_t smem;
-  int threads, tickets;  // counters a tile
+  int threads, tickets, stages;  // tickets: counters a tile
 };
 using W4FewKernelFn = void (*)(ge::W4MulParams);
 struct W4FewInstance {  // [without, with zeros]
   W4FewKernelFn fn[2];
   uint32_t smem[2];
-  int threads;
+  int threads, stages;
 };
-W4FewInstance w4_few_f16(int rows, bool gated, int ng);  // rows <= 16
+W4FewInstance w4_few_f16(int rows, bool gated, int ng);  // 8 rows of X a CTA, or, for more rows in all, 16
 W4FewInstance w4_few_bf16(int rows, bool gated, int ng);
 W4Instance w4_f16(int tp, bool gated, int ng);
 W4Instance w4_bf16(int tp, bool gated, int ng);

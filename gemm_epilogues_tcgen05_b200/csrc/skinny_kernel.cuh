@@ -255,7 +255,7 @@ struct GatedLane {
 // finished here. Called by the 128 epilogue threads alike.
 template <int GN, bool BF16>
 __device__ __forceinline__ void skinny_gated16(const SkinnyParams& p, float (&g)[16], float (&u)[16], int t0, GatedLane& w) {
-  float none[16];
+  [[maybe_unused]] float none[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     g[j] += GN == 64 && w.half ? w.bias_u : w.bias_g;

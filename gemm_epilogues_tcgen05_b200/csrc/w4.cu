@@ -42,6 +42,9 @@ ge::W4Params base_params(int64_t batch, int64_t rows, int64_t cols, int64_t grou
   return k;
 }
 
+// two tiles side by side a CTA (2^31 of them would be more memory than there is)
+int64_t pair_blocks(const ge::W4Params& k, int64_t batch) { return batch * k.rt * ((k.kt + 1) / 2); }
+
 // a warp takes a tile, at most 32 CTAs an SM
 int64_t tile_blocks(const ge::W4Params& k, int sms) {
   const int64_t want = (k.tiles + 7) / 8, most = (int64_t)sms * 32;
@@ -49,36 +52,104 @@ int64_t tile_blocks(const ge::W4Params& k, int sms) {
 }
 
 int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int64_t blocks, cudaStream_t stream) {
+  if (blocks >= (int64_t)1 << 31) return fail(GEMM_EPI_ERR_INVALID_ARG, "too many tiles for one launch");
   Launch l((int)blocks, 256, 0, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, k);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "4-bit weight launch");
 }
 
-// At most 16 rows: clusters along the features, the CTAs of one along the columns. A
-// warp's tiles are what a launch takes; the join over a cluster costs about what a tile does.
-cudaError_t plan_few(gemm_epi_plan_s* p, bool gated, int64_t group) {
+// The kernel whose warps do everything alone (w4_few.cuh), 16 rows at most a CTA: clusters along
+// the features, the CTAs of one along the columns. What a launch takes goes by
+// the half tiles of a warp; a join over a cluster costs about what four take. False: a
+// plan on tensor memory (w4_kernel.cuh) is the faster one.
+// Rows beyond 16 are another pass over the weight here, and a slower stage there, whose
+// launches take 9 to 16 us before the first of them. bf16, G = 128, us here (there):
+//   half tiles of a warp   2: T = 64, K = N = 1024                4.4 (12.1)
+//                          8: T = 32, K = N = 4096               10.3 (15.9), gated 16.1 (25.5)
+//                         14: T = 64, K = N = 4096               16.6 (18.1), gated 24.8 (28.8)
+//                         20: T = 32, K = 4096, N = 11008        21.2 (19.2), gated 32.1 (33.3)
+//                         30: T = 48, K = 4096, N = 11008        30.8 (22.1), gated 46.9 (38.5)
+// up to 16 rows always: T = 16, K = 4096, N = 11008 14.7 (16.4), gated 21.2 (27.1).
+bool plan_few(gemm_epi_plan_s* p, bool gated, int64_t group, cudaError_t* e) {
+  bool forced = false;
+  if (const char* f = getenv("GEMM_EPI_FORCE_KERNEL")) {  // tuning override
+    if (!strcmp(f, "tmem")) return false;
+    forced = !strcmp(f, "warp");
+  }
+  // (the grid of the other kernel; a stall needs a wait)
+  if (!forced && (getenv("GEMM_EPI_SKINNY_GRID") || p->inject_stall)) return false;
   W4Cfg& c = p->w4;
   c.few = (p->dtype == GEMM_EPI_BF16 ? ge_inst::w4_few_bf16 : ge_inst::w4_few_f16)((int)p->T, gated, (int)(128 / group));
-  for (int z = 0; z < 2; ++z) {
-    const cudaError_t e = cudaFuncSetAttribute(c.few.fn[z], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.few.smem[z]);
-    if (e != cudaSuccess) return e;
-  }
-  const int halves = (int)ceil_div(p->N, 16);  // of rows of tiles
-  int64_t best = INT64_MAX;
+  for (int z = 0; z < 2 && *e == cudaSuccess; ++z)
+    *e = cudaFuncSetAttribute(c.few.fn[z], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.few.smem[z]);
+  if (*e != cudaSuccess) return true;
+  c.stages = c.few.stages;
+  c.tp = p->T <= 8 ? 8 : 16;
+  c.row_blocks = ceil_div(p->T, c.tp);
+  const int halves = ceil_div(p->N, 16);  // of rows of tiles
+  int64_t best = INT64_MAX, steps = 0;
   for (int split = 1; split <= 8 && split <= c.kt; split *= 2) {
-    int clusters = split == 1 ? p->num_sms : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
+    int clusters = split == 1 ? p->num_sms
+                              : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
+    clusters /= c.row_blocks;
+    if (clusters < 1) break;
     if (clusters > halves) clusters = halves;
-    const int rows = (int)ceil_div(halves, clusters);
+    const int rows = ceil_div(halves, clusters);
     if (split > 1 && rows > ge::kW4FewWarps) break;  // (a warp keeps the sums of two rows of tiles)
-    const int64_t cost = ceil_div((int64_t)rows * ceil_div(c.kt, split), ge::kW4FewWarps) + 4 * (split > 1);
+    const int64_t tiles = ((int64_t)rows * ceil_div(c.kt, split) + ge::kW4FewWarps - 1) / ge::kW4FewWarps;
+    const int64_t cost = tiles + 4 * (split > 1);
     if (cost >= best) continue;
     best = cost;
+    steps = tiles;
     c.split = split;
     c.grid = clusters * split;
   }
-  p->grid = c.grid;
+  if (p->T > 16 && !forced && steps > 20) {
+    c.few = {};
+    c.split = 1;
+    return false;
+  }
+  p->grid = c.grid * c.row_blocks;
   c.max_segs = c.split;
-  return cudaSuccess;
+  return true;
+}
+
+// The kernel of many warps' roles (w4_kernel.cuh).
+cudaError_t plan_tmem(gemm_epi_plan_s* p, bool gated, int64_t group) {
+  W4Cfg& c = p->w4;
+  const int most = gated && group == 128 ? 64 : (int)group;  // rows of an instance
+  c.tp = p->T <= 16 ? 16 : p->T <= 32 ? 32 : p->T <= 64 ? 64 : 128;
+  if (c.tp > most) c.tp = most;
+  c.row_blocks = ceil_div(p->T, c.tp);
+  const ge_inst::W4Instance inst = (p->dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16 : ge_inst::w4_f16)(c.tp, gated, (int)(128 / group));
+  c.fn = inst.fn;
+  c.smem = inst.smem;
+  c.threads = inst.threads;
+  c.stages = inst.stages;
+  // equal shares of all blocks of 128 columns, at least two each
+  const int total = c.tiles * c.kt, share = p->num_sms / c.row_blocks;
+  c.grid = total / 2 < 1 ? 1 : total / 2 < share ? total / 2 : share;
+  if (const char* f = getenv("GEMM_EPI_SKINNY_GRID")) {  // tuning override
+    const int v = atoi(f);
+    if (v >= 1 && v <= total && v <= share) c.grid = v;
+  }
+  p->grid = c.grid * c.row_blocks;
+  for (int t = 0; t < c.tiles; ++t) {
+    const int64_t first = ge::skinny_owner((int64_t)t * c.kt, c.grid, total);
+    const int64_t last = ge::skinny_owner((int64_t)(t + 1) * c.kt - 1, c.grid, total);
+    if (last - first + 1 > c.max_segs) c.max_segs = (int)(last - first + 1);
+  }
+  cudaError_t e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
+  if (e == cudaSuccess && c.max_segs > 1) {
+    const size_t blocks = (size_t)c.row_blocks * (size_t)c.tiles, items = blocks * (size_t)inst.tickets;
+    p->sk_bytes = blocks * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
+    e = cudaMalloc((void**)&p->sk_partials, p->sk_bytes);
+    if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * items);
+    if (e == cudaSuccess) e = zero_counts(p->sk_tickets, items);
+    p->split_items = (int)items;
+    p->sk_bytes += sizeof(int) * items;
+  }
+  return e;
 }
 
 gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,
@@ -132,41 +203,7 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_e
   c.tiles = (int)tiles;
   c.kt = (int)kt;
   cudaError_t e = cudaSuccess;
-  if (T <= 16) {
-    e = plan_few(p, gated, group);
-  } else {
-  const int most = gated && group == 128 ? 64 : (int)group;  // rows of an instance
-  c.tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  if (c.tp > most) c.tp = most;
-  c.row_blocks = ceil_div(T, c.tp);
-  const ge_inst::W4Instance inst = (dtype == GEMM_EPI_BF16 ? ge_inst::w4_bf16 : ge_inst::w4_f16)(c.tp, gated, (int)(128 / group));
-  c.fn = inst.fn;
-  c.smem = inst.smem;
-  c.threads = inst.threads;
-  // equal shares of all blocks of 128 columns, at least two each
-  const int total = c.tiles * c.kt, share = sms / c.row_blocks;
-  c.grid = total / 2 < 1 ? 1 : total / 2 < share ? total / 2 : share;
-  if (const char* f = getenv("GEMM_EPI_SKINNY_GRID")) {  // tuning override
-    const int v = atoi(f);
-    if (v >= 1 && v <= total && v <= share) c.grid = v;
-  }
-  p->grid = c.grid * c.row_blocks;
-  for (int t = 0; t < c.tiles; ++t) {
-    const int64_t first = ge::skinny_owner((int64_t)t * c.kt, c.grid, total);
-    const int64_t last = ge::skinny_owner((int64_t)(t + 1) * c.kt - 1, c.grid, total);
-    if (last - first + 1 > c.max_segs) c.max_segs = (int)(last - first + 1);
-  }
-  e = cudaFuncSetAttribute(c.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
-  if (e == cudaSuccess && c.max_segs > 1) {
-    const size_t blocks = (size_t)c.row_blocks * (size_t)c.tiles, items = blocks * (size_t)inst.tickets;
-    p->sk_bytes = blocks * (size_t)c.max_segs * (gated ? 2 : 1) * (size_t)c.tp * 128 * sizeof(float);
-    e = cudaMalloc((void**)&p->sk_partials, p->sk_bytes);
-    if (e == cudaSuccess) e = cudaMalloc((void**)&p->sk_tickets, sizeof(int) * items);
-    if (e == cudaSuccess) e = zero_counts(p->sk_tickets, items);
-    p->split_items = (int)items;
-    p->sk_bytes += sizeof(int) * items;
-  }
-  }
+  if (!plan_few(p, gated, group, &e)) e = plan_tmem(p, gated, group);
   if (e == cudaSuccess) e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
   if (e == cudaSuccess) {
     *p->status_host = 0;
@@ -218,9 +255,7 @@ int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t grou
   k.q = q;
   k.scales = scales;
   k.zeros = zeros;
-  const int64_t blocks = batch * k.rt * ((k.kt + 1) / 2);  // two tiles a CTA
-  if (blocks >= (int64_t)1 << 31)
-    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_w4_quantize: too many tiles for one launch");
+  const int64_t blocks = pair_blocks(k, batch);
   if (dtype == GEMM_EPI_BF16)
     return run(zeros ? ge::w4_quantize_kernel<true, true> : ge::w4_quantize_kernel<true, false>, k, blocks, stream);
   return run(zeros ? ge::w4_quantize_kernel<false, true> : ge::w4_quantize_kernel<false, false>, k, blocks, stream);
@@ -269,8 +304,8 @@ int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t cols, int64_t gr
   k.out = out;
   const bool f32 = (flags & GEMM_EPI_FLAG_OUT_F32) != 0;
   if (dtype == GEMM_EPI_BF16)
-    return run(f32 ? ge::w4_dequantize_kernel<true, true> : ge::w4_dequantize_kernel<true, false>, k, tile_blocks(k, sms), stream);
-  return run(f32 ? ge::w4_dequantize_kernel<false, true> : ge::w4_dequantize_kernel<false, false>, k, tile_blocks(k, sms), stream);
+    return run(f32 ? ge::w4_dequantize_kernel<true, true> : ge::w4_dequantize_kernel<true, false>, k, pair_blocks(k, batch), stream);
+  return run(f32 ? ge::w4_dequantize_kernel<false, true> : ge::w4_dequantize_kernel<false, false>, k, pair_blocks(k, batch), stream);
 }
 
 gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype, int epilog,
@@ -328,7 +363,7 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
     k.kt_quot = (uint32_t)(c.kt / c.split);
     k.kt_rest = (uint32_t)(c.kt % c.split);
     k.X = X;
-    Launch l(c.grid, c.few.threads, c.few.smem[zeros != nullptr], c.split > 1, stream);
+    Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.few.threads, c.few.smem[zeros != nullptr], c.split > 1, stream);
     l.attr[1].val.clusterDim.x = (unsigned)c.split;
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.few.fn[zeros != nullptr], k);
     return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");

@@ -34,7 +34,7 @@ struct W4Few {
   static constexpr int LD = 36;                                 // floats between a sum's rows: no two lanes in a bank
   static constexpr uint32_t SUMS = MATS * NT * 8 * LD * 4;      // of a warp and a row of tiles
   static constexpr int ROOM = (232448 / kW4FewWarps - 8 - SUMS) / PLACE;
-  static constexpr int DEPTH = ROOM < 6 ? ROOM : 6;             // places of a warp's ring
+  static constexpr int DEPTH = ROOM < 3 ? ROOM : 3;             // places of a warp's ring
   static constexpr uint32_t WARP = DEPTH * PLACE + SUMS;        // its last row's sums take the ring's place
   static constexpr uint32_t BYTES = kW4FewWarps * (WARP + 8);
   static_assert(DEPTH >= 2 && SUMS <= DEPTH * PLACE && PLACE % 16 == 0 && SUMS % 16 == 0, "ring");
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   const uint32_t kb0 = w4_share(rank, p.kt_quot, p.kt_rest), nkb = w4_share(rank + 1, p.kt_quot, p.kt_rest) - kb0;
   const W4Runs runs(h0, h1, nkb);
   const uint32_t row0 = runs.row0, u0 = runs.begin(warp), u1 = runs.begin(warp + 1);
+  const int t0 = static_cast<int>(blockIdx.y) * (8 * NT), T = min(p.T - t0, 8 * NT);  // this CTA's rows of X
   uint8_t* ring = w4_smem + warp * L::WARP;
   // the rows of tiles whose sums a warp keeps: the first, the last
   int* kept = reinterpret_cast<int*>(w4_smem + kW4FewWarps * L::WARP);
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   };
   const auto bias_of = [&](uint32_t n) { return p.bias ? load_bias<BF16>(p.bias, p.bias_f32, n) : 0.f; };
 
-  const uint4* X = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) + static_cast<int64_t>(g) * p.K + c * 8);
+  const uint4* X = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) + (static_cast<int64_t>(t0) + g) * p.K + c * 8);
   const int64_t x_step = p.K;  // 8 rows, in units of 8 columns
   // a tile's products, of its halves from .. to - 1
   const auto multiply = [&](const uint8_t* place, const uint4 (&x)[4][NT], auto from, auto to) {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
       const int left = p.K - static_cast<int>(kb0 + kb) * 128;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int blocks = t * 8 + static_cast<int>(g) < p.T ? left : 0;
+        const int blocks = t * 8 + static_cast<int>(g) < T ? left : 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) x[b][t] = b * 32 < blocks ? __ldg(xk + t * x_step + b * 4) : make_uint4(0, 0, 0, 0);
       }
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              if (t * 8 + static_cast<int>(2 * c) + i < p.T)
-                w4_output<GATED, BF16>(p, acc[0][t][h][e + i], acc[MATS - 1][t][h][e + i], t * 8 + 2 * c + i, n, bias_a, bias_b);
+              if (t * 8 + static_cast<int>(2 * c) + i < T)
+                w4_output<GATED, BF16>(p, acc[0][t][h][e + i], acc[MATS - 1][t][h][e + i], t0 + t * 8 + 2 * c + i, n, bias_a, bias_b);
         }
     } else {
       const bool last = u + 1 == u1;
@@ -272,10 +273,9 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
   const uint32_t same = __match_any_sync(0xffffffffu, own);
   uint32_t leaders = __ballot_sync(0xffffffffu, own >= 0 && (same & ((1u << lane) - 1u)) == 0);
   uint32_t t = (rank << 4) + warp;  // (16 warps)
-  const uint32_t T = static_cast<uint32_t>(p.T);
   for (; leaders; leaders &= leaders - 1) {
     const int r = __shfl_sync(0xffffffffu, own, __ffs(leaders) - 1);
-    for (; t < T; t += (1u << p.split) * W) {
+    for (; t < static_cast<uint32_t>(T); t += (1u << p.split) * W) {
       float a = 0.f, b = 0.f;
       for (uint32_t s = 0; s < 1u << p.split; ++s) {
         const uint32_t base = split ? mapa_shared(smem_u32(w4_smem), s) : smem_u32(w4_smem);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
       const uint32_t half = 2 * (row0 + r) + (lane >> 4);
       const int n = static_cast<int>((row0 + r) * 32 + lane);
       if (half >= h0 && half < h1 && n < p.N)
-        w4_output<GATED, BF16>(p, a, b, t, n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
+        w4_output<GATED, BF16>(p, a, b, t0 + t, n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
     }
     t -= T;
   }

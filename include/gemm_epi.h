@@ -44,7 +44,7 @@
  *                                 A wait that spans many tiles counts from the
  *                                 last progress, so a launch may last longer
  *   tuning overrides of the plan's choices, for measurement and tests:
- *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny, GEMM_EPI_FORCE_BN=64|128|192|256,
+ *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny (4-bit weights: warp|tmem), GEMM_EPI_FORCE_BN=64|128|192|256,
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
  *   GEMM_EPI_SKINNY_PREFETCH, GEMM_EPI_TAIL_SPLIT=0|1, GEMM_EPI_CACHE_HINTS=0|1,
  *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped and microscaled plans),
@@ -126,7 +126,8 @@ typedef struct {
                           stream-K), 2 = tile kernel on CTA pairs (256-row tiles); grouped
                           plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
                           (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs);
-                          4-bit weights: 8. For 3 to 8 tile_m counts features and tile_n rows */
+                          4-bit weights: 8 (tile_m 32: each warp alone, 128: through tensor
+                          memory). For 3 to 8 tile_m counts features and tile_n rows */
   int tile_m, tile_n, tile_k, stages;  /* a gated layer's tiles count gate and up features alike */
   int split_k;         /* K slices per output tile (1 = none). Grouped plans: for experts of the mean
                           number of rows; a call that finds others may share a tile among fewer or

@@ -213,6 +213,58 @@ def test_products_of_any_scales(T, N, K, G, zeros):
         within(Y, a * up, (1 + u) * bound + (u + 2 * E) * (a * up).abs() + TINY[Y.dtype], "gated " + name)
 
 
+@pytest.mark.parametrize("T,N,K,G", CASES)
+@pytest.mark.parametrize("kernel", ["warp", "tmem"])
+def test_products_on_either_kernel(kernel, T, N, K, G, monkeypatch):
+    monkeypatch.setenv("GEMM_EPI_FORCE_KERNEL", kernel)
+    with W4Plan(T, N, K, torch.bfloat16, "NONE", group=G) as p:
+        assert p.info()["tile_m"] == {"warp": 32, "tmem": 128}[kernel]
+    for zeros in (False, True):
+        test_products_exact(T, N, K, G, zeros)
+        test_products_of_any_scales(T, N, K, G, zeros)
+
+
+@pytest.mark.parametrize("N", [8, 16, 24, 2368, 2376, 4752, 4744, 7112, 16 * 16 * 148 + 8])
+@pytest.mark.parametrize("T", [1, 9, 37])
+def test_shares_of_half_tiles(N, T, monkeypatch):
+    """Half rows of tiles, one to sixteen and more a CTA, of one to five columns of tiles."""
+    monkeypatch.setenv("GEMM_EPI_FORCE_KERNEL", "warp")
+    dt = torch.float16
+    for K in (32, 384, 640):
+        codes, s, z = weights(N, K, 32, dt, N + K, True, True, 2)
+        w4 = w4_pack(rowmajor(codes), s, z)
+        X = ints((T, K), 3, gen(T), dt)
+        y = X.double() @ values(codes, s, z, 32).reshape(-1, K).t()
+        with W4Plan(T, N, K, dt, "GATED", group=32, act="RELU", out_f32=True) as p:
+            Y = p.forward(X, *w4)
+            assert torch.equal(Y, p.forward(X, *w4))
+        r = y[:, :N].clamp(min=0) * y[:, N:]
+        within(Y, r, 2 * E * r.abs(), "gated")  # one fp32 product of exact sums
+        with W4Plan(T, N, K, dt, "NONE", group=32, out_f32=True) as p:
+            Y = p.forward(X, *w4_pack(rowmajor(codes[0].contiguous()), s[0].contiguous(), z[0].contiguous()))
+        assert torch.equal(Y.double(), y[:, :N])
+
+
+@pytest.mark.parametrize("kernel", ["warp", "tmem"])
+@pytest.mark.parametrize("T,N,K", [(1, 8, 32768), (8, 48, 16384), (13, 80, 16384), (30, 16, 24576)])
+def test_columns_shared_by_clusters(T, N, K, kernel, monkeypatch):
+    monkeypatch.setenv("GEMM_EPI_FORCE_KERNEL", kernel)
+    dt = torch.bfloat16
+    codes, s, z = weights(N, K, 128, dt, T, True, True, 2)
+    w4 = w4_pack(rowmajor(codes), s, z)
+    X = ints((T, K), 2, gen(T), dt)
+    y = X.double() @ values(codes, s, z, 128).reshape(-1, K).t()
+    with W4Plan(T, N, K, dt, "GATED", group=128, act="RELU", out_f32=True) as p:
+        assert p.info()["split_k"] > 1
+        Y = p.forward(X, *w4)
+        assert torch.equal(Y, p.forward(X, *w4))
+    r = y[:, :N].clamp(min=0) * y[:, N:]
+    within(Y, r, 2 * E * r.abs(), "gated")  # one fp32 product of exact sums
+    with W4Plan(T, N, K, dt, "NONE", group=128, out_f32=True) as p:
+        Y = p.forward(X, *w4_pack(rowmajor(codes[0].contiguous()), s[0].contiguous(), z[0].contiguous()))
+    assert torch.equal(Y.double(), y[:, :N])
+
+
 def test_wide_weight_and_many_tiles():
     """A vocabulary's worth of features, few columns: many tiles a CTA."""
     T, N, K, G = 2, 50000, 128, 128
