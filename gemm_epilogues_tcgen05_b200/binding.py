@@ -683,7 +683,11 @@ def _w4_args(values, name, q, scales, zeros, group, dtype, cols):
     if not values.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     index, batch, N, K = values.get_device(), 1 if values.dim() == 2 else values.shape[0], values.shape[-2], cols(values.shape)
-    nq, ns = lib().gemm_epi_w4_bytes(batch, N, K, group), lib().gemm_epi_w4_scales(batch, N, K, group)
+    if group in (32, 64, 128):  # (the sizes here: two calls of the library less; it checks the shape)
+        tiles = batch * ((N + 31) // 32) * ((K + 127) // 128)
+        nq, ns = 2048 * tiles, 32 * (128 // group) * tiles
+    else:
+        nq, ns = lib().gemm_epi_w4_bytes(batch, N, K, group), -1
     if nq < 0 or ns < 0:
         raise GemmEpiError(ERR_INVALID_ARG, gemm_epi_last_error())
     return (index, batch, N, K, _ptr_on(index, values, values.shape, values.dtype, name),

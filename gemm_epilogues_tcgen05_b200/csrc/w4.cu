@@ -92,8 +92,8 @@ bool plan_few(gemm_epi_plan_s* p, bool gated, int64_t group, cudaError_t* e) {
     int clusters = split == 1 ? p->num_sms
                               : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
     clusters /= c.row_blocks;
-    if (clusters < 1) break;
     if (clusters > halves) clusters = halves;
+    if (clusters < 1) clusters = 1;  // (fewer SMs than blocks of rows: they take turns)
     const int rows = ceil_div(halves, clusters);
     if (split > 1 && rows > ge::kW4FewWarps) break;  // (a warp keeps the sums of two rows of tiles)
     const int64_t tiles = ((int64_t)rows * ceil_div(c.kt, split) + ge::kW4FewWarps - 1) / ge::kW4FewWarps;
@@ -127,7 +127,7 @@ cudaError_t plan_tmem(gemm_epi_plan_s* p, bool gated, int64_t group) {
   c.threads = inst.threads;
   c.stages = inst.stages;
   // equal shares of all blocks of 128 columns, at least two each
-  const int total = c.tiles * c.kt, share = p->num_sms / c.row_blocks;
+  const int total = c.tiles * c.kt, share = p->num_sms > c.row_blocks ? p->num_sms / c.row_blocks : 1;
   c.grid = total / 2 < 1 ? 1 : total / 2 < share ? total / 2 : share;
   if (const char* f = getenv("GEMM_EPI_SKINNY_GRID")) {  // tuning override
     const int v = atoi(f);

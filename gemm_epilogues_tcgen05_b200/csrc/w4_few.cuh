@@ -1,23 +1,34 @@
-// w4_few.cuh -- at most 16 rows times a weight held in 4 bits (layout: w4_quant.cuh).
+// w4_few.cuh -- few rows times a weight held in 4 bits (layout: w4_quant.cuh), each warp
+// alone: Y[t][n] = epilog(sum_k X[t][k] s_g (q[n][k] - z_g)), and as a gated layer.
 //
-// With so few rows the product is a pass over the codes, and what costs is the way to
-// them: the kernel of more rows (w4_kernel.cuh) hands a block on between four kinds of
-// warps. Here every warp does all of it alone: it streams its own tiles of 32 features
-// x 128 columns through its own ring in shared memory (bulk copies, one barrier a
-// place), so that an SM has up to 200 KB under way from the first cycle, unpacks them into the
-// operands of mma.sync m16n8k16 (the features are its rows, the rows of X its eight
-// columns), and scales a group's sums in fp32. Tensor memory has no part in it:
-// 27 cycles a quarter SM for each of these MMAs are less than the stages cost there.
+// With few rows the product is a pass over the codes. The kernel through tensor
+// memory (w4_kernel.cuh) hands a block of columns on between four kinds of warps, 500 ns each time
+// and 9 us before the first. Here every warp does all of it: it streams its own
+// tiles of 32 features x 128 columns through its own ring in shared memory (cp.async,
+// no barrier), unpacks them into the operands of mma.sync m16n8k16 (the
+// features are its rows, the rows of X its eight columns), and scales a group's fp32
+// sums. No weight is rounded anywhere.
 //
 // A word of the layout holds eight columns of one feature, and a lane takes the words of its
 // features g, g + 8, ... and of the 8-column unit c (lane = 4 g + c): the order of the columns
 // inside an MMA is free as long as X has the same one, and X's eight columns of a unit are
 // 16 bytes of a row.
 //
-// Work split: clusters take runs of 32-feature rows of tiles, the CTAs of a cluster
-// parts of the columns, and a CTA's warps equal runs of its tiles, row after row. A
-// row's sums meet once, at the end, in shared memory (distributed over the cluster), in
-// a fixed order; no workspace.
+// Work split: clusters take runs of half rows of tiles (16 features), the CTAs of a
+// cluster parts of the columns (only where a launch would have few CTAs: a cluster costs 2
+// us), and a CTA's warps equal runs of its tiles, row after row. A row's sums meet once, at
+// the end, in shared memory (distributed over the cluster), in a fixed order; no workspace.
+// More rows of X than 16 (gridDim.y) are other CTAs', each 16 of them a pass over the codes.
+//
+// What bounds it is unpacking: seven instructions of half rate and four subtractions
+// for eight bf16 weights (fp16: five and four); the MMAs take 2 cycles a quarter SM. N = 128000, K =
+// 4096, T = 1, G = 128: 60.6 us, 4.4 TB/s, the ALU 61 % busy (with (w >> 4m & mask) | one
+// left to the compiler, two instructions each, 73 us; shifts as multiplications, on the
+// other pipe, 74). Small ones are bound by latency: K = 1024, N = 2048 3.5 us; K = 4096, N = 11008
+// (22.5 MB, 3.6 us at the rate of a copy) 9.8, T = 8 10.8, T = 16 14.7, gated 14.5, 16.8, 21.2; shares of
+// whole rows of tiles instead of half ones 10.7, 12.5, 16.6, gated 15.6, 17.9, 24.3. From
+// 9 rows on X comes from L2 again and again, and the less shared memory the ring takes the
+// more of it stays in L1: 3 places a warp 9.8 / 10.8 / 14.7 us for T = 1 / 8 / 16, 6 10.5 / 12.3 / 15.4.
 #pragma once
 
 #include "w4_kernel.cuh"

@@ -1,6 +1,7 @@
-// w4_kernel.cuh -- few rows times a weight held in 4 bits with group scales (layout:
-// w4_quant.cuh): Y[t][n] = epilog(sum_k X[t][k] s_g (q[n][k] - z_g)), and as a gated
-// layer (two matrices).
+// w4_kernel.cuh -- rows times a weight held in 4 bits with group scales (layout:
+// w4_quant.cuh), through tensor memory: Y[t][n] = epilog(sum_k X[t][k] s_g (q[n][k] - z_g)), and
+// as a gated layer (two matrices). For many rows and large weights; what w4_few.cuh is
+// for is measured at the plan.
 //
 // Swap-AB, as the few-row kernel: 128 features in the MMA's M slot, the rows of X,
 // padded to TP, in its N slot. The weight's operand comes from tensor memory: a
@@ -10,10 +11,9 @@
 // no unpacked weight passes through shared memory. One MMA chain per group
 // of G columns leaves the group's sums (fp32) in one of several accumulators, and
 // accumulating warps add them, times the scale of their lane's feature, to sums in registers:
-// no weight is rounded anywhere.
-// (The same on mma.sync fragments took 11.4 us for T = 1, K = 4096, N = 11008 and
-// 52 us for T = 64: its MMAs run at about a sixteenth of tcgen05's rate here, 27 cycles a
-// quarter SM for 16 x 8 x 16.)
+// no weight is rounded anywhere. K = 4096, N = 11008, G = 128: T = 64 22.7 us, T = 128 31.1,
+// gated 39.4 and 58.2 (the codes alone 3.6 and 7.1 us); a product of the unpacked 16-bit weight reads
+// 90 MB, 13.8 us, and the gated layer of it takes 35 us at T = 64.
 //
 // Warp roles:
 //   first 16 or 8: dequantise: lane quarter warp % 4, every fourth (second) stage of

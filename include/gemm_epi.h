@@ -560,6 +560,8 @@ GEMM_EPI_API int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t col
  * Y's; flags GEMM_EPI_FLAG_OUT_F32 or 0. Products are exact in fp32 before they are
  * summed: code - zero is a small integer, a group's sum is scaled in fp32. A plan keeps no
  * weight: one serves all layers of its shape.
+ * Beyond some 16 rows of a large weight (K N above 4096 x 4096) a row costs about what it
+ * costs with 16-bit weights; for more than 256, dequantise.
  */
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype,
                                               int epilog, gemm_epi_act act, uint32_t flags);
