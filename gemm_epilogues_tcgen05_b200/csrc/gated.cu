@@ -1,5 +1,6 @@
 // gated.cu -- C ABI of gated layers: plan validation and kernel choice, TMA
 // descriptors, launches.
+#include "gated_few.cuh"
 #include "host_tiles.h"
 #include "skinny_kernel.cuh"
 
@@ -95,12 +96,72 @@ void release(gemm_epi_plan_s* p) {
   delete p;
 }
 
+// Features of H of a few-row tile (128 where that makes as many tiles as half the SMs), and
+// whether the kernel takes whole tiles.
+int few_row_features(int64_t N, int sms) { return 2 * ceil_div(N, 128) >= sms ? 128 : 64; }
+bool whole_tiles(int64_t N, int sms) {
+  const int tiles = ceil_div(N, few_row_features(N, sms));
+  return tiles * 2 >= sms && tiles <= sms;
+}
+
+// The kernel whose warps work alone, for at most 16 rows of a small weight: it starts 2
+// to 3 us sooner, and streams at half the rate of TMA's. N x K, us, T = 1 (few-row kernel: T = 1):
+//   half tiles of a warp   2: K = 1024, N = 2048 4.6 (6.6)     4: K = N = 2048 7.7 (10.1)
+//                          8: K = 2048, N = 4096 10.4 (11.7), T = 16 11.6 (12.1); K = 4096, N = 2048 12.0 (12.2)
+//                         12: K = N = 3000 13.0 (12.7)         20: K = 4096, N = 11008 38.1 (31.8)
+// where the few-row kernel has whole tiles 6: K = 1024, N = 5632 8.8 (7.9), 12: K = 2048 13.9 (11.3).
+bool plan_few(gemm_epi_plan_s* p, bool bf16, cudaError_t* e) {
+  if (p->T > 16) return false;
+  bool forced = false;
+  if (const char* f = getenv("GEMM_EPI_FORCE_KERNEL")) {  // tuning override
+    forced = !strcmp(f, "warp");
+    if (!strcmp(f, "skinny")) return false;
+  }
+  const int kt = ceil_div(p->K, 32);
+  if ((p->N / 16 + 1) * (int64_t)kt >= (int64_t)1 << 28) return false;  // (32-bit shares)
+  // (the grid of the other kernel; a stall needs a wait)
+  if (!forced && (getenv("GEMM_EPI_SKINNY_GRID") || p->inject_stall)) return false;
+  const ge_inst::GatedFewInstance inst = ge_inst::gated_few(bf16, p->w_nk != 0, (int)p->T);
+  *e = cudaFuncSetAttribute(inst.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)inst.smem);
+  if (*e != cudaSuccess) return true;
+  const FewChoice choice = choose_few((const void*)inst.fn, 32 * ge::kFewWarps, inst.smem, p->N, kt, p->num_sms, 1, 3);
+  // (whole tiles are what the other kernel is best at)
+  const int64_t most = whole_tiles(p->N, p->num_sms) ? 4 : 8;
+  if (!forced && (choice.split > 0 || choice.steps > most)) return false;
+  p->gf.fn = inst.fn;
+  p->gf.smem = inst.smem;
+  p->gf.grid = choice.clusters << choice.split;
+  p->gf.few = few_split(choice, p->N, kt);
+  p->kernel = 1;
+  return true;
+}
+
+int run_few(gemm_epi_plan_s* p, const void* X, const void* W, const void* bias, void* H, void* aux, cudaStream_t stream) {
+  ge::GatedFewParams k{};
+  k.T = (int32_t)p->T;
+  k.N = (int32_t)p->N;
+  k.K = (int32_t)p->K;
+  k.act = p->act;
+  k.bias_f32 = p->bias_f32;
+  k.out_f32 = p->out_f32;
+  k.few = p->gf.few;
+  k.X = X;
+  k.W = W;
+  k.bias = bias;
+  k.out = H;
+  k.aux_out = aux;
+  Launch l(p->gf.grid, 32 * ge::kFewWarps, p->gf.smem, k.few.split > 0, stream);
+  l.attr[1].val.clusterDim.x = 1u << k.few.split;
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, p->gf.fn, k);
+  return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "gated few-row launch");
+}
+
 // The few-row kernel's schedule: whole tiles where there are between half as many
 // as SMs and as many -- of 128 features of H if there are that many, else of 64 -- and
 // otherwise equal shares of all k-blocks, at least 256 k each.
 cudaError_t plan_skinny(gemm_epi_plan_s* p, bool bf16, int sms) {
   const int tp = p->T <= 16 ? 16 : 32;
-  const int gn = 2 * ceil_div(p->N, 128) >= sms ? 128 : 64;
+  const int gn = few_row_features(p->N, sms);
   const ge_inst::GatedSkinnyInstance inst = skinny_instance(bf16, p->w_nk != 0, tp, gn);
   p->kernel = 1;
   p->sk.TP = tp;
@@ -112,7 +173,7 @@ cudaError_t plan_skinny(gemm_epi_plan_s* p, bool bf16, int sms) {
   const int n_tiles = ceil_div(p->N, gn);
   p->sk_kbt = ceil_div(p->K, (int64_t)ge::kBK * 2);
   p->sk_total = n_tiles * p->sk_kbt;
-  if (n_tiles * 2 >= sms && n_tiles <= sms) {
+  if (whole_tiles(p->N, sms)) {
     p->sk_grid = n_tiles;
   } else {
     const int g = p->sk_total / 2;
@@ -223,8 +284,11 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
   p->timeout_ns = wd.timeout_ns;
   p->inject_stall = wd.inject_stall;
   const bool forward = epilog != GEMM_EPI_DGATED, bf16 = dtype == GEMM_EPI_BF16;
-  cudaError_t e = forward && use_skinny(T) && skinny_fits(2 * N, K, sms) ? plan_skinny(p, bf16, sms)
-                                                                        : plan_tiles(p, bf16, forward, sms);
+  cudaError_t e = cudaSuccess;
+  if (!forward || !use_skinny(T))
+    e = plan_tiles(p, bf16, forward, sms);
+  else if (!plan_few(p, bf16, &e))
+    e = skinny_fits(2 * N, K, sms) ? plan_skinny(p, bf16, sms) : plan_tiles(p, bf16, forward, sms);
   if (e == cudaSuccess) e = cudaHostAlloc((void**)&p->status_host, sizeof(int), cudaHostAllocMapped);
   if (e == cudaSuccess) {
     *p->status_host = 0;
@@ -335,6 +399,7 @@ int gemm_epi_gated_execute(gemm_epi_plan_t plan, const void* X, const void* W, c
   DeviceScope scope(p->device);
   rc = begin_call(p, stream);
   if (rc) return rc;
+  if (p->gf.fn) return run_few(p, X, W, bias, H, aux, stream);
   if (p->kernel == 1) return run_skinny(p, X, W, bias, H, aux, stream);
   CUtensorMap a, b, y, z;
   rc = encode_2d(&a, X, (uint64_t)p->K, (uint64_t)p->T, ge::kBK, ge::kBM, "the row operand");

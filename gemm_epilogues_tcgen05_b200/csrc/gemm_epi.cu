@@ -651,6 +651,15 @@ int gemm_epi_query(gemm_epi_plan_t plan, gemm_epi_info* info) {
     info->grid = p->grid;
     info->launches = 1;
     info->workspace_bytes = p->sk_bytes;
+  } else if (p->gf.fn) {
+    info->tile_m = 32;
+    info->tile_n = p->T <= 8 ? 8 : 16;
+    info->tile_k = 32;
+    info->stages = 2;
+    info->split_k = 1 << p->gf.few.split;
+    info->grid = p->gf.grid;
+    info->launches = 1;
+    info->workspace_bytes = 0;
   } else if (p->kernel == 1) {
     info->tile_m = 128;  // features per tile (the MMA's M)
     info->tile_n = p->sk.TP;  // padded rows (the MMA's N)

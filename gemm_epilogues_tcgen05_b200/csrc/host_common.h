@@ -16,6 +16,7 @@
 #include <unordered_set>
 
 #include "../../include/gemm_epi.h"
+#include "few_rows.cuh"
 #include "kernel_table.h"
 
 namespace ge_host {
@@ -125,10 +126,18 @@ struct GroupedCfg {
 };
 
 // A plan of few rows times 4-bit weights.
+// A gated layer's kernel whose warps work alone, if there is a function.
+struct GatedFewCfg {
+  ge_inst::GatedFewKernelFn fn = nullptr;
+  uint32_t smem = 0;
+  int grid = 0;
+  ge::FewSplit few = {};
+};
+
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
   ge_inst::W4FewInstance few = {};       // the kernel of warps alone, if it has threads
-  int split = 1;                         // CTAs of its clusters
+  ge::FewSplit few_split = {};
   uint32_t smem = 0;
   int threads = 0, tp = 0, row_blocks = 1, tiles = 0, kt = 0, grid = 0, max_segs = 1, stages = 0;
 };
@@ -293,6 +302,7 @@ struct gemm_epi_plan_s {
   int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
   int out_f32 = 0;       // GEMM_EPI_FLAG_OUT_F32: Y / dZ / dW written as fp32
   int act = 0;           // kind 3, 4: gemm_epi_act
+  ge_host::GatedFewCfg gf;  // kind 3
   ge_host::W4Cfg w4;     // kind 4
   int cache_hints = 0;   // few-row kernel: L2 eviction policies on the operand loads (GEMM_EPI_CACHE_HINTS)
   // tensor-map cache

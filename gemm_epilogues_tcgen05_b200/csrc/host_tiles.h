@@ -126,4 +126,36 @@ inline Raster choose_raster(int64_t T, int64_t N, int64_t K, int tile_rows, int 
   return r;
 }
 
+// Clusters and CTAs of a kernel whose warps work alone (few_rows.cuh): `clusters` along
+// the half rows of tiles, 2^split CTAs of each along the kt columns of tiles, at most
+// `share` CTAs. What a launch takes goes by the half tiles of a warp (steps); a join over a
+// cluster costs as much as `join` of them. No split where a warp would have more than two rows' sums.
+struct FewChoice {
+  int split = 0, clusters = 0;
+  int64_t steps = 0;
+};
+inline FewChoice choose_few(const void* fn, int threads, uint32_t smem, int64_t N, int kt, int sms, int row_blocks, int join) {
+  FewChoice best;
+  const int halves = ceil_div(N, 16);
+  int64_t cost = INT64_MAX;
+  for (int split = 0; split <= 3 && 1 << split <= kt; ++split) {
+    int clusters = (split == 0 ? sms : resident_clusters(fn, 1 << split, threads, smem, sms)) / row_blocks;
+    if (clusters > halves) clusters = halves;
+    if (clusters < 1) clusters = 1;  // (fewer SMs than blocks of rows: they take turns)
+    const int64_t rows = ceil_div(halves, clusters);
+    if (split > 0 && rows > ge::kFewWarps) break;
+    const int64_t steps = (rows * ceil_div(kt, 1 << split) + ge::kFewWarps - 1) / ge::kFewWarps;
+    if (steps + (split > 0 ? join : 0) >= cost) continue;
+    cost = steps + (split > 0 ? join : 0);
+    best.split = split;
+    best.clusters = clusters;
+    best.steps = steps;
+  }
+  return best;
+}
+inline ge::FewSplit few_split(const FewChoice& c, int64_t N, int kt) {
+  const uint32_t halves = (uint32_t)ceil_div(N, 16), clusters = (uint32_t)c.clusters, ctas = 1u << c.split;
+  return {c.split, halves / clusters, halves % clusters, (uint32_t)kt / ctas, (uint32_t)kt % ctas};
+}
+
 }  // namespace ge_host

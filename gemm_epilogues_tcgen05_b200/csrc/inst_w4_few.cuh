@@ -11,7 +11,7 @@ template <int NT, bool GATED, int NG, bool BF>
 W4FewInstance w4_few_one() {
   return {{ge::w4_few_kernel<NT, GATED, NG, false, BF>, ge::w4_few_kernel<NT, GATED, NG, true, BF>},
           {ge::W4Few<NT, GATED ? 2 : 1, NG, false>::BYTES, ge::W4Few<NT, GATED ? 2 : 1, NG, true>::BYTES},
-          32 * ge::kW4FewWarps, ge::W4Few<NT, GATED ? 2 : 1, NG, true>::DEPTH};
+          32 * ge::kFewWarps, ge::W4Few<NT, GATED ? 2 : 1, NG, true>::DEPTH};
 }
 
 template <int NT, bool GATED, bool BF>

@@ -14,6 +14,7 @@ struct SkinnyParams;
 struct GroupedParams;
 struct MxParams;
 struct W4MulParams;
+struct GatedFewParams;
 }  // namespace ge
 
 namespace ge_inst {
@@ -90,6 +91,14 @@ GatedSkinnyInstance gated_skinny_f16_mn(int tp, int gn);
 GatedSkinnyInstance gated_skinny_f16_nk(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_mn(int tp, int gn);
 GatedSkinnyInstance gated_skinny_bf16_nk(int tp, int gn);
+
+// A gated layer of at most 16 rows (8, 16), each warp alone.
+using GatedFewKernelFn = void (*)(ge::GatedFewParams);
+struct GatedFewInstance {
+  GatedFewKernelFn fn;
+  uint32_t smem;
+};
+GatedFewInstance gated_few(bool bf16, bool w_nk, int rows);
 
 // Few rows times 4-bit weights: groups of 128 / ng columns, tp = 16, 32, 64 or 128
 // padded rows, at most 128 / ng and, gated, 64.

@@ -86,31 +86,16 @@ bool plan_few(gemm_epi_plan_s* p, bool gated, int64_t group, cudaError_t* e) {
   c.stages = c.few.stages;
   c.tp = p->T <= 8 ? 8 : 16;
   c.row_blocks = ceil_div(p->T, c.tp);
-  const int halves = ceil_div(p->N, 16);  // of rows of tiles
-  int64_t best = INT64_MAX, steps = 0;
-  for (int split = 1; split <= 8 && split <= c.kt; split *= 2) {
-    int clusters = split == 1 ? p->num_sms
-                              : resident_clusters((const void*)c.few.fn[0], split, c.few.threads, c.few.smem[0], p->num_sms);
-    clusters /= c.row_blocks;
-    if (clusters > halves) clusters = halves;
-    if (clusters < 1) clusters = 1;  // (fewer SMs than blocks of rows: they take turns)
-    const int rows = ceil_div(halves, clusters);
-    if (split > 1 && rows > ge::kW4FewWarps) break;  // (a warp keeps the sums of two rows of tiles)
-    const int64_t tiles = ((int64_t)rows * ceil_div(c.kt, split) + ge::kW4FewWarps - 1) / ge::kW4FewWarps;
-    const int64_t cost = tiles + 4 * (split > 1);
-    if (cost >= best) continue;
-    best = cost;
-    steps = tiles;
-    c.split = split;
-    c.grid = clusters * split;
-  }
-  if (p->T > 16 && !forced && steps > 20) {
+  const FewChoice choice =
+      choose_few((const void*)c.few.fn[0], c.few.threads, c.few.smem[0], p->N, c.kt, p->num_sms, c.row_blocks, 4);
+  if (p->T > 16 && !forced && choice.steps > 20) {
     c.few = {};
-    c.split = 1;
     return false;
   }
+  c.few_split = few_split(choice, p->N, c.kt);
+  c.grid = choice.clusters << choice.split;
   p->grid = c.grid * c.row_blocks;
-  c.max_segs = c.split;
+  c.max_segs = 1 << choice.split;
   return true;
 }
 
@@ -356,15 +341,10 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   k.timeout_ns = p->timeout_ns;
   k.inject_stall = p->inject_stall;
   if (c.few.threads) {
-    const uint32_t halves = (uint32_t)ceil_div(p->N, 16), clusters = (uint32_t)(c.grid / c.split);
-    while (1 << k.split < c.split) ++k.split;
-    k.half_quot = halves / clusters;
-    k.half_rest = halves % clusters;
-    k.kt_quot = (uint32_t)(c.kt / c.split);
-    k.kt_rest = (uint32_t)(c.kt % c.split);
+    k.few = c.few_split;
     k.X = X;
-    Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.few.threads, c.few.smem[zeros != nullptr], c.split > 1, stream);
-    l.attr[1].val.clusterDim.x = (unsigned)c.split;
+    Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.few.threads, c.few.smem[zeros != nullptr], c.few_split.split > 0, stream);
+    l.attr[1].val.clusterDim.x = 1u << c.few_split.split;
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.few.fn[zeros != nullptr], k);
     return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");
   }

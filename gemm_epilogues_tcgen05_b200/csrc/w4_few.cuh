@@ -31,93 +31,43 @@
 // more of it stays in L1: 3 places a warp 9.8 / 10.8 / 14.7 us for T = 1 / 8 / 16, 6 10.5 / 12.3 / 15.4.
 #pragma once
 
+#include "few_rows.cuh"
 #include "w4_kernel.cuh"
 
 namespace ge {
-
-constexpr int kW4FewWarps = 16;
 
 // NT: blocks of 8 rows of X; MATS: matrices; 128 / NG columns a group
 template <int NT, int MATS, int NG, bool ZEROS>
 struct W4Few {
   // a place of a warp's ring: codes, scales and zeros of a tile (of each matrix)
   static constexpr uint32_t TILE = kW4TileBytes + (ZEROS ? 96 : 64) * NG, PLACE = MATS * TILE;
-  static constexpr int LD = 36;                                 // floats between a sum's rows: no two lanes in a bank
+  static constexpr int LD = kFewLd;
   static constexpr uint32_t SUMS = MATS * NT * 8 * LD * 4;      // of a warp and a row of tiles
-  static constexpr int ROOM = (232448 / kW4FewWarps - 8 - SUMS) / PLACE;
+  static constexpr int ROOM = (232448 / kFewWarps - 8 - SUMS) / PLACE;
   static constexpr int DEPTH = ROOM < 3 ? ROOM : 3;             // places of a warp's ring
   static constexpr uint32_t WARP = DEPTH * PLACE + SUMS;        // its last row's sums take the ring's place
-  static constexpr uint32_t BYTES = kW4FewWarps * (WARP + 8);
+  static constexpr uint32_t BYTES = kFewWarps * (WARP + 8);
   static_assert(DEPTH >= 2 && SUMS <= DEPTH * PLACE && PLACE % 16 == 0 && SUMS % 16 == 0, "ring");
   static_assert(BYTES <= 232448, "above the per-CTA limit");
 };
 
-template <bool BF16>
-__device__ __forceinline__ void w4_mma(float (&d)[4], bool zero, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                       uint32_t b0, uint32_t b1) {
-  const float c0 = zero ? 0.f : d[0], c1 = zero ? 0.f : d[1], c2 = zero ? 0.f : d[2], c3 = zero ? 0.f : d[3];
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-  return v;
-}
-
-// The tiles of a CTA's half rows [h0, h1) of tiles, nkb columns of tiles wide, row after row.
-// A tile that both halves are wanted of weighs 2, one of the first or last row
-// may weigh 1; the warps have equal shares of the weight, runs of tiles. (No divisions:
-// a handful of them ahead of the first load, and in the join, cost 3 us.)
-template <int H>
-struct W4Half {
-  static constexpr int value = H;
-};
-
-struct W4Runs {
-  uint32_t nkb, row0, rows, first, last_at, weight;  // rows of tiles; first: log2 of the weight of the first row's tiles
-  __device__ __forceinline__ W4Runs(uint32_t h0, uint32_t h1, uint32_t nkb_) : nkb(nkb_), row0(h0 >> 1) {
-    rows = ((h1 + 1) >> 1) - row0;
-    first = (h0 & 1u) || h1 - h0 == 1 ? 0 : 1;
-    weight = (h1 - h0) * nkb;
-    last_at = (h1 & 1u) && rows > 1 ? weight - nkb : weight;  // weight ahead of a last row that weighs 1
-  }
-  // the first tile of warp w: of the tiles that begin at its share or later
-  __device__ __forceinline__ uint32_t begin(uint32_t w) const {
-    const uint32_t x = weight * w / kW4FewWarps;
-    if (x <= nkb << first) return (x + first) >> first;
-    if (x <= last_at) return nkb + ((x - (nkb << first) + 1) >> 1);
-    return (rows - 1) * nkb + x - last_at;
-  }
-};
-
-// one of `parts` shares of `total` = quot parts + rest
-__device__ __forceinline__ uint32_t w4_share(uint32_t i, uint32_t quot, uint32_t rest) { return i * quot + min(i, rest); }
-
 template <int NT, bool GATED, int NG, bool ZEROS, bool BF16>
-__global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4MulParams p) {
-  constexpr int MATS = GATED ? 2 : 1, W = kW4FewWarps;
+__global__ void __launch_bounds__(32 * kFewWarps, 1) w4_few_kernel(const W4MulParams p) {
+  constexpr int MATS = GATED ? 2 : 1;
   using L = W4Few<NT, MATS, NG, ZEROS>;
   extern __shared__ __align__(16) uint8_t w4_smem[];
   const uint32_t lane = lane_id(), warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
-  const uint32_t rank = blockIdx.x & ((1u << p.split) - 1u), cluster = blockIdx.x >> p.split;  // rank: along the columns
-  const bool split = p.split > 0;
+  const uint32_t rank = blockIdx.x & ((1u << p.few.split) - 1u), cluster = blockIdx.x >> p.few.split;  // rank: along the columns
+  const bool split = p.few.split > 0;
   // this cluster's half rows of tiles, this CTA's columns of them, this warp's tiles
-  const uint32_t h0 = w4_share(cluster, p.half_quot, p.half_rest), h1 = w4_share(cluster + 1, p.half_quot, p.half_rest);
-  const uint32_t kb0 = w4_share(rank, p.kt_quot, p.kt_rest), nkb = w4_share(rank + 1, p.kt_quot, p.kt_rest) - kb0;
-  const W4Runs runs(h0, h1, nkb);
+  const uint32_t h0 = few_share(cluster, p.few.half_quot, p.few.half_rest), h1 = few_share(cluster + 1, p.few.half_quot, p.few.half_rest);
+  const uint32_t kb0 = few_share(rank, p.few.kt_quot, p.few.kt_rest), nkb = few_share(rank + 1, p.few.kt_quot, p.few.kt_rest) - kb0;
+  const FewRuns runs(h0, h1, nkb);
   const uint32_t row0 = runs.row0, u0 = runs.begin(warp), u1 = runs.begin(warp + 1);
   const int t0 = static_cast<int>(blockIdx.y) * (8 * NT), T = min(p.T - t0, 8 * NT);  // this CTA's rows of X
   uint8_t* ring = w4_smem + warp * L::WARP;
   // the rows of tiles whose sums a warp keeps: the first, the last
-  int* kept = reinterpret_cast<int*>(w4_smem + kW4FewWarps * L::WARP);
+  int* kept = reinterpret_cast<int*>(w4_smem + kFewWarps * L::WARP);
   if (lane < 2) kept[2 * warp + lane] = -1;
   __syncwarp();
   wait_for_inputs();
@@ -205,8 +155,8 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
             hi(word[32], r, 4);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              w4_mma<BF16>(part[t], b == k * PER, r[0], r[4], r[1], r[5], x[b][t].x, x[b][t].y);
-              w4_mma<BF16>(part[t], false, r[2], r[6], r[3], r[7], x[b][t].z, x[b][t].w);
+              few_mma<BF16>(part[t], b == k * PER, r[0], r[4], r[1], r[5], x[b][t].x, x[b][t].y);
+              few_mma<BF16>(part[t], false, r[2], r[6], r[3], r[7], x[b][t].z, x[b][t].w);
             }
           }
           const uint16_t* sc = reinterpret_cast<const uint16_t*>(tile + kW4TileBytes + 64 * k + 2 * f);
@@ -236,11 +186,11 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
     __syncwarp();
     const uint32_t half = 2 * (row0 + row);
     if (half >= h0 && half + 1 < h1)
-      multiply(place, x, W4Half<0>(), W4Half<2>());
+      multiply(place, x, FewHalf<0>(), FewHalf<2>());
     else if (half >= h0)
-      multiply(place, x, W4Half<0>(), W4Half<1>());
+      multiply(place, x, FewHalf<0>(), FewHalf<1>());
     else
-      multiply(place, x, W4Half<1>(), W4Half<2>());
+      multiply(place, x, FewHalf<1>(), FewHalf<2>());
     __syncwarp();  // the place has been read
     fetch();
     place = place + L::PLACE == ring + L::DEPTH * L::PLACE ? ring : place + L::PLACE;
@@ -272,41 +222,13 @@ __global__ void __launch_bounds__(32 * kW4FewWarps, 1) w4_few_kernel(const W4Mul
     ++row;
   }
   cp_async_wait<0>();
-  __syncwarp();
-  if (split)
-    cluster_sync();
-  else
-    __syncthreads();
-
-  // ---- the rows that warps have kept: a warp takes a row of X of them (of a cluster's
-  // rows, the CTAs in turn), a lane a feature; lane e holds entry e of `kept`
-  const int own = kept[lane];
-  const uint32_t same = __match_any_sync(0xffffffffu, own);
-  uint32_t leaders = __ballot_sync(0xffffffffu, own >= 0 && (same & ((1u << lane) - 1u)) == 0);
-  uint32_t t = (rank << 4) + warp;  // (16 warps)
-  for (; leaders; leaders &= leaders - 1) {
-    const int r = __shfl_sync(0xffffffffu, own, __ffs(leaders) - 1);
-    for (; t < static_cast<uint32_t>(T); t += (1u << p.split) * W) {
-      float a = 0.f, b = 0.f;
-      for (uint32_t s = 0; s < 1u << p.split; ++s) {
-        const uint32_t base = split ? mapa_shared(smem_u32(w4_smem), s) : smem_u32(w4_smem);
-        uint32_t from = __ballot_sync(0xffffffffu, static_cast<int>(ld_cluster_u32(base + W * L::WARP + 4 * lane)) == r);
-        for (; from; from &= from - 1) {
-          const uint32_t e = __ffs(from) - 1;
-          const uint32_t at = base + (e >> 1) * L::WARP + (e & 1u ? 0 : L::DEPTH * L::PLACE) + (t * L::LD + lane) * 4;
-          a += __uint_as_float(ld_cluster_u32(at));
-          if constexpr (GATED) b += __uint_as_float(ld_cluster_u32(at + NT * 8 * L::LD * 4));
-        }
-      }
-      const uint32_t half = 2 * (row0 + r) + (lane >> 4);
-      const int n = static_cast<int>((row0 + r) * 32 + lane);
-      if (half >= h0 && half < h1 && n < p.N)
-        w4_output<GATED, BF16>(p, a, b, t0 + t, n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
-    }
-    t -= T;
-  }
-  __syncwarp();
-  if (split) cluster_sync();  // (sums that another CTA reads)
+  few_join<NT, MATS, L::WARP, L::DEPTH * L::PLACE>(
+      w4_smem, p.few.split, rank, T, [&](uint32_t r, uint32_t t, float a, float b) {
+        const uint32_t half = 2 * (row0 + r) + (lane >> 4);
+        const int n = static_cast<int>((row0 + r) * 32 + lane);
+        if (half >= h0 && half < h1 && n < p.N)
+          w4_output<GATED, BF16>(p, a, b, t0 + static_cast<int>(t), n, bias_of(n), GATED ? bias_of(p.N + n) : 0.f);
+      });
 }
 
 }  // namespace ge

@@ -35,6 +35,7 @@
 #pragma once
 
 #include "activation.cuh"
+#include "few_rows.cuh"
 #include "skinny_kernel.cuh"
 #include "w4_quant.cuh"
 
@@ -47,10 +48,7 @@ struct W4MulParams {
   int32_t max_segs;
   int32_t epi, act;      // EpiKind; gated: an ActKind
   int32_t bias_f32, out_f32;
-  // w4_few_kernel: log2 of the CTAs of a cluster; what a cluster has of the half rows of
-  // tiles, and its CTAs of the columns of tiles (the first `rest` one more)
-  int32_t split;
-  uint32_t half_quot, half_rest, kt_quot, kt_rest;
+  FewSplit few;          // w4_few_kernel alone, and X
   const void* X;
   const uint8_t* q;
   const void* scales;

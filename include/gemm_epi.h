@@ -44,7 +44,8 @@
  *                                 A wait that spans many tiles counts from the
  *                                 last progress, so a launch may last longer
  *   tuning overrides of the plan's choices, for measurement and tests:
- *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny (4-bit weights: warp|tmem), GEMM_EPI_FORCE_BN=64|128|192|256,
+ *   GEMM_EPI_FORCE_KERNEL=tile|pair|skinny (4-bit weights: warp|tmem; gated: warp too),
+ *   GEMM_EPI_FORCE_BN=64|128|192|256,
  *   GEMM_EPI_RASTER=m|n, GEMM_EPI_GROUP_M, GEMM_EPI_SKINNY_GRID, GEMM_EPI_SKINNY_KPS=1|2,
  *   GEMM_EPI_SKINNY_PREFETCH, GEMM_EPI_TAIL_SPLIT=0|1, GEMM_EPI_CACHE_HINTS=0|1,
  *   GEMM_EPI_FORCE_GROUPED=32|128|256 (rows per tile of grouped and microscaled plans),

@@ -173,6 +173,33 @@ def test_backward(shape, variant, monkeypatch):
         check_backward(dY, W2, Z, dZ, dbias if with_b else None, name, w_nk)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 8, 8), (2, 24, 40), (7, 72, 104), (8, 2048, 1024), (9, 40, 32), (13, 2376, 264), (16, 1032, 520),
+                                   (3, 4752, 96), (5, 7112, 64), (16, 16 * 16 * 148 + 8, 40), (1, 16, 16384), (16, 48, 10008)])
+@pytest.mark.parametrize("kernel", ["warp", "skinny"])
+def test_few_rows_on_either_kernel(T, N, K, kernel, monkeypatch):
+    """Half rows of tiles, one to more than sixteen a CTA; contractions that clusters share."""
+    monkeypatch.setenv("GEMM_EPI_FORCE_KERNEL", kernel)
+    for i, (name, dt, w_nk, bias, aux, f32) in enumerate(
+            [("SILU", "bf16", False, None, False, False), ("GELU", "fp16", True, "32", True, False),
+             ("RELU", "bf16", True, "16", True, True), ("SILU", "fp16", False, "16", True, True)]):
+        X, W, b = make(T, N, K, DT[dt], 20 + i, w_nk, bias)
+        hb, H = guarded((T, N), torch.float32 if f32 else DT[dt])
+        zb, Z = guarded((T, 2 * N), DT[dt])
+        with GatedPlan(T, N, K, DT[dt], "GATED_AUX" if aux else "GATED", act=name, w_nk=w_nk, out_f32=f32) as p:
+            if bias == "32":
+                p.set_bias_f32()
+            assert p.info()["kernel"] == 1 and (p.info()["tile_m"] == 32) == (kernel == "warp")
+            assert K < 16384 or p.info()["split_k"] > 1
+            p.gemm_epi_gated_execute(X, W, b, H, Z)
+            first = H.clone()
+            p.gemm_epi_gated_execute(X, W, b, H, Z)
+            torch.cuda.synchronize()
+            assert p.status() == 0
+        assert torch.equal(first, H) and guards_ok(hb) and guards_ok(zb)
+        assert aux or bool((Z == 77).all())
+        check_forward(X, W, b, H, Z if aux else None, name, w_nk)
+
+
 @pytest.mark.parametrize("T,N,K,grid", [(8, 64, 2048, "7"), (31, 136, 1032, "11"), (17, 72, 520, "3"), (32, 200, 4096, "61"),
                                         (5, 9600, 264, "70"), (32, 9800, 520, "140"), (16, 19200, 264, "33")])
 @pytest.mark.parametrize("w_nk", [False, True])
