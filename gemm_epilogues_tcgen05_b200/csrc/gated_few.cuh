@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) gated_few_kernel(const Gate
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       x[t] = t * 8 + static_cast<int>(g) < p.T && k < p.K
-                 ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) +
-                                                        static_cast<int64_t>(t * 8 + static_cast<int>(g)) * p.K + k))
+                 ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.X) +
+                                                   static_cast<int64_t>(t * 8 + static_cast<int>(g)) * p.K + k)
                  : make_uint4(0, 0, 0, 0);
   };
   // rows of ldmatrix: column 8 (r / 2) + r % 2 of matrix lane / 8, row r = lane % 8

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) w4_few_kernel(const W4MulPa
       for (int t = 0; t < NT; ++t) {
         const int blocks = t * 8 + static_cast<int>(g) < T ? left : 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) x[b][t] = b * 32 < blocks ? __ldg(xk + t * x_step + b * 4) : make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < 4; ++b) x[b][t] = b * 32 < blocks ? xk[t * x_step + b * 4] : make_uint4(0, 0, 0, 0);
       }
     }
     cp_async_wait<L::DEPTH - 1>();

@@ -60,9 +60,11 @@ __device__ __forceinline__ uint16_t w4_round16(float f) {
   return static_cast<uint16_t>(pack2<BF16>(f, 0.f) & 0xffffu);
 }
 
+// (No read-only loads in these kernels: they may start before the kernel ahead of them, which
+// writes their operands, has ended.)
 __device__ __forceinline__ uint4 w4_load_once(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4Params p) {
     const uint16_t* from = reinterpret_cast<const uint16_t*>(p.src) + (static_cast<int64_t>(m) * p.rows + row) * p.cols + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
+      const uint4 v = in ? reinterpret_cast<const uint4*>(from)[i] : make_uint4(0, 0, 0, 0);
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
@@ -211,8 +213,8 @@ static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
       const int row = i * kW4Rows + static_cast<int>(f);
       uint32_t src = 0;
       if (row < p.rows && col < p.cols)
-        src = __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.src) +
-                                                      (m * p.rows + row) * (p.cols / 2) + col / 2));
+        src = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.src) +
+                                                 (m * p.rows + row) * (p.cols / 2) + col / 2);
       const auto gather = [](uint32_t x) {  // the low 4 bits of each byte, side by side
         x &= 0x0f0f0f0fu;
         x = (x | (x >> 4)) & 0x00ff00ffu;
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Params p) {
     const uint32_t f = F32 ? k : 2 * k + (lane >> 4), row = row0 + f;
     if (row >= static_cast<uint32_t>(p.rows)) break;
     const int64_t at = (tile * ng + c0 / static_cast<uint32_t>(p.group)) * kW4Rows + f0 + f;
-    const float s = w4_float<BF16>(__ldg(reinterpret_cast<const uint16_t*>(p.scales) + at));
-    const float z = p.zeros ? static_cast<float>(__ldg(p.zeros + at)) : 8.f;
+    const float s = w4_float<BF16>(reinterpret_cast<const uint16_t*>(p.scales)[at]);
+    const float z = p.zeros ? static_cast<float>(p.zeros[at]) : 8.f;
     const uint32_t word = stage[warp][(c0 / 32) * 32 + f * 4 + (c0 / 8 & 3u)];
     float v[V];
 #pragma unroll

@@ -124,8 +124,8 @@ typedef struct {
   int64_t T, N, K;
   int dtype, epilog;
   int kernel;          /* 0 = tile kernel (one CTA per tile), 1 = few-row kernel (swap-AB,
-                          stream-K), 2 = tile kernel on CTA pairs (256-row tiles); grouped
-                          plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
+                          stream-K; gated layers with tile_m 32: each warp alone), 2 = tile
+                          kernel on CTA pairs (256-row tiles); grouped plans: 3, 4 = tiles of at most 32, 128 rows (one CTA), 5 = of 256
                           (CTA pairs); microscaled plans: 6 = 128 rows, 7 = 256 (CTA pairs);
                           4-bit weights: 8 (tile_m 32: each warp alone, 128: through tensor
                           memory). For 3 to 8 tile_m counts features and tile_n rows */
