@@ -56,9 +56,9 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
-# Units of kernels that no benchmark step launches (expert-grouped and
-# microscaled products): a change there leaves the steps' evidence valid.
-OTHER_KERNELS = ("grouped", "inst_grouped", "mx", "inst_mx")
+# Units of kernels that no benchmark step launches (expert-grouped and microscaled
+# products, gated layers, 4-bit weights): a change there leaves the steps' evidence valid.
+OTHER_KERNELS = ("grouped", "inst_grouped", "mx", "inst_mx", "gated", "inst_gated", "w4", "inst_w4", "few_rows")
 
 
 def kernel_source_hash(every_unit: bool = False) -> str:
