@@ -142,8 +142,7 @@ template <bool BF16>
 struct W4Unpack {
   uint32_t zero, zero16;
   __device__ __forceinline__ explicit W4Unpack(uint32_t z) {
-    z = (z & 127u) * 0x00010001u;
-    zero = z | (BF16 ? 0x43004300u : 0x64006400u);
+    zero = z * 0x00010001u + (BF16 ? 0x43004300u : 0x64006400u);  // (one multiply-add: z is below 128)
     const __half2 n = __hneg2(__hsub2(*reinterpret_cast<const __half2*>(&zero), __float2half2_rn(960.f)));  // -(64 + z)
     zero16 = BF16 ? 0u : *reinterpret_cast<const uint32_t*>(&n);
   }

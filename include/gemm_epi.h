@@ -472,7 +472,7 @@ GEMM_EPI_API int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, co
  * Arithmetic, outputs, rounding, the 16-bit types, flags, error codes, watchdog,
  * streams and ownership are those of one product; H is computed from Z before Z
  * is rounded. dbias is summed in a fixed order. GELU is z Phi(z) as grouped
- * products evaluate it; SILU's exponential and quotient are CUDA's fast ones
+ * products evaluate it; SILU's exponential and reciprocal are the approximate instructions
  * (error of H about 1e-6 of it). An activation of -infinity is NaN for SILU and 0
  * for GELU and RELU; RELU of NaN is 0, and RELU's derivative at 0 is 0. A call runs
  * on the plan's device whichever is current, and launches are programmatic, as
