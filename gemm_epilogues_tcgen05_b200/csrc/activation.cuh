@@ -83,10 +83,10 @@ enum ActKind : int { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU = 2 };
 //   SILU  a = z p, p = 1 / (1 + e^-z);  d = p (1 + z (1 - p)) = p + a (1 - p)
 //   GELU  a = max(z, 0) - |z| h(|z|);   d = Phi(z) + z phi(z), Phi(z) = h(-z) or 1 - h(z)
 //   RELU  a = max(z, 0), of NaN 0;      d = 1 where z > 0
-// The exponential is off by 2 ulp and its rounded argument's |z| ulp, the reciprocal by 1: p's 1e-6 at |z| =
-// 10 is far below the 16 bits that the inputs of d and nearly all outputs are
-// rounded to. p is 0 from z = -88.7 on, where e^-z leaves fp32; -inf gives NaN, as
-// -inf x 0 does.
+// With e = 2^-24: the exponential is off by 4 e (2 ulp) and its rounded argument's 1.22 |z| e, the
+// sum by e, the reciprocal by 2 e, so p by (1 - p) (4 + 1.22 |z|) e + 3 e of itself: a keeps its relative
+// accuracy in the negative tail (7e-6 at -88), and so does d beyond its zero at -1.28. p is 0
+// below z = -88.72, where e^-z leaves fp32; -inf gives NaN, as -inf x 0 does, and so does d at an infinity.
 __device__ __forceinline__ float reciprocal(float x) {  // (__fdividef gives 0 from 2^126 on)
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));

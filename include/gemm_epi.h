@@ -472,9 +472,12 @@ GEMM_EPI_API int gemm_epi_mx_execute(gemm_epi_plan_t plan, const uint8_t* Xq, co
  * Arithmetic, outputs, rounding, the 16-bit types, flags, error codes, watchdog,
  * streams and ownership are those of one product; H is computed from Z before Z
  * is rounded. dbias is summed in a fixed order. GELU is z Phi(z) as grouped
- * products evaluate it; SILU's exponential and reciprocal are the approximate instructions
- * (error of H about 1e-6 of it). An activation of -infinity is NaN for SILU and 0
- * for GELU and RELU; RELU of NaN is 0, and RELU's derivative at 0 is 0. A call runs
+ * products evaluate it (the erf form; the tanh form is not offered); SILU's exponential and
+ * reciprocal are the approximate instructions: act(z) is off by at most (8 + 1.3 |z|) 2^-24 of
+ * itself for z < 0 (5e-7 near 0, 3e-6 at -30, 7e-6 at -88) and 5e-7 for z > 0, and is 0 below
+ * -88.72, where e^-z leaves fp32. An activation of -infinity is NaN for SILU and 0
+ * for GELU and RELU; RELU of NaN is 0, and RELU's derivative at 0 is 0. The
+ * derivatives of SILU and GELU at an infinity are NaN (infinity x 0). A call runs
  * on the plan's device whichever is current, and launches are programmatic, as
  * those of grouped products. gemm_epi_free, _query, _status, _last_error and
  * _set_bias_f32 (forward) take these plans; the other calls return
