@@ -105,11 +105,19 @@ bool whole_tiles(int64_t N, int sms) {
 }
 
 // The kernel whose warps work alone, for at most 16 rows of a small weight: it starts 2
-// to 3 us sooner, and streams at half the rate of TMA's. N x K, us, T = 1 (few-row kernel: T = 1):
-//   half tiles of a warp   2: K = 1024, N = 2048 4.6 (6.6)     4: K = N = 2048 7.7 (10.1)
-//                          8: K = 2048, N = 4096 10.4 (11.7), T = 16 11.6 (12.1); K = 4096, N = 2048 12.0 (12.2)
-//                         12: K = N = 3000 13.0 (12.7)         20: K = 4096, N = 11008 38.1 (31.8)
-// where the few-row kernel has whole tiles 6: K = 1024, N = 5632 8.8 (7.9), 12: K = 2048 13.9 (11.3).
+// to 3 us sooner, and streams at half the rate of TMA's. By the half tiles of a warp, N x K (K x N), us,
+// T = 1, the few-row kernel's behind the stroke:
+//   2  K = 1024, N = 2048 4.6 / 6.6        4  K = N = 2048 7.7 / 10.1
+//   6  K = 3008, N = 1024 8.5 (9.6) / 10.0, N = 2048 9.4 (10.3) / 11.1
+//   7  K = 3584, N = 1024 9.8 (10.7) / 10.0, N = 2048 10.6 (11.5) / 11.5
+//   8  one half row a CTA: K = 4096, N = 1024 11.0 (11.8) / 10.0, N = 1536 11.4 (12.2) / 10.9, N = 2360 12.4
+//      (13.1) / 11.7; T = 16, N = 1536 12.5 / 11.3
+//   8  more half rows a CTA: K = 2048, N = 3000 9.2 (9.4) / 10.5, N = 4096 10.3 (9.5) / 11.6; T = 16 11.5 / 11.9
+//  12  K = N = 3000 12.9 / 12.6           20  K = 4096, N = 11008 38.1 / 31.8
+// where the few-row kernel has whole tiles 6: K = 1024, N = 5632 8.8 / 7.9, 12: K = 2048 13.9 / 11.3.
+// Where a split of the columns over a cluster is estimated fastest (few features, K from 2560
+// on), the few-row kernel is faster than with it and than without: K = 4096, N = 512 14.3 split, 10.7 whole
+// / 9.0, K = 8192, N = 256 15.8 split / 11.2. So only the override launches clusters here.
 bool plan_few(gemm_epi_plan_s* p, bool bf16, cudaError_t* e) {
   if (p->T > 16) return false;
   bool forced = false;
@@ -126,7 +134,7 @@ bool plan_few(gemm_epi_plan_s* p, bool bf16, cudaError_t* e) {
   if (*e != cudaSuccess) return true;
   const FewChoice choice = choose_few((const void*)inst.fn, 32 * ge::kFewWarps, inst.smem, p->N, kt, p->num_sms, 1, 3);
   // (whole tiles are what the other kernel is best at)
-  const int64_t most = whole_tiles(p->N, p->num_sms) ? 4 : 8;
+  const int64_t most = whole_tiles(p->N, p->num_sms) ? 4 : ceil_div(p->N, 16) <= p->num_sms ? 7 : 8;
   if (!forced && (choice.split > 0 || choice.steps > most)) return false;
   p->gf.fn = inst.fn;
   p->gf.smem = inst.smem;
