@@ -63,13 +63,17 @@ int run(void (*kernel)(ge::W4Params), const ge::W4Params& k, int64_t blocks, cud
 // the half tiles of a warp; a join over a cluster costs about what four take. False: a
 // plan on tensor memory (w4_kernel.cuh) is the faster one.
 // Rows beyond 16 are another pass over the weight here, and a slower stage there, whose
-// launches take 9 to 16 us before the first of them. bf16, G = 128, us here (there):
-//   half tiles of a warp   2: T = 64, K = N = 1024                4.4 (12.1)
-//                          8: T = 32, K = N = 4096               10.3 (15.9), gated 16.1 (25.5)
-//                         14: T = 64, K = N = 4096               16.6 (18.1), gated 24.8 (28.8)
-//                         20: T = 32, K = 4096, N = 11008        21.2 (19.2), gated 32.1 (33.3)
-//                         30: T = 48, K = 4096, N = 11008        30.8 (22.1), gated 46.9 (38.5)
-// up to 16 rows always: T = 16, K = 4096, N = 11008 14.7 (16.4), gated 21.2 (27.1).
+// launches take 9 to 16 us before the first of them. bf16, us here / there, G = 128 | G = 32 with zeros | gated, G = 128 |
+// gated, G = 32 with zeros:
+//   half tiles of a warp   8: T = 32, K = N = 4096             10.1 / 15.4 | 11.7 / 16.3 | 16.0 / 26.8 | 18.6 / 29.5
+//                         14: T = 64, K = N = 4096             16.4 / 18.1 | 18.6 / 19.8 | 24.7 / 30.6 | 28.5 / 35.6
+//                         16: T = 48, K = 4096, N = 6144       17.3 / 17.8 | 19.9 / 24.2 | 26.9 / 28.7 | 29.9 / 43.0
+//                         19: T = 64, K = 2048, N = 11008      22.3 / 18.7 | 26.5 / 25.4 | 34.6 / 30.2 | 39.5 / 42.7
+//                         20: T = 32, K = 4096, N = 11008      21.1 / 19.2 | 23.5 / 23.3 | 31.9 / 32.8 | 38.0 / 41.7
+//                         22: T = 48, K = 4096, N = 8192       24.3 / 19.7 | 27.6 / 28.2 | 36.3 / 33.9 | 41.4 / 51.6
+//                         30: T = 48, K = 4096, N = 11008      30.4 / 22.0 | 34.0 / 36.4 | 46.8 / 38.9 | 53.5 / 65.8
+// so up to 16 of a plain product and 20 of a gated one (G = 64: 19 23.2 / 19.2, gated 20 32.7 / 34.2, 22 37.6 / 39.3).
+// Up to 16 rows always: T = 16, K = 4096, N = 11008 14.7 / 16.4, gated 21.2 / 27.1.
 bool plan_few(gemm_epi_plan_s* p, bool gated, int64_t group, cudaError_t* e) {
   bool forced = false;
   if (const char* f = getenv("GEMM_EPI_FORCE_KERNEL")) {  // tuning override
@@ -88,7 +92,7 @@ bool plan_few(gemm_epi_plan_s* p, bool gated, int64_t group, cudaError_t* e) {
   c.row_blocks = ceil_div(p->T, c.tp);
   const FewChoice choice =
       choose_few((const void*)c.few.fn[0], c.few.threads, c.few.smem[0], p->N, c.kt, p->num_sms, c.row_blocks, 4);
-  if (p->T > 16 && !forced && choice.steps > 20) {
+  if (p->T > 16 && !forced && choice.steps > (gated ? 20 : 16)) {
     c.few = {};
     return false;
   }

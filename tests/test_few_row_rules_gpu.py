@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from gemm_epilogues_tcgen05_b200 import GatedPlan
+from gemm_epilogues_tcgen05_b200 import GatedPlan, W4Plan
 
 pytestmark = pytest.mark.gpu
 
@@ -17,3 +17,13 @@ def test_gated_layers(N, K, alone, T):
         info = p.info()
         assert info["kernel"] == 1 and (info["tile_m"] == 32) == alone
         assert not alone or info["split_k"] == 1
+
+
+@pytest.mark.parametrize("T,N,K,gated,alone", [(1, 128000, 4096, False, True), (16, 11008, 4096, False, True), (32, 4096, 4096, False, True),
+                                               (64, 4096, 4096, True, True), (48, 5000, 2048, False, True), (32, 11008, 4096, True, True),
+                                               (17, 11008, 4096, False, False), (32, 11008, 4096, False, False),
+                                               (64, 11008, 2048, False, False), (48, 11008, 4096, True, False), (128, 11008, 4096, True, False)])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_four_bit_weights(T, N, K, gated, alone, G):
+    with W4Plan(T, N, K, torch.bfloat16, "GATED" if gated else "NONE", group=G) as p:
+        assert p.info()["tile_m"] == (32 if alone else 128)
