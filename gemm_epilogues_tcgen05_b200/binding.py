@@ -42,6 +42,7 @@ ACTS = {"SILU": 0, "GELU": 1, "RELU": 2}  # gemm_epi_act
 MX_TRANSPOSED = 1  # GEMM_EPI_MX_TRANSPOSED
 FLAG_W_NK = 1  # GEMM_EPI_FLAG_W_NK
 FLAG_OUT_F32 = 2  # GEMM_EPI_FLAG_OUT_F32
+FLAG_NO_DBIAS = 4  # GEMM_EPI_FLAG_NO_DBIAS
 
 NOALLOC_SCRATCH_BYTES = 4 << 20  # GEMM_EPI_NOALLOC_SCRATCH_BYTES
 
@@ -614,12 +615,13 @@ class GatedPlan(_DevicePlan):
 
     epilog "GATED": H. "GATED_AUX": H and Z (T x 2N, 16-bit), which the backward
     reads. "DGATED": dZ (T x 2N) from dY (T x K), W2 (K x N) and Z, and the bias
-    gradient (2N). W is K x 2N (``w_nk``: 2N x K; W2: N x K); ``out_f32``: H or dZ
+    gradient (2N), for which the plan holds a workspace unless ``dbias`` is False.
+    W is K x 2N (``w_nk``: 2N x K; W2: N x K); ``out_f32``: H or dZ
     is fp32. bias may be None. Tensors must be on the device that was current
     when the plan was made; the default stream is that device's current one."""
 
     def __init__(self, T: int, N: int, K: int, dtype: torch.dtype, epilog: str = "GATED", act: str = "SILU",
-                 w_nk: bool = False, out_f32: bool = False):
+                 w_nk: bool = False, out_f32: bool = False, dbias: bool = True):
         self.T, self.N, self.K = T, N, K
         self.out_dtype = torch.float32 if out_f32 else dtype
         self.dtype = self.bias_dtype = dtype
@@ -628,7 +630,8 @@ class GatedPlan(_DevicePlan):
         self.w_shape = (cols, K) if w_nk else (K, cols)
         self._shapes = ((T, K), (T, N), (T, 2 * N), (2 * N,))
         self._own(lib().gemm_epi_gated_plan(T, N, K, DTYPES[dtype], self.epilog, ACTS[act] if isinstance(act, str) else act,
-                                            (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0)))
+                                            (FLAG_W_NK if w_nk else 0) | (FLAG_OUT_F32 if out_f32 else 0) |
+                                            (FLAG_NO_DBIAS if not dbias else 0)))
 
     def aux_spec(self):
         return (self._shapes[2], self.dtype) if self.epilog == GATED_EPILOGS["GATED_AUX"] else None

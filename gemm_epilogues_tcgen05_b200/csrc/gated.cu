@@ -239,7 +239,7 @@ cudaError_t plan_tiles(gemm_epi_plan_s* p, bool bf16, bool forward, int sms) {
   } else {
     p->grid = p->num_tiles < sms ? p->num_tiles : sms;
   }
-  if (forward) return cudaSuccess;
+  if (forward || p->no_dbias) return cudaSuccess;
   // the bias gradient's partial sums, a row for each 32 of T
   p->partial_bytes = (size_t)ceil_div(p->T, 32) * 2 * (size_t)p->N * sizeof(float);
   if (test_hook("GEMM_EPI_INJECT_PLAN_ALLOC_FAILURE")) return cudaErrorMemoryAllocation;
@@ -248,8 +248,9 @@ cudaError_t plan_tiles(gemm_epi_plan_s* p, bool bf16, bool forward, int sms) {
 
 gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype, gemm_epi_gated_epilog epilog,
                           gemm_epi_act act, uint32_t flags) {
-  if ((flags & ~(uint32_t)(GEMM_EPI_FLAG_W_NK | GEMM_EPI_FLAG_OUT_F32)) != 0) {
-    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags);
+  const uint32_t known = GEMM_EPI_FLAG_W_NK | GEMM_EPI_FLAG_OUT_F32 | (epilog == GEMM_EPI_DGATED ? GEMM_EPI_FLAG_NO_DBIAS : 0u);
+  if ((flags & ~known) != 0) {
+    fail(GEMM_EPI_ERR_INVALID_ARG, "unknown plan flags 0x%x", flags & ~known);
     return nullptr;
   }
   if (T < 1 || N < 8 || K < 8 || (N % 8) != 0 || (K % 8) != 0) {
@@ -286,6 +287,7 @@ gemm_epi_plan_t make_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
   p->act = act;
   p->w_nk = (flags & GEMM_EPI_FLAG_W_NK) ? 1 : 0;
   p->out_f32 = (flags & GEMM_EPI_FLAG_OUT_F32) ? 1 : 0;
+  p->no_dbias = (flags & GEMM_EPI_FLAG_NO_DBIAS) ? 1 : 0;
   p->device = dev;
   p->num_sms = sms;
   const WatchdogEnv wd = watchdog_env();
@@ -430,6 +432,8 @@ int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, const void* W2
   if (p->epilog != GEMM_EPI_DGATED)
     return fail(GEMM_EPI_ERR_EPILOG_MISMATCH, "gemm_epi_dgated_execute called on a forward plan");
   if (!dY || !W2 || !aux || !dZ) return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_dgated_execute: NULL dY, W2, aux or dZ");
+  if (dbias && p->no_dbias)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "gemm_epi_dgated_execute: dbias on a plan made with GEMM_EPI_FLAG_NO_DBIAS");
   if (!aligned(dY, 16) || !aligned(W2, 16) || !aligned(aux, 16) || !aligned(dZ, 16) || !aligned(dbias, 4))
     return fail(GEMM_EPI_ERR_MISALIGNED, "gemm_epi_dgated_execute: dY, W2, aux, dZ need 16-byte, dbias 4-byte alignment");
   DeviceScope scope(p->device);

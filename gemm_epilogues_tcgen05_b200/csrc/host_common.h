@@ -125,7 +125,6 @@ struct GroupedCfg {
   int slices = 1;  // WGRAD: row slices of the optional bias gradient
 };
 
-// A plan of few rows times 4-bit weights.
 // A gated layer's kernel whose warps work alone, if there is a function.
 struct GatedFewCfg {
   ge_inst::GatedFewKernelFn fn = nullptr;
@@ -134,6 +133,7 @@ struct GatedFewCfg {
   ge::FewSplit few = {};
 };
 
+// A plan of few rows times 4-bit weights.
 struct W4Cfg {
   ge_inst::W4KernelFn fn = nullptr;
   ge_inst::W4FewInstance few = {};       // the kernel of warps alone, if it has threads
@@ -302,6 +302,7 @@ struct gemm_epi_plan_s {
   int w_nk = 0;          // GEMM_EPI_FLAG_W_NK: W / W2 given N x K (K contiguous)
   int out_f32 = 0;       // GEMM_EPI_FLAG_OUT_F32: Y / dZ / dW written as fp32
   int act = 0;           // kind 3, 4: gemm_epi_act
+  int no_dbias = 0;      // GEMM_EPI_FLAG_NO_DBIAS
   ge_host::GatedFewCfg gf;  // kind 3
   ge_host::W4Cfg w4;     // kind 4
   int cache_hints = 0;   // few-row kernel: L2 eviction policies on the operand loads (GEMM_EPI_CACHE_HINTS)

@@ -152,8 +152,8 @@ typedef struct {
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
                               gemm_epi_epilog epilog);
 
-/* Flags of gemm_epi_plan_ex. */
-enum { GEMM_EPI_FLAG_W_NK = 1u, GEMM_EPI_FLAG_OUT_F32 = 2u };
+/* Flags of gemm_epi_plan_ex; GEMM_EPI_FLAG_NO_DBIAS of DGATED plans alone. */
+enum { GEMM_EPI_FLAG_W_NK = 1u, GEMM_EPI_FLAG_OUT_F32 = 2u, GEMM_EPI_FLAG_NO_DBIAS = 4u };
 
 /*
  * gemm_epi_plan_ex: gemm_epi_plan with flags (gemm_epi_plan passes 0).
@@ -494,7 +494,9 @@ typedef enum {
  * gemm_epi_gated_plan: T >= 1; N and K multiples of 8, N at most 2^23, the rest as
  * gemm_epi_plan_ex. N is the number of columns of H, also for DGATED, where K is
  * the contraction length of dY.W2. Flags GEMM_EPI_FLAG_W_NK (W or W2) and
- * GEMM_EPI_FLAG_OUT_F32 (H or dZ; aux stays 16-bit). gemm_epi_query reports
+ * GEMM_EPI_FLAG_OUT_F32 (H or dZ; aux stays 16-bit). A DGATED plan holds a workspace of ceil(T / 32)
+ * x 2N fp32 for the bias gradient; with GEMM_EPI_FLAG_NO_DBIAS it holds none, and its
+ * calls refuse a dbias (GEMM_EPI_ERR_INVALID_ARG). gemm_epi_query reports
  * kernels 0 to 2. Both weight layouts have a few-row kernel (forward, T <= 32).
  */
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_gated_plan(int64_t T, int64_t N, int64_t K, gemm_epi_dtype dtype,
