@@ -718,8 +718,9 @@ def gemm_epi_w4_dequantize(q, scales, zeros, out, group=128, stream=None):
 
 
 def gemm_epi_w4_pack(codes, src_scales, src_zeros, q, scales, zeros=None, stream=None):
-    """Codes ((batch x) N x K / 2 bytes, the lower column in the low 4 bits), scales ((batch x)
-    N x K / group) and zeros (the same, uint8, or None) as a checkpoint has them, to the product's layout."""
+    """Row-major codes ((batch x) N x K / 2 bytes, the lower column in the low 4 bits), scales ((batch x)
+    N x K / group) and zeros (the same, uint8 of 0 .. 127, or None) to the product's layout. A group
+    whose zero point is 128 or more gets a NaN scale."""
     if getattr(src_scales, "dtype", None) not in DTYPES or getattr(codes, "dtype", None) is not torch.uint8:
         raise ValueError("codes must be uint8, scales float16 or bfloat16")
     K, groups = 2 * codes.shape[-1], src_scales.shape[-1]

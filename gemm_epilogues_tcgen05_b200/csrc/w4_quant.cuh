@@ -44,6 +44,7 @@ struct W4Params {
 };
 
 constexpr int kW4Rows = 32, kW4TileBytes = 2048;
+constexpr uint16_t kW4Nan = 0x7fff;  // a NaN of either 16-bit type
 
 // byte of the word of feature f (0..31) and 8-column unit u (0..15) in a tile
 __device__ __forceinline__ uint32_t w4_word(uint32_t f, uint32_t u) { return 512 * (u >> 2) + 16 * f + 4 * (u & 3u); }
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4Params p) {
 }
 
 // Codes as a checkpoint has them (rows x cols / 2 bytes), scales and zeros rows x
-// cols / G, to the layout. Copies only.
+// cols / G, to the layout. Copies, but for a zero point of 128 or more, which the product's operands have
+// no room for: the group gets a NaN scale.
 static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
   __shared__ __align__(16) uint32_t stage[8][kW4TileBytes / 4];
   wait_for_inputs();
@@ -226,8 +228,10 @@ static __global__ void __launch_bounds__(256) w4_pack_kernel(const W4Params p) {
       const int row = i * kW4Rows + static_cast<int>(lane), g = j * static_cast<int>(ng) + static_cast<int>(k);
       const bool in = row < p.rows && g < groups;
       const int64_t from = in ? (m * p.rows + row) * groups + g : 0, at = (tile * ng + k) * kW4Rows + lane;
-      reinterpret_cast<uint16_t*>(p.scales)[at] = in ? reinterpret_cast<const uint16_t*>(p.src_scales)[from] : 0;
-      if (p.zeros) p.zeros[at] = in ? (p.src_zeros[from] & 127u) : 0;
+      const uint32_t zero = in && p.zeros ? p.src_zeros[from] : 0u;
+      reinterpret_cast<uint16_t*>(p.scales)[at] =
+          zero > 127u ? kW4Nan : in ? reinterpret_cast<const uint16_t*>(p.src_scales)[from] : 0;
+      if (p.zeros) p.zeros[at] = static_cast<uint8_t>(zero & 127u);
     }
     w4_store_tile(p.q + tile * kW4TileBytes, stage[warp]);
   }
@@ -259,7 +263,8 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const W4Params p) {
     if (row >= static_cast<uint32_t>(p.rows)) break;
     const int64_t at = (tile * ng + c0 / static_cast<uint32_t>(p.group)) * kW4Rows + f0 + f;
     const float s = w4_float<BF16>(reinterpret_cast<const uint16_t*>(p.scales)[at]);
-    const float z = p.zeros ? static_cast<float>(p.zeros[at]) : 8.f;
+    float z = p.zeros ? static_cast<float>(p.zeros[at]) : 8.f;
+    if (z > 127.f) z = __uint_as_float(0x7fc00000u);  // not a zero point (w4_pack leaves none)
     const uint32_t word = stage[warp][(c0 / 32) * 32 + f * 4 + (c0 / 8 & 3u)];
     float v[V];
 #pragma unroll

@@ -516,7 +516,9 @@ GEMM_EPI_API int gemm_epi_dgated_execute(gemm_epi_plan_t plan, const void* dY, c
  * consecutive columns, for products with few 16-bit rows (decoding: the weight is
  * what is read, at a quarter of its 16-bit size).
  *   W[n][k] = scale[n][k / G] (code[n][k] - zero[n][k / G]), code 0 .. 15; zero is 8
- *   everywhere where no zeros are given (NULL), else 0 .. 127 (one byte)
+ *   everywhere where no zeros are given (NULL), else a byte of 0 .. 127
+ * A larger byte is not a zero point: _pack gives its group a NaN scale, _dequantize gives NaN,
+ * and the product, which must not be given one, does not look.
  * gemm_epi_w4_quantize, of a group w: without zeros scale = max|w| / 7 rounded to the
  * 16-bit type and code = w / scale rounded (ties to even), held to -8 .. 7, plus 8; with
  * zeros, lo = min(w, 0), hi = max(w, 0), scale = (hi - lo) / 15 rounded to the type,
@@ -543,10 +545,12 @@ GEMM_EPI_API int64_t gemm_epi_w4_scales(int64_t batch, int64_t rows, int64_t col
 GEMM_EPI_API int gemm_epi_w4_quantize(int64_t batch, int64_t rows, int64_t cols, int64_t group, gemm_epi_dtype dtype,
                                       const void* W, uint8_t* q, void* scales, uint8_t* zeros, cudaStream_t stream);
 
-/* gemm_epi_w4_pack: codes (rows x cols / 2 bytes, the lower column in the low 4
- * bits), scales (rows x cols / group, 16-bit) and zeros (the same, bytes, of which 7
- * bits count; NULL on both sides or neither) as a checkpoint has them, to the
- * layout above. codes 16-byte, src_scales 2-byte aligned, the rest as above. */
+/* gemm_epi_w4_pack: row-major codes (rows x cols / 2 bytes, the lower column in the low 4
+ * bits), scales (rows x cols / group, 16-bit) and zeros (the same, a byte each; NULL on
+ * both sides or neither) to the layout above; a group whose zero point is 128 or more
+ * stands for NaN. Checkpoints that hold codes as 32-bit words, columns x rows, or with interleaved
+ * columns, packed zero points, or zero points less one, are rearranged to this first.
+ * codes 16-byte, src_scales 2-byte aligned, the rest as above. */
 GEMM_EPI_API int gemm_epi_w4_pack(int64_t batch, int64_t rows, int64_t cols, int64_t group, const uint8_t* codes,
                                   const void* src_scales, const uint8_t* src_zeros, uint8_t* q, void* scales,
                                   uint8_t* zeros, cudaStream_t stream);
