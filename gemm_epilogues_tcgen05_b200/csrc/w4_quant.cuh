@@ -16,9 +16,9 @@
 // a register's halves. Scales (and zeros) of a tile: [128 / G groups][f]. Rows
 // and columns past the matrix are code 0 with scale 0.
 //
-// Bound by memory: a weight of 11008 x 4096 is 90 MB to read and 23.2 to write, which takes
-// 17 us at the rate of a copy; quantised with zeros it takes 27.7 us, without 26.1, back to 16-bit values 22.0
-// and to fp32 ones (180 MB) 31.9. (A lane with 8 columns, 16 of them sharing a group's
+// A weight of 11008 x 4096 is 90 MB to read and 23.2 to write, 17 us at the rate of a copy.
+// Quantising it takes 27.7 us with zeros, 26.1 without: 60 % of that rate, the quotients and conversions
+// take the rest. The inverse is bound by memory: 22.0 us to 16-bit values, 31.9 to fp32 ones (180 MB). (A lane with 8 columns, 16 of them sharing a group's
 // scale and its divisions, took 85.)
 #pragma once
 
@@ -81,10 +81,15 @@ __device__ __forceinline__ void w4_store_tile(uint8_t* q, const uint32_t* stage)
   __syncwarp();
 }
 
-// w / s exactly as rounded division gives it where that quotient decides a
-// rounding: q0 = w r is off by a few units of its last place, and the step with
-// the exact remainder makes it right whenever the quotient is a number of few bits, as
-// a tie is; another quotient of 16-bit numbers is 2^-14 or more from every tie.
+// w / s with the error that the codes' rounding allows: a quotient corrected by one exact
+// remainder (P. W. Markstein, Computation of elementary functions on the IBM RISC System/6000
+// processor, IBM J. Res. Dev. 34, 1990). w and s are integers a, b < 2^11 times powers of two, |w / s| < 32.
+//   Ties, w / s = m + 1/2: a number of few bits. r = 1 / s rounded, so q0 = w r is off by a few units of its last
+//   place; w - q0 s is a few such units times s, which fp32 holds (s >= 1e-30: no underflow), and the step
+//   w / s - q0 is off by 2^-23 of itself: the result rounds to m + 1/2 exactly.
+//   Others are (2 w - (2 m + 1) s) / (2 s) from a tie, whose numerator is a multiple of the smaller of s / b
+//   and 2 w / a: at least 1 / (2 b) >= 2^-12, or (w / s) / a >= 2^-13 where |w / s| >= 1/4 (below it no tie is
+//   nearer than 1/4). The result is off by 32 x 2^-23 at most and stays on its side.
 __device__ __forceinline__ float w4_divide(float w, float s, float r) {
   const float q0 = w * r;
   return fmaf(fmaf(-q0, s, w), r, q0);
