@@ -376,6 +376,7 @@ int run_skinny(gemm_epi_plan_s* p, const void* X, const void* W, const void* bia
   k.act = p->act;
   Launch l(p->sk_grid, ge::kThreads, p->sk.smem, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, p->sk.fn, w, x, k);
+  if (p->inject_stall == 2) p->inject_stall = 0;
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "gated few-row launch");
 }
 

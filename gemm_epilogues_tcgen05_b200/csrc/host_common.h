@@ -64,8 +64,8 @@ inline bool inject_encode_failure() { return test_hook("GEMM_EPI_INJECT_ENCODE_F
 // (2 s; GEMM_EPI_WAIT_TIMEOUT_MS overrides) and, for the watchdog tests,
 // GEMM_EPI_INJECT_STALL -- the MMA issuer withholds its first tile's
 // completion signal, so the epilogue's wait runs out and the kernel reports
-// ERR_TIMEOUT (2, grouped and microscaled plans: one CTA of the first launch
-// only). Read when a plan is created and on every call of the allocation-free
+// ERR_TIMEOUT (2, grouped and microscaled plans, 4-bit weights and gated few-row plans: one CTA
+// of the first launch only). Read when a plan is created and on every call of the allocation-free
 // entry point.
 struct WatchdogEnv {
   uint64_t timeout_ns = 2000000000ull;

@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // (fault injection: the epilogue then waits on a barrier nothing arrives on)
-        if (!(p.inject_stall && scount == 1)) umma_commit(&tfull[buf]);
+        if (!(p.inject_stall && scount == 1 && (!GATED || p.inject_stall == 1 || blockIdx.x == 0))) umma_commit(&tfull[buf]);
       }
       umma_commit(drain);
       wait_bounded(drain, 0, wp, abort_flag, 5, /*honour_abort=*/false);

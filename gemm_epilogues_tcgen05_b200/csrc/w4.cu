@@ -357,6 +357,7 @@ int gemm_epi_w4_execute(gemm_epi_plan_t plan, const void* X, const uint8_t* q, c
   if (rc) return rc;
   Launch l(dim3((unsigned)c.grid, (unsigned)c.row_blocks, 1), c.threads, c.smem, false, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, c.fn, x, k);
+  if (p->inject_stall == 2) p->inject_stall = 0;
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the product with 4-bit weights");
 }
 

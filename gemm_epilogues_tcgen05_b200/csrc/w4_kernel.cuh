@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(W4Smem<TP, NG>::THREADS, 1)
           const uint64_t bdesc = smem_desc_sw128(x + (kk >> 2) * L::X_SUB + (kk & 3) * 32, 16, 1024);
           umma_f16_ts(d + kk / PER * TP, a + kk * 8, bdesc, IDESC, kk % PER > 0 ? 1u : 0u);
           // (fault injection: the accumulating warps then wait for sums that are never announced)
-          if (kk == 7 && !(p.inject_stall && it == 0)) umma_commit(&dfull[s]);
+          if (kk == 7 && !(p.inject_stall && it == 0 && (p.inject_stall == 1 || (blockIdx.x | blockIdx.y) == 0))) umma_commit(&dfull[s]);
         }
       }
     }

@@ -55,8 +55,8 @@
  *   default, or after them)
  *   fault injection for the library's own tests, honoured only while
  *   GEMM_EPI_TEST_HOOKS=1 is also set: GEMM_EPI_INJECT_STALL (a kernel
- *   withholds its first tile's completion signal, so its watchdog fires; 2, on
- *   grouped and microscaled plans: one CTA of the first launch only),
+ *   withholds its first tile's completion signal, so its watchdog fires; 2, on grouped and
+ *   microscaled plans, 4-bit weights and few-row gated plans: one CTA of the first launch only),
  *   GEMM_EPI_INJECT_ENCODE_FAILURE (every tensor-map encode fails),
  *   GEMM_EPI_INJECT_PLAN_ALLOC_FAILURE (the DRELU_BGRAD workspace
  *   allocation fails).
