@@ -570,8 +570,16 @@ GEMM_EPI_API int gemm_epi_w4_dequantize(int64_t batch, int64_t rows, int64_t col
  * Y's; flags GEMM_EPI_FLAG_OUT_F32 or 0. Products are exact in fp32 before they are
  * summed: code - zero is a small integer, a group's sum is scaled in fp32. A plan keeps no
  * weight: one serves all layers of its shape.
- * Beyond some 16 rows of a large weight (K N above 4096 x 4096) a row costs about what it
- * costs with 16-bit weights; for more than 256, dequantise.
+ * Made for few rows. us on one B200, bf16, G = 128 / G = 32 with zeros / the plan of a 16-bit K x N weight:
+ *   T                        16                   32                   64                   128
+ *   K = 4096, N = 11008      14.4 / 15.7 / 17.5   19.2 / 23.5 / 17.4   22.3 / 36.7 / 18.6   31.0 / 63.0 / 22.5
+ *     gated                  21.2 / 24.3 / 30.3   32.0 / 38.0 / 31.8   39.6 / 65.8 / 35.5   58.2 / 118 / 35.9
+ *   K = N = 4096             7.0 / 7.9 / 12.5     10.1 / 11.7 / 14.6   16.4 / 18.5 / 18.4   23.2 / 28.2 / 26.0
+ *     gated                  10.5 / 11.9 / 19.2   16.0 / 18.6 / 21.0   25.0 / 28.6 / 20.8   34.3 / 52.2 / 21.1
+ * So a 16-bit copy of the weight is the faster one from 17 to 32 rows of a large weight on (of 4096 x
+ * 4096 from 48 to 64), where there is memory for it. One made for the call (gemm_epi_w4_dequantize: 21 to 23 us
+ * at 4096 x 11008, twice that for a gated layer's two) pays from about 100 rows with G = 32, and beyond 256
+ * it is the only way.
  */
 GEMM_EPI_API gemm_epi_plan_t gemm_epi_w4_plan(int64_t T, int64_t N, int64_t K, int64_t group, gemm_epi_dtype dtype,
                                               int epilog, gemm_epi_act act, uint32_t flags);
